@@ -5,7 +5,8 @@
  * "KDA Chunk Prefill on Ascend A3" (sections "Function and tensor contract"
  * and "Mathematical definition") and, for single-token decode, on the page
  * "flashinfer.kda_decode.packed_kda_decode" (section "Parameters"), plus
- * the prefill's optional backward (kda_chunk_backward).
+ * the prefill's optional backward (kda_chunk_backward) and, for the layers of
+ * a hybrid model that attend over all tokens, attention (kda_attn_*).
  *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller.  The
@@ -482,6 +483,180 @@ int kda_chunk_backward(const void* q, const void* k, const void* v,
  */
 size_t kda_chunk_backward_workspace_size(int32_t B, int32_t T, int32_t H, int32_t HV,
                                          int32_t K, int32_t V, int32_t num_seqs);
+
+/* ------------------------------------------------------------------------
+ * Full attention: the layers that a hybrid model runs between its KDA layers.
+ * They take their inputs as the entry points above do (packed sequences by
+ * cu_seqlens, a cache addressed by int32 tables, caller-owned workspaces, every
+ * launch on the caller's stream) and share these conventions:
+ *   - heads are 128 wide (Dh == 128); HQ % HKV == 0 and query head h reads
+ *     key/value head h / (HQ / HKV).
+ *   - a stride is the number of elements from one token's row to the next:
+ *     at least heads * 128, at most 2^23, a multiple of 8.  Heads are compact
+ *     within a row.  Rows of a batch follow one another at that stride, so
+ *     q, k and v may be slices of one projection's rows.
+ *   - scale multiplies every score: positive and below 1e30 (128^-1/2 is usual).
+ *   - softmax statistics and all sums are float32; the weights (and, in the
+ *     backward, the scores' gradients) are rounded once to bf16 as operands of
+ *     the second matrix product, outputs once when they are stored.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kda_attn_prefill -- causal attention over whole prompts.
+ *
+ * For token i of a sequence and query head h, over its tokens j <= i:
+ *     z_j = scale q_i . k_j,  lse_i = log sum_j exp(z_j),
+ *     o_i = sum_j exp(z_j - lse_i) v_j.
+ *   q           bf16 [B, T, HQ, 128], k, v bf16 [B, T, HKV, 128], at q_stride,
+ *               k_stride, v_stride
+ *   cu_seqlens, num_seqs   as for kda_chunk_prefill, except that the last
+ *               offset may be less than T and the first more than 0: tokens
+ *               outside the sequences are neither read nor written.  An offset
+ *               is taken as min(max(offset, 0), T), a sequence that would end
+ *               before it starts as empty; sequences that overlap give
+ *               undefined outputs.
+ *   o           bf16 [B, T, HQ, 128], dense
+ *   lse         fp32 [B, HQ, T], dense, or NULL
+ * A token's values reach no other sequence's outputs, whatever they are.
+ * Within a sequence, an infinity or NaN in v_j also reaches rows before j in
+ * the same 32 rows (as 0 * v_j).
+ * Sizes: B >= 1, T >= 0 (0 enqueues nothing), 1 <= HQ <= 65535.  o and lse must
+ * not alias inputs.  Deterministic.
+ */
+int kda_attn_prefill(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                     int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T,
+                     int32_t HQ, int32_t HKV, int32_t Dh, float scale, void* o, float* lse, void* stream);
+
+/*
+ * kda_attn_backward -- gradients of kda_attn_prefill: of sum(o * d_out) with
+ * respect to q, k and v.
+ *
+ *   q .. scale  as for kda_attn_prefill, and its outputs o and lse
+ *   d_out       bf16 [B, T, HQ, 128], dense
+ *   dq          [B, T, HQ, 128], dk, dv [B, T, HKV, 128], dense, bf16
+ *               (KDA_GRAD_INPUT_DTYPE) or float32 (KDA_GRAD_FLOAT32); dk and dv
+ *               are summed over the query heads that share a head.  Tokens
+ *               outside the sequences are left as they were.
+ *   workspace   at least kda_attn_backward_workspace_size(...) bytes; contents
+ *               on entry do not matter; calls that share one must not overlap
+ * Deterministic: no atomics, one order of every sum.
+ */
+int kda_attn_backward(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, const void* o, const float* lse, const void* d_out,
+                      const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T, int32_t HQ, int32_t HKV,
+                      int32_t Dh, float scale, void* dq, void* dk, void* dv, int32_t grad_dtype,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kda_attn_backward_workspace_size -- bytes of workspace kda_attn_backward
+ * needs on the current device (num_seqs: 0 when cu_seqlens is NULL); 0 for
+ * sizes it rejects and for T == 0.  8 bytes per token and query head; where
+ * there are too few key tiles to fill the device, also 1 KB per token,
+ * key/value head and part (16 parts at most).
+ */
+size_t kda_attn_backward_workspace_size(int32_t B, int32_t T, int32_t HQ, int32_t HKV, int32_t Dh,
+                                        int32_t num_seqs);
+
+/*
+ * The paged cache.  Page p holds page_size successive tokens of one sequence:
+ * codes [HKV][page_size][128] in e4m3 (OCP, no infinities) at
+ * cache + p * page_stride bytes, and scale[p * HKV + head] in float32, keys and
+ * values apart; a value is code * scale.  page_size: 16, 32, 64, 128 or 256
+ * (others KDA_ERR_UNSUPPORTED); page_stride: at least HKV * page_size * 128, at
+ * most 2^32, a multiple of 16; num_pages * page_size < 2^31.  A slot is
+ * page * page_size + offset.
+ */
+
+/*
+ * kda_attn_tables -- the tables of one serving step, from the requests'
+ * lengths: page table, slot map, packed offsets and new lengths.
+ *
+ *   cached_lens int32 [N]  tokens of each request that the cache holds
+ *   new_lens    int32 [N]  tokens that this step adds (0: none).  Negative
+ *               lengths count as 0; their sum must stay below 2^31.
+ *   page_table  int32, row n at page_table + n * table_stride, table_width
+ *               entries, in place: entry c of row n is the page of tokens
+ *               c * page_size .. of request n.  The first
+ *               ceil(cached_lens[n] / page_size) entries are kept, the new
+ *               tokens' further entries are written, the rest are left.
+ *   free_pages  int32 [num_free]  page ids, taken from place *free_head on
+ *               (0 if free_head is NULL), request after request.  Where they
+ *               run out, -1 is written instead.
+ *   num_tokens  entries of `slots`
+ *   cu_seqlens  int32 [N + 1]  offsets of the new tokens, packed
+ *   slots       int32 [num_tokens]  slot of each new token; -1 behind the last
+ *               one, and for tokens without a page or past table_width pages
+ *   kv_lens     int32 [N]  cached_lens + new_lens
+ *   next_head   int32 [1]  *free_head + the pages asked for: the next call's
+ *               free_head; past num_free where pages were missing
+ * kv_lens must not alias the lengths, nor next_head free_head.
+ * Sizes: 1 <= N <= 8192, table_width >= 1, table_stride >= table_width.
+ */
+int kda_attn_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t N, int32_t* page_table,
+                    int64_t table_stride, int32_t table_width, const int32_t* free_pages, int32_t num_free,
+                    const int32_t* free_head, int32_t page_size, int32_t num_tokens, int32_t* cu_seqlens,
+                    int32_t* slots, int32_t* kv_lens, int32_t* next_head, void* stream);
+
+/*
+ * kda_attn_cache_store -- new keys and values into the paged cache.
+ *
+ *   k, v        bf16 [T, HKV, 128] at k_stride, v_stride
+ *   slots       int32 [T]  each token's slot; outside [0, num_pages *
+ *               page_size) -- -1 among them -- it is not stored
+ *   k_cache, v_cache, k_scale, v_scale   the cache, in place
+ * Per (page, head) that gets tokens, with a the largest finite magnitude of
+ * the new tokens' values and 2^e the least power of two, e >= -64, with
+ * 448 * 2^e >= a: if the first new token stands at offset 0 the scale becomes
+ * 2^e (the page is taken over), otherwise max(scale, 2^e), and if that is more
+ * than before the codes of the earlier offsets are multiplied by the quotient
+ * and rounded again.  New codes are value / scale, rounded to nearest even;
+ * infinities and NaN become NaN.  Codes at later offsets are left.
+ * The tokens of one page must stand one after another with successive slots
+ * (as kda_attn_tables deals them); otherwise its scale is undefined.
+ */
+int kda_attn_cache_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                         int32_t T, int32_t HKV, int32_t Dh, void* k_cache, void* v_cache, float* k_scale,
+                         float* v_scale, int32_t page_size, int64_t page_stride, int32_t num_pages, void* stream);
+
+/*
+ * kda_attn_decode -- attention of the last Q tokens of every sequence over
+ * the paged cache (which holds them already).
+ *
+ * Query i of sequence n stands at position kv_lens[n] - Q + i; over the tokens
+ * j up to there, with page_table as above:
+ *     z_j = scale q . (kc_j ks),  o = sum_j softmax(z)_j vc_j vs,
+ *     lse = log sum_j exp(z_j).
+ *   q           bf16 [N, Q, HQ, 128] at q_stride from token to token
+ *   page_table  int32, row n at page_table + n * table_stride.  A page outside
+ *               [0, num_pages) holds no tokens: they are left out.
+ *   kv_lens     int32 [N]  negative counts as 0, more than table_width pages
+ *               as that many.  A query before position 0 or without tokens
+ *               gives o = 0 and lse = -inf.
+ *   o           bf16 [N, Q, HQ, 128], dense
+ *   lse         fp32 [N, Q, HQ], dense, or NULL
+ *   workspace   at least kda_attn_decode_workspace_size(...) bytes; contents on
+ *               entry do not matter; calls that share one must not overlap
+ * What lies in a page behind the sequence's end does not reach the outputs,
+ * whatever it is.  A NaN code within the last Q - 1 values also reaches the
+ * queries before it.  How a sequence is cut among waves depends on all
+ * sequences of the call, so the last bits of a row may differ from batch to
+ * batch; the same call gives the same bits.
+ * Sizes: N >= 0 (0 enqueues nothing), 1 <= Q <= 1024, num_pages >= 1,
+ * N * Q * HQ <= 2^26.
+ */
+int kda_attn_decode(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, int32_t page_size, int64_t page_stride,
+                    int32_t num_pages, const int32_t* page_table, int64_t table_stride, int32_t table_width,
+                    const int32_t* kv_lens, int32_t N, int32_t Q, int32_t HQ, int32_t HKV, int32_t Dh, float scale,
+                    void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kda_attn_decode_workspace_size -- bytes of workspace kda_attn_decode needs on
+ * the current device; 0 for sizes it rejects.  About 8 or 17 KB (up to 16 or
+ * more query rows, Q * HQ / HKV) per wave the device holds and per (sequence,
+ * head, 32 rows).
+ */
+size_t kda_attn_decode_workspace_size(int32_t N, int32_t Q, int32_t HQ, int32_t HKV, int32_t Dh);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,15 @@ Entry points (same names as the C ABI, without the ``kda_`` prefix):
   packed_decode(mixed_qkv, raw_gate, raw_beta, A_log, dt_bias, state_pool,
                 state_indices)                    -> o
   state_to_pool(state, state_pool, state_indices)       -> state_pool
+  chunk_backward(q, k, v, g, beta, initial_state, d_out, ...)
+                                                  -> (dq, dk, dv, dg, dbeta, d_initial_state)
+and for the full-attention layers of a hybrid stack (attn.py):
+  attn_prefill(q, k, v, cu_seqlens=None)          -> (o, lse)
+  attn_backward(q, k, v, o, lse, d_out, cu_seqlens=None) -> (dq, dk, dv)
+  attn_tables(cached_lens, new_lens, page_table, free_pages, free_head, page_size, num_tokens)
+                                                  -> (cu_seqlens, slots, kv_lens, next_head)
+  attn_cache_store(k, v, k_cache, v_cache, k_scale, v_scale, slots)
+  attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens) -> (o, lse)
 """
 
 import ctypes
@@ -31,7 +40,9 @@ LIB_PATH = os.path.join(_HERE, "libkda.so")
 EXPORTS = ("kda_status_string", "kda_build_id", "kda_qk_l2norm", "kda_chunk_prefill", "kda_chunk_prefill_split",
            "kda_chunk_prefill_fused", "kda_chunk_prefill_noalloc", "kda_chunk_prefill_partition",
            "kda_chunk_prefill_workspace_size", "kda_prefill_overlap_wait_limit", "kda_decode", "kda_packed_decode",
-           "kda_state_to_pool", "kda_chunk_backward", "kda_chunk_backward_workspace_size")
+           "kda_state_to_pool", "kda_chunk_backward", "kda_chunk_backward_workspace_size", "kda_attn_prefill",
+           "kda_attn_backward", "kda_attn_backward_workspace_size", "kda_attn_tables", "kda_attn_cache_store",
+           "kda_attn_decode", "kda_attn_decode_workspace_size")
 
 _lib = None
 
@@ -90,6 +101,26 @@ def load():
                                        _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, ctypes.c_size_t, _vp]
     lib.kda_chunk_backward_workspace_size.restype = ctypes.c_size_t
     lib.kda_chunk_backward_workspace_size.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32, _i32]
+    _f32, _size = ctypes.c_float, ctypes.c_size_t
+    lib.kda_attn_prefill.restype = ctypes.c_int
+    lib.kda_attn_prefill.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                     _f32, _vp, _vp, _vp]
+    lib.kda_attn_backward.restype = ctypes.c_int
+    lib.kda_attn_backward.argtypes = [_vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                      _i32, _i32, _f32, _vp, _vp, _vp, _i32, _vp, _size, _vp]
+    lib.kda_attn_backward_workspace_size.restype = _size
+    lib.kda_attn_backward_workspace_size.argtypes = [_i32, _i32, _i32, _i32, _i32, _i32]
+    lib.kda_attn_tables.restype = ctypes.c_int
+    lib.kda_attn_tables.argtypes = [_vp, _vp, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _vp,
+                                    _vp, _vp]
+    lib.kda_attn_cache_store.restype = ctypes.c_int
+    lib.kda_attn_cache_store.argtypes = [_vp, _vp, _i64, _i64, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32,
+                                         _i64, _i32, _vp]
+    lib.kda_attn_decode.restype = ctypes.c_int
+    lib.kda_attn_decode.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _vp, _i64, _i32, _vp, _i32,
+                                    _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _size, _vp]
+    lib.kda_attn_decode_workspace_size.restype = _size
+    lib.kda_attn_decode_workspace_size.argtypes = [_i32, _i32, _i32, _i32, _i32]
     _lib = lib
     return lib
 
@@ -444,3 +475,7 @@ def packed_decode(mixed_qkv, raw_gate, raw_beta, A_log, dt_bias, state_pool, sta
                                  _ptr(state_indices), B, H, K, V, _ptr(out), _stream())
     _check(code, "kda_packed_decode")
     return out
+
+
+from .attn import (attn_backward, attn_backward_workspace_size, attn_cache_store, attn_decode,  # noqa: E402,F401
+                   attn_decode_workspace_size, attn_prefill, attn_tables)

@@ -1,0 +1,284 @@
+// The paged 8-bit cache of the full-attention layers: what fills it (export
+// kda_attn_cache_store) and the tables that say where (export
+// kda_attn_tables).
+//
+// A page holds page_size successive tokens of one sequence, for every
+// key/value head [page_size][128] codes in e4m3 and one float32 scale; keys
+// and values apart.  A value is code x scale.  Scales made here are powers of
+// two: e4m3 codes have the same relative step at every power of two, so a
+// finer scale would buy nothing, and a page whose scale has to grow when a
+// larger token is appended only shifts the exponents of what it holds (exact
+// but for codes that fall below e4m3's normal range).
+#include "attn_device.h"
+#include "kda_host.h"
+
+namespace {
+
+using namespace kda::attn;
+
+// ---------------------------------------------------------------- store
+
+constexpr int kStoreWaves = 4;
+constexpr int kWindow = 16;        // tokens that a workgroup looks at
+constexpr int kLeast = -64;        // smallest exponent of a scale
+
+struct StoreParams {
+  const uint16_t *k, *v;
+  int64_t k_stride, v_stride;
+  const int32_t* slots;
+  int T, HKV, page_size, shift;
+  int64_t num_slots, page_stride;
+  uint8_t *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+};
+
+// Larger of the finite magnitudes in eight bf16 values and `top` (bits).
+__device__ __forceinline__ uint32_t finite_top(const u32x4 x, uint32_t top) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = x[i] & 0x7fffu, hi = (x[i] >> 16) & 0x7fffu;
+    if (lo < 0x7f80u) top = max(top, lo);
+    if (hi < 0x7f80u) top = max(top, hi);
+  }
+  return top;
+}
+
+// Two words of codes from eight values, each rounded to nearest even once;
+// infinities and NaN become NaN.
+__device__ __forceinline__ u32x2 to_codes(const u32x4 x, float f) {
+  u32x2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    int w = 0;
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(kda::bf16lo(x[2 * i]) * f, kda::bf16hi(x[2 * i]) * f, w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(kda::bf16lo(x[2 * i + 1]) * f, kda::bf16hi(x[2 * i + 1]) * f, w, true);
+    r[i] = uint32_t(w);
+  }
+  return r;
+}
+
+// Four codes times f, rounded again.
+__device__ __forceinline__ uint32_t rescale(uint32_t w, float f) {
+  int r = 0;
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_cvt_f32_fp8(int(w), 0) * f,
+                                      __builtin_amdgcn_cvt_f32_fp8(int(w), 1) * f, r, false);
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_cvt_f32_fp8(int(w), 2) * f,
+                                      __builtin_amdgcn_cvt_f32_fp8(int(w), 3) * f, r, true);
+  return uint32_t(r);
+}
+
+// One wave stores `n` tokens of one head, the first of them at offset `off` of
+// a page.  rows: the first token's row; page: the (page, head)'s codes.
+__device__ __forceinline__ void store_run(const uint16_t* rows, int64_t stride, int n, uint8_t* page, int off,
+                                          float* scale, int lane) {
+  const int row = lane >> 4, at = (lane & 15) * 8;
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int i = row; i < n; i += 4) top = finite_top(*reinterpret_cast<const u32x4*>(rows + i * stride + at), top);
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) top = max(top, uint32_t(__shfl_xor(int(top), i, 64)));
+  // least e with 448 x 2^e >= top, 448 = 1.75 x 2^8
+  const int e = max(int(top >> 7) - 127 - 8 + int((top & 127) > 96), kLeast);
+  const float fits = __uint_as_float(uint32_t(127 + e) << 23);
+  const float was = off ? *scale : 0.0f;
+  const float now = fmaxf(was, fits);
+  if (off && now != was) {                     // the page's earlier tokens take the new scale
+    const float f = was / now;
+    const int words = off * (D / 16);          // 16 codes each
+    for (int i = lane; i < words; i += 64) {
+      u32x4* p = reinterpret_cast<u32x4*>(page) + i;
+      u32x4 w = *p;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = rescale(w[j], f);
+      *p = w;
+    }
+  }
+  if (lane == 0) *scale = now;
+  const float f = 1.0f / now;
+#pragma unroll 4
+  for (int i = row; i < n; i += 4) {
+    const u32x4 x = *reinterpret_cast<const u32x4*>(rows + i * stride + at);
+    *reinterpret_cast<u32x2*>(page + (off + i) * D + at) = to_codes(x, f);
+  }
+}
+
+// A run is a stretch of tokens whose slots follow one another within a page.
+// One wave takes one run of one head, so a page's scale has one writer.
+__global__ __launch_bounds__(64 * kStoreWaves) void attn_cache_store_kernel(StoreParams p) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int head = blockIdx.x % unsigned(p.HKV);
+  const int t0 = int(blockIdx.x / unsigned(p.HKV)) * kWindow;
+  auto slot_at = [&](int t) -> int {           // -1: no such token, or not stored
+    const int s = t >= 0 && t < p.T ? p.slots[t] : -1;
+    return s >= 0 && s < p.num_slots ? s : -1;
+  };
+  const int mine = lane < kWindow ? slot_at(t0 + lane) : -1;
+  const int before = lane < kWindow ? slot_at(t0 + lane - 1) : -1;
+  const bool leads = mine >= 0 && ((mine & (p.page_size - 1)) == 0 || before < 0 || before != mine - 1);
+  uint64_t runs = __ballot(leads);
+  for (int k = 0; runs; ++k) {
+    const int i = __builtin_ctzll(runs);
+    runs &= runs - 1;
+    if (k % kStoreWaves != wave) continue;
+    const int t = t0 + i, slot = __builtin_amdgcn_readlane(mine, i);
+    const int off = slot & (p.page_size - 1), most = p.page_size - off;
+    int n = 0;
+    for (bool whole = true; whole && n < most; ) {
+      const uint64_t same = __ballot(n + lane < most && slot_at(t + n + lane) == slot + n + lane);
+      whole = same == ~uint64_t(0);
+      n += whole ? 64 : __builtin_ctzll(~same);
+    }
+    const int64_t page = slot >> p.shift;
+    const int64_t codes = page * p.page_stride + int64_t(head) * p.page_size * D;
+    const int64_t scale = page * p.HKV + head;
+    store_run(p.k + t * p.k_stride + head * D, p.k_stride, n, p.k_cache + codes, off, p.k_scale + scale, lane);
+    store_run(p.v + t * p.v_stride + head * D, p.v_stride, n, p.v_cache + codes, off, p.v_scale + scale, lane);
+  }
+}
+
+// ---------------------------------------------------------------- tables
+
+constexpr int kTableThreads = 512;
+constexpr int kMostRequests = 8192;
+constexpr int kTokensPerBlock = 2048;
+
+struct TableParams {
+  const int32_t *cached, *fresh;
+  int32_t* table;
+  int64_t table_stride;
+  int width, N, page_size, shift, tokens, num_free;
+  const int32_t *free_pages, *free_head;
+  int32_t *cu, *slots, *lens, *next_head;
+};
+
+// Every workgroup makes the two prefix sums (new tokens, new pages) over all
+// requests for itself in LDS, then looks up its share of the tokens and of the
+// new pages: one launch, no word passed between workgroups.
+__global__ __launch_bounds__(kTableThreads) void attn_tables_kernel(TableParams p) {
+  __shared__ int32_t cu[kMostRequests + 1], pages[kMostRequests + 1];
+  __shared__ int32_t wave_sums[2][kTableThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (p.N + kTableThreads - 1) / kTableThreads;
+
+  auto old_len = [&](int n) { return max(p.cached[n], 0); };
+  auto new_len = [&](int n) { return max(p.fresh[n], 0); };
+  auto pages_of = [&](int64_t tokens) { return int(min((tokens + p.page_size - 1) >> p.shift, int64_t(p.width))); };
+
+  int tok = 0, pg = 0;
+  for (int i = 0; i < per; ++i) {
+    const int n = tid * per + i;
+    if (n >= p.N) break;
+    const int64_t a = old_len(n), b = a + new_len(n);
+    tok += int(b - a);
+    pg += pages_of(b) - pages_of(a);
+  }
+  int tok_at = tok, pg_at = pg;                // inclusive sums over the wave, then over the workgroup
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int x = __shfl_up(tok_at, d, 64), y = __shfl_up(pg_at, d, 64);
+    if (lane >= d) tok_at += x, pg_at += y;
+  }
+  if (lane == 63) wave_sums[0][wave] = tok_at, wave_sums[1][wave] = pg_at;
+  __syncthreads();
+  tok_at -= tok, pg_at -= pg;
+  for (int w = 0; w < wave; ++w) tok_at += wave_sums[0][w], pg_at += wave_sums[1][w];
+  for (int i = 0; i < per; ++i) {
+    const int n = tid * per + i;
+    if (n >= p.N) break;
+    const int64_t a = old_len(n), b = a + new_len(n);
+    cu[n] = tok_at, pages[n] = pg_at;
+    tok_at += int(b - a);
+    pg_at += pages_of(b) - pages_of(a);
+    if (n == p.N - 1) cu[p.N] = tok_at, pages[p.N] = pg_at;
+  }
+  __syncthreads();
+
+  const int head = p.free_head ? max(*p.free_head, 0) : 0;
+  const int total_tokens = cu[p.N], total_pages = pages[p.N];
+  auto free_page = [&](int j) -> int {         // the j-th page that this call takes, -1 if there is none
+    const int64_t at = int64_t(head) + j;
+    return j >= 0 && at < p.num_free ? p.free_pages[at] : -1;
+  };
+  auto find = [&](const int32_t* sums, int x) {   // the request n with sums[n] <= x < sums[n + 1]
+    int lo = 0, hi = p.N;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sums[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+
+  const int first = blockIdx.x * kTokensPerBlock, last = min(first + kTokensPerBlock, p.tokens);
+  for (int t = first + tid; t < last; t += kTableThreads) {
+    int slot = -1;
+    if (t < total_tokens) {
+      const int n = find(cu, t);
+      const int64_t pos = int64_t(old_len(n)) + t - cu[n];
+      const int64_t c = pos >> p.shift;
+      if (c >= 0 && c < p.width) {
+        const int held = pages_of(old_len(n));
+        const int id = c < held ? p.table[n * p.table_stride + c] : free_page(pages[n] + int(c) - held);
+        if (id >= 0 && id <= (0x7fffffff >> p.shift)) slot = int((uint32_t(id) << p.shift) + (pos & (p.page_size - 1)));
+      }
+    }
+    p.slots[t] = slot;
+  }
+  const int threads = gridDim.x * kTableThreads, me = blockIdx.x * kTableThreads + tid;
+  for (int j = me; j < total_pages; j += threads) {
+    const int n = find(pages, j);
+    const int c = pages_of(old_len(n)) + j - pages[n];
+    if (c >= 0 && c < p.width) p.table[n * p.table_stride + c] = free_page(j);
+  }
+  for (int n = me; n <= p.N; n += threads) {
+    p.cu[n] = cu[n];
+    if (n < p.N) p.lens[n] = int(min(int64_t(old_len(n)) + new_len(n), int64_t(0x7fffffff)));
+  }
+  if (me == 0) *p.next_head = int(min(int64_t(head) + total_pages, int64_t(0x7fffffff)));
+}
+
+}  // namespace
+
+extern "C" int kda_attn_cache_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                                    const int32_t* slots, int32_t T, int32_t HKV, int32_t Dh, void* k_cache,
+                                    void* v_cache, float* k_scale, float* v_scale, int32_t page_size,
+                                    int64_t page_stride, int32_t num_pages, void* stream) {
+  if (T < 0) return KDA_ERR_SHAPE;
+  int e = kda::attn_heads(HKV, HKV, Dh);
+  if (e == KDA_OK) e = kda::attn_stride(k_stride, HKV);
+  if (e == KDA_OK) e = kda::attn_stride(v_stride, HKV);
+  if (e == KDA_OK) e = kda::attn_cache(HKV, page_size, page_stride, num_pages);
+  if (e != KDA_OK) return e;
+  if (T == 0 || num_pages == 0) return KDA_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return KDA_ERR_NULL;
+  for (const void* x : {k, v, static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
+    if (!kda::aligned16(x)) return KDA_ERR_ALIGN;
+  const int64_t blocks = (int64_t(T) + kWindow - 1) / kWindow * HKV;
+  if (blocks > 0x7fffffff) return KDA_ERR_SHAPE;
+  const StoreParams p{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_stride, v_stride, slots,
+                      T, HKV, page_size, __builtin_ctz(page_size), int64_t(num_pages) * page_size, page_stride,
+                      static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale};
+  hipLaunchKernelGGL(attn_cache_store_kernel, dim3(unsigned(blocks)), dim3(64 * kStoreWaves), 0,
+                     kda::as_stream(stream), p);
+  return kda::launch_status();
+}
+
+extern "C" int kda_attn_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t N, int32_t* page_table,
+                               int64_t table_stride, int32_t table_width, const int32_t* free_pages,
+                               int32_t num_free, const int32_t* free_head, int32_t page_size, int32_t num_tokens,
+                               int32_t* cu_seqlens, int32_t* slots, int32_t* kv_lens, int32_t* next_head,
+                               void* stream) {
+  if (N < 1 || N > kMostRequests || table_width < 1 || table_stride < table_width || num_free < 0 || num_tokens < 0)
+    return KDA_ERR_SHAPE;
+  if (!kda::attn_page(page_size)) return KDA_ERR_UNSUPPORTED;
+  if (!cached_lens || !new_lens || !page_table || !cu_seqlens || !kv_lens || !next_head || (num_tokens && !slots) ||
+      (num_free && !free_pages))
+    return KDA_ERR_NULL;
+  // read by every workgroup, written by one
+  if (kv_lens == cached_lens || kv_lens == new_lens || next_head == free_head) return KDA_ERR_SHAPE;
+  const TableParams p{cached_lens, new_lens, page_table, table_stride, table_width, N, page_size,
+                      __builtin_ctz(page_size), num_tokens, num_free, free_pages, free_head,
+                      cu_seqlens, slots, kv_lens, next_head};
+  const unsigned blocks = unsigned((int64_t(num_tokens) + kTokensPerBlock - 1) / kTokensPerBlock);
+  hipLaunchKernelGGL(attn_tables_kernel, dim3(blocks ? blocks : 1), dim3(kTableThreads), 0, kda::as_stream(stream), p);
+  return kda::launch_status();
+}

@@ -1,0 +1,515 @@
+// Attention of a few new tokens per sequence over the paged 8-bit cache
+// (export kda_attn_decode).
+//
+// For query token i of Q (its position is len - Q + i) and query head h, over
+// the tokens j <= len - Q + i of the sequence:
+//     z_j = scale q . (kc_j ks_page(j)),   o = sum_j softmax(z)_j vc_j vs_page(j).
+// The Q queries of the HQ / HKV heads that share a key/value head are rows of
+// one matrix, so each byte of the cache is read once for all of them.
+//
+// The cache's bytes bound it: 256 per token and key/value head.  The work is
+// therefore dealt out by tokens: all (sequence, head, row tile) segments in
+// order, in units of 64 tokens, form one line of U units that is cut into
+// equal pieces, one per wave, whatever the sequences' lengths are -- which only
+// the device knows.  Waves never meet: each keeps its own running maximum, sum
+// and output in registers and its loads in flight.  A segment that lies in one
+// wave's piece is finished there; otherwise its waves leave float32 parts that
+// attn_decode_join_kernel brings together in order.
+//
+// S^T = K Q^T and O^T += V^T P^T on 16x16x32 matrix instructions, codes widened
+// to bfloat16 (exact).  Contraction orders are chosen so that no data moves
+// between lanes: K's columns in the order in which a lane loads 32 bytes of a
+// row, V's rows in the order in which the accumulator of S^T holds the keys,
+// and V's 8-byte loads (one key, 8 columns) turned into 8 operands by byte
+// permutes inside the lane.
+#include "attn_device.h"
+#include "kda_host.h"
+
+namespace {
+
+using namespace kda::attn;
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kUnit = 64;                    // tokens
+constexpr float kSlack = 8.0f;               // see attn_prefill.hip: rescale only when the maximum grew this much
+
+struct Params {
+  const uint16_t* q;
+  int64_t q_stride;
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  int N, Q, HQ, HKV, width, shift, num_pages;
+  int64_t page_stride;
+  float scale;
+  uint16_t* o;
+  float* lse;
+  int rows, tile_rows, row_tiles;            // Q x group; rows of one tile; tiles
+  int waves;
+  float* parts;                              // [waves + segments][tile_rows][D + 2]
+};
+
+// ---------------------------------------------------------------- who does what
+
+__device__ __forceinline__ int length(const Params& p, int n) {
+  const int64_t most = int64_t(p.width) << p.shift;
+  return int(min(int64_t(max(p.lens[n], 0)), min(most, int64_t(0x7fffffff))));
+}
+// An empty sequence has one unit too: somebody writes its zeros.
+__device__ __forceinline__ int units_of(int len) { return max((len + kUnit - 1) / kUnit, 1); }
+
+__device__ __forceinline__ int64_t wave_sum(int64_t x) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d, 64);
+  return x;
+}
+
+// Units of all sequences before `stop` (of one head and row tile), by a wave.
+__device__ __forceinline__ int64_t units_before(const Params& p, int stop) {
+  int64_t sum = 0;
+  for (int n = threadIdx.x & 63; n < stop; n += 64) sum += units_of(length(p, n));
+  return wave_sum(sum);
+}
+
+struct Place {
+  int n;             // sequence
+  int64_t before;    // units of the sequences before it, times heads and row tiles
+};
+
+// The sequence that holds unit u of the line; per = heads x row tiles.
+__device__ __forceinline__ Place find_unit(const Params& p, int64_t u, int per) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = p.N;
+  int64_t before = 0;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64;
+    const int a = min(lo + lane * step, hi), b = min(a + step, hi);
+    int64_t own = 0;
+    for (int n = a; n < b; ++n) own += units_of(length(p, n));
+    own *= per;
+    int64_t end = own;                       // inclusive sum over the lanes
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int64_t x = __shfl_up(end, d, 64);
+      if (lane >= d) end += x;
+    }
+    const uint64_t upto = __ballot(before + end <= u);      // lanes whose sequences all end before u
+    const int k = min(int(__builtin_popcountll(upto)), (hi - lo + step - 1) / step - 1);
+    before += __shfl(end - own, k, 64);
+    lo += k * step;
+    hi = min(lo + step, hi);
+  }
+  return {__builtin_amdgcn_readfirstlane(lo), before};
+}
+
+// ---------------------------------------------------------------- codes to operands
+
+// Eight codes (two words) as eight bfloat16 values.
+__device__ __forceinline__ bf16x8 widen(uint32_t a, uint32_t b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+  const bf16x2 w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+  const bf16x2 w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+  const bf16x2 w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+  return (bf16x8){w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
+}
+
+// Pages of up to 64 successive tiles of 16 tokens, one per lane.
+struct Pages {
+  int id;            // -1: no tokens there
+  float ks, vs;
+};
+
+template <int NT>
+__global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
+  // waves of one place in all workgroups follow one another: a short line fills every compute unit evenly
+  const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6) * int(gridDim.x) + int(blockIdx.x));
+  const int per = p.HKV * p.row_tiles;
+  const int64_t total = units_before(p, p.N) * per;
+  const int64_t waves = min(total, int64_t(p.waves));      // each has one unit at least
+  if (w >= waves) return;
+  int64_t u = total * w / waves;
+  const int64_t end = total * (w + 1) / waves;
+  const Place at = find_unit(p, u, per);
+  int n = at.n;
+  int len = length(p, n), units = units_of(len);
+  int seg = int((u - at.before) / units), first = int((u - at.before) - int64_t(seg) * units);
+  const int G = p.HQ / p.HKV;
+  const float c = p.scale * kLog2e;
+
+  while (u < end) {
+    // -------- one segment: sequence n, head hkv, rows row0 .. row0 + tile_rows - 1
+    const int hkv = seg / p.row_tiles, row0 = (seg - hkv * p.row_tiles) * p.tile_rows;
+    const int last = int(min(int64_t(units), first + end - u));     // units first .. last - 1
+    const int rows = min(p.rows - row0, 16 * NT);
+
+    bf16x8 q[NT][4];
+    int limit[NT];                           // tokens that the lane's row sees
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = row0 + min(16 * t + l16, rows - 1), i = r / G;
+      const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (hkv * G + r - i * G) * D + 32 * g4;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) q[t][s] = *reinterpret_cast<const bf16x8*>(src + 8 * s);
+      limit[t] = len - p.Q + i + 1;
+    }
+    f32x4 o[NT][8];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t] = -INFINITY, l[t] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[t][d] = (f32x4)(0.0f);
+    }
+
+    const int32_t* table = p.table + n * p.table_stride;
+    auto pages_at = [&](int unit) {          // of the 64 tiles from `unit` on
+      Pages x{-1, 0.0f, 0.0f};
+      const int64_t token = int64_t(unit) * kUnit + lane * 16;
+      if (token < len) {
+        const int id = table[token >> p.shift];
+        if (id >= 0 && id < p.num_pages) {
+          x.id = id;
+          x.ks = p.k_scale[int64_t(id) * p.HKV + hkv] * c;
+          x.vs = p.v_scale[int64_t(id) * p.HKV + hkv];
+        }
+      }
+      return x;
+    };
+    // First byte of tile j (0 .. 3) of a unit whose pages start at lane `from`;
+    // a tile without tokens reads page 0, and is masked.
+    auto tile_at = [&](const Pages& x, int unit, int from, int j) {
+      const int id = max(__builtin_amdgcn_readlane(x.id, from + j), 0);
+      const int inside = (unit * kUnit + 16 * j) & ((1 << p.shift) - 1);
+      return int64_t(id) * p.page_stride + ((int64_t(hkv) << p.shift) + inside) * D;
+    };
+    u32x4 kr[4][2];                          // tile j: 32 bytes of row l16 from byte 32 g4
+    u32x2 vr[4][4];                          // tile j: bytes 8 l16 .. + 7 of rows 4 g4 .. + 3
+    auto load_k = [&](const Pages& x, int unit, int from) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* b = p.k_cache + tile_at(x, unit, from, j);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) kr[j][i] = *reinterpret_cast<const u32x4*>(b + uint32_t(l16 * D + 32 * g4 + 16 * i));
+      }
+    };
+    auto load_v = [&](const Pages& x, int unit, int from) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint8_t* b = p.v_cache + tile_at(x, unit, from, j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vr[j][i] = *reinterpret_cast<const u32x2*>(b + uint32_t((4 * g4 + i) * D + 8 * l16));
+      }
+    };
+
+    Pages now = pages_at(first);
+    load_k(now, first, 0);
+    load_v(now, first, 0);
+    int from = 0;                            // the unit's first tile in `now`
+    for (int unit = first; unit < last; ++unit) {
+      const int key0 = unit * kUnit;
+      const bool masked = key0 + kUnit > len - p.Q + 1 || (__ballot(now.id < 0) >> from & 15) != 0;
+      f32x4 s[NT][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[t][j] = (f32x4)(0.0f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const bf16x8 a = widen(kr[j][k >> 1][2 * (k & 1)], kr[j][k >> 1][2 * (k & 1) + 1]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) s[t][j] = mfma16(a, q[t][k], s[t][j]);
+        }
+      }
+      float ks[4], vs[4];
+      bool none[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ks[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.ks), from + j));
+        vs[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(now.vs), from + j));
+        none[j] = __builtin_amdgcn_readlane(now.id, from + j) < 0;
+      }
+      // the next unit's keys, in flight over the softmax and the second product
+      const bool more = unit + 1 < last;
+      Pages then = now;
+      int then_from = from + 4;
+      if (more) {
+        if (then_from == 64) then = pages_at(unit + 1), then_from = 0;
+        load_k(then, unit + 1, then_from);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[t][j] *= ks[j];
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (none[j] || key0 + 16 * j + 4 * g4 + e >= limit[t]) s[t][j][e] = -INFINITY;
+        }
+        float mx = s[t][0][0];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[t][j][e]);
+        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+        mx = half_max(mx);
+        if (__any(mx - m[t] > kSlack)) {
+          const float top = fmaxf(m[t], mx);
+          const float f = __builtin_amdgcn_exp2f(m[t] - (top == -INFINITY ? 0.0f : top));
+          m[t] = top;
+          l[t] *= f;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) o[t][d] *= f;
+        }
+        const float b = m[t] == -INFINITY ? 0.0f : m[t];    // a row that has seen nothing stays at zero
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = __builtin_amdgcn_exp2f(s[t][j][e] - b);
+            l[t] += x;
+            s[t][j][e] = x * vs[j];
+          }
+      }
+      if (masked) {                          // what lies behind the end may be anything: NaN codes too
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (none[j] || key0 + 16 * j + 4 * g4 + i >= len) vr[j][i] = (u32x2){0, 0};
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        bf16x8 pb[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = s[t][j][e], x[4 + e] = s[t][j + 1][e];
+          pb[t] = pack8(x);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)          // columns 8 l16 + 4 b + 0 .. 3
+#pragma unroll
+          for (int d = 0; d < 4; d += 2) {
+            // bytes d and d + 1 of eight keys -> the codes of column d, then of column d + 1
+            uint32_t two[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int jj = j + (e >> 1), i = 2 * (e & 1);
+              two[e] = __builtin_amdgcn_perm(vr[jj][i + 1][b], vr[jj][i][b], d ? 0x07030602u : 0x05010400u);
+            }
+            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+            bf16x2 lo[4], hi[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              lo[e] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(two[e], 1.0f, false);
+              hi[e] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(two[e], 1.0f, true);
+            }
+            const bf16x8 a0 = {lo[0][0], lo[0][1], lo[1][0], lo[1][1], lo[2][0], lo[2][1], lo[3][0], lo[3][1]};
+            const bf16x8 a1 = {hi[0][0], hi[0][1], hi[1][0], hi[1][1], hi[2][0], hi[2][1], hi[3][0], hi[3][1]};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              o[t][4 * b + d] = mfma16(a0, pb[t], o[t][4 * b + d]);
+              o[t][4 * b + d + 1] = mfma16(a1, pb[t], o[t][4 * b + d + 1]);
+            }
+          }
+      }
+      if (more) load_v(then, unit + 1, then_from);
+      now = then;
+      from = then_from;
+    }
+
+    // -------- its rows: finished, or a part.  Lane (l16, g4) holds row l16,
+    // columns 8 (4 g4 + e) + d in o[d][e].
+    const bool whole = first == 0 && last == units;
+    const int64_t segment = int64_t(n) * per + seg;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float sum = l[t] + __shfl_xor(l[t], 16, 64);
+      sum = half_sum(sum);
+      const int r = 16 * t + l16;
+      if (r >= rows) continue;
+      if (whole) {
+        const int i = (row0 + r) / G, head = hkv * G + row0 + r - i * G;
+        const int64_t out = (int64_t(n) * p.Q + i) * p.HQ + head;
+        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x[8];
+#pragma unroll
+          for (int d = 0; d < 8; ++d) x[d] = o[t][d][e] * f;
+          *reinterpret_cast<bf16x8*>(p.o + out * D + 8 * (4 * g4 + e)) = pack8(x);
+        }
+        if (p.lse && g4 == 0) p.lse[out] = (m[t] + __log2f(sum)) * kLn2;
+      } else {
+        float* part = p.parts + ((segment + w) * p.tile_rows + r) * (D + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int d = 0; d < 8; d += 4)
+            *reinterpret_cast<f32x4*>(part + 8 * (4 * g4 + e) + d) =
+                (f32x4){o[t][d][e], o[t][d + 1][e], o[t][d + 2][e], o[t][d + 3][e]};
+        if (g4 == 0) part[D] = m[t], part[D + 1] = sum;
+      }
+    }
+    u += last - first;
+    first = 0;
+    if (++seg == per) {
+      seg = 0;
+      if (++n < p.N) len = length(p, n), units = units_of(len);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- joining the parts
+
+// A workgroup per (segment, row).  Wave w of the line has units
+// floor(U w / waves) .. floor(U (w + 1) / waves) - 1, so unit u belongs to
+// wave ceil((u + 1) waves / U) - 1.
+constexpr int kStreams = kThreads / 32;
+__global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(Params p) {
+  __shared__ float weights[kThreads], red[kStreams][D], stat[kWaves];
+  const int per = p.HKV * p.row_tiles;
+  const int r = int(blockIdx.x % unsigned(p.tile_rows));
+  const int64_t segment = blockIdx.x / unsigned(p.tile_rows);
+  const int n = int(segment / per), seg = int(segment - int64_t(n) * per);
+  const int hkv = seg / p.row_tiles, row = (seg - hkv * p.row_tiles) * p.tile_rows + r;
+  if (row >= p.rows) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t total = units_before(p, p.N) * per;
+  const int units = units_of(length(p, n));
+  const int64_t a = units_before(p, n) * per + int64_t(seg) * units, b = a + units - 1;
+  const int64_t waves = min(total, int64_t(p.waves));
+  const int w0 = int(((a + 1) * waves + total - 1) / total - 1);
+  const int w1 = int(((b + 1) * waves + total - 1) / total - 1);
+  if (w0 == w1) return;                      // finished by its wave
+  const int64_t step = int64_t(p.tile_rows) * (D + 4);
+  const float* part = p.parts + ((segment + w0) * p.tile_rows + r) * (D + 4);
+  const int count = w1 - w0 + 1;             // slots of successive waves follow one another
+
+  auto over_all = [&](float x, bool top) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const float y = __shfl_xor(x, d, 64);
+      x = top ? fmaxf(x, y) : x + y;
+    }
+    __syncthreads();
+    if (lane == 0) stat[wave] = x;
+    __syncthreads();
+    x = stat[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) x = top ? fmaxf(x, stat[i]) : x + stat[i];
+    return x;
+  };
+  float m = -INFINITY;
+  for (int i = tid; i < count; i += kThreads) m = fmaxf(m, part[i * step + D]);
+  m = over_all(m, true);
+  const float base = m == -INFINITY ? 0.0f : m;
+  const int stream = tid >> 5, col = (tid & 31) * 4;
+  f32x4 acc = (f32x4)(0.0f);
+  float sum = 0.0f;
+  for (int i0 = 0; i0 < count; i0 += kThreads) {
+    __syncthreads();
+    const int i = i0 + tid;
+    float f = 0.0f;
+    if (i < count) {
+      f = __builtin_amdgcn_exp2f(part[i * step + D] - base);
+      sum += f * part[i * step + D + 1];
+    }
+    weights[tid] = f;
+    __syncthreads();
+    const int here = min(count - i0, kThreads);
+#pragma unroll 4
+    for (int k = stream; k < here; k += kStreams)
+      acc += *reinterpret_cast<const f32x4*>(part + (i0 + k) * step + col) * weights[k];
+  }
+  sum = over_all(sum, false);
+  *reinterpret_cast<f32x4*>(&red[stream][col]) = acc;
+  __syncthreads();
+  if (tid < 32) {
+#pragma unroll
+    for (int s = 1; s < kStreams; ++s) acc += *reinterpret_cast<const f32x4*>(&red[s][col]);
+    const int G = p.HQ / p.HKV, i = row / G;
+    const int64_t out = (int64_t(n) * p.Q + i) * p.HQ + hkv * G + row - i * G;
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    acc *= f;
+    *reinterpret_cast<u32x2*>(p.o + out * D + col) =
+        (u32x2){kda::pack_bf16(acc[0], acc[1]), kda::pack_bf16(acc[2], acc[3])};
+    if (p.lse && tid == 0) p.lse[out] = (m + __log2f(sum)) * kLn2;
+  }
+}
+
+struct Plan {
+  int rows, tile_rows, row_tiles, waves;
+  int64_t segments;
+  size_t bytes;
+};
+
+// Rows in tiles of 16 (one matrix instruction) or 32.  Eight waves per compute
+// unit, two per SIMD: with 16 KB of a unit in flight in each they cover the
+// memory's latency.
+Plan plan_for(int64_t N, int64_t Q, int HQ, int HKV) {
+  Plan x;
+  x.rows = int(Q * (HQ / HKV));
+  x.tile_rows = x.rows <= 16 ? 16 : 32;
+  x.row_tiles = (x.rows + x.tile_rows - 1) / x.tile_rows;
+  x.waves = kda::device_cus() * 8;
+  x.segments = N * HKV * x.row_tiles;
+  x.bytes = size_t(x.waves + x.segments) * x.tile_rows * (D + 4) * sizeof(float);
+  return x;
+}
+
+int sizes(int32_t N, int32_t Q, int32_t HQ, int32_t HKV, int32_t Dh) {
+  const int e = kda::attn_heads(HQ, HKV, Dh);
+  if (e != KDA_OK) return e;
+  if (N < 0 || Q < 1 || Q > 1024 || int64_t(N) * HKV * Q * (HQ / HKV) > (1 << 26)) return KDA_ERR_SHAPE;
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" size_t kda_attn_decode_workspace_size(int32_t N, int32_t Q, int32_t HQ, int32_t HKV, int32_t Dh) {
+  return sizes(N, Q, HQ, HKV, Dh) == KDA_OK && N > 0 ? plan_for(N, Q, HQ, HKV).bytes : 0;
+}
+
+extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale, int32_t page_size, int64_t page_stride,
+                               int32_t num_pages, const int32_t* page_table, int64_t table_stride,
+                               int32_t table_width, const int32_t* kv_lens, int32_t N, int32_t Q, int32_t HQ,
+                               int32_t HKV, int32_t Dh, float scale, void* o, float* lse, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  int e = sizes(N, Q, HQ, HKV, Dh);
+  if (e == KDA_OK) e = kda::attn_scale(scale);
+  if (e == KDA_OK) e = kda::attn_stride(q_stride, HQ);
+  if (e == KDA_OK) e = kda::attn_cache(HKV, page_size, page_stride, num_pages);
+  if (e != KDA_OK) return e;
+  if (num_pages < 1 || table_width < 1 || table_stride < table_width) return KDA_ERR_SHAPE;
+  if (N == 0) return KDA_OK;
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !kv_lens || !o || !workspace)
+    return KDA_ERR_NULL;
+  for (const void* x : {q, k_cache, v_cache, static_cast<const void*>(o), static_cast<const void*>(workspace)})
+    if (!kda::aligned16(x)) return KDA_ERR_ALIGN;
+  const Plan x = plan_for(N, Q, HQ, HKV);
+  if (workspace_bytes < x.bytes) return KDA_ERR_WORKSPACE;
+  if (x.segments * x.tile_rows > 0x7fffffff) return KDA_ERR_SHAPE;
+  const Params p{static_cast<const uint16_t*>(q), q_stride, static_cast<const uint8_t*>(k_cache),
+                 static_cast<const uint8_t*>(v_cache), k_scale, v_scale, page_table, table_stride, kv_lens,
+                 N, Q, HQ, HKV, table_width, __builtin_ctz(page_size), num_pages, page_stride, scale,
+                 static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, x.waves,
+                 static_cast<float*>(workspace)};
+  const hipStream_t st = kda::as_stream(stream);
+  const dim3 grid(unsigned(x.waves / kWaves));
+  if (x.tile_rows == 16)
+    hipLaunchKernelGGL(attn_decode_kernel<1>, grid, dim3(kThreads), 0, st, p);
+  else
+    hipLaunchKernelGGL(attn_decode_kernel<2>, grid, dim3(kThreads), 0, st, p);
+  hipLaunchKernelGGL(attn_decode_join_kernel, dim3(unsigned(x.segments * x.tile_rows)), dim3(kThreads), 0, st, p);
+  return kda::launch_status();
+}

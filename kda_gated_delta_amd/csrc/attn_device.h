@@ -1,0 +1,210 @@
+// Device helpers shared by the full-attention kernels (gfx950 / CDNA4,
+// wave64): matrix-instruction types, cross-half exchange, packed-sequence
+// lookup and the swizzled tile loads.
+#pragma once
+
+#include "kda_device.h"
+
+namespace kda {
+namespace attn {
+
+constexpr int D = kHead;                 // head width of q, k and v
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_ptr;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+// Matrix product D = A B + C with A 32 x 16, B 16 x 32.  Lane l holds row
+// (A) or column (B) l % 32 at contraction indices 8 (l / 32) .. + 7, and of C
+// and D column l % 32 at rows 8 (r / 4) + 4 (l / 32) + r % 4 for r = 0 .. 15.
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+// The same with 16 x 32 by 32 x 16: row or column l % 16 at indices
+// 8 (l / 16) .. + 7; of C and D column l % 16 at rows 4 (l / 16) + r.
+__device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+
+// Sum and maximum of a lane's value and that of the lane 32 away.
+__device__ __forceinline__ u32x2 halves(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return (u32x2){r[0], r[1]};
+}
+__device__ __forceinline__ float half_max(float x) {
+  const u32x2 r = halves(x);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const u32x2 r = halves(x);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Eight float32 values to a matrix operand, each rounded to bfloat16 once.
+__device__ __forceinline__ bf16x8 pack8(const float* x) {
+  const u32x4 v = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+  return as_bf16x8(v);
+}
+
+// ---------------------------------------------------------------- packed sequences
+
+// A launch covers the rows of every sequence in tiles of BM tokens.  With
+// equal sequences tile and sequence follow from the index.  With packed ones
+// tile t of sequence n has index floor(cu[n] / BM) + n + t: a sequence of L
+// tokens has at most floor(L / BM) + 1 tiles, so indices never meet, and there
+// are at most floor(T / BM) + N of them.
+struct Rows {
+  int64_t first;   // the sequence's first token, counted over the whole batch
+  int b, start;    // the same as batch row and place in it
+  int len;         // its tokens
+  int row0;        // the tile's first row within it; >= len: no such tile
+};
+
+// Largest n in [0, N) with floor(cu[n] / BM) + n <= slot (0 if none): the
+// whole wave looks at 64 places at once.  cu need not be valid: it is read
+// within its N + 1 entries only.
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int slot, int BM) {
+  int lo = 0, hi = N;                         // the answer is in [lo, hi)
+  const int lane = threadIdx.x & 63;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 63) / 64;
+    const int at = lo + lane * step;
+    const bool ok = at < hi && max(cu[at], 0) / BM <= slot - at;
+    const uint64_t m = __ballot(ok);
+    const int k = m ? 63 - __builtin_clzll(m) : 0;
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+__device__ __forceinline__ Rows find_rows(const int32_t* cu, int N, int T, int slot, int BM) {
+  Rows r;
+  if (!cu) {
+    r.b = slot % unsigned(N);
+    r.start = 0;
+    r.first = int64_t(r.b) * T;
+    r.len = T;
+    r.row0 = int(slot / unsigned(N)) * BM;
+    return r;
+  }
+  const int n = find_sequence(cu, N, slot, BM);
+  const int c0 = min(max(cu[n], 0), T), c1 = min(cu[n + 1], T);
+  r.b = 0;
+  r.first = r.start = c0;
+  r.len = max(c1 - c0, 0);
+  const int t = slot - c0 / BM - n;
+  r.row0 = t < 0 || t > r.len / BM ? r.len : t * BM;
+  return r;
+}
+
+// ---------------------------------------------------------------- tiles in LDS
+
+// A tile of 64 rows of 128 bf16 lies in LDS as 64 lines of 256 bytes, loaded
+// straight from memory in 16-byte pieces (1 KB, four lines, by one instruction
+// of a wave).  Piece c of line r is stored at place c ^ swizzle(r), which
+// serves both ways of reading: 16 successive lines hold one piece in 16
+// different places (read_rows), and 4 successive lines hold one 64-byte block
+// in the four quarters of their 256 bytes (read_columns), so neither meets a
+// bank twice.  The load writes lane after lane; the swizzle is made by what
+// each lane reads.  Lines at or past `rows` read as zero (the buffer's size
+// ends there), so nothing behind a sequence enters a product.
+constexpr int kTile = 64;                 // rows of a tile
+constexpr int kTileBytes = kTile * 256;
+
+__device__ __forceinline__ int swizzle(int line) { return 4 * (line & 3) + ((line >> 2) & 3); }
+
+template <int WAVES>
+struct TileLoad {
+  uint32_t lane_off;                      // byte offset of this lane's piece in the wave's first 1 KB block
+  uint32_t step;                          // bytes between the wave's blocks: 4 * WAVES lines
+  static_assert(16 % WAVES == 0 && WAVES % 4 == 0, "the swizzle must be the same in all blocks of a wave");
+
+  __device__ __forceinline__ void init(int wave, int lane, int64_t stride) {
+    const int line = 4 * wave + (lane >> 4);
+    lane_off = uint32_t(line * stride * 2) + ((lane & 15) ^ swizzle(line)) * 16;
+    step = uint32_t(4 * WAVES * stride * 2);
+  }
+  // base: the tile's first row; rows: how many of its rows exist (1 or more).
+  __device__ __forceinline__ void issue(const uint16_t* base, int64_t stride, int rows, unsigned char* lds,
+                                        int wave) const {
+    const uint32_t bytes = uint32_t(min(rows, kTile)) * uint32_t(stride * 2);
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, bytes, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < 16 / WAVES; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr*)(lds + (wave + j * WAVES) * 1024), 16, lane_off,
+                                               j * step, 0, 0);
+  }
+};
+
+// 64 float32 of `src`, of which `rows` exist (the others read as zero), by one
+// wave.
+__device__ __forceinline__ void load_floats(const float* src, int rows, unsigned char* lds, int lane) {
+  const auto rsrc =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(src), 0, uint32_t(min(rows, kTile)) * 4, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr*)lds, 4, lane * 4, 0, 0, 0);
+}
+
+// Rows r .. r + 31 of a tile as an A or B operand: contraction indices
+// 16 s + 8 h .. + 7 of row r + l32.
+__device__ __forceinline__ bf16x8 read_rows(const unsigned char* tile, int r, int l32, int h, int s) {
+  const int line = r + l32;
+  return *reinterpret_cast<const bf16x8*>(tile + line * 256 + (((2 * s + h) ^ swizzle(line)) * 16));
+}
+
+// The transpose of a tile's rows r + 16 m .. + 15 at columns c .. c + 31, as an
+// A or B operand: lane l32 takes column c + l32 at rows
+// r + 16 m + 4 h + j % 4 + 8 (j / 4) for j = 0 .. 7, the order in which the
+// accumulator of a 32 x 32 product holds its rows.  (A transposing read
+// gathers, in every 16 lanes, element i & 3 of the 8-byte pieces addressed by
+// lanes (i >> 2) + 4 e into element e of lane i.)
+__device__ __forceinline__ bf16x8 read_columns(const unsigned char* tile, int r, int m, int c, int lane) {
+  const int j = lane & 15, h = lane >> 5;
+  const int line = r + 16 * m + 4 * h + (j >> 2);
+  const int col = c + (lane & 16) + 4 * (j & 3);
+  const int piece = col >> 3, half = (col & 4) * 2;
+  const unsigned char* p = tile + line * 256 + half;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + (piece ^ swizzle(line)) * 16));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * 256 + (piece ^ swizzle(line + 8)) * 16));
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// Row stores of a transposed accumulator (columns = rows of the output): the
+// lane pair (l, l + 32) holds columns d of one row in groups of four; exchanged,
+// each lane stores 16 bytes.
+__device__ __forceinline__ void store_row32(uint16_t* row, const f32x16& acc, float f, int h) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    uint32_t a0 = pack_bf16(acc[4 * i] * f, acc[4 * i + 1] * f), a1 = pack_bf16(acc[4 * i + 2] * f, acc[4 * i + 3] * f);
+    uint32_t b0 = pack_bf16(acc[4 * i + 4] * f, acc[4 * i + 5] * f), b1 = pack_bf16(acc[4 * i + 6] * f, acc[4 * i + 7] * f);
+    const auto x = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+    const auto y = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+    *reinterpret_cast<u32x4*>(row + 8 * (i + h)) = (u32x4){x[0], y[0], x[1], y[1]};
+  }
+}
+
+// The same in float32.
+__device__ __forceinline__ void store_row32(float* row, const f32x16& acc, float f, int h) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<f32x4*>(row + 8 * i + 4 * h) =
+        (f32x4){acc[4 * i] * f, acc[4 * i + 1] * f, acc[4 * i + 2] * f, acc[4 * i + 3] * f};
+}
+
+// vmcnt(0), nothing else
+constexpr int kWaitLoads = 0x0F70;
+
+}  // namespace attn
+}  // namespace kda

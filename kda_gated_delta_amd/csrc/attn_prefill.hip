@@ -1,0 +1,174 @@
+// Causal attention over whole prompts (export kda_attn_prefill).
+//
+// For every query head h and token i of a sequence, with key/value head
+// h / (HQ / HKV), z_ij = scale q_i . k_j for j <= i:
+//     lse_i = log sum_j exp(z_ij),   o_i = sum_j exp(z_ij - lse_i) v_j.
+//
+// One pass over the keys with a running maximum and sum.  A wave owns 32
+// query rows and keeps their output transposed, O^T [128][32], in its
+// registers.  Per tile of 64 keys (K and V in LDS, two buffers, loaded
+// straight from memory while the previous tile is used):
+//     S^T = K Q^T          (rows = keys, so a query's scores lie in one lane pair)
+//     P^T = exp2(c S^T - c m)
+//     O^T += V^T P^T       (V^T by transposing LDS reads)
+// The accumulator of S^T holds, in each lane, exactly the contraction indices
+// that the next product wants of its B operand (in the order read_columns
+// takes V's rows), so P never leaves its registers: no exchange, no LDS.
+#include "attn_device.h"
+#include "kda_host.h"
+
+namespace {
+
+using namespace kda::attn;
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int BM = 32 * kWaves;            // query rows of a workgroup
+
+struct Params {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;    // elements from token to token
+  const int32_t* cu;
+  int N, T, HQ, HKV, slots;
+  float scale;
+  uint16_t* o;
+  float* lse;
+};
+
+// How far (in powers of two) a row's maximum may grow before its sum and
+// output are brought to the new one: weights stay below 2^8, far inside
+// float32 and bfloat16, and most tiles skip the 64 multiplications.
+constexpr float kSlack = 8.0f;
+
+__global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(Params p) {
+  __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l32 = lane & 31, h = lane >> 5;
+
+  // Neighbouring workgroups take the heads of one tile, key/value heads
+  // fastest: workgroups are dealt to the eight XCDs in turn, so a head's keys
+  // stay in one XCD's cache.  Late tiles, which have most keys, start first.
+  const unsigned id = blockIdx.x, kv_heads = p.HKV, G = unsigned(p.HQ) / kv_heads;
+  const int hkv = int(id % kv_heads);
+  const int hq = hkv * G + int((id / kv_heads) % G);
+  const Rows rows = find_rows(p.cu, p.N, p.T, p.slots - 1 - int(id / unsigned(p.HQ)), BM);
+  if (rows.row0 >= rows.len) return;
+
+  const int r0 = rows.row0 + wave * 32;                   // this wave's first row
+  const int r = min(r0 + l32, rows.len - 1);              // this lane's; rows behind the end repeat the last one
+  bf16x8 q[8];                                            // as B operands
+  const uint16_t* src = p.q + (rows.first + r) * p.q_stride + hq * D + 8 * h;
+#pragma unroll
+  for (int s = 0; s < 8; ++s) q[s] = *reinterpret_cast<const bf16x8*>(src + 16 * s);
+  f32x16 o[4];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) o[d] = (f32x16)(0.0f);
+  float m = -INFINITY, l = 0.0f;                          // l: this lane's keys only, until the end
+  const float c = p.scale * kLog2e;
+
+  const int keys = min(rows.len, rows.row0 + BM);         // keys that the last row of the tile sees
+  const int tiles = (keys + kTile - 1) / kTile;
+  TileLoad<kWaves> kload, vload;
+  kload.init(wave, lane, p.k_stride);
+  vload.init(wave, lane, p.v_stride);
+  const uint16_t* kb = p.k + rows.first * p.k_stride + hkv * D;
+  const uint16_t* vb = p.v + rows.first * p.v_stride + hkv * D;
+  kload.issue(kb, p.k_stride, rows.len, lds, wave);
+  vload.issue(vb, p.v_stride, rows.len, lds + kTileBytes, wave);
+
+  for (int t = 0; t < tiles; ++t) {
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    kda::lds_barrier();
+    unsigned char* kt = lds + (t & 1) * 2 * kTileBytes;
+    const unsigned char* vt = kt + kTileBytes;
+    if (t + 1 < tiles) {
+      unsigned char* next = lds + ((t + 1) & 1) * 2 * kTileBytes;
+      const int64_t at = int64_t(t + 1) * kTile;
+      kload.issue(kb + at * p.k_stride, p.k_stride, rows.len - int(at), next, wave);
+      vload.issue(vb + at * p.v_stride, p.v_stride, rows.len - int(at), next + kTileBytes, wave);
+    }
+    const int key0 = t * kTile;
+    if (key0 > r0 + 31) continue;                         // wholly after this wave's rows
+
+    f32x16 s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s[u] = (f32x16)(0.0f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[u] = mfma32(read_rows(kt, 32 * u, l32, h, k), q[k], s[u]);
+    }
+    if (key0 + kTile - 1 > r0) {                          // some (row, key) pairs lie after the diagonal
+      const int last = r0 + l32 - key0;                   // the last key of the tile that the row sees
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (32 * u + 8 * (e >> 2) + 4 * h + (e & 3) > last) s[u][e] = -INFINITY;
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[u][e]);
+    mx = half_max(mx);
+    if (__any((mx - m) * c > kSlack)) {
+      const float now = fmaxf(m, mx);
+      const float f = __builtin_amdgcn_exp2f((m - now) * c);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= f;
+    }
+    const float b = m * c;
+    float sum = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[u][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][e], c, -b));
+        sum += s[u][e];
+      }
+    l += sum;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = s[u][8 * k + j];
+        const bf16x8 w = pack8(x);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[d] = mfma32(read_columns(vt, 32 * u, k, 32 * d, lane), w, o[d]);
+      }
+  }
+
+  const float total = half_sum(l);
+  if (r0 + l32 >= rows.len) return;                       // both lanes of a pair alike
+  const float f = 1.0f / total;
+  uint16_t* dst = p.o + ((rows.first + r) * p.HQ + hq) * D;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) store_row32(dst + 32 * d, o[d], f, h);
+  if (p.lse && h == 0)
+    p.lse[(int64_t(rows.b) * p.HQ + hq) * p.T + rows.start + r] = m * p.scale + __logf(total);
+}
+
+}  // namespace
+
+extern "C" int kda_attn_prefill(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T,
+                                int32_t HQ, int32_t HKV, int32_t Dh, float scale, void* o, float* lse,
+                                void* stream) {
+  const int e = kda::attn_check(cu_seqlens, num_seqs, B, T, HQ, HKV, Dh, scale, q_stride, k_stride, v_stride);
+  if (e != KDA_OK) return e;
+  if (T == 0) return KDA_OK;
+  if (!q || !k || !v || !o) return KDA_ERR_NULL;
+  if (!kda::aligned16(q) || !kda::aligned16(k) || !kda::aligned16(v) || !kda::aligned16(o) || (lse && !kda::aligned16(lse)))
+    return KDA_ERR_ALIGN;
+  const int64_t slots = cu_seqlens ? int64_t(T) / BM + num_seqs : int64_t(B) * ((T + BM - 1) / BM);
+  if (slots * HQ > 0x7fffffff) return KDA_ERR_SHAPE;
+  const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+                 q_stride, k_stride, v_stride, cu_seqlens, cu_seqlens ? num_seqs : B, T, HQ, HKV, int(slots), scale,
+                 static_cast<uint16_t*>(o), lse};
+  hipLaunchKernelGGL(attn_prefill_kernel, dim3(unsigned(slots * HQ)), dim3(kThreads), 0, kda::as_stream(stream), p);
+  return kda::launch_status();
+}

@@ -36,4 +36,38 @@ inline int launch_status() {
   return e == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
+// Sizes shared by the full-attention entry points: heads 128 wide, query
+// heads in equal groups, packed sequences in one batch row, strides that keep
+// every row 16-byte aligned and a 64-row tile's offsets within 31 bits.
+inline int attn_heads(int32_t HQ, int32_t HKV, int32_t D) {
+  if (HQ < 1 || HKV < 1 || HQ > 65535 || HQ % HKV != 0) return KDA_ERR_SHAPE;
+  return D == 128 ? KDA_OK : KDA_ERR_UNSUPPORTED;
+}
+inline int attn_stride(int64_t stride, int32_t heads) {
+  if (stride < int64_t(heads) * 128 || stride > (int64_t(1) << 23)) return KDA_ERR_SHAPE;
+  return stride % 8 == 0 ? KDA_OK : KDA_ERR_ALIGN;
+}
+// Pages of 16 to 256 tokens, a power of two; slot numbers (page x page_size +
+// offset) fit int32.
+inline bool attn_page(int32_t page_size) {
+  return page_size >= 16 && page_size <= 256 && (page_size & (page_size - 1)) == 0;
+}
+inline int attn_cache(int32_t HKV, int32_t page_size, int64_t page_stride, int32_t num_pages) {
+  if (!attn_page(page_size)) return KDA_ERR_UNSUPPORTED;
+  if (num_pages < 0 || int64_t(num_pages) * page_size > 0x7fffffff) return KDA_ERR_SHAPE;
+  if (page_stride < int64_t(HKV) * page_size * 128 || page_stride > (int64_t(1) << 32)) return KDA_ERR_SHAPE;
+  return page_stride % 16 == 0 ? KDA_OK : KDA_ERR_ALIGN;
+}
+inline int attn_scale(float scale) { return scale > 0.0f && scale < 1e30f ? KDA_OK : KDA_ERR_SHAPE; }
+inline int attn_check(const int32_t* cu, int32_t num_seqs, int32_t B, int32_t T, int32_t HQ, int32_t HKV, int32_t D,
+                      float scale, int64_t q_stride, int64_t k_stride, int64_t v_stride) {
+  if (B < 1 || T < 0 || (cu && (B != 1 || num_seqs < 1))) return KDA_ERR_SHAPE;
+  int e = attn_heads(HQ, HKV, D);
+  if (e == KDA_OK) e = attn_scale(scale);
+  if (e == KDA_OK) e = attn_stride(q_stride, HQ);
+  if (e == KDA_OK) e = attn_stride(k_stride, HKV);
+  if (e == KDA_OK) e = attn_stride(v_stride, HKV);
+  return e;
+}
+
 }  // namespace kda

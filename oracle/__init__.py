@@ -22,6 +22,7 @@ Modules
   handoff    prefill final states stored into the bf16 decode pool
   packed_decode  the decode step from packed QKV and raw gate/beta logits
   backward   gradients of the forward by float64 autodiff of the recurrence
+  attention  full attention, its gradients, the e4m3 cache and its tables
 
 Pinning status: every public function here is pinned by tests that do not
 re-type its formula (closed forms, the pages' worked example, invariants,
