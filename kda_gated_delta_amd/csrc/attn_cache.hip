@@ -19,7 +19,6 @@ using namespace kda::attn;
 // ---------------------------------------------------------------- store
 
 constexpr int kStoreWaves = 4;
-constexpr int kWindow = 16;        // tokens that a workgroup looks at
 constexpr int kLeast = -64;        // smallest exponent of a scale
 
 struct StoreParams {
@@ -67,25 +66,34 @@ __device__ __forceinline__ uint32_t rescale(uint32_t w, float f) {
   return uint32_t(r);
 }
 
-// One wave stores `n` tokens of one head, the first of them at offset `off` of
-// a page.  rows: the first token's row; page: the (page, head)'s codes.
+// One wave stores `n` tokens of one head, keys or values, the first of them at
+// offset `off` of a page.  rows: the first token's row; page: the (page, head)'s
+// codes.  Up to 64 tokens are read once and kept in registers between the
+// maximum and the codes; longer runs (pages of 128 and 256) are read twice.
 __device__ __forceinline__ void store_run(const uint16_t* rows, int64_t stride, int n, uint8_t* page, int off,
                                           float* scale, int lane) {
   const int row = lane >> 4, at = (lane & 15) * 8;
+  const float was = off ? *scale : 0.0f;
+  u32x4 kept[16];
   uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (4 * i < n) kept[i] = *reinterpret_cast<const u32x4*>(rows + min(4 * i + row, n - 1) * stride + at);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (4 * i < n) top = finite_top(kept[i], top);
 #pragma unroll 4
-  for (int i = row; i < n; i += 4) top = finite_top(*reinterpret_cast<const u32x4*>(rows + i * stride + at), top);
+  for (int i = 64 + row; i < n; i += 4) top = finite_top(*reinterpret_cast<const u32x4*>(rows + i * stride + at), top);
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) top = max(top, uint32_t(__shfl_xor(int(top), i, 64)));
   // least e with 448 x 2^e >= top, 448 = 1.75 x 2^8
   const int e = max(int(top >> 7) - 127 - 8 + int((top & 127) > 96), kLeast);
   const float fits = __uint_as_float(uint32_t(127 + e) << 23);
-  const float was = off ? *scale : 0.0f;
   const float now = fmaxf(was, fits);
   if (off && now != was) {                     // the page's earlier tokens take the new scale
     const float f = was / now;
-    const int words = off * (D / 16);          // 16 codes each
-    for (int i = lane; i < words; i += 64) {
+    const int pieces = off * (D / 16);         // 16 codes each
+    for (int i = lane; i < pieces; i += 64) {
       u32x4* p = reinterpret_cast<u32x4*>(page) + i;
       u32x4 w = *p;
 #pragma unroll
@@ -95,31 +103,37 @@ __device__ __forceinline__ void store_run(const uint16_t* rows, int64_t stride, 
   }
   if (lane == 0) *scale = now;
   const float f = 1.0f / now;
+  uint8_t* dst = page + (off + row) * D + at;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (4 * i + row < n) *reinterpret_cast<u32x2*>(dst + 4 * i * D) = to_codes(kept[i], f);
 #pragma unroll 4
-  for (int i = row; i < n; i += 4) {
-    const u32x4 x = *reinterpret_cast<const u32x4*>(rows + i * stride + at);
-    *reinterpret_cast<u32x2*>(page + (off + i) * D + at) = to_codes(x, f);
-  }
+  for (int i = 64 + row; i < n; i += 4)
+    *reinterpret_cast<u32x2*>(page + (off + i) * D + at) =
+        to_codes(*reinterpret_cast<const u32x4*>(rows + i * stride + at), f);
 }
 
 // A run is a stretch of tokens whose slots follow one another within a page.
-// One wave takes one run of one head, so a page's scale has one writer.
+// One wave takes the keys or the values of one run of one head, so a page's
+// scale has one writer.  A workgroup looks at WINDOW tokens for the runs that
+// begin there.
+template <int WINDOW>
 __global__ __launch_bounds__(64 * kStoreWaves) void attn_cache_store_kernel(StoreParams p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int head = blockIdx.x % unsigned(p.HKV);
-  const int t0 = int(blockIdx.x / unsigned(p.HKV)) * kWindow;
+  const int t0 = int(blockIdx.x / unsigned(p.HKV)) * WINDOW;
   auto slot_at = [&](int t) -> int {           // -1: no such token, or not stored
     const int s = t >= 0 && t < p.T ? p.slots[t] : -1;
     return s >= 0 && s < p.num_slots ? s : -1;
   };
-  const int mine = lane < kWindow ? slot_at(t0 + lane) : -1;
-  const int before = lane < kWindow ? slot_at(t0 + lane - 1) : -1;
+  const int mine = lane < WINDOW ? slot_at(t0 + lane) : -1;
+  const int before = lane < WINDOW ? slot_at(t0 + lane - 1) : -1;
   const bool leads = mine >= 0 && ((mine & (p.page_size - 1)) == 0 || before < 0 || before != mine - 1);
   uint64_t runs = __ballot(leads);
-  for (int k = 0; runs; ++k) {
+  for (int k = 0; runs; k += 2) {              // tasks k (keys) and k + 1 (values)
     const int i = __builtin_ctzll(runs);
     runs &= runs - 1;
-    if (k % kStoreWaves != wave) continue;
+    if ((k ^ wave) & (kStoreWaves - 2)) continue;
     const int t = t0 + i, slot = __builtin_amdgcn_readlane(mine, i);
     const int off = slot & (p.page_size - 1), most = p.page_size - off;
     int n = 0;
@@ -131,9 +145,19 @@ __global__ __launch_bounds__(64 * kStoreWaves) void attn_cache_store_kernel(Stor
     const int64_t page = slot >> p.shift;
     const int64_t codes = page * p.page_stride + int64_t(head) * p.page_size * D;
     const int64_t scale = page * p.HKV + head;
-    store_run(p.k + t * p.k_stride + head * D, p.k_stride, n, p.k_cache + codes, off, p.k_scale + scale, lane);
-    store_run(p.v + t * p.v_stride + head * D, p.v_stride, n, p.v_cache + codes, off, p.v_scale + scale, lane);
+    if (wave & 1)
+      store_run(p.v + t * p.v_stride + head * D, p.v_stride, n, p.v_cache + codes, off, p.v_scale + scale, lane);
+    else
+      store_run(p.k + t * p.k_stride + head * D, p.k_stride, n, p.k_cache + codes, off, p.k_scale + scale, lane);
   }
+}
+
+template <int WINDOW>
+int64_t store_blocks(const StoreParams& p) { return (int64_t(p.T) + WINDOW - 1) / WINDOW * p.HKV; }
+template <int WINDOW>
+void launch_store(const StoreParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL(attn_cache_store_kernel<WINDOW>, dim3(unsigned(store_blocks<WINDOW>(p))), dim3(64 * kStoreWaves),
+                     0, stream, p);
 }
 
 // ---------------------------------------------------------------- tables
@@ -252,13 +276,18 @@ extern "C" int kda_attn_cache_store(const void* k, const void* v, int64_t k_stri
   if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return KDA_ERR_NULL;
   for (const void* x : {k, v, static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
     if (!kda::aligned16(x)) return KDA_ERR_ALIGN;
-  const int64_t blocks = (int64_t(T) + kWindow - 1) / kWindow * HKV;
-  if (blocks > 0x7fffffff) return KDA_ERR_SHAPE;
   const StoreParams p{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_stride, v_stride, slots,
                       T, HKV, page_size, __builtin_ctz(page_size), int64_t(num_pages) * page_size, page_stride,
                       static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale};
-  hipLaunchKernelGGL(attn_cache_store_kernel, dim3(unsigned(blocks)), dim3(64 * kStoreWaves), 0,
-                     kda::as_stream(stream), p);
+  // Few tokens (a decode step: every one a run of its own) want a workgroup
+  // for each two, so that no wave has a second run; in prompts, where a run is a page,
+  // most workgroups find none and wide windows keep them few.
+  if (store_blocks<2>(p) <= 8 * kda::device_cus())
+    launch_store<2>(p, kda::as_stream(stream));
+  else if (store_blocks<16>(p) <= 0x7fffffff)
+    launch_store<16>(p, kda::as_stream(stream));
+  else
+    return KDA_ERR_SHAPE;
   return kda::launch_status();
 }
 

@@ -49,7 +49,8 @@ struct Params {
   float* lse;
   int rows, tile_rows, row_tiles;            // Q x group; rows of one tile; tiles
   int waves;
-  float* parts;                              // [waves + segments][tile_rows][D + 2]
+  float* parts;                              // [waves + segments][tile_rows][D + 4]: output, maximum, sum
+  int *owner, *last_owner;                   // [segments]: first and last wave of those cut, -1 for the others
 };
 
 // ---------------------------------------------------------------- who does what
@@ -61,30 +62,23 @@ __device__ __forceinline__ int length(const Params& p, int n) {
 // An empty sequence has one unit too: somebody writes its zeros.
 __device__ __forceinline__ int units_of(int len) { return max((len + kUnit - 1) / kUnit, 1); }
 
-__device__ __forceinline__ int64_t wave_sum(int64_t x) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d, 64);
-  return x;
-}
-
-// Units of all sequences before `stop` (of one head and row tile), by a wave.
-__device__ __forceinline__ int64_t units_before(const Params& p, int stop) {
-  int64_t sum = 0;
-  for (int n = threadIdx.x & 63; n < stop; n += 64) sum += units_of(length(p, n));
-  return wave_sum(sum);
-}
-
-struct Place {
-  int n;             // sequence
-  int64_t before;    // units of the sequences before it, times heads and row tiles
+// Where a wave's piece of the line begins.
+struct Piece {
+  int64_t from, to;  // its units
+  int n;             // the sequence that holds the first
+  int64_t before;    // units of the sequences before it
 };
 
-// The sequence that holds unit u of the line; per = heads x row tiles.
-__device__ __forceinline__ Place find_unit(const Params& p, int64_t u, int per) {
+// The line has U = per x (units of all sequences) units, per = heads x row
+// tiles; wave w of W = min(waves, U) takes floor(U w / W) .. floor(U (w + 1) / W) - 1.
+// A 64-way search: each lane sums a stretch of sequences, the wave adds up and
+// picks the stretch that holds the unit, down to one sequence.
+__device__ __forceinline__ Piece find_piece(const Params& p, int w, int per) {
   const int lane = threadIdx.x & 63;
+  Piece x{0, 0, 0, 0};
   int lo = 0, hi = p.N;
-  int64_t before = 0;
-  while (hi - lo > 1) {
+  bool top = true;
+  do {
     const int step = (hi - lo + 63) / 64;
     const int a = min(lo + lane * step, hi), b = min(a + step, hi);
     int64_t own = 0;
@@ -93,16 +87,24 @@ __device__ __forceinline__ Place find_unit(const Params& p, int64_t u, int per) 
     int64_t end = own;                       // inclusive sum over the lanes
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-      const int64_t x = __shfl_up(end, d, 64);
-      if (lane >= d) end += x;
+      const int64_t y = __shfl_up(end, d, 64);
+      if (lane >= d) end += y;
     }
-    const uint64_t upto = __ballot(before + end <= u);      // lanes whose sequences all end before u
+    if (top) {
+      const int64_t total = __shfl(end, 63, 64), waves = min(total, int64_t(p.waves));
+      if (w >= waves) return x;              // nothing for this wave
+      x.from = total * w / waves;
+      x.to = total * (w + 1) / waves;
+      top = false;
+    }
+    const uint64_t upto = __ballot(x.before + end <= x.from);   // lanes whose sequences all end before it
     const int k = min(int(__builtin_popcountll(upto)), (hi - lo + step - 1) / step - 1);
-    before += __shfl(end - own, k, 64);
+    x.before += __shfl(end - own, k, 64);
     lo += k * step;
     hi = min(lo + step, hi);
-  }
-  return {__builtin_amdgcn_readfirstlane(lo), before};
+  } while (hi - lo > 1);
+  x.n = __builtin_amdgcn_readfirstlane(lo);
+  return x;
 }
 
 // ---------------------------------------------------------------- codes to operands
@@ -129,15 +131,12 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
   // waves of one place in all workgroups follow one another: a short line fills every compute unit evenly
   const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6) * int(gridDim.x) + int(blockIdx.x));
   const int per = p.HKV * p.row_tiles;
-  const int64_t total = units_before(p, p.N) * per;
-  const int64_t waves = min(total, int64_t(p.waves));      // each has one unit at least
-  if (w >= waves) return;
-  int64_t u = total * w / waves;
-  const int64_t end = total * (w + 1) / waves;
-  const Place at = find_unit(p, u, per);
-  int n = at.n;
+  const Piece piece = find_piece(p, w, per);
+  int64_t u = piece.from;
+  const int64_t end = piece.to;
+  int n = piece.n;
   int len = length(p, n), units = units_of(len);
-  int seg = int((u - at.before) / units), first = int((u - at.before) - int64_t(seg) * units);
+  int seg = int((u - piece.before) / units), first = int((u - piece.before) - int64_t(seg) * units);
   const int G = p.HQ / p.HKV;
   const float c = p.scale * kLog2e;
 
@@ -330,6 +329,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
     // columns 8 (4 g4 + e) + d in o[d][e].
     const bool whole = first == 0 && last == units;
     const int64_t segment = int64_t(n) * per + seg;
+    if (first == 0 && lane == 0) p.owner[segment] = whole ? -1 : w;
+    if (first != 0 && last == units && lane == 0) p.last_owner[segment] = w;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float sum = l[t] + __shfl_xor(l[t], 16, 64);
@@ -370,26 +371,20 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
 
 // ---------------------------------------------------------------- joining the parts
 
-// A workgroup per (segment, row).  Wave w of the line has units
-// floor(U w / waves) .. floor(U (w + 1) / waves) - 1, so unit u belongs to
-// wave ceil((u + 1) waves / U) - 1.
+// A workgroup per (segment, row).
 constexpr int kStreams = kThreads / 32;
 __global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(Params p) {
   __shared__ float weights[kThreads], red[kStreams][D], stat[kWaves];
-  const int per = p.HKV * p.row_tiles;
-  const int r = int(blockIdx.x % unsigned(p.tile_rows));
-  const int64_t segment = blockIdx.x / unsigned(p.tile_rows);
+  const int per = p.HKV * p.row_tiles, tile = min(p.rows, p.tile_rows);
+  const int64_t segment = blockIdx.x / unsigned(tile);
+  const int w0 = p.owner[segment];
+  if (w0 < 0) return;                        // finished by its wave
+  const int w1 = p.last_owner[segment];
+  const int r = int(blockIdx.x % unsigned(tile));
   const int n = int(segment / per), seg = int(segment - int64_t(n) * per);
   const int hkv = seg / p.row_tiles, row = (seg - hkv * p.row_tiles) * p.tile_rows + r;
   if (row >= p.rows) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t total = units_before(p, p.N) * per;
-  const int units = units_of(length(p, n));
-  const int64_t a = units_before(p, n) * per + int64_t(seg) * units, b = a + units - 1;
-  const int64_t waves = min(total, int64_t(p.waves));
-  const int w0 = int(((a + 1) * waves + total - 1) / total - 1);
-  const int w1 = int(((b + 1) * waves + total - 1) / total - 1);
-  if (w0 == w1) return;                      // finished by its wave
   const int64_t step = int64_t(p.tile_rows) * (D + 4);
   const float* part = p.parts + ((segment + w0) * p.tile_rows + r) * (D + 4);
   const int count = w1 - w0 + 1;             // slots of successive waves follow one another
@@ -449,7 +444,7 @@ __global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(Params p) {
 struct Plan {
   int rows, tile_rows, row_tiles, waves;
   int64_t segments;
-  size_t bytes;
+  size_t parts, bytes;
 };
 
 // Rows in tiles of 16 (one matrix instruction) or 32.  Eight waves per compute
@@ -462,7 +457,8 @@ Plan plan_for(int64_t N, int64_t Q, int HQ, int HKV) {
   x.row_tiles = (x.rows + x.tile_rows - 1) / x.tile_rows;
   x.waves = kda::device_cus() * 8;
   x.segments = N * HKV * x.row_tiles;
-  x.bytes = size_t(x.waves + x.segments) * x.tile_rows * (D + 4) * sizeof(float);
+  x.parts = size_t(x.waves + x.segments) * x.tile_rows * (D + 4) * sizeof(float);
+  x.bytes = x.parts + size_t(x.segments) * 2 * sizeof(int);
   return x;
 }
 
@@ -499,17 +495,18 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
   const Plan x = plan_for(N, Q, HQ, HKV);
   if (workspace_bytes < x.bytes) return KDA_ERR_WORKSPACE;
   if (x.segments * x.tile_rows > 0x7fffffff) return KDA_ERR_SHAPE;
+  int* owner = reinterpret_cast<int*>(static_cast<char*>(workspace) + x.parts);
   const Params p{static_cast<const uint16_t*>(q), q_stride, static_cast<const uint8_t*>(k_cache),
                  static_cast<const uint8_t*>(v_cache), k_scale, v_scale, page_table, table_stride, kv_lens,
                  N, Q, HQ, HKV, table_width, __builtin_ctz(page_size), num_pages, page_stride, scale,
                  static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, x.waves,
-                 static_cast<float*>(workspace)};
+                 static_cast<float*>(workspace), owner, owner + x.segments};
   const hipStream_t st = kda::as_stream(stream);
   const dim3 grid(unsigned(x.waves / kWaves));
   if (x.tile_rows == 16)
     hipLaunchKernelGGL(attn_decode_kernel<1>, grid, dim3(kThreads), 0, st, p);
   else
     hipLaunchKernelGGL(attn_decode_kernel<2>, grid, dim3(kThreads), 0, st, p);
-  hipLaunchKernelGGL(attn_decode_join_kernel, dim3(unsigned(x.segments * x.tile_rows)), dim3(kThreads), 0, st, p);
+  hipLaunchKernelGGL(attn_decode_join_kernel, dim3(unsigned(x.segments * min(x.rows, x.tile_rows))), dim3(kThreads), 0, st, p);
   return kda::launch_status();
 }
