@@ -16,12 +16,13 @@
 // wave's piece is finished there; otherwise its waves leave float32 parts that
 // attn_decode_join_kernel brings together in order.
 //
-// S^T = K Q^T and O^T += V^T P^T on 16x16x32 matrix instructions, codes widened
-// to bfloat16 (exact).  Contraction orders are chosen so that no data moves
-// between lanes: K's columns in the order in which a lane loads 32 bytes of a
-// row, V's rows in the order in which the accumulator of S^T holds the keys,
-// and V's 8-byte loads (one key, 8 columns) turned into 8 operands by byte
-// permutes inside the lane.
+// S^T = K Q^T takes the codes as they are, 128 columns to an instruction, with
+// each query row split into two e4m3 terms (split_row); O^T += V^T P^T runs in
+// bfloat16 on V's codes widened (exact).  Contraction orders are chosen so that
+// no data moves between lanes: K's columns as a lane loads 32 bytes of a row,
+// V's rows in the order in which the accumulator of S^T holds the keys, and V's
+// 8-byte loads (one key, 8 columns) turned into 8 operands by byte permutes
+// inside the lane.
 #include "attn_device.h"
 #include "kda_host.h"
 
@@ -64,18 +65,20 @@ __device__ __forceinline__ int units_of(int len) { return max((len + kUnit - 1) 
 
 // Where a wave's piece of the line begins.
 struct Piece {
+  int w;             // the wave's place in the line
   int64_t from, to;  // its units
+  int64_t lo, hi;    // its workgroup's units, if its waves are neighbours in the line; else empty
   int n;             // the sequence that holds the first
   int64_t before;    // units of the sequences before it
 };
 
 // The line has U = per x (units of all sequences) units, per = heads x row
-// tiles; wave w of W = min(waves, U) takes floor(U w / W) .. floor(U (w + 1) / W) - 1.
+// tiles; place w of W = min(waves, U) takes floor(U w / W) .. floor(U (w + 1) / W) - 1.
 // A 64-way search: each lane sums a stretch of sequences, the wave adds up and
 // picks the stretch that holds the unit, down to one sequence.
-__device__ __forceinline__ Piece find_piece(const Params& p, int w, int per) {
+__device__ __forceinline__ Piece find_piece(const Params& p, int wave, int per) {
   const int lane = threadIdx.x & 63;
-  Piece x{0, 0, 0, 0};
+  Piece x{0, 0, 0, 0, 0, 0, 0};
   int lo = 0, hi = p.N;
   bool top = true;
   do {
@@ -92,9 +95,21 @@ __device__ __forceinline__ Piece find_piece(const Params& p, int w, int per) {
     }
     if (top) {
       const int64_t total = __shfl(end, 63, 64), waves = min(total, int64_t(p.waves));
-      if (w >= waves) return x;              // nothing for this wave
-      x.from = total * w / waves;
-      x.to = total * (w + 1) / waves;
+      // floor(total i / waves) without a long division for each i
+      const unsigned parts = unsigned(waves);
+      const int64_t each = total <= 0x7fffffff ? int64_t(unsigned(total) / parts) : total / waves;
+      const unsigned left = unsigned(total - each * waves);
+      auto cut = [&](int i) { return each * i + int64_t(left * unsigned(i) / parts); };
+      if (total >= p.waves) {
+        x.w = int(blockIdx.x) * kWaves + wave;
+        x.lo = cut(x.w - wave);
+        x.hi = cut(x.w - wave + kWaves);
+      } else {                               // a short line is spread over all workgroups
+        x.w = wave * int(gridDim.x) + int(blockIdx.x);
+        if (x.w >= waves) return x;          // nothing for this wave
+      }
+      x.from = cut(x.w);
+      x.to = cut(x.w + 1);
       top = false;
     }
     const uint64_t upto = __ballot(x.before + end <= x.from);   // lanes whose sequences all end before it
@@ -109,14 +124,49 @@ __device__ __forceinline__ Piece find_piece(const Params& p, int w, int per) {
 
 // ---------------------------------------------------------------- codes to operands
 
-// Eight codes (two words) as eight bfloat16 values.
-__device__ __forceinline__ bf16x8 widen(uint32_t a, uint32_t b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
-  const bf16x2 w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
-  const bf16x2 w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
-  const bf16x2 w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
-  return (bf16x8){w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
+// A query row as two terms in e4m3: 32 values q 2^-e = hi + lo, where the
+// row's largest magnitude lies in (224, 448].  hi keeps four significant bits
+// of bfloat16's eight and lo the other four, so nothing is lost of values
+// within 2^-10 of the largest; smaller ones are off by at most 2^-18 of it.  The
+// first product then takes the cache's codes as they are.  Returns 2^e.
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ float split_row(const bf16x8 (&q)[4], i32x8& hi, i32x8& lo) {
+  float top = 0.0f;
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(float(q[s][j])));
+  top = fmaxf(top, __shfl_xor(top, 16, 64));
+  top = half_max(top);
+  // 448 = 1.75 x 2^8; infinities end as NaN whatever e is
+  const int bits = int(__float_as_uint(top) >> 16) & 0x7fff;
+  const int e = max(min((bits >> 7) - 127 - 8 + int((bits & 127) > 96), 119), -110);
+  const float f = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      float x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = float(q[s][j + i]) * f;
+      int w = 0, r = 0;
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], w, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true);
+      y[0] = x[0] - __builtin_amdgcn_cvt_f32_fp8(w, 0), y[1] = x[1] - __builtin_amdgcn_cvt_f32_fp8(w, 1);
+      y[2] = x[2] - __builtin_amdgcn_cvt_f32_fp8(w, 2), y[3] = x[3] - __builtin_amdgcn_cvt_f32_fp8(w, 3);
+      r = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], r, false);
+      r = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], r, true);
+      hi[2 * s + j / 4] = w;
+      lo[2 * s + j / 4] = r;
+    }
+  return __uint_as_float(uint32_t(127 + e) << 23);
+}
+
+// D = A B + C with A 16 x 128 and B 128 x 16 in e4m3: lane l holds row or
+// column l % 16 at 32 of the 128 indices, those of its 16-lane group; which
+// ones is the same for A and B, so both simply take 32 bytes of a row.
+__device__ __forceinline__ f32x4 mfma16_codes(i32x8 a, i32x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);   // scales 2^0
 }
 
 // Pages of up to 64 successive tiles of 16 tokens, one per lane.
@@ -128,10 +178,11 @@ struct Pages {
 template <int NT>
 __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
   const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
-  // waves of one place in all workgroups follow one another: a short line fills every compute unit evenly
-  const int w = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6) * int(gridDim.x) + int(blockIdx.x));
+  __shared__ __align__(16) float merged[kWaves][16 * NT][D + 4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = p.HKV * p.row_tiles;
-  const Piece piece = find_piece(p, w, per);
+  const Piece piece = find_piece(p, wave, per);
+  const int w = piece.w;
   int64_t u = piece.from;
   const int64_t end = piece.to;
   int n = piece.n;
@@ -146,16 +197,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
     const int last = int(min(int64_t(units), first + end - u));     // units first .. last - 1
     const int rows = min(p.rows - row0, 16 * NT);
 
-    bf16x8 q[NT][4];
-    int limit[NT];                           // tokens that the lane's row sees
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int r = row0 + min(16 * t + l16, rows - 1), i = r / G;
-      const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (hkv * G + r - i * G) * D + 32 * g4;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) q[t][s] = *reinterpret_cast<const bf16x8*>(src + 8 * s);
-      limit[t] = len - p.Q + i + 1;
-    }
     f32x4 o[NT][8];
     float m[NT], l[NT];
 #pragma unroll
@@ -166,14 +207,14 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
     }
 
     const int32_t* table = p.table + n * p.table_stride;
-    auto pages_at = [&](int unit) {          // of the 64 tiles from `unit` on
+    auto pages_at = [&](int unit) {          // of the 64 tiles from `unit` on, as far as the piece goes
       Pages x{-1, 0.0f, 0.0f};
       const int64_t token = int64_t(unit) * kUnit + lane * 16;
-      if (token < len) {
+      if (token < min(int64_t(len), int64_t(last) * kUnit)) {
         const int id = table[token >> p.shift];
         if (id >= 0 && id < p.num_pages) {
           x.id = id;
-          x.ks = p.k_scale[int64_t(id) * p.HKV + hkv] * c;
+          x.ks = p.k_scale[int64_t(id) * p.HKV + hkv];
           x.vs = p.v_scale[int64_t(id) * p.HKV + hkv];
         }
       }
@@ -205,9 +246,23 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
       }
     };
 
+    // the chain table -> codes is the longest: it starts before the queries
     Pages now = pages_at(first);
     load_k(now, first, 0);
     load_v(now, first, 0);
+    i32x8 hi[NT], lo[NT];
+    float qscale[NT];                        // of the lane's row, with the scores' scale in powers of two
+    int limit[NT];                           // tokens that the lane's row sees
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = row0 + min(16 * t + l16, rows - 1), i = r / G;
+      const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (hkv * G + r - i * G) * D + 32 * g4;
+      bf16x8 q[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) q[s] = *reinterpret_cast<const bf16x8*>(src + 8 * s);
+      qscale[t] = split_row(q, hi[t], lo[t]) * c;
+      limit[t] = len - p.Q + i + 1;
+    }
     int from = 0;                            // the unit's first tile in `now`
     for (int unit = first; unit < last; ++unit) {
       const int key0 = unit * kUnit;
@@ -215,14 +270,11 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
       f32x4 s[NT][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        i32x8 a;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) s[t][j] = (f32x4)(0.0f);
+        for (int i = 0; i < 8; ++i) a[i] = int(kr[j][i >> 2][i & 3]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bf16x8 a = widen(kr[j][k >> 1][2 * (k & 1)], kr[j][k >> 1][2 * (k & 1) + 1]);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) s[t][j] = mfma16(a, q[t][k], s[t][j]);
-        }
+        for (int t = 0; t < NT; ++t) s[t][j] = mfma16_codes(a, hi[t], mfma16_codes(a, lo[t], (f32x4)(0.0f)));
       }
       float ks[4], vs[4];
       bool none[4];
@@ -243,7 +295,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[t][j] *= ks[j];
+        for (int j = 0; j < 4; ++j) s[t][j] *= ks[j] * qscale[t];
         if (masked) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -331,6 +383,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
     const int64_t segment = int64_t(n) * per + seg;
     if (first == 0 && lane == 0) p.owner[segment] = whole ? -1 : w;
     if (first != 0 && last == units && lane == 0) p.last_owner[segment] = w;
+    // All four waves of the workgroup inside one segment: one part for them.
+    const int64_t start = u - first;         // the segment's first unit in the line
+    const bool merge = piece.lo < piece.hi && start <= piece.lo && piece.hi <= start + units;
+    float* parts = p.parts + (segment + w) * p.tile_rows * (D + 4);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float sum = l[t] + __shfl_xor(l[t], 16, 64);
@@ -350,15 +406,46 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
         }
         if (p.lse && g4 == 0) p.lse[out] = (m[t] + __log2f(sum)) * kLn2;
       } else {
-        float* part = p.parts + ((segment + w) * p.tile_rows + r) * (D + 4);
+        auto put = [&](auto* part) {         // LDS or global memory
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int d = 0; d < 8; d += 4)
-            *reinterpret_cast<f32x4*>(part + 8 * (4 * g4 + e) + d) =
-                (f32x4){o[t][d][e], o[t][d + 1][e], o[t][d + 2][e], o[t][d + 3][e]};
-        if (g4 == 0) part[D] = m[t], part[D + 1] = sum;
+            for (int d = 0; d < 8; d += 4)
+              *reinterpret_cast<f32x4*>(part + 8 * (4 * g4 + e) + d) =
+                  (f32x4){o[t][d][e], o[t][d + 1][e], o[t][d + 2][e], o[t][d + 3][e]};
+          if (g4 == 0) part[D] = m[t], part[D + 1] = sum;
+        };
+        if (merge)
+          put(&merged[wave][r][0]);
+        else
+          put(parts + r * (D + 4));
       }
+    }
+    if (merge) {                             // the same for all four waves, and each one's only segment
+      __syncthreads();
+      // 32 threads per row; the first wave's slot takes the sum, the others' say that they are empty
+      const int col = (threadIdx.x & 31) * 4;
+      for (int r = threadIdx.x >> 5; r < rows; r += kThreads / 32) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) top = fmaxf(top, merged[i][r][D]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        f32x4 acc = (f32x4)(0.0f);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) {
+          const float f = __builtin_amdgcn_exp2f(merged[i][r][D] - base);
+          acc += *reinterpret_cast<const f32x4*>(&merged[i][r][col]) * f;
+          sum += merged[i][r][D + 1] * f;
+        }
+        float* part = p.parts + ((segment + w - wave) * p.tile_rows + r) * (D + 4);
+        *reinterpret_cast<f32x4*>(part + col) = acc;
+        if (col == 0) {
+          part[D] = top, part[D + 1] = sum;
+          for (int i = 1; i < kWaves; ++i) part[i * p.tile_rows * (D + 4) + D] = -INFINITY;
+        }
+      }
+      return;
     }
     u += last - first;
     first = 0;
@@ -371,10 +458,13 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
 
 // ---------------------------------------------------------------- joining the parts
 
-// A workgroup per (segment, row).
-constexpr int kStreams = kThreads / 32;
-__global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(Params p) {
-  __shared__ float weights[kThreads], red[kStreams][D], stat[kWaves];
+// A workgroup per (segment, row): THREADS / 32 streams of 32 lanes add up the
+// parts that hold anything, four columns to a lane.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void attn_decode_join_kernel(Params p) {
+  constexpr int kStreams = THREADS / 32, kW = THREADS / 64;
+  __shared__ float weights[THREADS], red[kStreams][D], stat[kW];
+  __shared__ int places[THREADS], counts[kW];
   const int per = p.HKV * p.row_tiles, tile = min(p.rows, p.tile_rows);
   const int64_t segment = blockIdx.x / unsigned(tile);
   const int w0 = p.owner[segment];
@@ -400,30 +490,36 @@ __global__ __launch_bounds__(kThreads) void attn_decode_join_kernel(Params p) {
     __syncthreads();
     x = stat[0];
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) x = top ? fmaxf(x, stat[i]) : x + stat[i];
+    for (int i = 1; i < kW; ++i) x = top ? fmaxf(x, stat[i]) : x + stat[i];
     return x;
   };
   float m = -INFINITY;
-  for (int i = tid; i < count; i += kThreads) m = fmaxf(m, part[i * step + D]);
+  for (int i = tid; i < count; i += THREADS) m = fmaxf(m, part[i * step + D]);
   m = over_all(m, true);
   const float base = m == -INFINITY ? 0.0f : m;
   const int stream = tid >> 5, col = (tid & 31) * 4;
   f32x4 acc = (f32x4)(0.0f);
   float sum = 0.0f;
-  for (int i0 = 0; i0 < count; i0 += kThreads) {
-    __syncthreads();
+  for (int i0 = 0; i0 < count; i0 += THREADS) {
     const int i = i0 + tid;
-    float f = 0.0f;
-    if (i < count) {
-      f = __builtin_amdgcn_exp2f(part[i * step + D] - base);
-      sum += f * part[i * step + D + 1];
-    }
-    weights[tid] = f;
+    const float f = i < count ? __builtin_amdgcn_exp2f(part[i * step + D] - base) : 0.0f;
+    const bool some = f != 0.0f;             // NaN too
+    if (some) sum += f * part[i * step + D + 1];
+    const uint64_t have = __ballot(some);
     __syncthreads();
-    const int here = min(count - i0, kThreads);
-#pragma unroll 4
+    if (lane == 0) counts[wave] = __builtin_popcountll(have);
+    __syncthreads();
+    int at = __builtin_popcountll(have & ((uint64_t(1) << lane) - 1)), here = 0;
+#pragma unroll
+    for (int k = 0; k < kW; ++k) {
+      if (k < wave) at += counts[k];
+      here += counts[k];
+    }
+    if (some) places[at] = i, weights[at] = f;
+    __syncthreads();
+#pragma unroll 8
     for (int k = stream; k < here; k += kStreams)
-      acc += *reinterpret_cast<const f32x4*>(part + (i0 + k) * step + col) * weights[k];
+      acc += *reinterpret_cast<const f32x4*>(part + places[k] * step + col) * weights[k];
   }
   sum = over_all(sum, false);
   *reinterpret_cast<f32x4*>(&red[stream][col]) = acc;
@@ -507,6 +603,11 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
     hipLaunchKernelGGL(attn_decode_kernel<1>, grid, dim3(kThreads), 0, st, p);
   else
     hipLaunchKernelGGL(attn_decode_kernel<2>, grid, dim3(kThreads), 0, st, p);
-  hipLaunchKernelGGL(attn_decode_join_kernel, dim3(unsigned(x.segments * min(x.rows, x.tile_rows))), dim3(kThreads), 0, st, p);
+  const dim3 joins(unsigned(x.segments * min(x.rows, x.tile_rows)));
+  // few segments have many parts each
+  if (x.waves / x.segments >= 64)
+    hipLaunchKernelGGL(attn_decode_join_kernel<1024>, joins, dim3(1024), 0, st, p);
+  else
+    hipLaunchKernelGGL(attn_decode_join_kernel<256>, joins, dim3(256), 0, st, p);
   return kda::launch_status();
 }
