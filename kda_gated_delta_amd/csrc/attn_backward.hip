@@ -50,10 +50,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(Params p) {
   __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, h = lane >> 5;
-  const unsigned id = blockIdx.x, kv_heads = p.HKV, G = unsigned(p.HQ) / kv_heads;
-  const int hkv = int(id % kv_heads);
-  const int hq = hkv * G + int((id / kv_heads) % G);
-  const Rows rows = find_rows(p.cu, p.N, p.T, p.slots - 1 - int(id / unsigned(p.HQ)), BM);
+  int slot, hkv, hq;
+  if (!find_head(blockIdx.x, p.slots, p.HQ, p.HKV, slot, hkv, hq)) return;
+  const Rows rows = find_rows<false>(p.cu, p.N, p.T, slot, p.slots, BM);
   if (rows.row0 >= rows.len) return;
 
   const int r0 = rows.row0 + wave * 32;
@@ -184,9 +183,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dkv_kernel(Params p) {
   const unsigned id = blockIdx.x, kv_heads = p.HKV;
   const int G = p.HQ / p.HKV;
   const int hkv = int(id % kv_heads);
-  // early keys, which most rows see, start first
   const int part = int((id / kv_heads) % unsigned(p.parts));
-  const Rows rows = find_rows(p.cu, p.N, p.T, int(id / (kv_heads * p.parts)), BM);
+  const Rows rows = find_rows<true>(p.cu, p.N, p.T, int(id / (kv_heads * p.parts)), p.slots, BM);
   if (rows.row0 >= rows.len) return;
 
   const int k0 = rows.row0 + wave * 32;                    // this wave's first key
@@ -329,7 +327,7 @@ size_t stat_floats(int64_t B, int64_t T, int64_t HQ) { return size_t((B * T * HQ
 
 template <typename Out>
 int launch(const Params& p, hipStream_t stream) {
-  hipLaunchKernelGGL(attn_dq_kernel<Out>, dim3(unsigned(p.slots * p.HQ)), dim3(kThreads), 0, stream, p);
+  hipLaunchKernelGGL(attn_dq_kernel<Out>, dim3(unsigned(head_blocks(p.slots, p.HQ, p.HKV))), dim3(kThreads), 0, stream, p);
   const dim3 grid(unsigned(p.slots * p.HKV * p.parts));
   if (p.parts == 1) {
     hipLaunchKernelGGL(attn_dkv_kernel<Out>, grid, dim3(kThreads), 0, stream, p);
@@ -370,7 +368,7 @@ extern "C" int kda_attn_backward(const void* q, const void* k, const void* v, in
   const int64_t slots = slots_for(B, T, seqs);
   const int parts = parts_for(slots, T, N, seqs > 0, HQ, HKV);
   const int64_t quads = int64_t(B) * T * HKV * (D / 4);
-  if (slots * HQ > 0x7fffffff || slots * HKV * parts > 0x7fffffff || (quads + 255) / 256 > 0x7fffffff)
+  if (head_blocks(slots, HQ, HKV) > 0x7fffffff || slots * HKV * parts > 0x7fffffff || (quads + 255) / 256 > 0x7fffffff)
     return KDA_ERR_SHAPE;
   float* ws = static_cast<float*>(workspace);
   const size_t stats = stat_floats(B, T, HQ), grads = size_t(parts) * B * T * HKV * D;

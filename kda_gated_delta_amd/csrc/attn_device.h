@@ -73,13 +73,13 @@ struct Rows {
 // Largest n in [0, N) with floor(cu[n] / BM) + n <= slot (0 if none): the
 // whole wave looks at 64 places at once.  cu need not be valid: it is read
 // within its N + 1 entries only.
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int slot, int BM) {
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int T, int slot, int BM) {
   int lo = 0, hi = N;                         // the answer is in [lo, hi)
   const int lane = threadIdx.x & 63;
   while (hi - lo > 1) {
     const int step = (hi - lo + 63) / 64;
     const int at = lo + lane * step;
-    const bool ok = at < hi && max(cu[at], 0) / BM <= slot - at;
+    const bool ok = at < hi && min(max(cu[at], 0), T) / BM <= slot - at;
     const uint64_t m = __ballot(ok);
     const int k = m ? 63 - __builtin_clzll(m) : 0;
     lo += k * step;
@@ -88,22 +88,88 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int slot,
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-__device__ __forceinline__ Rows find_rows(const int32_t* cu, int N, int T, int slot, int BM) {
+// Tile `rank` of all packed sequences' tiles, those with the largest index first
+// (N <= 64).  A lane holds one sequence's number of tiles; #tiles with an index
+// >= t is looked up for 64 values of t at once.  Returns the sequence, -1 if
+// there are not so many tiles, and the index.
+__device__ __forceinline__ int find_ranked(int own_tiles, int N, int most, int rank, int& index) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = most + 1, above = 0;       // the index is in [lo, hi); #tiles with an index >= hi
+  bool first = true;
+  while (hi - lo > 1 || first) {
+    const int step = (hi - lo + 63) / 64, t = lo + lane * step;
+    int count = 0;
+    for (int n = 0; n < N; ++n) count += max(__builtin_amdgcn_readlane(own_tiles, n) - t, 0);
+    if (first && rank >= __builtin_amdgcn_readfirstlane(count)) return -1;
+    first = false;
+    const uint64_t more = __ballot(t < hi && count > rank);   // a stretch of lanes from 0
+    const int k = 63 - __builtin_clzll(more);
+    if (k < 63 && lo + (k + 1) * step < hi) {
+      above = __builtin_amdgcn_readlane(count, k + 1);
+      hi = lo + (k + 1) * step;
+    }
+    lo += k * step;
+  }
+  index = lo;
+  uint64_t have = __ballot(lane < N && own_tiles > lo);
+  for (int j = rank - above; j > 0; --j) have &= have - 1;
+  return __builtin_ctzll(have);
+}
+
+// Workgroups are dealt to the eight XCDs in turn, and each XCD has its own
+// cache.  The query heads of one tile that share a key/value head read the same
+// keys at about the same time: they follow one another on one XCD.  Of a
+// launch of head_blocks(slots, HQ, HKV) workgroups, false for the few past the
+// end.
+constexpr int kXcds = 8;
+__host__ __device__ inline int64_t head_blocks(int64_t slots, int HQ, int HKV) {
+  return (slots * HKV + kXcds - 1) / kXcds * kXcds * (HQ / HKV);
+}
+__device__ __forceinline__ bool find_head(unsigned id, int slots, int HQ, int HKV, int& slot, int& hkv, int& hq) {
+  const unsigned G = unsigned(HQ) / unsigned(HKV), j = id / kXcds;
+  const unsigned pair = id % kXcds + kXcds * (j / G);
+  slot = int(pair / unsigned(HKV));
+  hkv = int(pair % unsigned(HKV));
+  hq = hkv * int(G) + int(j % G);
+  return slot < slots;
+}
+
+// The rows of workgroup `slot` (of slots) of a launch.  kEarly: the tiles that
+// have most work are a sequence's first (backward's keys), else its last; they
+// come first in the launch, so that the short ones fill the end.  With up to 64
+// packed sequences that holds over all of them, otherwise within each.
+template <bool kEarly>
+__device__ __forceinline__ Rows find_rows(const int32_t* cu, int N, int T, int slot, int slots, int BM) {
   Rows r;
   if (!cu) {
+    const int tiles = slots / unsigned(N), t = int(slot / unsigned(N));
     r.b = slot % unsigned(N);
     r.start = 0;
     r.first = int64_t(r.b) * T;
     r.len = T;
-    r.row0 = int(slot / unsigned(N)) * BM;
+    r.row0 = (kEarly ? t : tiles - 1 - t) * BM;
     return r;
   }
-  const int n = find_sequence(cu, N, slot, BM);
+  int n, t = -1;
+  if (N <= 64) {
+    const int lane = threadIdx.x & 63;
+    int own = 0;
+    if (lane < N) {
+      const int c0 = min(max(cu[lane], 0), T), c1 = min(cu[lane + 1], T);
+      own = max(c1 - c0 + BM - 1, 0) / BM;
+    }
+    n = find_ranked(own, N, T / BM + 1, slot, t);
+    if (n >= 0 && kEarly) t = __builtin_amdgcn_readlane(own, n) - 1 - t;
+    n = max(n, 0);
+  } else {
+    const int at = kEarly ? slot : slots - 1 - slot;
+    n = find_sequence(cu, N, T, at, BM);
+    t = at - min(max(cu[n], 0), T) / BM - n;
+  }
   const int c0 = min(max(cu[n], 0), T), c1 = min(cu[n + 1], T);
   r.b = 0;
   r.first = r.start = c0;
   r.len = max(c1 - c0, 0);
-  const int t = slot - c0 / BM - n;
   r.row0 = t < 0 || t > r.len / BM ? r.len : t * BM;
   return r;
 }

@@ -45,13 +45,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(Params p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, h = lane >> 5;
 
-  // Neighbouring workgroups take the heads of one tile, key/value heads
-  // fastest: workgroups are dealt to the eight XCDs in turn, so a head's keys
-  // stay in one XCD's cache.  Late tiles, which have most keys, start first.
-  const unsigned id = blockIdx.x, kv_heads = p.HKV, G = unsigned(p.HQ) / kv_heads;
-  const int hkv = int(id % kv_heads);
-  const int hq = hkv * G + int((id / kv_heads) % G);
-  const Rows rows = find_rows(p.cu, p.N, p.T, p.slots - 1 - int(id / unsigned(p.HQ)), BM);
+  int slot, hkv, hq;
+  if (!find_head(blockIdx.x, p.slots, p.HQ, p.HKV, slot, hkv, hq)) return;
+  const Rows rows = find_rows<false>(p.cu, p.N, p.T, slot, p.slots, BM);
   if (rows.row0 >= rows.len) return;
 
   const int r0 = rows.row0 + wave * 32;                   // this wave's first row
@@ -165,10 +161,10 @@ extern "C" int kda_attn_prefill(const void* q, const void* k, const void* v, int
   if (!kda::aligned16(q) || !kda::aligned16(k) || !kda::aligned16(v) || !kda::aligned16(o) || (lse && !kda::aligned16(lse)))
     return KDA_ERR_ALIGN;
   const int64_t slots = cu_seqlens ? int64_t(T) / BM + num_seqs : int64_t(B) * ((T + BM - 1) / BM);
-  if (slots * HQ > 0x7fffffff) return KDA_ERR_SHAPE;
+  if (head_blocks(slots, HQ, HKV) > 0x7fffffff) return KDA_ERR_SHAPE;
   const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                  q_stride, k_stride, v_stride, cu_seqlens, cu_seqlens ? num_seqs : B, T, HQ, HKV, int(slots), scale,
                  static_cast<uint16_t*>(o), lse};
-  hipLaunchKernelGGL(attn_prefill_kernel, dim3(unsigned(slots * HQ)), dim3(kThreads), 0, kda::as_stream(stream), p);
+  hipLaunchKernelGGL(attn_prefill_kernel, dim3(unsigned(head_blocks(slots, HQ, HKV))), dim3(kThreads), 0, kda::as_stream(stream), p);
   return kda::launch_status();
 }
