@@ -25,7 +25,8 @@ struct StoreParams {
   const uint16_t *k, *v;
   int64_t k_stride, v_stride;
   const int32_t* slots;
-  int T, HKV, page_size, shift;
+  int T, HKV, page_size, shift, wshift;
+  unsigned items;
   int64_t num_slots, page_stride;
   uint8_t *k_cache, *v_cache;
   float *k_scale, *v_scale;
@@ -115,49 +116,54 @@ __device__ __forceinline__ void store_run(const uint16_t* rows, int64_t stride, 
 
 // A run is a stretch of tokens whose slots follow one another within a page.
 // One wave takes the keys or the values of one run of one head, so a page's
-// scale has one writer.  A workgroup looks at WINDOW tokens for the runs that
-// begin there.
-template <int WINDOW>
-__global__ __launch_bounds__(64 * kStoreWaves) void attn_cache_store_kernel(StoreParams p) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int head = blockIdx.x % unsigned(p.HKV);
-  const int t0 = int(blockIdx.x / unsigned(p.HKV)) * WINDOW;
-  auto slot_at = [&](int t) -> int {           // -1: no such token, or not stored
+// scale has one writer.  An item is (window of 2^wshift tokens, head, keys or
+// values): the wave looks there for the runs that begin.  Waves go from item to
+// item, the next one's slots already on their way.
+__global__ __launch_bounds__(64 * kStoreWaves, 4) void attn_cache_store_kernel(StoreParams p) {
+  const int lane = threadIdx.x & 63, window = 1 << p.wshift;
+  const unsigned waves = gridDim.x * kStoreWaves;
+  unsigned item = __builtin_amdgcn_readfirstlane(blockIdx.x * kStoreWaves + (threadIdx.x >> 6));
+  auto slot_at = [&](int64_t t) -> int {       // -1: no such token, or not stored
     const int s = t >= 0 && t < p.T ? p.slots[t] : -1;
     return s >= 0 && s < p.num_slots ? s : -1;
   };
-  const int mine = lane < WINDOW ? slot_at(t0 + lane) : -1;
-  const int before = lane < WINDOW ? slot_at(t0 + lane - 1) : -1;
-  const bool leads = mine >= 0 && ((mine & (p.page_size - 1)) == 0 || before < 0 || before != mine - 1);
-  uint64_t runs = __ballot(leads);
-  for (int k = 0; runs; k += 2) {              // tasks k (keys) and k + 1 (values)
-    const int i = __builtin_ctzll(runs);
-    runs &= runs - 1;
-    if ((k ^ wave) & (kStoreWaves - 2)) continue;
-    const int t = t0 + i, slot = __builtin_amdgcn_readlane(mine, i);
-    const int off = slot & (p.page_size - 1), most = p.page_size - off;
-    int n = 0;
-    for (bool whole = true; whole && n < most; ) {
-      const uint64_t same = __ballot(n + lane < most && slot_at(t + n + lane) == slot + n + lane);
-      whole = same == ~uint64_t(0);
-      n += whole ? 64 : __builtin_ctzll(~same);
+  auto begin_of = [&](unsigned i) { return int64_t(i / (2u * unsigned(p.HKV))) << p.wshift; };
+  int mine = -1, before = -1;
+  auto look = [&](unsigned i) {
+    mine = before = -1;
+    if (i < p.items && lane < window) mine = slot_at(begin_of(i) + lane), before = slot_at(begin_of(i) + lane - 1);
+  };
+  look(item);
+  while (item < p.items) {
+    const int64_t t0 = begin_of(item);
+    const unsigned part = item % (2u * unsigned(p.HKV));
+    const int head = int(part >> 1);
+    const bool leads = mine >= 0 && ((mine & (p.page_size - 1)) == 0 || before < 0 || before != mine - 1);
+    uint64_t runs = __ballot(leads);
+    const int slots = mine;
+    item = item + waves < item ? p.items : item + waves;
+    look(item);
+    while (runs) {
+      const int i = __builtin_ctzll(runs);
+      runs &= runs - 1;
+      const int64_t t = t0 + i;
+      const int slot = __builtin_amdgcn_readlane(slots, i);
+      const int off = slot & (p.page_size - 1), most = p.page_size - off;
+      int n = 0;
+      for (bool whole = true; whole && n < most; ) {
+        const uint64_t same = __ballot(n + lane < most && slot_at(t + n + lane) == slot + n + lane);
+        whole = same == ~uint64_t(0);
+        n += whole ? 64 : __builtin_ctzll(~same);
+      }
+      const int64_t page = slot >> p.shift;
+      const int64_t codes = page * p.page_stride + int64_t(head) * p.page_size * D;
+      const int64_t scale = page * p.HKV + head;
+      if (part & 1)
+        store_run(p.v + t * p.v_stride + head * D, p.v_stride, n, p.v_cache + codes, off, p.v_scale + scale, lane);
+      else
+        store_run(p.k + t * p.k_stride + head * D, p.k_stride, n, p.k_cache + codes, off, p.k_scale + scale, lane);
     }
-    const int64_t page = slot >> p.shift;
-    const int64_t codes = page * p.page_stride + int64_t(head) * p.page_size * D;
-    const int64_t scale = page * p.HKV + head;
-    if (wave & 1)
-      store_run(p.v + t * p.v_stride + head * D, p.v_stride, n, p.v_cache + codes, off, p.v_scale + scale, lane);
-    else
-      store_run(p.k + t * p.k_stride + head * D, p.k_stride, n, p.k_cache + codes, off, p.k_scale + scale, lane);
   }
-}
-
-template <int WINDOW>
-int64_t store_blocks(const StoreParams& p) { return (int64_t(p.T) + WINDOW - 1) / WINDOW * p.HKV; }
-template <int WINDOW>
-void launch_store(const StoreParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL(attn_cache_store_kernel<WINDOW>, dim3(unsigned(store_blocks<WINDOW>(p))), dim3(64 * kStoreWaves),
-                     0, stream, p);
 }
 
 // ---------------------------------------------------------------- tables
@@ -276,18 +282,23 @@ extern "C" int kda_attn_cache_store(const void* k, const void* v, int64_t k_stri
   if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return KDA_ERR_NULL;
   for (const void* x : {k, v, static_cast<const void*>(k_cache), static_cast<const void*>(v_cache)})
     if (!kda::aligned16(x)) return KDA_ERR_ALIGN;
+  // Every run costs a wave its latency, every empty window a look.  A decode
+  // step's tokens are a run each and want a window each; in prompts a run is a
+  // page.  Windows grow until two items are left for a wave, up to 16 tokens:
+  // 256 single tokens x 8 heads take FIGURE_A us (window 1), 35000 tokens of
+  // prompts FIGURE_B us (window 16).
+  const int64_t waves = 16 * int64_t(kda::device_cus()), each = 2 * int64_t(HKV);
+  int wshift = 0;
+  while (wshift < 4 && (int64_t(T) >> wshift) * each > 2 * waves) ++wshift;
+  const int64_t items = ((int64_t(T) + (1 << wshift) - 1) >> wshift) * each;
+  if (items > 0x7fffffff) return KDA_ERR_SHAPE;
   const StoreParams p{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_stride, v_stride, slots,
-                      T, HKV, page_size, __builtin_ctz(page_size), int64_t(num_pages) * page_size, page_stride,
+                      T, HKV, page_size, __builtin_ctz(page_size), wshift, unsigned(items),
+                      int64_t(num_pages) * page_size, page_stride,
                       static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale};
-  // Few tokens (a decode step: every one a run of its own) want a workgroup
-  // for each two, so that no wave has a second run; in prompts, where a run is a page,
-  // most workgroups find none and wide windows keep them few.
-  if (store_blocks<2>(p) <= 8 * kda::device_cus())
-    launch_store<2>(p, kda::as_stream(stream));
-  else if (store_blocks<16>(p) <= 0x7fffffff)
-    launch_store<16>(p, kda::as_stream(stream));
-  else
-    return KDA_ERR_SHAPE;
+  const int64_t blocks = ((items < waves ? items : waves) + kStoreWaves - 1) / kStoreWaves;
+  hipLaunchKernelGGL(attn_cache_store_kernel, dim3(unsigned(blocks)), dim3(64 * kStoreWaves), 0,
+                     kda::as_stream(stream), p);
   return kda::launch_status();
 }
 
