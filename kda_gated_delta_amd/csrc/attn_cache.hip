@@ -158,10 +158,10 @@ __global__ __launch_bounds__(64 * kStoreWaves, 4) void attn_cache_store_kernel(S
       const int64_t page = slot >> p.shift;
       const int64_t codes = page * p.page_stride + int64_t(head) * p.page_size * D;
       const int64_t scale = page * p.HKV + head;
-      if (part & 1)
-        store_run(p.v + t * p.v_stride + head * D, p.v_stride, n, p.v_cache + codes, off, p.v_scale + scale, lane);
-      else
-        store_run(p.k + t * p.k_stride + head * D, p.k_stride, n, p.k_cache + codes, off, p.k_scale + scale, lane);
+      const bool v = part & 1;
+      const int64_t stride = v ? p.v_stride : p.k_stride;
+      store_run((v ? p.v : p.k) + t * stride + head * D, stride, n, (v ? p.v_cache : p.k_cache) + codes, off,
+                (v ? p.v_scale : p.k_scale) + scale, lane);
     }
   }
 }

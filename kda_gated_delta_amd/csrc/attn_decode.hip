@@ -63,12 +63,19 @@ __device__ __forceinline__ int length(const Params& p, int n) {
 // An empty sequence has one unit too: somebody writes its zeros.
 __device__ __forceinline__ int units_of(int len) { return max((len + kUnit - 1) / kUnit, 1); }
 
+// A lane's value for the whole wave, in scalar registers.
+__device__ __forceinline__ int64_t lane_value(int64_t x, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(uint64_t(x)), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(uint64_t(x) >> 32), lane);
+  return int64_t(uint64_t(hi) << 32 | lo);
+}
+
 // Where a wave's piece of the line begins.
 struct Piece {
   int w;             // the wave's place in the line
   int64_t from, to;  // its units
   int64_t lo, hi;    // its workgroup's units, if its waves are neighbours in the line; else empty
-  int n;             // the sequence that holds the first
+  int n, len;        // the sequence that holds the first, and its length
   int64_t before;    // units of the sequences before it
 };
 
@@ -78,14 +85,15 @@ struct Piece {
 // picks the stretch that holds the unit, down to one sequence.
 __device__ __forceinline__ Piece find_piece(const Params& p, int wave, int per) {
   const int lane = threadIdx.x & 63;
-  Piece x{0, 0, 0, 0, 0, 0, 0};
+  Piece x{};
   int lo = 0, hi = p.N;
   bool top = true;
   do {
     const int step = (hi - lo + 63) / 64;
     const int a = min(lo + lane * step, hi), b = min(a + step, hi);
     int64_t own = 0;
-    for (int n = a; n < b; ++n) own += units_of(length(p, n));
+    int len = 0;
+    for (int n = a; n < b; ++n) len = length(p, n), own += units_of(len);
     own *= per;
     int64_t end = own;                       // inclusive sum over the lanes
 #pragma unroll
@@ -94,7 +102,7 @@ __device__ __forceinline__ Piece find_piece(const Params& p, int wave, int per) 
       if (lane >= d) end += y;
     }
     if (top) {
-      const int64_t total = __shfl(end, 63, 64), waves = min(total, int64_t(p.waves));
+      const int64_t total = lane_value(end, 63), waves = min(total, int64_t(p.waves));
       // floor(total i / waves) without a long division for each i
       const unsigned parts = unsigned(waves);
       const int64_t each = total <= 0x7fffffff ? int64_t(unsigned(total) / parts) : total / waves;
@@ -114,11 +122,12 @@ __device__ __forceinline__ Piece find_piece(const Params& p, int wave, int per) 
     }
     const uint64_t upto = __ballot(x.before + end <= x.from);   // lanes whose sequences all end before it
     const int k = min(int(__builtin_popcountll(upto)), (hi - lo + step - 1) / step - 1);
-    x.before += __shfl(end - own, k, 64);
+    x.before += lane_value(end - own, k);
+    x.len = __builtin_amdgcn_readlane(len, k);     // in the last round a stretch is one sequence
     lo += k * step;
     hi = min(lo + step, hi);
   } while (hi - lo > 1);
-  x.n = __builtin_amdgcn_readfirstlane(lo);
+  x.n = lo;
   return x;
 }
 
@@ -186,8 +195,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
   int64_t u = piece.from;
   const int64_t end = piece.to;
   int n = piece.n;
-  int len = length(p, n), units = units_of(len);
-  int seg = int((u - piece.before) / units), first = int((u - piece.before) - int64_t(seg) * units);
+  int len = piece.len, units = units_of(len);
+  const int64_t inside = u - piece.before;
+  int seg = int(inside <= 0x7fffffff ? int64_t(unsigned(inside) / unsigned(units)) : inside / units);
+  int first = int(inside - int64_t(seg) * units);
   const int G = p.HQ / p.HKV;
   const float c = p.scale * kLog2e;
 
@@ -220,29 +231,32 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
       }
       return x;
     };
-    // First byte of tile j (0 .. 3) of a unit whose pages start at lane `from`;
-    // a tile without tokens reads page 0, and is masked.
-    auto tile_at = [&](const Pages& x, int unit, int from, int j) {
+    // Tile j (0 .. 3) of a unit whose pages start at lane `from`, as a buffer of
+    // 2 KB (its address stays in scalar registers); a tile without tokens reads
+    // page 0, and is masked.
+    auto tile_at = [&](const uint8_t* cache, const Pages& x, int unit, int from, int j) {
       const int id = max(__builtin_amdgcn_readlane(x.id, from + j), 0);
       const int inside = (unit * kUnit + 16 * j) & ((1 << p.shift) - 1);
-      return int64_t(id) * p.page_stride + ((int64_t(hkv) << p.shift) + inside) * D;
+      const int64_t at = int64_t(id) * p.page_stride + ((int64_t(hkv) << p.shift) + inside) * D;
+      return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(cache) + at, 0, 16 * D, 0x00020000);
     };
+    const int k_off = l16 * D + 32 * g4, v_off = 4 * g4 * D + 8 * l16;
     u32x4 kr[4][2];                          // tile j: 32 bytes of row l16 from byte 32 g4
     u32x2 vr[4][4];                          // tile j: bytes 8 l16 .. + 7 of rows 4 g4 .. + 3
     auto load_k = [&](const Pages& x, int unit, int from) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint8_t* b = p.k_cache + tile_at(x, unit, from, j);
+        const auto tile = tile_at(p.k_cache, x, unit, from, j);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) kr[j][i] = *reinterpret_cast<const u32x4*>(b + uint32_t(l16 * D + 32 * g4 + 16 * i));
+        for (int i = 0; i < 2; ++i) kr[j][i] = __builtin_amdgcn_raw_buffer_load_b128(tile, k_off + 16 * i, 0, 0);
       }
     };
     auto load_v = [&](const Pages& x, int unit, int from) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint8_t* b = p.v_cache + tile_at(x, unit, from, j);
+        const auto tile = tile_at(p.v_cache, x, unit, from, j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vr[j][i] = *reinterpret_cast<const u32x2*>(b + uint32_t((4 * g4 + i) * D + 8 * l16));
+        for (int i = 0; i < 4; ++i) vr[j][i] = __builtin_amdgcn_raw_buffer_load_b64(tile, v_off + i * D, 0, 0);
       }
     };
 
