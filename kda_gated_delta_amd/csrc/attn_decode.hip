@@ -16,13 +16,15 @@
 // wave's piece is finished there; otherwise its waves leave float32 parts that
 // attn_decode_join_kernel brings together in order.
 //
-// S^T = K Q^T takes the codes as they are, 128 columns to an instruction, with
-// each query row split into two e4m3 terms (split_row); O^T += V^T P^T runs in
-// bfloat16 on V's codes widened (exact).  Contraction orders are chosen so that
-// no data moves between lanes: K's columns as a lane loads 32 bytes of a row,
-// V's rows in the order in which the accumulator of S^T holds the keys, and V's
-// 8-byte loads (one key, 8 columns) turned into 8 operands by byte permutes
-// inside the lane.
+// S^T = K Q^T and O^T += V^T P^T on 16x16x32 matrix instructions, codes widened
+// to bfloat16 (exact).  (The instructions that take e4m3 codes as they are add
+// their products with fewer bits than float32 has: with each query split into
+// two e4m3 terms, exactly, a score was off by 1e-5 of its products' magnitudes,
+// and the kernel no faster.)  Contraction orders are chosen so that no data
+// moves between lanes: K's columns as a lane loads 32 bytes of a row, V's rows
+// in the order in which the accumulator of S^T holds the keys, and V's 8-byte
+// loads (one key, 8 columns) turned into 8 operands by byte permutes inside the
+// lane.
 #include "attn_device.h"
 #include "kda_host.h"
 
@@ -133,49 +135,14 @@ __device__ __forceinline__ Piece find_piece(const Params& p, int wave, int per) 
 
 // ---------------------------------------------------------------- codes to operands
 
-// A query row as two terms in e4m3: 32 values q 2^-e = hi + lo, where the
-// row's largest magnitude lies in (224, 448].  hi keeps four significant bits
-// of bfloat16's eight and lo the other four, so nothing is lost of values
-// within 2^-10 of the largest; smaller ones are off by at most 2^-18 of it.  The
-// first product then takes the cache's codes as they are.  Returns 2^e.
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-__device__ __forceinline__ float split_row(const bf16x8 (&q)[4], i32x8& hi, i32x8& lo) {
-  float top = 0.0f;
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(float(q[s][j])));
-  top = fmaxf(top, __shfl_xor(top, 16, 64));
-  top = half_max(top);
-  // 448 = 1.75 x 2^8; infinities end as NaN whatever e is
-  const int bits = int(__float_as_uint(top) >> 16) & 0x7fff;
-  const int e = max(min((bits >> 7) - 127 - 8 + int((bits & 127) > 96), 119), -110);
-  const float f = __uint_as_float(uint32_t(127 - e) << 23);
-#pragma unroll
-  for (int s = 0; s < 4; ++s)
-#pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-      float x[4], y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = float(q[s][j + i]) * f;
-      int w = 0, r = 0;
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], w, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true);
-      y[0] = x[0] - __builtin_amdgcn_cvt_f32_fp8(w, 0), y[1] = x[1] - __builtin_amdgcn_cvt_f32_fp8(w, 1);
-      y[2] = x[2] - __builtin_amdgcn_cvt_f32_fp8(w, 2), y[3] = x[3] - __builtin_amdgcn_cvt_f32_fp8(w, 3);
-      r = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], r, false);
-      r = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], r, true);
-      hi[2 * s + j / 4] = w;
-      lo[2 * s + j / 4] = r;
-    }
-  return __uint_as_float(uint32_t(127 + e) << 23);
-}
-
-// D = A B + C with A 16 x 128 and B 128 x 16 in e4m3: lane l holds row or
-// column l % 16 at 32 of the 128 indices, those of its 16-lane group; which
-// ones is the same for A and B, so both simply take 32 bytes of a row.
-__device__ __forceinline__ f32x4 mfma16_codes(i32x8 a, i32x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);   // scales 2^0
+// Eight codes (two words) as eight bfloat16 values.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ bf16x8 widen(uint32_t a, uint32_t b) {
+  const bf16x2 w0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+  const bf16x2 w1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+  const bf16x2 w2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+  const bf16x2 w3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+  return (bf16x8){w0[0], w0[1], w1[0], w1[1], w2[0], w2[1], w3[0], w3[1]};
 }
 
 // Pages of up to 64 successive tiles of 16 tokens, one per lane.
@@ -225,7 +192,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
         const int id = table[token >> p.shift];
         if (id >= 0 && id < p.num_pages) {
           x.id = id;
-          x.ks = p.k_scale[int64_t(id) * p.HKV + hkv];
+          x.ks = p.k_scale[int64_t(id) * p.HKV + hkv] * c;
           x.vs = p.v_scale[int64_t(id) * p.HKV + hkv];
         }
       }
@@ -264,17 +231,14 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
     Pages now = pages_at(first);
     load_k(now, first, 0);
     load_v(now, first, 0);
-    i32x8 hi[NT], lo[NT];
-    float qscale[NT];                        // of the lane's row, with the scores' scale in powers of two
+    bf16x8 q[NT][4];
     int limit[NT];                           // tokens that the lane's row sees
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = row0 + min(16 * t + l16, rows - 1), i = r / G;
       const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (hkv * G + r - i * G) * D + 32 * g4;
-      bf16x8 q[4];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) q[s] = *reinterpret_cast<const bf16x8*>(src + 8 * s);
-      qscale[t] = split_row(q, hi[t], lo[t]) * c;
+      for (int s = 0; s < 4; ++s) q[t][s] = *reinterpret_cast<const bf16x8*>(src + 8 * s);
       limit[t] = len - p.Q + i + 1;
     }
     int from = 0;                            // the unit's first tile in `now`
@@ -284,11 +248,14 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
       f32x4 s[NT][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        i32x8 a;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = int(kr[j][i >> 2][i & 3]);
+        for (int t = 0; t < NT; ++t) s[t][j] = (f32x4)(0.0f);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) s[t][j] = mfma16_codes(a, hi[t], mfma16_codes(a, lo[t], (f32x4)(0.0f)));
+        for (int k = 0; k < 4; ++k) {
+          const bf16x8 a = widen(kr[j][k >> 1][2 * (k & 1)], kr[j][k >> 1][2 * (k & 1) + 1]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) s[t][j] = mfma16(a, q[t][k], s[t][j]);
+        }
       }
       float ks[4], vs[4];
       bool none[4];
@@ -309,7 +276,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[t][j] *= ks[j] * qscale[t];
+        for (int j = 0; j < 4; ++j) s[t][j] *= ks[j];
         if (masked) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -370,7 +337,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
               const int jj = j + (e >> 1), i = 2 * (e & 1);
               two[e] = __builtin_amdgcn_perm(vr[jj][i + 1][b], vr[jj][i][b], d ? 0x07030602u : 0x05010400u);
             }
-            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
             bf16x2 lo[4], hi[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

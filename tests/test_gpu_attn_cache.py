@@ -258,6 +258,33 @@ def test_decode_peaked_and_scaled(gpu_lib):
         check_decode(o, lse, q, cache, table, lens, scale)
 
 
+@pytest.mark.parametrize("longest", [1, 3, 40])
+def test_decode_scores_are_float32(gpu_lib, longest):
+    """Few tokens: lse is a score or a few, and shows what the products' sum lost.
+
+    A score is a float32 sum of 128 exact products, then two products and, with the
+    softmax, a few roundings more: at most 140, each off by at most 2^-24 of the
+    sum of magnitudes A and independent of the others, so that over thousands of
+    rows the errors' root mean square stays below sqrt(140) 2^-24 A.
+    """
+    rng = np.random.default_rng(longest)
+    lens, P, HKV, HQ = [int(x) for x in rng.integers(1, longest + 1, 40)], 16, 4, 32
+    table, pages = tables_for(lens, P, seed=longest)
+    cache = usual_cache(30 + longest, pages, HKV, P)
+    q = rand(31, len(lens), 1, HQ, D).to(DEV)
+    _, lse = gpu_lib.attn_decode(q, *cache, ints(table), ints(lens))
+    codes = [codes_of(c) for c in cache[:2]]
+    _, want, _ = ref.attn_decode(f64(q), *codes, f64(cache[2]), f64(cache[3]), table, lens)
+    keys = np.abs(ref.e4m3_table()[codes[0]]) * f64(cache[2])[..., None, None]
+    size = np.zeros_like(want)                     # A: the largest of the row's scores' magnitudes
+    for n, length in enumerate(lens):
+        k = keys[table[n, :-(-length // P)]].transpose(1, 0, 2, 3).reshape(HKV, -1, D)[:, :length]
+        for h in range(HQ):
+            size[n, 0, h] = (k[h * HKV // HQ] @ np.abs(f64(q))[n, 0, h]).max() * D ** -0.5
+    off = np.sqrt(np.mean((f64(lse) - want) ** 2) / np.mean(size ** 2))
+    assert off <= np.sqrt(140) * 2.0 ** -24, off
+
+
 def test_decode_many_waves(gpu_lib):
     """More 64-token units than waves: pieces of several units that begin and end inside sequences."""
     rng = np.random.default_rng(3)
