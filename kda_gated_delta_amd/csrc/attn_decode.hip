@@ -50,7 +50,7 @@ struct Params {
   float scale;
   uint16_t* o;
   float* lse;
-  int rows, tile_rows, row_tiles;            // Q x group; rows of one tile; tiles
+  int rows, tile_rows, row_tiles, join_rows; // Q x group; rows of one tile; tiles; rows of a joining workgroup
   int waves;
   float* parts;                              // [waves + segments][tile_rows][D + 4]: output, maximum, sum
   int *owner, *last_owner;                   // [segments]: first and last wave of those cut, -1 for the others
@@ -422,7 +422,10 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
         *reinterpret_cast<f32x4*>(part + col) = acc;
         if (col == 0) {
           part[D] = top, part[D + 1] = sum;
-          for (int i = 1; i < kWaves; ++i) part[i * p.tile_rows * (D + 4) + D] = -INFINITY;
+          for (int i = 1; i < kWaves; ++i) {
+            part[i * p.tile_rows * (D + 4) + D] = -INFINITY;
+            part[i * p.tile_rows * (D + 4) + D + 1] = 0.0f;
+          }
         }
       }
       return;
@@ -438,25 +441,25 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
 
 // ---------------------------------------------------------------- joining the parts
 
-// A workgroup per (segment, row): THREADS / 32 streams of 32 lanes add up the
-// parts that hold anything, four columns to a lane.
+// A workgroup takes join_rows rows of a segment, one after another: THREADS / 32
+// streams of 32 lanes add up the parts that hold anything, four columns to a
+// lane.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void attn_decode_join_kernel(Params p) {
   constexpr int kStreams = THREADS / 32, kW = THREADS / 64;
   __shared__ float weights[THREADS], red[kStreams][D], stat[kW];
   __shared__ int places[THREADS], counts[kW];
   const int per = p.HKV * p.row_tiles, tile = min(p.rows, p.tile_rows);
-  const int64_t segment = blockIdx.x / unsigned(tile);
+  const int groups = (tile + p.join_rows - 1) / p.join_rows;
+  const int64_t segment = blockIdx.x / unsigned(groups);
   const int w0 = p.owner[segment];
   if (w0 < 0) return;                        // finished by its wave
   const int w1 = p.last_owner[segment];
-  const int r = int(blockIdx.x % unsigned(tile));
   const int n = int(segment / per), seg = int(segment - int64_t(n) * per);
-  const int hkv = seg / p.row_tiles, row = (seg - hkv * p.row_tiles) * p.tile_rows + r;
-  if (row >= p.rows) return;
+  const int hkv = seg / p.row_tiles, row0 = (seg - hkv * p.row_tiles) * p.tile_rows;
+  const int first = int(blockIdx.x % unsigned(groups)) * p.join_rows;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t step = int64_t(p.tile_rows) * (D + 4);
-  const float* part = p.parts + ((segment + w0) * p.tile_rows + r) * (D + 4);
   const int count = w1 - w0 + 1;             // slots of successive waves follow one another
 
   auto over_all = [&](float x, bool top) {
@@ -473,47 +476,52 @@ __global__ __launch_bounds__(THREADS) void attn_decode_join_kernel(Params p) {
     for (int i = 1; i < kW; ++i) x = top ? fmaxf(x, stat[i]) : x + stat[i];
     return x;
   };
-  float m = -INFINITY;
-  for (int i = tid; i < count; i += THREADS) m = fmaxf(m, part[i * step + D]);
-  m = over_all(m, true);
-  const float base = m == -INFINITY ? 0.0f : m;
-  const int stream = tid >> 5, col = (tid & 31) * 4;
-  f32x4 acc = (f32x4)(0.0f);
-  float sum = 0.0f;
-  for (int i0 = 0; i0 < count; i0 += THREADS) {
-    const int i = i0 + tid;
-    const float f = i < count ? __builtin_amdgcn_exp2f(part[i * step + D] - base) : 0.0f;
-    const bool some = f != 0.0f;             // NaN too
-    if (some) sum += f * part[i * step + D + 1];
-    const uint64_t have = __ballot(some);
-    __syncthreads();
-    if (lane == 0) counts[wave] = __builtin_popcountll(have);
-    __syncthreads();
-    int at = __builtin_popcountll(have & ((uint64_t(1) << lane) - 1)), here = 0;
+  for (int r = first; r < min(min(first + p.join_rows, tile), p.rows - row0); ++r) {
+    const int row = row0 + r;
+    const float* part = p.parts + ((segment + w0) * p.tile_rows + r) * (D + 4);
+    float m = -INFINITY;
+    for (int i = tid; i < count; i += THREADS) m = fmaxf(m, part[i * step + D]);
+    m = over_all(m, true);
+    const float base = m == -INFINITY ? 0.0f : m;
+    const int stream = tid >> 5, col = (tid & 31) * 4;
+    f32x4 acc = (f32x4)(0.0f);
+    float sum = 0.0f;
+    for (int i0 = 0; i0 < count; i0 += THREADS) {
+      const int i = i0 + tid;
+      float f = 0.0f, of = 0.0f;
+      if (i < count) f = __builtin_amdgcn_exp2f(part[i * step + D] - base), of = part[i * step + D + 1];
+      const bool some = f != 0.0f || of != of; // a part whose scores are all NaN has no maximum
+      if (some) sum += f * of;
+      const uint64_t have = __ballot(some);
+      __syncthreads();
+      if (lane == 0) counts[wave] = __builtin_popcountll(have);
+      __syncthreads();
+      int at = __builtin_popcountll(have & ((uint64_t(1) << lane) - 1)), here = 0;
 #pragma unroll
-    for (int k = 0; k < kW; ++k) {
-      if (k < wave) at += counts[k];
-      here += counts[k];
-    }
-    if (some) places[at] = i, weights[at] = f;
-    __syncthreads();
+      for (int k = 0; k < kW; ++k) {
+        if (k < wave) at += counts[k];
+        here += counts[k];
+      }
+      if (some) places[at] = i, weights[at] = f;
+      __syncthreads();
 #pragma unroll 8
-    for (int k = stream; k < here; k += kStreams)
-      acc += *reinterpret_cast<const f32x4*>(part + places[k] * step + col) * weights[k];
-  }
-  sum = over_all(sum, false);
-  *reinterpret_cast<f32x4*>(&red[stream][col]) = acc;
-  __syncthreads();
-  if (tid < 32) {
+      for (int k = stream; k < here; k += kStreams)
+        acc += *reinterpret_cast<const f32x4*>(part + places[k] * step + col) * weights[k];
+    }
+    sum = over_all(sum, false);
+    *reinterpret_cast<f32x4*>(&red[stream][col]) = acc;
+    __syncthreads();
+    if (tid < 32) {
 #pragma unroll
-    for (int s = 1; s < kStreams; ++s) acc += *reinterpret_cast<const f32x4*>(&red[s][col]);
-    const int G = p.HQ / p.HKV, i = row / G;
-    const int64_t out = (int64_t(n) * p.Q + i) * p.HQ + hkv * G + row - i * G;
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-    acc *= f;
-    *reinterpret_cast<u32x2*>(p.o + out * D + col) =
-        (u32x2){kda::pack_bf16(acc[0], acc[1]), kda::pack_bf16(acc[2], acc[3])};
-    if (p.lse && tid == 0) p.lse[out] = (m + __log2f(sum)) * kLn2;
+      for (int s = 1; s < kStreams; ++s) acc += *reinterpret_cast<const f32x4*>(&red[s][col]);
+      const int G = p.HQ / p.HKV, i = row / G;
+      const int64_t out = (int64_t(n) * p.Q + i) * p.HQ + hkv * G + row - i * G;
+      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+      acc *= f;
+      *reinterpret_cast<u32x2*>(p.o + out * D + col) =
+          (u32x2){kda::pack_bf16(acc[0], acc[1]), kda::pack_bf16(acc[2], acc[3])};
+      if (p.lse && tid == 0) p.lse[out] = (m + __log2f(sum)) * kLn2;
+    }
   }
 }
 
@@ -571,11 +579,16 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
   const Plan x = plan_for(N, Q, HQ, HKV);
   if (workspace_bytes < x.bytes) return KDA_ERR_WORKSPACE;
   if (x.segments * x.tile_rows > 0x7fffffff) return KDA_ERR_SHAPE;
+  // Most segments of a large batch are finished by one wave, and a workgroup that
+  // finds nothing to join is not free: about 4096 of them, with more rows each.
+  const int tile = x.rows < x.tile_rows ? x.rows : x.tile_rows;
+  const int64_t share = (x.segments * tile + 4095) / 4096;
+  const int join_rows = int(share < tile ? share : tile);
   int* owner = reinterpret_cast<int*>(static_cast<char*>(workspace) + x.parts);
   const Params p{static_cast<const uint16_t*>(q), q_stride, static_cast<const uint8_t*>(k_cache),
                  static_cast<const uint8_t*>(v_cache), k_scale, v_scale, page_table, table_stride, kv_lens,
                  N, Q, HQ, HKV, table_width, __builtin_ctz(page_size), num_pages, page_stride, scale,
-                 static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, x.waves,
+                 static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, join_rows, x.waves,
                  static_cast<float*>(workspace), owner, owner + x.segments};
   const hipStream_t st = kda::as_stream(stream);
   const dim3 grid(unsigned(x.waves / kWaves));
@@ -583,7 +596,7 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
     hipLaunchKernelGGL(attn_decode_kernel<1>, grid, dim3(kThreads), 0, st, p);
   else
     hipLaunchKernelGGL(attn_decode_kernel<2>, grid, dim3(kThreads), 0, st, p);
-  const dim3 joins(unsigned(x.segments * min(x.rows, x.tile_rows)));
+  const dim3 joins(unsigned(x.segments * ((tile + join_rows - 1) / join_rows)));
   // few segments have many parts each
   if (x.waves / x.segments >= 64)
     hipLaunchKernelGGL(attn_decode_join_kernel<1024>, joins, dim3(1024), 0, st, p);

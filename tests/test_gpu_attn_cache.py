@@ -232,6 +232,27 @@ def test_decode_reads_no_further(gpu_lib, Q):
     check_decode(o2, lse2, q, cache, table, lens)
 
 
+@pytest.mark.parametrize("cache_at", [0, 1])
+def test_decode_nan_where_it_is_seen(gpu_lib, cache_at):
+    """One NaN code (whole rows of them: all scores of some waves' pieces) reaches the rows that see it, and no others."""
+    lens, P = [300, 5000, 64], 64
+    table, pages = tables_for(lens, P, seed=5)
+    cache = usual_cache(10, pages, 2, P)
+    q = rand(11, 3, 1, 8, D).to(DEV)
+    o, _ = gpu_lib.attn_decode(q, *cache, ints(table), ints(lens))
+    raw = cache[cache_at].view(torch.uint8)
+    raw[int(table[0, 1]), 0, 3, 9] = 0x7f
+    for page in table[1, 10:40]:
+        raw[int(page), 1] = 0xff
+    got, lse = gpu_lib.attn_decode(q, *cache, ints(table), ints(lens))
+    assert torch.equal(got[2], o[2]) and torch.equal(got[0, :, 4:], o[0, :, 4:]) and torch.equal(got[1, :, :4], o[1, :, :4])
+    assert got[1, :, 4:].isnan().all()
+    if cache_at == 0:
+        assert got[0, :, :4].isnan().all() and lse[0, :, :4].isnan().all() and lse[1, :, 4:].isnan().all()
+    else:
+        assert got[0, :, :4, 9].isnan().all() and torch.equal(got[0, :, :4, :9], o[0, :, :4, :9])
+
+
 def test_decode_pages_missing(gpu_lib):
     """A page outside the cache holds no tokens; lengths beyond the table and below 0 are cut."""
     lens, P = [100, 64, 40, 500, -3], 16
