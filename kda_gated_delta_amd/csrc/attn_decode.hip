@@ -441,9 +441,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
 
 // ---------------------------------------------------------------- joining the parts
 
-// A workgroup takes join_rows rows of a segment, one after another: THREADS / 32
-// streams of 32 lanes add up the parts that hold anything, four columns to a
-// lane.
+// A workgroup takes join_rows rows of a segment.  Of few parts (at most 64) a
+// wave adds up a row's alone, without a barrier, two columns to a lane; of many,
+// THREADS / 32 streams of 32 lanes do, row after row, four columns to a lane.
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void attn_decode_join_kernel(Params p) {
   constexpr int kStreams = THREADS / 32, kW = THREADS / 64;
@@ -462,6 +462,48 @@ __global__ __launch_bounds__(THREADS) void attn_decode_join_kernel(Params p) {
   const int64_t step = int64_t(p.tile_rows) * (D + 4);
   const int count = w1 - w0 + 1;             // slots of successive waves follow one another
 
+  const int limit = min(min(first + p.join_rows, tile), p.rows - row0), G = p.HQ / p.HKV;
+  if (count <= 64) {
+    for (int r = first + wave; r < limit; r += kW) {
+      const float* part = p.parts + ((segment + w0) * p.tile_rows + r) * (D + 4);
+      float mine = -INFINITY, of = 0.0f;
+      if (lane < count) mine = part[lane * step + D], of = part[lane * step + D + 1];
+      float m = mine;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) m = fmaxf(m, __shfl_xor(m, d, 64));
+      const float f = __builtin_amdgcn_exp2f(mine - (m == -INFINITY ? 0.0f : m));
+      const bool some = f != 0.0f || of != of; // a part whose scores are all NaN has no maximum
+      float sum = some ? f * of : 0.0f;
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
+      float x = 0.0f, y = 0.0f;
+      uint64_t have = __ballot(some);
+      while (have) {                         // four at a time: their loads go out together
+        float w[4];
+        const float2* at[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = have ? __builtin_ctzll(have) : -1;
+          w[k] = i < 0 ? 0.0f : __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
+          at[k] = i < 0 ? nullptr : reinterpret_cast<const float2*>(part + i * step) + lane;
+          have &= have - 1;                  // 0 stays 0
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (at[k]) {
+            const float2 o = *at[k];
+            x = __builtin_fmaf(o.x, w[k], x), y = __builtin_fmaf(o.y, w[k], y);
+          }
+      }
+      const int row = row0 + r, i = row / G;
+      const int64_t out = (int64_t(n) * p.Q + i) * p.HQ + hkv * G + row - i * G;
+      const float g = sum == 0.0f ? 0.0f : 1.0f / sum;
+      *reinterpret_cast<uint32_t*>(p.o + out * D + 2 * lane) = kda::pack_bf16(x * g, y * g);
+      if (p.lse && lane == 0) p.lse[out] = (m + __log2f(sum)) * kLn2;
+    }
+    return;
+  }
+
   auto over_all = [&](float x, bool top) {
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -476,7 +518,7 @@ __global__ __launch_bounds__(THREADS) void attn_decode_join_kernel(Params p) {
     for (int i = 1; i < kW; ++i) x = top ? fmaxf(x, stat[i]) : x + stat[i];
     return x;
   };
-  for (int r = first; r < min(min(first + p.join_rows, tile), p.rows - row0); ++r) {
+  for (int r = first; r < limit; ++r) {
     const int row = row0 + r;
     const float* part = p.parts + ((segment + w0) * p.tile_rows + r) * (D + 4);
     float m = -INFINITY;
@@ -514,7 +556,7 @@ __global__ __launch_bounds__(THREADS) void attn_decode_join_kernel(Params p) {
     if (tid < 32) {
 #pragma unroll
       for (int s = 1; s < kStreams; ++s) acc += *reinterpret_cast<const f32x4*>(&red[s][col]);
-      const int G = p.HQ / p.HKV, i = row / G;
+      const int i = row / G;
       const int64_t out = (int64_t(n) * p.Q + i) * p.HQ + hkv * G + row - i * G;
       const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
       acc *= f;
@@ -579,10 +621,14 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
   const Plan x = plan_for(N, Q, HQ, HKV);
   if (workspace_bytes < x.bytes) return KDA_ERR_WORKSPACE;
   if (x.segments * x.tile_rows > 0x7fffffff) return KDA_ERR_SHAPE;
-  // Most segments of a large batch are finished by one wave, and a workgroup that
-  // finds nothing to join is not free: about 4096 of them, with more rows each.
+  // Rows of a joining workgroup: one where segments are few and have many parts
+  // each, four (a wave each) otherwise, and more where there would be over 4096
+  // workgroups: most segments of a large batch are finished by one wave, and a
+  // workgroup that finds nothing to join is not free.
   const int tile = x.rows < x.tile_rows ? x.rows : x.tile_rows;
-  const int64_t share = (x.segments * tile + 4095) / 4096;
+  const bool many = x.waves / x.segments >= 64;
+  int64_t share = (x.segments * tile + 4095) / 4096;
+  if (!many && share < 4) share = 4;
   const int join_rows = int(share < tile ? share : tile);
   int* owner = reinterpret_cast<int*>(static_cast<char*>(workspace) + x.parts);
   const Params p{static_cast<const uint16_t*>(q), q_stride, static_cast<const uint8_t*>(k_cache),
@@ -597,8 +643,7 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
   else
     hipLaunchKernelGGL(attn_decode_kernel<2>, grid, dim3(kThreads), 0, st, p);
   const dim3 joins(unsigned(x.segments * ((tile + join_rows - 1) / join_rows)));
-  // few segments have many parts each
-  if (x.waves / x.segments >= 64)
+  if (many)
     hipLaunchKernelGGL(attn_decode_join_kernel<1024>, joins, dim3(1024), 0, st, p);
   else
     hipLaunchKernelGGL(attn_decode_join_kernel<256>, joins, dim3(256), 0, st, p);
