@@ -45,10 +45,15 @@ struct Params {
 
 // ---------------------------------------------------------------- dQ
 
-template <typename Out>
-__global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(Params p) {
-  __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+// kSplit = 2: a second set of four waves takes every other key tile, as in the
+// forward, for launches that would leave half of the wave slots empty.
+template <typename Out, int kSplit>
+__global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p) {
+  constexpr int kHalf = 4 * kTileBytes;    // two buffers of K and V
+  __shared__ __align__(1024) unsigned char all[kSplit * kHalf];
+  const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int half = kSplit == 1 ? 0 : id / kWaves, wave = id - half * kWaves;
+  unsigned char* lds = all + half * kHalf;
   const int l32 = lane & 31, h = lane >> 5;
   int slot, hkv, hq;
   if (!find_head(blockIdx.x, p.slots, p.HQ, p.HKV, slot, hkv, hq)) return;
@@ -81,8 +86,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(Params p) {
   vload.init(wave, lane, p.v_stride);
   const uint16_t* kb = p.k + rows.first * p.k_stride + hkv * D;
   const uint16_t* vb = p.v + rows.first * p.v_stride + hkv * D;
-  auto issue = [&](int t) {
-    unsigned char* buf = lds + (t & 1) * 2 * kTileBytes;
+  auto issue = [&](int t, int at_buf) {
+    unsigned char* buf = lds + at_buf * 2 * kTileBytes;
     const int64_t at = int64_t(t) * kTile;
     kload.issue(kb + at * p.k_stride, p.k_stride, rows.len - int(at), buf, wave);
     vload.issue(vb + at * p.v_stride, p.v_stride, rows.len - int(at), buf + kTileBytes, wave);
@@ -103,7 +108,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(Params p) {
         if (8 * (e >> 2) + 4 * h + (e & 3) > last) s[e] = g[e] = 0.0f;
     }
   };
-  issue(0);
 
   // delta.  The rounding of o to bfloat16 enters it, and with it every score's
   // gradient of the row.  Where o is a mean of many values it is small beside
@@ -112,10 +116,11 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(Params p) {
   // delta is made as sum_j P_ij (dO V^T)_ij, to which it is equal.
   float delta = 0.0f;
   if (rows.row0 == 0) {
+    issue(0, 0);
     for (int t = 0; t < tiles; ++t) {
       __builtin_amdgcn_s_waitcnt(kWaitLoads);
       kda::lds_barrier();
-      if (t + 1 < tiles) issue(t + 1);
+      if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
       for (int w = 0; w < 2; ++w) {
         const int key0 = t * kTile + 32 * w;
         if (key0 > r0 + 31) break;
@@ -126,8 +131,9 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(Params p) {
       }
     }
     kda::lds_barrier();
-    issue(0);
+    if (half < tiles) issue(half, 0);
   } else {
+    if (half < tiles) issue(half, 0);
     const uint16_t* os = p.o + ((rows.first + r) * p.HQ + hq) * D + 8 * h;
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
@@ -137,16 +143,18 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(Params p) {
     }
   }
   delta = half_sum(delta);
-  if (r0 + l32 < rows.len && h == 0) {
+  if (r0 + l32 < rows.len && h == 0 && half == 0) {
     p.lse2[stat] = lse2;
     p.delta[stat] = delta;
   }
 
-  for (int t = 0; t < tiles; ++t) {
+  for (int i = 0; i * kSplit < tiles; ++i) {               // as often for both halves: they share the barrier
+    const int t = i * kSplit + half;
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     kda::lds_barrier();
-    const unsigned char* kt = lds + (t & 1) * 2 * kTileBytes;
-    if (t + 1 < tiles) issue(t + 1);
+    const unsigned char* kt = lds + (i & 1) * 2 * kTileBytes;
+    if (t + kSplit < tiles) issue(t + kSplit, (i + 1) & 1);
+    if (t >= tiles) continue;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const int key0 = t * kTile + 32 * w;
@@ -165,6 +173,22 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dq_kernel(Params p) {
         for (int d = 0; d < 4; ++d) dq[d] = mfma32(read_columns(kt, 32 * w, k, 32 * d, lane), b, dq[d]);
       }
     }
+  }
+  if constexpr (kSplit == 2) {                             // the second half's sums through LDS
+    kda::lds_barrier();
+    float* place = reinterpret_cast<float*>(all) + wave * 64 * 64 + lane;
+    if (half == 1) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) place[(16 * d + e) * 64] = dq[d][e];
+    }
+    kda::lds_barrier();
+    if (half == 1) return;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) dq[d][e] += place[(16 * d + e) * 64];
   }
   if (r0 + l32 >= rows.len) return;
   Out* dst = static_cast<Out*>(p.dq) + ((rows.first + r) * p.HQ + hq) * D;
@@ -307,14 +331,17 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(Params p) {
 
 // Workgroups that share a key tile.  A unit is one (key tile, key/value head);
 // two workgroups fit a compute unit, and units of early keys have many times
-// the work of late ones, so the device wants about four per compute unit.  A
-// part should still walk eight query tiles.
+// the work of late ones, so the device wants about four per compute unit
+// (measured at 8192 tokens, 16 query and 4 key/value heads: 1, 2, 3, 4, 6 parts
+// take 2.44, 1.65, 1.43, 1.33, 1.35 ms for the training pass).  A part should
+// still walk two query tiles: with one the parts' sum costs more than the walk
+// (2000 tokens, 4 heads: 127 us with two, 148 with one, 150 with eight).
 int parts_for(int64_t slots, int T, int N, bool packed, int HQ, int HKV) {
   const int64_t units = slots * HKV, want = 4 * int64_t(kda::device_cus());
   if (units >= want) return 1;
   const int64_t len = packed ? T / N : T;                  // a typical sequence
   const int64_t walk = (len / kTile / 2 + 1) * (HQ / HKV);
-  const int64_t most = walk / 8 < 1 ? 1 : (walk / 8 > 16 ? 16 : walk / 8);
+  const int64_t most = walk / 2 < 1 ? 1 : (walk / 2 > 16 ? 16 : walk / 2);
   const int64_t parts = (want + units - 1) / units;
   return int(parts < most ? parts : most);
 }
@@ -327,7 +354,11 @@ size_t stat_floats(int64_t B, int64_t T, int64_t HQ) { return size_t((B * T * HQ
 
 template <typename Out>
 int launch(const Params& p, hipStream_t stream) {
-  hipLaunchKernelGGL(attn_dq_kernel<Out>, dim3(unsigned(head_blocks(p.slots, p.HQ, p.HKV))), dim3(kThreads), 0, stream, p);
+  const int64_t blocks = head_blocks(p.slots, p.HQ, p.HKV);
+  if (blocks <= kda::device_cus())
+    hipLaunchKernelGGL((attn_dq_kernel<Out, 2>), dim3(unsigned(blocks)), dim3(2 * kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((attn_dq_kernel<Out, 1>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, p);
   const dim3 grid(unsigned(p.slots * p.HKV * p.parts));
   if (p.parts == 1) {
     hipLaunchKernelGGL(attn_dkv_kernel<Out>, grid, dim3(kThreads), 0, stream, p);

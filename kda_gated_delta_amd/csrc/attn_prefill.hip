@@ -22,7 +22,6 @@ namespace {
 using namespace kda::attn;
 
 constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 constexpr int BM = 32 * kWaves;            // query rows of a workgroup
 
 struct Params {
@@ -40,9 +39,17 @@ struct Params {
 // float32 and bfloat16, and most tiles skip the 64 multiplications.
 constexpr float kSlack = 8.0f;
 
-__global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(Params p) {
-  __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+// kSplit = 2: a second set of four waves takes every other key tile of the same
+// rows, and the two halves of a row are joined at the end.  For launches that
+// would leave half of the device's wave slots empty: the walk over the keys is a
+// chain, and two waves per SIMD halve it.
+template <int kSplit>
+__global__ __launch_bounds__(64 * kWaves * kSplit, 2) void attn_prefill_kernel(Params p) {
+  constexpr int kHalf = 4 * kTileBytes;    // two buffers of K and V
+  __shared__ __align__(1024) unsigned char all[kSplit * kHalf];
+  const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int half = kSplit == 1 ? 0 : id / kWaves, wave = id - half * kWaves;
+  unsigned char* lds = all + half * kHalf;
   const int l32 = lane & 31, h = lane >> 5;
 
   int slot, hkv, hq;
@@ -69,22 +76,23 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(Params p) {
   vload.init(wave, lane, p.v_stride);
   const uint16_t* kb = p.k + rows.first * p.k_stride + hkv * D;
   const uint16_t* vb = p.v + rows.first * p.v_stride + hkv * D;
-  kload.issue(kb, p.k_stride, rows.len, lds, wave);
-  vload.issue(vb, p.v_stride, rows.len, lds + kTileBytes, wave);
+  auto issue = [&](int t, int buf) {
+    unsigned char* to = lds + buf * 2 * kTileBytes;
+    const int64_t at = int64_t(t) * kTile;
+    kload.issue(kb + at * p.k_stride, p.k_stride, rows.len - int(at), to, wave);
+    vload.issue(vb + at * p.v_stride, p.v_stride, rows.len - int(at), to + kTileBytes, wave);
+  };
+  if (half < tiles) issue(half, 0);
 
-  for (int t = 0; t < tiles; ++t) {
+  for (int i = 0; i * kSplit < tiles; ++i) {              // as often for both halves: they share the barrier
+    const int t = i * kSplit + half;
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     kda::lds_barrier();
-    unsigned char* kt = lds + (t & 1) * 2 * kTileBytes;
+    const unsigned char* kt = lds + (i & 1) * 2 * kTileBytes;
     const unsigned char* vt = kt + kTileBytes;
-    if (t + 1 < tiles) {
-      unsigned char* next = lds + ((t + 1) & 1) * 2 * kTileBytes;
-      const int64_t at = int64_t(t + 1) * kTile;
-      kload.issue(kb + at * p.k_stride, p.k_stride, rows.len - int(at), next, wave);
-      vload.issue(vb + at * p.v_stride, p.v_stride, rows.len - int(at), next + kTileBytes, wave);
-    }
+    if (t + kSplit < tiles) issue(t + kSplit, (i + 1) & 1);
     const int key0 = t * kTile;
-    if (key0 > r0 + 31) continue;                         // wholly after this wave's rows
+    if (t >= tiles || key0 > r0 + 31) continue;           // wholly after this wave's rows
 
     f32x16 s[2];
 #pragma unroll
@@ -138,7 +146,31 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(Params p) {
       }
   }
 
-  const float total = half_sum(l);
+  float total = half_sum(l);
+  if constexpr (kSplit == 2) {
+    // The second half's output, maximum and sum, 66 floats per lane, through LDS.
+    // Its rows may have seen no key there (maximum -inf, output and sum 0).
+    kda::lds_barrier();
+    float* place = reinterpret_cast<float*>(all) + wave * 66 * 64 + lane;
+    if (half == 1) {
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) place[(16 * d + e) * 64] = o[d][e];
+      place[64 * 64] = m;
+      place[65 * 64] = total;
+    }
+    kda::lds_barrier();
+    if (half == 1) return;
+    const float m2 = place[64 * 64], top = fmaxf(m, m2);
+    const float f1 = __builtin_amdgcn_exp2f((m - top) * c), f2 = __builtin_amdgcn_exp2f((m2 - top) * c);
+    total = total * f1 + place[65 * 64] * f2;
+    m = top;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * f1 + place[(16 * d + e) * 64] * f2;
+  }
   if (r0 + l32 >= rows.len) return;                       // both lanes of a pair alike
   const float f = 1.0f / total;
   uint16_t* dst = p.o + ((rows.first + r) * p.HQ + hq) * D;
@@ -165,6 +197,10 @@ extern "C" int kda_attn_prefill(const void* q, const void* k, const void* v, int
   const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                  q_stride, k_stride, v_stride, cu_seqlens, cu_seqlens ? num_seqs : B, T, HQ, HKV, int(slots), scale,
                  static_cast<uint16_t*>(o), lse};
-  hipLaunchKernelGGL(attn_prefill_kernel, dim3(unsigned(head_blocks(slots, HQ, HKV))), dim3(kThreads), 0, kda::as_stream(stream), p);
+  const int64_t blocks = head_blocks(slots, HQ, HKV);
+  if (blocks <= kda::device_cus())
+    hipLaunchKernelGGL(attn_prefill_kernel<2>, dim3(unsigned(blocks)), dim3(128 * kWaves), 0, kda::as_stream(stream), p);
+  else
+    hipLaunchKernelGGL(attn_prefill_kernel<1>, dim3(unsigned(blocks)), dim3(64 * kWaves), 0, kda::as_stream(stream), p);
   return kda::launch_status();
 }
