@@ -82,11 +82,12 @@ def _ptr(t):
 def _call(dev, name, *args):
     """Call an entry point with device `dev` current, on its current stream."""
     fn = getattr(_kda.load(), name)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
     if torch.cuda.current_device() == dev:
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        code = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+            code = fn(*args, stream)
     if code:
         _kda._check(code, name)
 
@@ -126,8 +127,8 @@ def attn_prefill(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None):
         lse = q.new_empty((B, HQ, T), dtype=_F32)
     else:
         _dense(lse, "lse", _F32, dev, (B, HQ, T))
-    _call(dev, "kda_attn_prefill", _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(cu_seqlens), N, B, T, HQ, HKV, D,
-          _scale(scale), _ptr(out), _ptr(lse))
+    _call(dev, "kda_attn_prefill", q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(cu_seqlens), N, B, T, HQ, HKV, D,
+          _scale(scale), out.data_ptr(), lse.data_ptr())
     return out, lse
 
 
@@ -154,9 +155,9 @@ def attn_backward(q, k, v, o, lse, d_out, cu_seqlens=None, scale=None, workspace
     dq = q.new_empty((B, T, HQ, D), dtype=dtype)
     dk = q.new_empty((B, T, HKV, D), dtype=dtype)
     dv = q.new_empty((B, T, HKV, D), dtype=dtype)
-    _call(dev, "kda_attn_backward", _ptr(q), _ptr(k), _ptr(v), qs, ks, vs, _ptr(o), _ptr(lse), _ptr(d_out),
-          _ptr(cu_seqlens), N, B, T, HQ, HKV, D, _scale(scale), _ptr(dq), _ptr(dk), _ptr(dv),
-          _kda.GRAD_INPUT_DTYPE if grad_dtype == "input" else _kda.GRAD_FLOAT32, _ptr(workspace), workspace.numel())
+    _call(dev, "kda_attn_backward", q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, o.data_ptr(), lse.data_ptr(), d_out.data_ptr(),
+          _ptr(cu_seqlens), N, B, T, HQ, HKV, D, _scale(scale), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+          _kda.GRAD_INPUT_DTYPE if grad_dtype == "input" else _kda.GRAD_FLOAT32, workspace.data_ptr(), workspace.numel())
     return dq, dk, dv
 
 
@@ -201,9 +202,9 @@ def attn_tables(cached_lens, new_lens, page_table, free_pages, free_head, page_s
             return t
         cu_seqlens, slots = made(cu_seqlens, "cu_seqlens", N + 1), made(slots, "slots", num_tokens)
         kv_lens, next_head = made(kv_lens, "kv_lens", N), made(next_head, "next_head", 1)
-    _call(dev, "kda_attn_tables", _ptr(cached_lens), _ptr(new_lens), N, _ptr(page_table),
-          table_stride, W, _ptr(free_pages), free_pages.numel(), _ptr(free_head), page_size,
-          num_tokens, _ptr(cu_seqlens), _ptr(slots), _ptr(kv_lens), _ptr(next_head))
+    _call(dev, "kda_attn_tables", cached_lens.data_ptr(), new_lens.data_ptr(), N, page_table.data_ptr(),
+          table_stride, W, free_pages.data_ptr(), free_pages.numel(), _ptr(free_head), page_size,
+          num_tokens, cu_seqlens.data_ptr(), slots.data_ptr(), kv_lens.data_ptr(), next_head.data_ptr())
     return cu_seqlens, slots, kv_lens, next_head
 
 
@@ -235,8 +236,8 @@ def attn_cache_store(k, v, k_cache, v_cache, k_scale, v_scale, slots):
     ks, vs = _rows(k, "k", HKV, (T,)), _rows(v, "v", HKV, (T,))
     pages, size, stride = _cache(k_cache, v_cache, k_scale, v_scale, dev, HKV)
     _dense(slots, "slots", _I32, dev, (T,))
-    _call(dev, "kda_attn_cache_store", _ptr(k), _ptr(v), ks, vs, _ptr(slots), T, HKV, D, _ptr(k_cache), _ptr(v_cache),
-          _ptr(k_scale), _ptr(v_scale), size, stride, pages)
+    _call(dev, "kda_attn_cache_store", k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, HKV, D, k_cache.data_ptr(), v_cache.data_ptr(),
+          k_scale.data_ptr(), v_scale.data_ptr(), size, stride, pages)
 
 
 def attn_decode_workspace_size(N, Q, HQ, HKV):
@@ -271,7 +272,7 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, scal
         workspace = q.new_empty(max(attn_decode_workspace_size(N, Q, HQ, HKV), 16), dtype=torch.uint8)
     else:
         _dense(workspace, "workspace", torch.uint8, dev)
-    _call(dev, "kda_attn_decode", _ptr(q), qs, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), size, stride,
-          pages, _ptr(page_table), table_stride, W, _ptr(kv_lens), N, Q, HQ, HKV, D,
-          _scale(scale), _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel())
+    _call(dev, "kda_attn_decode", q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), size, stride,
+          pages, page_table.data_ptr(), table_stride, W, kv_lens.data_ptr(), N, Q, HQ, HKV, D,
+          _scale(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out, lse

@@ -17,6 +17,8 @@
 #include "attn_device.h"
 #include "kda_host.h"
 
+#include <type_traits>
+
 namespace {
 
 using namespace kda::attn;
@@ -38,6 +40,19 @@ struct Params {
 // output are brought to the new one: weights stay below 2^8, far inside
 // float32 and bfloat16, and most tiles skip the 64 multiplications.
 constexpr float kSlack = 8.0f;
+
+// Whether any row of a tile's first half, or two, holds an infinity or NaN.
+__device__ __forceinline__ bool any_not_finite(const unsigned char* tile, int halves, int lane) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 top = {0, 0};
+#pragma unroll 8
+  for (int i = 0; i < 8 * halves; ++i) {
+    const u32x4 x = *reinterpret_cast<const u32x4*>(tile + i * 1024 + lane * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[j] & 0x7fff7fffu));
+  }
+  return __any(top[0] >= 0x7f80 || top[1] >= 0x7f80);
+}
 
 // kSplit = 2: a second set of four waves takes every other key tile of the same
 // rows, and the two halves of a row are joined at the end.  For launches that
@@ -82,32 +97,26 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void attn_prefill_kernel(P
     kload.issue(kb + at * p.k_stride, p.k_stride, rows.len - int(at), to, wave);
     vload.issue(vb + at * p.v_stride, p.v_stride, rows.len - int(at), to + kTileBytes, wave);
   };
-  if (half < tiles) issue(half, 0);
-
-  for (int i = 0; i * kSplit < tiles; ++i) {              // as often for both halves: they share the barrier
-    const int t = i * kSplit + half;
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
-    kda::lds_barrier();
-    const unsigned char* kt = lds + (i & 1) * 2 * kTileBytes;
-    const unsigned char* vt = kt + kTileBytes;
-    if (t + kSplit < tiles) issue(t + kSplit, (i + 1) & 1);
-    const int key0 = t * kTile;
-    if (t >= tiles || key0 > r0 + 31) continue;           // wholly after this wave's rows
-
+  int late = -1;                                          // first key of a tile left for the end
+  auto tile = [&](const unsigned char* kt, const unsigned char* vt, int key0, auto diagonal) {
+    // where the diagonal crosses the first half of a tile the second is not seen
+    const int halves_seen = decltype(diagonal)::value && r0 == key0 ? 1 : 2;
     f32x16 s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       s[u] = (f32x16)(0.0f);
+      if (u >= halves_seen) continue;
 #pragma unroll
       for (int k = 0; k < 8; ++k) s[u] = mfma32(read_rows(kt, 32 * u, l32, h, k), q[k], s[u]);
     }
-    if (key0 + kTile - 1 > r0) {                          // some (row, key) pairs lie after the diagonal
+    if constexpr (decltype(diagonal)::value) {
       const int last = r0 + l32 - key0;                   // the last key of the tile that the row sees
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (32 * u + 8 * (e >> 2) + 4 * h + (e & 3) > last) s[u][e] = -INFINITY;
+      if (any_not_finite(vt, halves_seen, lane)) late = key0;
     }
     float mx = s[0][0];
 #pragma unroll
@@ -133,8 +142,10 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void attn_prefill_kernel(P
         sum += s[u][e];
       }
     l += sum;
+    if (decltype(diagonal)::value && late >= 0) return;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) {
+      if (u >= halves_seen) continue;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float x[8];
@@ -144,6 +155,65 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void attn_prefill_kernel(P
 #pragma unroll
         for (int d = 0; d < 4; ++d) o[d] = mfma32(read_columns(vt, 32 * u, k, 32 * d, lane), w, o[d]);
       }
+    }
+  };
+
+  // The i-th tile of this half is there, the next on its way.  All waves pass as
+  // often.
+  const int rounds = (tiles + kSplit - 1) / kSplit;
+  auto arrive = [&](int i) {
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    kda::lds_barrier();
+    if ((i + 1) * kSplit + half < tiles) issue((i + 1) * kSplit + half, (i + 1) & 1);
+  };
+  auto take = [&](int i, auto diagonal) {
+    const unsigned char* kt = lds + (i & 1) * 2 * kTileBytes;
+    tile(kt, kt + kTileBytes, (i * kSplit + half) * kTile, diagonal);
+  };
+  if (half < tiles) issue(half, 0);
+  // Tiles before the diagonal, the one that it crosses (if it is this half's),
+  // and those that other waves of the workgroup still take.
+  const int whole = min(r0 / kTile, tiles);               // tiles that all rows of the wave see
+  int i = 0;
+  for (; i * kSplit + half < whole; ++i) {
+    arrive(i);
+    take(i, std::false_type{});
+  }
+  if (i < rounds) {
+    arrive(i);
+    if (i * kSplit + half == r0 / kTile) take(i, std::true_type{});
+    ++i;
+  }
+  for (; i < rounds; ++i) arrive(i);
+
+  // A weight of zero does not keep an infinity or NaN of a later row of V out of a
+  // product.  If the tile that the diagonal crosses, a wave's last, holds one, its
+  // keys are added here one by one, from memory, each to the rows that see it.
+  if (late >= 0) {
+#pragma unroll 1
+    for (int key = late; key < min(r0 + 32, rows.len); ++key) {
+      const uint16_t* kr = kb + key * p.k_stride + 8 * h;
+      const uint16_t* vr = vb + key * p.v_stride + 4 * h;
+      float x = 0.0f;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const bf16x8 y = *reinterpret_cast<const bf16x8*>(kr + 16 * s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x = __builtin_fmaf(float(q[s][j]), float(y[j]), x);
+      }
+      x = __builtin_amdgcn_exp2f(__builtin_fmaf(half_sum(x), c, -m * c));
+      if (key > r0 + l32) continue;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const u32x2 y = *reinterpret_cast<const u32x2*>(vr + 32 * d + 8 * e);
+          o[d][4 * e] = __builtin_fmaf(x, kda::bf16lo(y[0]), o[d][4 * e]);
+          o[d][4 * e + 1] = __builtin_fmaf(x, kda::bf16hi(y[0]), o[d][4 * e + 1]);
+          o[d][4 * e + 2] = __builtin_fmaf(x, kda::bf16lo(y[1]), o[d][4 * e + 2]);
+          o[d][4 * e + 3] = __builtin_fmaf(x, kda::bf16hi(y[1]), o[d][4 * e + 3]);
+        }
+    }
   }
 
   float total = half_sum(l);

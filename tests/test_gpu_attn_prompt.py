@@ -203,6 +203,32 @@ def test_sequences_do_not_meet(gpu_lib, bad):
     assert torch.equal(o[:, :40], o3[:, :40]) and not torch.equal(o[:, 40:70], o3[:, 40:70])
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at", [[0], [1, 5], [31], [32, 40], [63], [64], [95, 96], [150, 299]])
+def test_later_values_do_not_reach_earlier_rows(gpu_lib, at, bad):
+    """Infinities and NaN in v (or k) of a token: the rows before it are as if it were not there."""
+    q, k, v, up, _ = case(1, 300, 4, 2, None, seed=65)
+    want, wl, o_abs = ref.attn_prefill(f64(q), f64(k), f64(v))
+    ew = U + 2.1 * eps(f64(q), f64(k), 300)
+    v2 = v.clone()
+    for j in at:
+        v2[0, j, 1, 7 * j % D] = bad
+    o, lse = gpu_lib.attn_prefill(q, k, v2)
+    seen = np.arange(300) >= at[0]
+    clean = np.ones((300, 4, D), bool)
+    for j in at:
+        clean[j:, 2:, 7 * j % D] = False
+    got = f64(o)[0]
+    assert np.isfinite(got[clean]).all() and not np.isfinite(got[~clean]).any()
+    tol = (ew * o_abs + U * np.abs(want)) * 1.01
+    assert (np.abs(got - want[0])[clean] <= tol[0][clean]).all()
+    check(lse, wl, eps(f64(q), f64(k), 300) + 2.0 ** -22 * (1 + np.abs(wl)), "lse")
+    k2 = k.clone()
+    k2[0, at[0], 1, 3] = bad
+    o2, _ = gpu_lib.attn_prefill(q, k2, v)
+    assert (np.abs(f64(o2) - want)[:, ~seen] <= tol[:, ~seen]).all() and torch.equal(o2[:, :, :2], gpu_lib.attn_prefill(q, k, v)[0][:, :, :2])
+
+
 def test_another_stream(gpu_lib):
     q, k, v, up, _ = case(1, 400, 4, 2, None, seed=70)
     o, lse = gpu_lib.attn_prefill(q, k, v)
