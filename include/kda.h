@@ -517,9 +517,8 @@ size_t kda_chunk_backward_workspace_size(int32_t B, int32_t T, int32_t H, int32_
  *               undefined outputs.
  *   o           bf16 [B, T, HQ, 128], dense
  *   lse         fp32 [B, HQ, T], dense, or NULL
- * A token's values reach no other sequence's outputs, whatever they are.
- * Within a sequence, an infinity or NaN in v_j also reaches rows before j in
- * the same 32 rows (as 0 * v_j).
+ * A token reaches the outputs of its own sequence from its own row on and no
+ * others, also where it holds infinities or NaN.
  * Sizes: B >= 1, T >= 0 (0 enqueues nothing), 1 <= HQ <= 65535.  o and lse must
  * not alias inputs.  Deterministic.
  */
@@ -539,6 +538,9 @@ int kda_attn_prefill(const void* q, const void* k, const void* v, int64_t q_stri
  *               outside the sequences are left as they were.
  *   workspace   at least kda_attn_backward_workspace_size(...) bytes; contents
  *               on entry do not matter; calls that share one must not overlap
+ * A token reaches only its own sequence's gradients, whatever it holds; there
+ * an infinity or NaN may also reach rows of the same 32 that do not depend on
+ * it (as a product with a weight of 0).
  * Deterministic: no atomics, one order of every sum.
  */
 int kda_attn_backward(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
@@ -637,8 +639,8 @@ int kda_attn_cache_store(const void* k, const void* v, int64_t k_stride, int64_t
  *   workspace   at least kda_attn_decode_workspace_size(...) bytes; contents on
  *               entry do not matter; calls that share one must not overlap
  * What lies in a page behind the sequence's end does not reach the outputs,
- * whatever it is.  A NaN code within the last Q - 1 values also reaches the
- * queries before it.  How a sequence is cut among waves depends on all
+ * whatever it is, and a NaN code only the queries that see its token.  The
+ * scales of pages that hold tokens are finite.  How a sequence is cut among waves depends on all
  * sequences of the call, so the last bits of a row may differ from batch to
  * batch; the same call gives the same bits.
  * Sizes: N >= 0 (0 enqueues nothing), 1 <= Q <= 1024, num_pages >= 1,

@@ -242,6 +242,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
       limit[t] = len - p.Q + i + 1;
     }
     int from = 0;                            // the unit's first tile in `now`
+    uint32_t late = 0;                       // units left for the end, from that of token len - Q + 1 on
     for (int unit = first; unit < last; ++unit) {
       const int key0 = unit * kUnit;
       const bool masked = key0 + kUnit > len - p.Q + 1 || (__ballot(now.id < 0) >> from & 15) != 0;
@@ -309,12 +310,33 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
             s[t][j][e] = x * vs[j];
           }
       }
-      if (masked) {                          // what lies behind the end may be anything: NaN codes too
+      // What lies behind the end may be anything, NaN codes too, which a weight of
+      // zero does not keep out of a product.  Nor would it keep a NaN among the
+      // last Q - 1 tokens out of the queries before it: such a unit's are left for
+      // the end of the segment.
+      if (masked) {
+        auto clear = [&](int from_key) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (none[j] || key0 + 16 * j + 4 * g4 + i >= len) vr[j][i] = (u32x2){0, 0};
+            for (int i = 0; i < 4; ++i)
+              if (none[j] || key0 + 16 * j + 4 * g4 + i >= from_key) vr[j][i] = (u32x2){0, 0};
+        };
+        clear(len);
+        if (p.Q > 1) {
+          const int some = len - p.Q + 1;    // the first token that not all queries see
+          uint32_t nan = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key0 + 16 * j + 4 * g4 + i >= some)
+                nan |= ((vr[j][i][0] & 0x7f7f7f7fu) + 0x01010101u) | ((vr[j][i][1] & 0x7f7f7f7fu) + 0x01010101u);
+          if (__any(nan & 0x80808080u)) {
+            clear(some);
+            late |= 1u << (unit - max(some, 0) / kUnit);
+          }
+        }
       }
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
@@ -355,6 +377,42 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
       if (more) load_v(then, unit + 1, then_from);
       now = then;
       from = then_from;
+    }
+
+    // -------- the tokens that were left: one by one, each to the queries that see it
+    while (late) {
+      const int unit = max(len - p.Q + 1, 0) / kUnit + __builtin_ctz(late);
+      late &= late - 1;
+#pragma unroll 1
+      for (int key = max(unit * kUnit, max(len - p.Q + 1, 0)); key < min((unit + 1) * kUnit, len); ++key) {
+        const int id = table[key >> p.shift];
+        if (id < 0 || id >= p.num_pages) continue;
+        const float ks = p.k_scale[int64_t(id) * p.HKV + hkv] * c, vs = p.v_scale[int64_t(id) * p.HKV + hkv];
+        const int64_t at = int64_t(id) * p.page_stride + ((int64_t(hkv) << p.shift) + (key & ((1 << p.shift) - 1))) * D;
+        const u32x4* kp = reinterpret_cast<const u32x4*>(p.k_cache + at + 32 * g4);
+        const u32x4* vp = reinterpret_cast<const u32x4*>(p.v_cache + at + 32 * g4);
+        float kx[32], vx[32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bf16x8 a = widen(kp[i >> 1][2 * (i & 1)], kp[i >> 1][2 * (i & 1) + 1]);
+          const bf16x8 b = widen(vp[i >> 1][2 * (i & 1)], vp[i >> 1][2 * (i & 1) + 1]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) kx[8 * i + j] = float(a[j]), vx[8 * i + j] = float(b[j]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          float x = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x = __builtin_fmaf(float(q[t][i >> 3][i & 7]), kx[i], x);
+          x += __shfl_xor(x, 16, 64);
+          x = __builtin_amdgcn_exp2f(half_sum(x) * ks - (m[t] == -INFINITY ? 0.0f : m[t])) * vs;
+          if (key >= limit[t]) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[t][d][e] = __builtin_fmaf(x, vx[8 * e + d], o[t][d][e]);
+        }
+      }
     }
 
     // -------- its rows: finished, or a part.  Lane (l16, g4) holds row l16,

@@ -253,6 +253,34 @@ def test_decode_nan_where_it_is_seen(gpu_lib, cache_at):
         assert got[0, :, :4, 9].isnan().all() and torch.equal(got[0, :, :4, :9], o[0, :, :4, :9])
 
 
+@pytest.mark.parametrize("Q,HQ", [(2, 2), (5, 8), (7, 10), (70, 4)])
+def test_decode_later_nan_does_not_reach_earlier_queries(gpu_lib, Q, HQ):
+    """A NaN among the newest values: the queries before it are as if it were not there, the others hold it."""
+    lens, P = [6, 64, 130, 300, 2 * Q], 16
+    table, pages = tables_for(lens, P, seed=14)
+    cache = usual_cache(40, pages, 2, P)
+    q = rand(41, len(lens), Q, HQ, D).to(DEV)
+    codes = [codes_of(c) for c in cache[:2]]
+    want, wl, o_abs = ref.attn_decode(f64(q), *codes, f64(cache[2]), f64(cache[3]), table, lens)
+    keys = ref.e4m3_table()[codes[0]] * f64(cache[2])[..., None, None]
+    tol = ((U + 2.1 * eps(f64(q), keys, max(lens))) * o_abs + U * np.abs(want)) * 1.01 + 1e-30
+    raw = cache[1].view(torch.uint8)
+    bad = np.zeros((len(lens), Q), bool)
+    for n, length in enumerate(lens):
+        at = max(length - 1 - n % Q, 0)                        # a token that the last queries see, from this one on
+        raw[int(table[n, at // P]), 1, at % P, 5 + n] = 0x7f
+        bad[n] = np.arange(Q) >= Q - length + at
+    o, lse = gpu_lib.attn_decode(q, *cache, ints(table), ints(lens))
+    got = f64(o)
+    clean = np.ones(got.shape, bool)
+    for n in range(len(lens)):
+        clean[n, bad[n], HQ // 2:, 5 + n] = False
+    assert np.isnan(got[~clean]).all() and np.isfinite(got[clean]).all()
+    assert (np.abs(got - want)[clean] <= tol[clean]).all()
+    seen = np.isfinite(wl)
+    assert np.array_equal(np.isneginf(f64(lse)), ~seen)
+
+
 def test_decode_pages_missing(gpu_lib):
     """A page outside the cache holds no tokens; lengths beyond the table and below 0 are cut."""
     lens, P = [100, 64, 40, 500, -3], 16
