@@ -591,7 +591,8 @@ size_t kda_attn_backward_workspace_size(int32_t B, int32_t T, int32_t HQ, int32_
  *   kv_lens     int32 [N]  cached_lens + new_lens
  *   next_head   int32 [1]  *free_head + the pages asked for: the next call's
  *               free_head; past num_free where pages were missing
- * kv_lens must not alias the lengths, nor next_head free_head.
+ * The outputs must not alias inputs or each other (page_table apart); lengths
+ * or a head that a call replaces are copied over after it.
  * Sizes: 1 <= N <= 8192, table_width >= 1, table_stride >= table_width.
  */
 int kda_attn_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t N, int32_t* page_table,
@@ -613,8 +614,9 @@ int kda_attn_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t
  * than before the codes of the earlier offsets are multiplied by the quotient
  * and rounded again.  New codes are value / scale, rounded to nearest even;
  * infinities and NaN become NaN.  Codes at later offsets are left.
- * The tokens of one page must stand one after another with successive slots
- * (as kda_attn_tables deals them); otherwise its scale is undefined.
+ * The slots that are stored must differ, and the tokens of one page must stand
+ * one after another with successive slots (as kda_attn_tables deals them);
+ * otherwise that page's contents are undefined.
  */
 int kda_attn_cache_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slots,
                          int32_t T, int32_t HKV, int32_t Dh, void* k_cache, void* v_cache, float* k_scale,
@@ -644,7 +646,7 @@ int kda_attn_cache_store(const void* k, const void* v, int64_t k_stride, int64_t
  * sequences of the call, so the last bits of a row may differ from batch to
  * batch; the same call gives the same bits.
  * Sizes: N >= 0 (0 enqueues nothing), 1 <= Q <= 1024, num_pages >= 1,
- * N * Q * HQ <= 2^26.
+ * N * Q * HQ <= 2^26, table_width * page_size <= 2^30.
  */
 int kda_attn_decode(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
                     const float* k_scale, const float* v_scale, int32_t page_size, int64_t page_stride,

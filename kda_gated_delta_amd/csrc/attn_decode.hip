@@ -58,10 +58,7 @@ struct Params {
 
 // ---------------------------------------------------------------- who does what
 
-__device__ __forceinline__ int length(const Params& p, int n) {
-  const int64_t most = int64_t(p.width) << p.shift;
-  return int(min(int64_t(max(p.lens[n], 0)), min(most, int64_t(0x7fffffff))));
-}
+__device__ __forceinline__ int length(const Params& p, int n) { return min(max(p.lens[n], 0), p.width << p.shift); }
 // An empty sequence has one unit too: somebody writes its zeros.
 __device__ __forceinline__ int units_of(int len) { return max((len + kUnit - 1) / kUnit, 1); }
 
@@ -95,6 +92,7 @@ __device__ __forceinline__ Piece find_piece(const Params& p, int wave, int per) 
     const int a = min(lo + lane * step, hi), b = min(a + step, hi);
     int64_t own = 0;
     int len = 0;
+#pragma unroll 8
     for (int n = a; n < b; ++n) len = length(p, n), own += units_of(len);
     own *= per;
     int64_t end = own;                       // inclusive sum over the lanes
@@ -671,6 +669,7 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
   if (e == KDA_OK) e = kda::attn_cache(HKV, page_size, page_stride, num_pages);
   if (e != KDA_OK) return e;
   if (num_pages < 1 || table_width < 1 || table_stride < table_width) return KDA_ERR_SHAPE;
+  if (int64_t(table_width) * page_size > (1 << 30)) return KDA_ERR_SHAPE;   // token numbers and a unit or two fit int32
   if (N == 0) return KDA_OK;
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !kv_lens || !o || !workspace)
     return KDA_ERR_NULL;

@@ -128,6 +128,7 @@ def test_decode_refusals():
     assert decode(Q=0) == E_SHAPE and decode(Q=1025) == E_SHAPE and decode(N=1 << 20, Q=1024) == E_SHAPE
     assert decode(HQ=5) == E_SHAPE and decode(qs=504) == E_SHAPE and decode(qs=516) == E_ALIGN
     assert decode(pages=0) == E_SHAPE and decode(width=0) == E_SHAPE and decode(tstride=7) == E_SHAPE
+    assert decode(width=(1 << 24) + 1, tstride=1 << 25) == E_SHAPE
     assert decode(scale=float("nan")) == E_SHAPE and decode(scale=0.0) == E_SHAPE
     for name in ("q", "table", "lens", "o", "ws"):
         assert decode(**{name: NULL}) == E_NULL
