@@ -73,7 +73,7 @@ __device__ __forceinline__ int64_t lane_value(int64_t x, int lane) {
 struct Piece {
   int w;             // the wave's place in the line
   int64_t from, to;  // its units
-  int64_t lo, hi;    // its workgroup's units, if its waves are neighbours in the line; else empty
+  int64_t lo, hi;    // its workgroup's units, if all its waves have some; else empty
   int n, len;        // the sequence that holds the first, and its length
   int64_t before;    // units of the sequences before it
 };
@@ -108,13 +108,11 @@ __device__ __forceinline__ Piece find_piece(const Params& p, int wave, int per) 
       const int64_t each = total <= 0x7fffffff ? int64_t(unsigned(total) / parts) : total / waves;
       const unsigned left = unsigned(total - each * waves);
       auto cut = [&](int i) { return each * i + int64_t(left * unsigned(i) / parts); };
-      if (total >= p.waves) {
-        x.w = int(blockIdx.x) * kWaves + wave;
+      x.w = int(blockIdx.x) * kWaves + wave;
+      if (x.w >= waves) return x;            // nothing for this wave
+      if (x.w - wave + kWaves <= waves) {
         x.lo = cut(x.w - wave);
         x.hi = cut(x.w - wave + kWaves);
-      } else {                               // a short line is spread over all workgroups
-        x.w = wave * int(gridDim.x) + int(blockIdx.x);
-        if (x.w >= waves) return x;          // nothing for this wave
       }
       x.from = cut(x.w);
       x.to = cut(x.w + 1);
@@ -534,21 +532,20 @@ __global__ __launch_bounds__(THREADS) void attn_decode_join_kernel(Params p) {
       for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
       float x = 0.0f, y = 0.0f;
       uint64_t have = __ballot(some);
-      while (have) {                         // four at a time: their loads go out together
-        float w[4];
-        const float2* at[4];
+      while (have) {                         // eight at a time: their loads go out together
+        int i[8];
+        float2 v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int i = have ? __builtin_ctzll(have) : -1;
-          w[k] = i < 0 ? 0.0f : __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i));
-          at[k] = i < 0 ? nullptr : reinterpret_cast<const float2*>(part + i * step) + lane;
+        for (int k = 0; k < 8; ++k) {
+          i[k] = have ? __builtin_ctzll(have) : -1;
+          v[k] = reinterpret_cast<const float2*>(part + (have ? i[k] : i[0]) * step)[lane];
           have &= have - 1;                  // 0 stays 0
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (at[k]) {
-            const float2 o = *at[k];
-            x = __builtin_fmaf(o.x, w[k], x), y = __builtin_fmaf(o.y, w[k], y);
+        for (int k = 0; k < 8; ++k)
+          if (i[k] >= 0) {
+            const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), i[k]));
+            x = __builtin_fmaf(v[k].x, w, x), y = __builtin_fmaf(v[k].y, w, y);
           }
       }
       const int row = row0 + r, i = row / G;
