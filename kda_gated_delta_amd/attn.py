@@ -127,8 +127,8 @@ def attn_prefill(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None):
         lse = q.new_empty((B, HQ, T), dtype=_F32)
     else:
         _dense(lse, "lse", _F32, dev, (B, HQ, T))
-    _call(dev, "kda_attn_prefill", q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(cu_seqlens), N, B, T, HQ, HKV, D,
-          _scale(scale), out.data_ptr(), lse.data_ptr())
+    _call(dev, "kda_attn_prefill", q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, _ptr(cu_seqlens), N, B, T,
+          HQ, HKV, D, _scale(scale), out.data_ptr(), lse.data_ptr())
     return out, lse
 
 
@@ -155,9 +155,11 @@ def attn_backward(q, k, v, o, lse, d_out, cu_seqlens=None, scale=None, workspace
     dq = q.new_empty((B, T, HQ, D), dtype=dtype)
     dk = q.new_empty((B, T, HKV, D), dtype=dtype)
     dv = q.new_empty((B, T, HKV, D), dtype=dtype)
-    _call(dev, "kda_attn_backward", q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, o.data_ptr(), lse.data_ptr(), d_out.data_ptr(),
-          _ptr(cu_seqlens), N, B, T, HQ, HKV, D, _scale(scale), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-          _kda.GRAD_INPUT_DTYPE if grad_dtype == "input" else _kda.GRAD_FLOAT32, workspace.data_ptr(), workspace.numel())
+    _call(dev, "kda_attn_backward", q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, o.data_ptr(),
+          lse.data_ptr(), d_out.data_ptr(), _ptr(cu_seqlens), N, B, T, HQ, HKV, D, _scale(scale),
+          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+          _kda.GRAD_INPUT_DTYPE if grad_dtype == "input" else _kda.GRAD_FLOAT32, workspace.data_ptr(),
+          workspace.numel())
     return dq, dk, dv
 
 
@@ -236,8 +238,8 @@ def attn_cache_store(k, v, k_cache, v_cache, k_scale, v_scale, slots):
     ks, vs = _rows(k, "k", HKV, (T,)), _rows(v, "v", HKV, (T,))
     pages, size, stride = _cache(k_cache, v_cache, k_scale, v_scale, dev, HKV)
     _dense(slots, "slots", _I32, dev, (T,))
-    _call(dev, "kda_attn_cache_store", k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, HKV, D, k_cache.data_ptr(), v_cache.data_ptr(),
-          k_scale.data_ptr(), v_scale.data_ptr(), size, stride, pages)
+    _call(dev, "kda_attn_cache_store", k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, HKV, D,
+          k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), size, stride, pages)
 
 
 def attn_decode_workspace_size(N, Q, HQ, HKV):
@@ -272,7 +274,7 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, scal
         workspace = q.new_empty(max(attn_decode_workspace_size(N, Q, HQ, HKV), 16), dtype=torch.uint8)
     else:
         _dense(workspace, "workspace", torch.uint8, dev)
-    _call(dev, "kda_attn_decode", q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), size, stride,
-          pages, page_table.data_ptr(), table_stride, W, kv_lens.data_ptr(), N, Q, HQ, HKV, D,
-          _scale(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _call(dev, "kda_attn_decode", q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), size, stride, pages, page_table.data_ptr(), table_stride, W, kv_lens.data_ptr(), N, Q,
+          HQ, HKV, D, _scale(scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out, lse

@@ -46,7 +46,7 @@ struct Params {
 // ---------------------------------------------------------------- dQ
 
 // kSplit = 2: a second set of four waves takes every other key tile, as in the
-// forward, for launches that would leave half of the wave slots empty.
+// forward (attn_split says when).
 template <typename Out, int kSplit>
 __global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p) {
   constexpr int kHalf = 4 * kTileBytes;    // two buffers of K and V
@@ -230,7 +230,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dkv_kernel(Params p) {
 
   // Query tiles from the one that holds the first key (row0 is a multiple of 64).
   const int t0 = rows.row0 / kTile, per_head = (rows.len + kTile - 1) / kTile - t0;
-  const int begin = int(int64_t(per_head) * G * part / p.parts), end = int(int64_t(per_head) * G * (part + 1) / p.parts);
+  const int begin = int(int64_t(per_head) * G * part / p.parts);
+  const int end = int(int64_t(per_head) * G * (part + 1) / p.parts);
   TileLoad<kWaves> qload, uload;
   const int64_t u_stride = int64_t(p.HQ) * D;
   qload.init(wave, lane, p.q_stride);
@@ -339,7 +340,7 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(Params p) {
 int parts_for(int64_t slots, int T, int N, bool packed, int HQ, int HKV) {
   const int64_t units = slots * HKV, want = 4 * int64_t(kda::device_cus());
   if (units >= want) return 1;
-  const int64_t len = packed ? T / N : T;                  // a typical sequence
+  const int64_t len = kda::attn_typical(T, N, packed);
   const int64_t walk = (len / kTile / 2 + 1) * (HQ / HKV);
   const int64_t most = walk / 2 < 1 ? 1 : (walk / 2 > 16 ? 16 : walk / 2);
   const int64_t parts = (want + units - 1) / units;
@@ -355,7 +356,7 @@ size_t stat_floats(int64_t B, int64_t T, int64_t HQ) { return size_t((B * T * HQ
 template <typename Out>
 int launch(const Params& p, hipStream_t stream) {
   const int64_t blocks = head_blocks(p.slots, p.HQ, p.HKV);
-  if (blocks <= kda::device_cus())
+  if (kda::attn_split(blocks, p.T, p.N, p.cu != nullptr))
     hipLaunchKernelGGL((attn_dq_kernel<Out, 2>), dim3(unsigned(blocks)), dim3(2 * kThreads), 0, stream, p);
   else
     hipLaunchKernelGGL((attn_dq_kernel<Out, 1>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, p);
@@ -392,7 +393,8 @@ extern "C" int kda_attn_backward(const void* q, const void* k, const void* v, in
   if (T == 0) return KDA_OK;
   if (!q || !k || !v || !o || !lse || !d_out || !dq || !dk || !dv || !workspace) return KDA_ERR_NULL;
   for (const void* x : {q, k, v, o, static_cast<const void*>(lse), d_out, static_cast<const void*>(dq),
-                        static_cast<const void*>(dk), static_cast<const void*>(dv), static_cast<const void*>(workspace)})
+                        static_cast<const void*>(dk), static_cast<const void*>(dv),
+                        static_cast<const void*>(workspace)})
     if (!kda::aligned16(x)) return KDA_ERR_ALIGN;
   const int seqs = cu_seqlens ? num_seqs : 0, N = cu_seqlens ? num_seqs : B;
   if (workspace_bytes < kda_attn_backward_workspace_size(B, T, HQ, HKV, Dh, seqs)) return KDA_ERR_WORKSPACE;

@@ -285,8 +285,8 @@ extern "C" int kda_attn_cache_store(const void* k, const void* v, int64_t k_stri
   // Every run costs a wave its latency, every empty window a look.  A decode
   // step's tokens are a run each and want a window each; in prompts a run is a
   // page.  Windows grow until two items are left for a wave, up to 16 tokens:
-  // 256 single tokens x 8 heads take FIGURE_A us (window 1), 35000 tokens of
-  // prompts FIGURE_B us (window 16).
+  // 256 single tokens x 8 heads take 5.4 us (window 1), 35000 tokens of
+  // prompts 40 us (window 16).
   const int64_t waves = 16 * int64_t(kda::device_cus()), each = 2 * int64_t(HKV);
   int wshift = 0;
   while (wshift < 4 && (int64_t(T) >> wshift) * each > 2 * waves) ++wshift;

@@ -253,8 +253,8 @@ __device__ __forceinline__ bf16x8 read_columns(const unsigned char* tile, int r,
 __device__ __forceinline__ void store_row32(uint16_t* row, const f32x16& acc, float f, int h) {
 #pragma unroll
   for (int i = 0; i < 4; i += 2) {
-    uint32_t a0 = pack_bf16(acc[4 * i] * f, acc[4 * i + 1] * f), a1 = pack_bf16(acc[4 * i + 2] * f, acc[4 * i + 3] * f);
-    uint32_t b0 = pack_bf16(acc[4 * i + 4] * f, acc[4 * i + 5] * f), b1 = pack_bf16(acc[4 * i + 6] * f, acc[4 * i + 7] * f);
+    auto pair = [&](int j) { return pack_bf16(acc[4 * i + j] * f, acc[4 * i + j + 1] * f); };
+    const uint32_t a0 = pair(0), a1 = pair(2), b0 = pair(4), b1 = pair(6);
     const auto x = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
     const auto y = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
     *reinterpret_cast<u32x4*>(row + 8 * (i + h)) = (u32x4){x[0], y[0], x[1], y[1]};

@@ -55,9 +55,8 @@ __device__ __forceinline__ bool any_not_finite(const unsigned char* tile, int ha
 }
 
 // kSplit = 2: a second set of four waves takes every other key tile of the same
-// rows, and the two halves of a row are joined at the end.  For launches that
-// would leave half of the device's wave slots empty: the walk over the keys is a
-// chain, and two waves per SIMD halve it.
+// rows, and the two halves of a row are joined at the end (attn_split says when):
+// the walk over the keys is a chain, and two waves per SIMD halve it.
 template <int kSplit>
 __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void attn_prefill_kernel(Params p) {
   constexpr int kHalf = 4 * kTileBytes;    // two buffers of K and V
@@ -260,17 +259,19 @@ extern "C" int kda_attn_prefill(const void* q, const void* k, const void* v, int
   if (e != KDA_OK) return e;
   if (T == 0) return KDA_OK;
   if (!q || !k || !v || !o) return KDA_ERR_NULL;
-  if (!kda::aligned16(q) || !kda::aligned16(k) || !kda::aligned16(v) || !kda::aligned16(o) || (lse && !kda::aligned16(lse)))
-    return KDA_ERR_ALIGN;
+  for (const void* x : {q, k, v, static_cast<const void*>(o), static_cast<const void*>(lse)})
+    if (!kda::aligned16(x)) return KDA_ERR_ALIGN;            // no lse: a null pointer passes
   const int64_t slots = cu_seqlens ? int64_t(T) / BM + num_seqs : int64_t(B) * ((T + BM - 1) / BM);
   if (head_blocks(slots, HQ, HKV) > 0x7fffffff) return KDA_ERR_SHAPE;
   const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                  q_stride, k_stride, v_stride, cu_seqlens, cu_seqlens ? num_seqs : B, T, HQ, HKV, int(slots), scale,
                  static_cast<uint16_t*>(o), lse};
   const int64_t blocks = head_blocks(slots, HQ, HKV);
-  if (blocks <= kda::device_cus())
-    hipLaunchKernelGGL(attn_prefill_kernel<2>, dim3(unsigned(blocks)), dim3(128 * kWaves), 0, kda::as_stream(stream), p);
+  if (kda::attn_split(blocks, T, p.N, cu_seqlens != nullptr))
+    hipLaunchKernelGGL(attn_prefill_kernel<2>, dim3(unsigned(blocks)), dim3(128 * kWaves), 0,
+                       kda::as_stream(stream), p);
   else
-    hipLaunchKernelGGL(attn_prefill_kernel<1>, dim3(unsigned(blocks)), dim3(64 * kWaves), 0, kda::as_stream(stream), p);
+    hipLaunchKernelGGL(attn_prefill_kernel<1>, dim3(unsigned(blocks)), dim3(64 * kWaves), 0,
+                       kda::as_stream(stream), p);
   return kda::launch_status();
 }
