@@ -642,9 +642,9 @@ int kda_attn_cache_store(const void* k, const void* v, int64_t k_stride, int64_t
  *               entry do not matter; calls that share one must not overlap
  * What lies in a page behind the sequence's end does not reach the outputs,
  * whatever it is, and a NaN code only the queries that see its token.  The
- * scales of pages that hold tokens are finite.  How a sequence is cut among waves depends on all
- * sequences of the call, so the last bits of a row may differ from batch to
- * batch; the same call gives the same bits.
+ * scales of pages that hold tokens are finite.  How a sequence is cut among
+ * waves depends on all sequences of the call, so the last bits of a row may
+ * differ from batch to batch; the same call gives the same bits.
  * Sizes: N >= 0 (0 enqueues nothing), 1 <= Q <= 1024, num_pages >= 1,
  * N * Q * HQ <= 2^26, table_width * page_size <= 2^30.
  */

@@ -18,7 +18,15 @@
 // Every product takes its left operand from LDS (rows, or columns through
 // transposing reads) and its right one from registers; P and dS go from the
 // accumulator of one product into the operand of the next without leaving the
-// lane, rounded once to bfloat16.
+// lane, rounded once to bfloat16.  Sums are float32 throughout.
+//
+// Matrix unit and power bound both walks, as in the forward.  8192 tokens, 16
+// query heads on 4: dQ 374 us (three products, 1100 TFLOP/s), dK and dV 580 us
+// (four, 950; 256 registers, of which 20 live in scratch: with one wave per SIMD
+// and none there it is 5% slower), the parts' sum 22 us (4.8 TB/s), and 275 us of
+// forward before them.  7 packed sequences of up to 2011 tokens, 12 heads on 4:
+// 93, 167, 27 and 69 us: there the longest sequence's first keys are the chain
+// that the others wait for.
 #include "attn_device.h"
 #include "kda_host.h"
 

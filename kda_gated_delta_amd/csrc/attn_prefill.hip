@@ -14,6 +14,16 @@
 // The accumulator of S^T holds, in each lane, exactly the contraction indices
 // that the next product wants of its B operand (in the order read_columns
 // takes V's rows), so P never leaves its registers: no exchange, no LDS.
+// P is rounded to bfloat16 for its product; maximum, sum and output are float32.
+//
+// The matrix unit and the chip's power bound it.  8192 tokens, 32 query heads on
+// 8: 512 us, 1074 TFLOP/s, where a large library product reaches 1170 on the same
+// card; matrix unit 55% busy, vector unit about 50%, LDS 28% and without bank
+// conflicts, at 1.8 GHz (with inputs of zeros the clock stays up and it takes
+// 20 to 25% less).  16 packed sequences of up to 4096 tokens, 16 heads on 2: 410
+// us.  129 tokens, 8 heads: 7 us, the latency of one walk.  64 query rows per
+// wave (half the LDS reads, one wave per SIMD) reach 798 TFLOP/s; the scores of
+// the next tile formed beside the weights of this one were 3% slower.
 #include "attn_device.h"
 #include "kda_host.h"
 

@@ -283,3 +283,43 @@ def test_gradients_are_the_differences(gpu_lib):
         slope = ((ref.attn_prefill(*y[0])[0] - ref.attn_prefill(*y[1])[0]) * u).sum() / 2e-5
         tol = (2 * (U + 4.2 * eps(x[0], x[1], 90)) * moved[i] * np.abs(d)).sum()
         assert abs((grads[i] * d).sum() - slope) <= tol
+
+
+LONG = [  # walks long enough for two sets of waves on a row tile's keys
+    (1, 512, 2, 1, None), (2, 600, 4, 2, None), (1, 1216, 4, 1, [0, 513, 1153]), (1, 1800, 2, 2, [64, 64, 1777]),
+    (1, 2053, 17, 17, None),                                 # more workgroups than compute units
+]
+
+
+@pytest.mark.parametrize("B,T,HQ,HKV,cu", LONG)
+def test_long_walks(gpu_lib, B, T, HQ, HKV, cu):
+    q, k, v, up, c = case(B, T, HQ, HKV, cu, seed=200)
+    o, lse = gpu_lib.attn_prefill(q, k, v, cu_seqlens=c)
+    grads = gpu_lib.attn_backward(q, k, v, o, lse, up, cu_seqlens=c)
+    if HQ == HKV:                                            # each head apart: the first and the last will do
+        heads = [0, HQ - 1]
+        q, k, v, up, o = (x[:, :, heads] for x in (q, k, v, up, o))
+        lse, grads = lse[:, heads], [g[:, :, heads] for g in grads]
+    check_prompt(o, lse, q, k, v, cu)
+    check_grads(grads, q, k, v, up, cu)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at", [[3], [255], [256, 300], [448, 639], [639]])
+def test_later_values_in_long_walks(gpu_lib, at, bad):
+    """As above, with the keys of a row tile dealt to two sets of waves."""
+    T = 640
+    q, k, v, up, _ = case(1, T, 2, 2, None, seed=230)
+    clean, lse = gpu_lib.attn_prefill(q, k, v)
+    v2 = v.clone()
+    seen = torch.zeros(T, 2, D, dtype=torch.bool, device=DEV)
+    for j in at:
+        v2[0, j, 1, 7 * j % D] = bad
+        seen[j:, 1, 7 * j % D] = True
+    o, lse2 = gpu_lib.attn_prefill(q, k, v2)
+    assert torch.equal(lse, lse2) and not torch.isfinite(o[0][seen]).any()
+    want, _, o_abs = ref.attn_prefill(f64(q), f64(k), f64(v))
+    tol = ((U + 2.1 * eps(f64(q), f64(k), T)) * o_abs + U * np.abs(want)) * 1.01
+    keep = (~seen).cpu().numpy()
+    assert (np.abs(f64(o) - want)[0][keep] <= tol[0][keep]).all()
+    check_prompt(clean, lse, q, k, v)
