@@ -18,7 +18,7 @@
 //
 // The matrix unit and the chip's power bound it.  8192 tokens, 32 query heads on
 // 8: 512 us, 1074 TFLOP/s, where a large library product reaches 1170 on the same
-// card; matrix unit 55% busy, vector unit about 50%, LDS 28% and without bank
+// card; matrix unit 55% busy, vector unit about 50%, LDS 10% and without bank
 // conflicts, at 1.8 GHz (with inputs of zeros the clock stays up and it takes
 // 20 to 25% less).  16 packed sequences of up to 4096 tokens, 16 heads on 2: 410
 // us.  129 tokens, 8 heads: 7 us, the latency of one walk.  64 query rows per

@@ -476,3 +476,35 @@ def test_decode_continues_the_prompt(gpu_lib):
     _, _, o_abs = ref.attn_prefill(f64(q), f64(k), f64(v))
     tol = (np.exp(2 * dz) * (1 + 2.0 ** -4) - 1 + 4 * U) * o_abs[0, -1]
     check(d[0, 0], f64(o)[0, -1], tol, "cache against prompt")
+
+
+@pytest.mark.parametrize("lens,Q,HQ,HKV", [([700, 90, 0], 100, 2, 1), ([1300], 1024, 2, 2), ([1024, 1], 1024, 1, 1)])
+def test_decode_many_queries(gpu_lib, lens, Q, HQ, HKV):
+    """A stretch of a prompt against the cache: many row tiles, up to the most queries a call takes."""
+    table, pages = tables_for(lens, 64, seed=21)
+    cache = usual_cache(60, pages, HKV, 64)
+    q = rand(61, len(lens), Q, HQ, D).to(DEV)
+    o, lse = gpu_lib.attn_decode(q, *cache, ints(table), ints(lens))
+    check_decode(o, lse, q, cache, table, lens)
+
+
+def test_decode_two_at_once(gpu_lib):
+    """Calls on two streams, each with a workspace of its own, do not meet."""
+    calls = []
+    for i, (lens, HQ, HKV) in enumerate((([900, 3000, 40], 8, 2), ([5000, 1], 20, 4))):
+        table, pages = tables_for(lens, 32, seed=30 + i)
+        cache = usual_cache(70 + i, pages, HKV, 32)
+        q = rand(72 + i, len(lens), 2, HQ, D).to(DEV)
+        calls.append((q, *cache, ints(table), ints(lens)))
+    alone = [gpu_lib.attn_decode(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(8):
+        for i, (c, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(gpu_lib.attn_decode(*c))
+    torch.cuda.synchronize()
+    for want, results in zip(alone, got):
+        for o, lse in results:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
