@@ -92,6 +92,16 @@ def _call(dev, name, *args):
         _kda._check(code, name)
 
 
+def _workspace(like, dev, size, *sizes):
+    """Workspace for a call on device `dev`, whose compute units its size follows."""
+    if torch.cuda.current_device() == dev:
+        n = size(*sizes)
+    else:
+        with torch.cuda.device(dev):
+            n = size(*sizes)
+    return like.new_empty(max(n, 16), dtype=torch.uint8)
+
+
 def _scale(scale):
     return D ** -0.5 if scale is None else float(scale)
 
@@ -115,7 +125,8 @@ def attn_prefill(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None):
     """Causal attention over whole prompts.  q [B,T,HQ,128], k and v
     [B,T,HKV,128] bf16 (tokens may be slices of wider rows); query head h reads
     key/value head h // (HQ // HKV).  cu_seqlens int32 [N+1] (with B == 1):
-    packed sequences; rows outside them are neither read nor written.  scale
+    packed sequences; rows outside them are neither read nor written (and hold
+    anything in outputs that are allocated here).  scale
     defaults to 128**-0.5.  Returns (o [B,T,HQ,128] bf16, lse [B,HQ,T] float32,
     the logarithm of each row's sum of exponentials)."""
     dev, B, T, HQ, HKV, (qs, ks, vs), N = _prompt(q, k, v, cu_seqlens)
@@ -133,14 +144,16 @@ def attn_prefill(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None):
 
 
 def attn_backward_workspace_size(B, T, HQ, HKV, num_seqs=0):
-    """Bytes of workspace attn_backward needs (num_seqs = 0 without cu_seqlens)."""
+    """Bytes of workspace attn_backward needs on the current device (num_seqs = 0
+    without cu_seqlens)."""
     return int(_kda.load().kda_attn_backward_workspace_size(B, T, HQ, HKV, D, num_seqs))
 
 
 def attn_backward(q, k, v, o, lse, d_out, cu_seqlens=None, scale=None, workspace=None, grad_dtype="input"):
     """Gradients of sum(o * d_out) for attn_prefill with the same inputs, of
     which o and lse are the outputs.  d_out [B,T,HQ,128] bf16.  Returns (dq, dk,
-    dv), bf16 (grad_dtype "input") or float32 ("float32")."""
+    dv), bf16 (grad_dtype "input") or float32 ("float32"); rows outside the
+    sequences hold anything."""
     if grad_dtype not in ("input", "float32"):
         raise ValueError("grad_dtype must be 'input' or 'float32'")
     dev, B, T, HQ, HKV, (qs, ks, vs), N = _prompt(q, k, v, cu_seqlens)
@@ -148,7 +161,7 @@ def attn_backward(q, k, v, o, lse, d_out, cu_seqlens=None, scale=None, workspace
     _dense(d_out, "d_out", _BF16, dev, (B, T, HQ, D))
     _dense(lse, "lse", _F32, dev, (B, HQ, T))
     if workspace is None:
-        workspace = q.new_empty(max(attn_backward_workspace_size(B, T, HQ, HKV, N), 16), dtype=torch.uint8)
+        workspace = _workspace(q, dev, attn_backward_workspace_size, B, T, HQ, HKV, N)
     else:
         _dense(workspace, "workspace", torch.uint8, dev)
     dtype = _BF16 if grad_dtype == "input" else _F32
@@ -243,7 +256,7 @@ def attn_cache_store(k, v, k_cache, v_cache, k_scale, v_scale, slots):
 
 
 def attn_decode_workspace_size(N, Q, HQ, HKV):
-    """Bytes of workspace attn_decode needs."""
+    """Bytes of workspace attn_decode needs on the current device."""
     return int(_kda.load().kda_attn_decode_workspace_size(N, Q, HQ, HKV, D))
 
 
@@ -271,7 +284,7 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, scal
     else:
         _dense(lse, "lse", _F32, dev, (N, Q, HQ))
     if workspace is None:
-        workspace = q.new_empty(max(attn_decode_workspace_size(N, Q, HQ, HKV), 16), dtype=torch.uint8)
+        workspace = _workspace(q, dev, attn_decode_workspace_size, N, Q, HQ, HKV)
     else:
         _dense(workspace, "workspace", torch.uint8, dev)
     _call(dev, "kda_attn_decode", q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
