@@ -83,7 +83,7 @@ def _call(dev, name, *args):
     """Call an entry point with device `dev` current, on its current stream."""
     fn = getattr(_kda.load(), name)
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:                  # (a GPU tensor was made: the runtime is up)
         code = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -94,7 +94,7 @@ def _call(dev, name, *args):
 
 def _workspace(like, dev, size, *sizes):
     """Workspace for a call on device `dev`, whose compute units its size follows."""
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         n = size(*sizes)
     else:
         with torch.cuda.device(dev):
@@ -131,7 +131,7 @@ def attn_prefill(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None):
     the logarithm of each row's sum of exponentials)."""
     dev, B, T, HQ, HKV, (qs, ks, vs), N = _prompt(q, k, v, cu_seqlens)
     if out is None:
-        out = q.new_empty((B, T, HQ, D))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _dense(out, "out", _BF16, dev, (B, T, HQ, D))
     if lse is None:
@@ -276,7 +276,7 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, scal
     W, table_stride = _table(page_table, N, dev)
     _dense(kv_lens, "kv_lens", _I32, dev, (N,))
     if out is None:
-        out = q.new_empty((N, Q, HQ, D))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _dense(out, "out", _BF16, dev, (N, Q, HQ, D))
     if lse is None:

@@ -14,7 +14,8 @@
 // the device knows.  Waves never meet: each keeps its own running maximum, sum
 // and output in registers and its loads in flight.  A segment that lies in one
 // wave's piece is finished there; otherwise its waves leave float32 parts that
-// attn_decode_join_kernel brings together in order.
+// attn_decode_join_kernel brings together in order.  Where the tables are short
+// and the segments few, a workgroup takes a segment alone instead.
 //
 // S^T = K Q^T and O^T += V^T P^T on 16x16x32 matrix instructions, codes widened
 // to bfloat16 (exact).  (The instructions that take e4m3 codes as they are add
@@ -42,6 +43,7 @@ using namespace kda::attn;
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
+constexpr int kAloneWaves = 8;               // of a workgroup that takes a segment alone
 constexpr int kUnit = 64;                    // tokens
 constexpr float kSlack = 8.0f;               // see attn_prefill.hip: rescale only when the maximum grew this much
 
@@ -66,7 +68,8 @@ struct Params {
 
 // ---------------------------------------------------------------- who does what
 
-__device__ __forceinline__ int length(const Params& p, int n) { return min(max(p.lens[n], 0), p.width << p.shift); }
+template <typename P>
+__device__ __forceinline__ int length(P& p, int n) { return min(max(p.lens[n], 0), p.width << p.shift); }
 // An empty sequence has one unit too: somebody writes its zeros.
 __device__ __forceinline__ int units_of(int len) { return max((len + kUnit - 1) / kUnit, 1); }
 
@@ -155,29 +158,52 @@ struct Pages {
   float ks, vs;
 };
 
-template <int NT>
-__global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
+// kAlone: a workgroup of eight waves takes a segment alone, an eighth of its
+// units each, and finishes it: no parts, no second launch (alone says when).
+template <int NT, bool kAlone>
+__global__ __launch_bounds__(kAlone ? 64 * kAloneWaves : kThreads, 2) void attn_decode_kernel(Params p) {
+  constexpr int kGroup = kAlone ? kAloneWaves : kWaves;
   const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
-  __shared__ __align__(16) float merged[kWaves][16 * NT][D + 4];
+  __shared__ __align__(16) float merged[kGroup][16 * NT][D + 4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int per = p.HKV * p.row_tiles;
-  const Piece piece = find_piece(p, wave, per);
-  const int w = piece.w;
-  int64_t u = piece.from;
-  const int64_t end = piece.to;
-  int n = piece.n;
-  int len = piece.len, units = units_of(len);
-  const int64_t inside = u - piece.before;
-  int seg = int(inside <= 0x7fffffff ? int64_t(unsigned(inside) / unsigned(units)) : inside / units);
-  int first = int(inside - int64_t(seg) * units);
+  int64_t left = 1;                          // units of the wave's piece that are still to do
+  int w = 0, n, len, units, seg, first;
+  bool merge = kAlone;                       // all waves of the workgroup inside one segment: one part for them
+  if constexpr (kAlone) {
+    n = int(blockIdx.x / unsigned(per));
+    seg = int(blockIdx.x - unsigned(n) * unsigned(per));
+    len = length(p, n);
+    units = units_of(len);
+    first = units * wave / kGroup;
+  } else {
+    const Piece piece = find_piece(p, wave, per);
+    w = piece.w;
+    left = piece.to - piece.from;
+    n = piece.n;
+    len = piece.len;
+    units = units_of(len);
+    const int64_t inside = piece.from - piece.before;
+    seg = int(inside <= 0x7fffffff ? int64_t(unsigned(inside) / unsigned(units)) : inside / units);
+    first = int(inside - int64_t(seg) * units);
+    const int64_t start = piece.from - first;                     // the segment's first unit in the line
+    merge = piece.lo < piece.hi && start <= piece.lo && piece.hi <= start + units;
+  }
   const int G = p.HQ / p.HKV;
   const float c = p.scale * kLog2e;
 
-  while (u < end) {
+  // The arguments are read anew for each segment: kept over the walk of the one
+  // before, they would take scalar registers that it has not got.
+  typedef const __attribute__((address_space(4))) Params Arguments;
+  Arguments* arguments = (Arguments*)__builtin_amdgcn_kernarg_segment_ptr();
+  while (left > 0) {
+    asm volatile("" : "+s"(arguments));
+    Arguments& args = *arguments;
     // -------- one segment: sequence n, head hkv, rows row0 .. row0 + tile_rows - 1
-    const int hkv = seg / p.row_tiles, row0 = (seg - hkv * p.row_tiles) * p.tile_rows;
-    const int last = int(min(int64_t(units), first + end - u));     // units first .. last - 1
-    const int rows = min(p.rows - row0, 16 * NT);
+    const int hkv = seg / args.row_tiles, row0 = (seg - hkv * args.row_tiles) * args.tile_rows;
+    const int last = kAlone ? units * (wave + 1) / kGroup         // units first .. last - 1, none perhaps
+                            : int(min(int64_t(units), first + left));
+    const int rows = min(args.rows - row0, 16 * NT);
 
     f32x4 o[NT][8];
     float m[NT], l[NT];
@@ -188,16 +214,16 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
       for (int d = 0; d < 8; ++d) o[t][d] = (f32x4)(0.0f);
     }
 
-    const int32_t* table = p.table + n * p.table_stride;
+    const int32_t* table = args.table + n * args.table_stride;
     auto pages_at = [&](int unit) {          // of the 64 tiles from `unit` on, as far as the piece goes
       Pages x{-1, 0.0f, 0.0f};
       const int64_t token = int64_t(unit) * kUnit + lane * 16;
       if (token < min(int64_t(len), int64_t(last) * kUnit)) {
-        const int id = table[token >> p.shift];
-        if (id >= 0 && id < p.num_pages) {
+        const int id = table[token >> args.shift];
+        if (id >= 0 && id < args.num_pages) {
           x.id = id;
-          x.ks = p.k_scale[int64_t(id) * p.HKV + hkv] * c;
-          x.vs = p.v_scale[int64_t(id) * p.HKV + hkv];
+          x.ks = args.k_scale[int64_t(id) * args.HKV + hkv] * c;
+          x.vs = args.v_scale[int64_t(id) * args.HKV + hkv];
         }
       }
       return x;
@@ -207,8 +233,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
     // page 0, and is masked.
     auto tile_at = [&](const uint8_t* cache, const Pages& x, int unit, int from, int j) {
       const int id = max(__builtin_amdgcn_readlane(x.id, from + j), 0);
-      const int inside = (unit * kUnit + 16 * j) & ((1 << p.shift) - 1);
-      const int64_t at = int64_t(id) * p.page_stride + ((int64_t(hkv) << p.shift) + inside) * D;
+      const int inside = (unit * kUnit + 16 * j) & ((1 << args.shift) - 1);
+      const int64_t at = int64_t(id) * args.page_stride + ((int64_t(hkv) << args.shift) + inside) * D;
       return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(cache) + at, 0, 16 * D, 0x00020000);
     };
     const int k_off = l16 * D + 32 * g4, v_off = 4 * g4 * D + 8 * l16;
@@ -217,7 +243,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
     auto load_k = [&](const Pages& x, int unit, int from) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const auto tile = tile_at(p.k_cache, x, unit, from, j);
+        const auto tile = tile_at(args.k_cache, x, unit, from, j);
 #pragma unroll
         for (int i = 0; i < 2; ++i) kr[j][i] = __builtin_amdgcn_raw_buffer_load_b128(tile, k_off + 16 * i, 0, 0);
       }
@@ -225,7 +251,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
     auto load_v = [&](const Pages& x, int unit, int from) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const auto tile = tile_at(p.v_cache, x, unit, from, j);
+        const auto tile = tile_at(args.v_cache, x, unit, from, j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) vr[j][i] = __builtin_amdgcn_raw_buffer_load_b64(tile, v_off + i * D, 0, 0);
       }
@@ -240,16 +266,16 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = row0 + min(16 * t + l16, rows - 1), i = r / G;
-      const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (hkv * G + r - i * G) * D + 32 * g4;
+      const uint16_t* src = args.q + (int64_t(n) * args.Q + i) * args.q_stride + (hkv * G + r - i * G) * D + 32 * g4;
 #pragma unroll
       for (int s = 0; s < 4; ++s) q[t][s] = *reinterpret_cast<const bf16x8*>(src + 8 * s);
-      limit[t] = len - p.Q + i + 1;
+      limit[t] = len - args.Q + i + 1;
     }
     int from = 0;                            // the unit's first tile in `now`
     uint32_t late = 0;                       // units left for the end, from that of token len - Q + 1 on
     for (int unit = first; unit < last; ++unit) {
       const int key0 = unit * kUnit;
-      const bool masked = key0 + kUnit > len - p.Q + 1 || (__ballot(now.id < 0) >> from & 15) != 0;
+      const bool masked = key0 + kUnit > len - args.Q + 1 || (__ballot(now.id < 0) >> from & 15) != 0;
       f32x4 s[NT][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -327,8 +353,8 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
               if (none[j] || key0 + 16 * j + 4 * g4 + i >= from_key) vr[j][i] = (u32x2){0, 0};
         };
         clear(len);
-        if (p.Q > 1) {
-          const int some = len - p.Q + 1;    // the first token that not all queries see
+        if (args.Q > 1) {
+          const int some = len - args.Q + 1;    // the first token that not all queries see
           uint32_t nan = 0;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -385,16 +411,16 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
 
     // -------- the tokens that were left: one by one, each to the queries that see it
     while (late) {
-      const int unit = max(len - p.Q + 1, 0) / kUnit + __builtin_ctz(late);
+      const int unit = max(len - args.Q + 1, 0) / kUnit + __builtin_ctz(late);
       late &= late - 1;
 #pragma unroll 1
-      for (int key = max(unit * kUnit, max(len - p.Q + 1, 0)); key < min((unit + 1) * kUnit, len); ++key) {
-        const int id = table[key >> p.shift];
-        if (id < 0 || id >= p.num_pages) continue;
-        const float ks = p.k_scale[int64_t(id) * p.HKV + hkv] * c, vs = p.v_scale[int64_t(id) * p.HKV + hkv];
-        const int64_t at = int64_t(id) * p.page_stride + ((int64_t(hkv) << p.shift) + (key & ((1 << p.shift) - 1))) * D;
-        const u32x4* kp = reinterpret_cast<const u32x4*>(p.k_cache + at + 32 * g4);
-        const u32x4* vp = reinterpret_cast<const u32x4*>(p.v_cache + at + 32 * g4);
+      for (int key = max(unit * kUnit, max(len - args.Q + 1, 0)); key < min((unit + 1) * kUnit, len); ++key) {
+        const int id = table[key >> args.shift];
+        if (id < 0 || id >= args.num_pages) continue;
+        const float ks = args.k_scale[int64_t(id) * args.HKV + hkv] * c, vs = args.v_scale[int64_t(id) * args.HKV + hkv];
+        const int64_t at = int64_t(id) * args.page_stride + ((int64_t(hkv) << args.shift) + (key & ((1 << args.shift) - 1))) * D;
+        const u32x4* kp = reinterpret_cast<const u32x4*>(args.k_cache + at + 32 * g4);
+        const u32x4* vp = reinterpret_cast<const u32x4*>(args.v_cache + at + 32 * g4);
         float kx[32], vx[32];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -421,14 +447,11 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
 
     // -------- its rows: finished, or a part.  Lane (l16, g4) holds row l16,
     // columns 8 (4 g4 + e) + d in o[d][e].
-    const bool whole = first == 0 && last == units;
+    const bool whole = !kAlone && first == 0 && last == units;
     const int64_t segment = int64_t(n) * per + seg;
-    if (first == 0 && lane == 0) p.owner[segment] = whole ? -1 : w;
-    if (first != 0 && last == units && lane == 0) p.last_owner[segment] = w;
-    // All four waves of the workgroup inside one segment: one part for them.
-    const int64_t start = u - first;         // the segment's first unit in the line
-    const bool merge = piece.lo < piece.hi && start <= piece.lo && piece.hi <= start + units;
-    float* parts = p.parts + (segment + w) * p.tile_rows * (D + 4);
+    if (!kAlone && first == 0 && lane == 0) args.owner[segment] = whole ? -1 : w;
+    if (!kAlone && first != 0 && last == units && lane == 0) args.last_owner[segment] = w;
+    float* parts = args.parts + (segment + w) * args.tile_rows * (D + 4);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float sum = l[t] + __shfl_xor(l[t], 16, 64);
@@ -437,16 +460,16 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
       if (r >= rows) continue;
       if (whole) {
         const int i = (row0 + r) / G, head = hkv * G + row0 + r - i * G;
-        const int64_t out = (int64_t(n) * p.Q + i) * p.HQ + head;
+        const int64_t out = (int64_t(n) * args.Q + i) * args.HQ + head;
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float x[8];
 #pragma unroll
           for (int d = 0; d < 8; ++d) x[d] = o[t][d][e] * f;
-          *reinterpret_cast<bf16x8*>(p.o + out * D + 8 * (4 * g4 + e)) = pack8(x);
+          *reinterpret_cast<bf16x8*>(args.o + out * D + 8 * (4 * g4 + e)) = pack8(x);
         }
-        if (p.lse && g4 == 0) p.lse[out] = (m[t] + __log2f(sum)) * kLn2;
+        if (args.lse && g4 == 0) args.lse[out] = (m[t] + __log2f(sum)) * kLn2;
       } else {
         auto put = [&](auto* part) {         // LDS or global memory
 #pragma unroll
@@ -463,40 +486,49 @@ __global__ __launch_bounds__(kThreads, 2) void attn_decode_kernel(Params p) {
           put(parts + r * (D + 4));
       }
     }
-    if (merge) {                             // the same for all four waves, and each one's only segment
+    if (merge) {                             // the same for all the waves, and each one's only segment
       __syncthreads();
       // 32 threads per row; the first wave's slot takes the sum, the others' say that they are empty
       const int col = (threadIdx.x & 31) * 4;
-      for (int r = threadIdx.x >> 5; r < rows; r += kThreads / 32) {
+      for (int r = threadIdx.x >> 5; r < rows; r += kGroup * 2) {
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) top = fmaxf(top, merged[i][r][D]);
+        for (int i = 0; i < kGroup; ++i) top = fmaxf(top, merged[i][r][D]);
         const float base = top == -INFINITY ? 0.0f : top;
         f32x4 acc = (f32x4)(0.0f);
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) {
+        for (int i = 0; i < kGroup; ++i) {
           const float f = __builtin_amdgcn_exp2f(merged[i][r][D] - base);
           acc += *reinterpret_cast<const f32x4*>(&merged[i][r][col]) * f;
           sum += merged[i][r][D + 1] * f;
         }
-        float* part = p.parts + ((segment + w - wave) * p.tile_rows + r) * (D + 4);
+        if constexpr (kAlone) {
+          const int i = (row0 + r) / G;
+          const int64_t out = (int64_t(n) * args.Q + i) * args.HQ + hkv * G + row0 + r - i * G;
+          acc *= sum == 0.0f ? 0.0f : 1.0f / sum;
+          *reinterpret_cast<u32x2*>(args.o + out * D + col) =
+              (u32x2){kda::pack_bf16(acc[0], acc[1]), kda::pack_bf16(acc[2], acc[3])};
+          if (args.lse && col == 0) args.lse[out] = (top + __log2f(sum)) * kLn2;
+          continue;
+        }
+        float* part = args.parts + ((segment + w - wave) * args.tile_rows + r) * (D + 4);
         *reinterpret_cast<f32x4*>(part + col) = acc;
         if (col == 0) {
           part[D] = top, part[D + 1] = sum;
           for (int i = 1; i < kWaves; ++i) {
-            part[i * p.tile_rows * (D + 4) + D] = -INFINITY;
-            part[i * p.tile_rows * (D + 4) + D + 1] = 0.0f;
+            part[i * args.tile_rows * (D + 4) + D] = -INFINITY;
+            part[i * args.tile_rows * (D + 4) + D + 1] = 0.0f;
           }
         }
       }
       return;
     }
-    u += last - first;
+    left -= last - first;
     first = 0;
     if (++seg == per) {
       seg = 0;
-      if (++n < p.N) len = length(p, n), units = units_of(len);
+      if (++n < args.N) len = length(args, n), units = units_of(len);
     }
   }
 }
@@ -649,6 +681,22 @@ Plan plan_for(int64_t N, int64_t Q, int HQ, int HKV) {
   return x;
 }
 
+// Whether every segment has a workgroup alone.  The host knows what the tables
+// can hold, not the lengths.  A wave then walks up to an eighth of a segment, at
+// 2.6 us per unit where little else runs; the line balances that, for a second
+// launch and the parts' way through memory.  32 heads on 8, lengths up to the
+// stated one, line and alone in us:
+//   1 sequence: 1000 tokens 15.4 and 13.0, 2000 15.4 and 15.6, 4000 15.2 and 25.8
+//   8: 1500 tokens 15.1 and 13.6, 2000 16.2 and 16.3, 4000 17.9 and 26.8
+//   24: 1000 tokens 16.0 and 12.8, 2000 20.8 and 16.9, 4000 33.2 and 32.6
+//   64: 250 tokens 15.8 and 12.8, 1000 26.3 and 21.6, 4000 70 and 64
+//   128: 60 tokens 15.1 and 18.3 (a workgroup fills a compute unit, and four wait for each)
+bool alone(int64_t segments, int64_t tokens) {
+  const int64_t cus = kda::device_cus();
+  if (segments > 2 * cus) return false;
+  return tokens <= 24 * kUnit || (tokens <= 64 * kUnit && 4 * segments >= 3 * cus);
+}
+
 int sizes(int32_t N, int32_t Q, int32_t HQ, int32_t HKV, int32_t Dh) {
   const int e = kda::attn_heads(HQ, HKV, Dh);
   if (e != KDA_OK) return e;
@@ -699,11 +747,19 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
                  static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, join_rows, x.waves,
                  static_cast<float*>(workspace), owner, owner + x.segments};
   const hipStream_t st = kda::as_stream(stream);
+  if (alone(x.segments, int64_t(table_width) * page_size)) {
+    const dim3 grid(unsigned(x.segments));
+    if (x.tile_rows == 16)
+      hipLaunchKernelGGL((attn_decode_kernel<1, true>), grid, dim3(64 * kAloneWaves), 0, st, p);
+    else
+      hipLaunchKernelGGL((attn_decode_kernel<2, true>), grid, dim3(64 * kAloneWaves), 0, st, p);
+    return kda::launch_status();
+  }
   const dim3 grid(unsigned(x.waves / kWaves));
   if (x.tile_rows == 16)
-    hipLaunchKernelGGL(attn_decode_kernel<1>, grid, dim3(kThreads), 0, st, p);
+    hipLaunchKernelGGL((attn_decode_kernel<1, false>), grid, dim3(kThreads), 0, st, p);
   else
-    hipLaunchKernelGGL(attn_decode_kernel<2>, grid, dim3(kThreads), 0, st, p);
+    hipLaunchKernelGGL((attn_decode_kernel<2, false>), grid, dim3(kThreads), 0, st, p);
   const dim3 joins(unsigned(x.segments * ((tile + join_rows - 1) / join_rows)));
   if (many)
     hipLaunchKernelGGL(attn_decode_join_kernel<1024>, joins, dim3(1024), 0, st, p);

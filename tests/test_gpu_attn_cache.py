@@ -508,3 +508,46 @@ def test_decode_two_at_once(gpu_lib):
     for want, results in zip(alone, got):
         for o, lse in results:
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+class Wide:
+    """The library with page tables that could hold much more than they do: decode then cuts all sequences into equal
+    pieces, where short tables give each (sequence, head) a workgroup."""
+
+    def __init__(self, lib):
+        self.lib = lib
+
+    def __getattr__(self, name):
+        return getattr(self.lib, name)
+
+    def attn_decode(self, q, k_cache, v_cache, k_scale, v_scale, table, lens, **kw):
+        pad = table.new_full((table.shape[0], 5000 // k_cache.shape[2]), -1)
+        return self.lib.attn_decode(q, k_cache, v_cache, k_scale, v_scale, torch.cat([table, pad], 1), lens, **kw)
+
+
+@pytest.mark.parametrize("lens,Q,HQ,HKV,P", DECODE)
+def test_decode_wide_tables(gpu_lib, lens, Q, HQ, HKV, P):
+    test_decode(Wide(gpu_lib), lens, Q, HQ, HKV, P)
+
+
+@pytest.mark.parametrize("Q,HQ", [(1, 2), (2, 2), (5, 8), (70, 4)])
+def test_decode_wide_tables_masks(gpu_lib, Q, HQ):
+    """What the tests above mask, cut among waves."""
+    wide = Wide(gpu_lib)
+    test_decode_reads_no_further(wide, min(Q, 3))
+    if Q > 1:
+        test_decode_later_nan_does_not_reach_earlier_queries(wide, Q, HQ)
+    test_decode_peaked_and_scaled(wide)
+
+
+@pytest.mark.parametrize("N,longest", [(1, 1536), (1, 1537), (64, 1000), (65, 1000), (24, 4096), (23, 4096), (24, 4097)])
+def test_decode_alone_and_cut(gpu_lib, N, longest):
+    """Both sides of the rule that says which of the two it is (64-token pages, 8 heads)."""
+    rng = np.random.default_rng(N + longest)
+    lens = [longest] + [int(x) for x in rng.integers(0, longest + 1, N - 1)]
+    table, pages = tables_for(lens, 64, spare=0, seed=22)
+    table = table[:, :-(-longest // 64)]
+    cache = usual_cache(62, pages, 8, 64)
+    q = rand(63, N, 1, 8, D).to(DEV)
+    o, lse = gpu_lib.attn_decode(q, *cache, ints(table), ints(lens))
+    check_decode(o, lse, q, cache, table, lens)
