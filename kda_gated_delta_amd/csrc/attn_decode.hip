@@ -28,12 +28,12 @@
 // lane.  Weights are rounded to bfloat16 (times the page's scale of the values, a
 // power of two where the store made it); maximum, sum and output are float32.
 //
-// 64 sequences of up to 16384 tokens, 32 heads on 8: 1.03 GB of codes in 190 us,
-// 5.4 TB/s, and 5 to 7 us of joining; three or four waves per SIMD, or 16 waves
-// on a compute unit, are no faster.  2 sequences of up to 131072 tokens, 4 queries of 16
-// heads on 2: 68 MB in 25 us and 10 of joining.  There, and the more for one
-// sequence of 1000 tokens (8 and 4 us), the chain lengths -> table -> scales and
-// codes -> products is what it takes, not the bytes.
+// 64 sequences of up to 16384 tokens, 32 heads on 8: 1.03 GB of codes in 187 us,
+// 5.5 TB/s, and 5 to 7 us of joining; three or four waves per SIMD, or twice as
+// many pieces, are slower.  2 sequences of up to 131072 tokens, 4 queries of 16
+// heads on 2: 68 MB in 22.5 us and 10 of joining.  There, and the more for one
+// sequence of 1000 tokens (10.7 us in one launch), the chain lengths -> table ->
+// scales and codes -> products is what it takes, not the bytes.
 #include "attn_device.h"
 #include "kda_host.h"
 
