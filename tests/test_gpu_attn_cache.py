@@ -551,3 +551,8 @@ def test_decode_alone_and_cut(gpu_lib, N, longest):
     q = rand(63, N, 1, 8, D).to(DEV)
     o, lse = gpu_lib.attn_decode(q, *cache, ints(table), ints(lens))
     check_decode(o, lse, q, cache, table, lens)
+
+
+def test_steps_with_wide_tables(gpu_lib):
+    test_prompts_then_steps(Wide(gpu_lib))
+    test_captured_steps(Wide(gpu_lib))
