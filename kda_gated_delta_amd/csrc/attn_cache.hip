@@ -26,7 +26,7 @@ struct StoreParams {
   int64_t k_stride, v_stride;
   const int32_t* slots;
   int T, HKV, page_size, shift, wshift;
-  unsigned items;
+  unsigned items, waves;
   int64_t num_slots, page_stride;
   uint8_t *k_cache, *v_cache;
   float *k_scale, *v_scale;
@@ -67,24 +67,42 @@ __device__ __forceinline__ uint32_t rescale(uint32_t w, float f) {
   return uint32_t(r);
 }
 
+// Rows of a run as a buffer that ends behind the last one: rows past it read as
+// zero and are not written, so a wave handles groups of four rows without a branch.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t as_buffer(const void* at, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(at), 0, int(bytes), 0x00020000);
+}
+
 // One wave stores `n` tokens of one head, keys or values, the first of them at
 // offset `off` of a page.  rows: the first token's row; page: the (page, head)'s
-// codes.  Up to 64 tokens are read once and kept in registers between the
-// maximum and the codes; longer runs (pages of 128 and 256) are read twice.
+// codes.  GROUPS x 4 tokens are read once and kept in registers between the
+// maximum and the codes; what is over (pages of 128 and 256) is read twice.
+template <int GROUPS>
 __device__ __forceinline__ void store_run(const uint16_t* rows, int64_t stride, int n, uint8_t* page, int off,
                                           float* scale, int lane) {
-  const int row = lane >> 4, at = (lane & 15) * 8;
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  const int row = lane >> 4, at = (lane & 15) * 8, here = min(n, 4 * GROUPS);
+  const auto src = as_buffer(rows, ((here - 1) * stride + D) * 2);
   const float was = off ? *scale : 0.0f;
-  u32x4 kept[16];
-  uint32_t top = 0;
+  u32x4 kept[GROUPS];
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (4 * i < n) kept[i] = *reinterpret_cast<const u32x4*>(rows + min(4 * i + row, n - 1) * stride + at);
+  for (int i = 0; i < GROUPS; ++i)
+    kept[i] = __builtin_amdgcn_raw_buffer_load_b128(src, int((4 * i + row) * stride + at) * 2, 0, 0);
+  u16x2 most = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (4 * i < n) top = finite_top(kept[i], top);
+  for (int i = 0; i < GROUPS; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, kept[i][j] & 0x7fff7fffu));
+  uint32_t top = max(most[0], most[1]);
+  if (__any(top >= 0x7f80u)) {                 // an infinity or NaN: only finite values count
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) top = finite_top(kept[i], top);
+  }
 #pragma unroll 4
-  for (int i = 64 + row; i < n; i += 4) top = finite_top(*reinterpret_cast<const u32x4*>(rows + i * stride + at), top);
+  for (int i = 4 * GROUPS + row; i < n; i += 4)
+    top = finite_top(*reinterpret_cast<const u32x4*>(rows + i * stride + at), top);
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) top = max(top, uint32_t(__shfl_xor(int(top), i, 64)));
   // least e with 448 x 2^e >= top, 448 = 1.75 x 2^8
@@ -104,12 +122,12 @@ __device__ __forceinline__ void store_run(const uint16_t* rows, int64_t stride, 
   }
   if (lane == 0) *scale = now;
   const float f = 1.0f / now;
-  uint8_t* dst = page + (off + row) * D + at;
+  const auto dst = as_buffer(page + off * D, here * D);
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (4 * i + row < n) *reinterpret_cast<u32x2*>(dst + 4 * i * D) = to_codes(kept[i], f);
+  for (int i = 0; i < GROUPS; ++i)
+    __builtin_amdgcn_raw_buffer_store_b64(to_codes(kept[i], f), dst, (4 * i + row) * D + at, 0, 0);
 #pragma unroll 4
-  for (int i = 64 + row; i < n; i += 4)
+  for (int i = 4 * GROUPS + row; i < n; i += 4)
     *reinterpret_cast<u32x2*>(page + (off + i) * D + at) =
         to_codes(*reinterpret_cast<const u32x4*>(rows + i * stride + at), f);
 }
@@ -119,14 +137,17 @@ __device__ __forceinline__ void store_run(const uint16_t* rows, int64_t stride, 
 // scale has one writer.  An item is (window of 2^wshift tokens, head, keys or
 // values): the wave looks there for the runs that begin.  Waves go from item to
 // item, the next one's slots already on their way.
-// Memory bounds it where there is much to store: 35000 tokens of prompts x 8
-// heads, 215 MB, take 40 us (5.4 TB/s) into one cache, 54 into three in turn,
-// whose pages no cache level holds.  256 single tokens x 8 heads take 5.5 us, the
-// latency of slots, rows, scale and codes one after another.
+// Memory bounds it where there is much to store: 35000 tokens x 8 heads, 215 MB,
+// take 36 us (6 TB/s, keys and values fresh in the last cache level), 54 of
+// prompts over three caches in turn, which no cache level holds.  256 single
+// tokens x 8 heads take 5.5 us, the latency of slots, rows, scale and codes one
+// after another.  With a branch for each four rows, and loads that waited for
+// them, one page took 13 us instead of 5.
 __global__ __launch_bounds__(64 * kStoreWaves, 4) void attn_cache_store_kernel(StoreParams p) {
   const int lane = threadIdx.x & 63, window = 1 << p.wshift;
-  const unsigned waves = gridDim.x * kStoreWaves;
+  const unsigned waves = p.waves;
   unsigned item = __builtin_amdgcn_readfirstlane(blockIdx.x * kStoreWaves + (threadIdx.x >> 6));
+  if (item >= waves) return;
   auto slot_at = [&](int64_t t) -> int {       // -1: no such token, or not stored
     const int s = t >= 0 && t < p.T ? p.slots[t] : -1;
     return s >= 0 && s < p.num_slots ? s : -1;
@@ -160,12 +181,17 @@ __global__ __launch_bounds__(64 * kStoreWaves, 4) void attn_cache_store_kernel(S
         n += whole ? 64 : __builtin_ctzll(~same);
       }
       const int64_t page = slot >> p.shift;
-      const int64_t codes = page * p.page_stride + int64_t(head) * p.page_size * D;
-      const int64_t scale = page * p.HKV + head;
       const bool v = part & 1;
       const int64_t stride = v ? p.v_stride : p.k_stride;
-      store_run((v ? p.v : p.k) + t * stride + head * D, stride, n, (v ? p.v_cache : p.k_cache) + codes, off,
-                (v ? p.v_scale : p.k_scale) + scale, lane);
+      const uint16_t* rows = (v ? p.v : p.k) + t * stride + head * D;
+      uint8_t* codes = (v ? p.v_cache : p.k_cache) + page * p.page_stride + int64_t(head) * p.page_size * D;
+      float* scale = (v ? p.v_scale : p.k_scale) + page * p.HKV + head;
+      if (n <= 4)
+        store_run<1>(rows, stride, n, codes, off, scale, lane);
+      else if (n <= 16)
+        store_run<4>(rows, stride, n, codes, off, scale, lane);
+      else
+        store_run<16>(rows, stride, n, codes, off, scale, lane);
     }
   }
 }
@@ -289,19 +315,22 @@ extern "C" int kda_attn_cache_store(const void* k, const void* v, int64_t k_stri
     if (!kda::aligned16(x)) return KDA_ERR_ALIGN;
   // Every run costs a wave its latency, every empty window a look.  A decode
   // step's tokens are a run each and want a window each; in prompts a run is a
-  // page.  Windows grow until two items are left for a wave, up to 16 tokens:
-  // 256 single tokens x 8 heads take 5.4 us (window 1), 35000 tokens of
-  // prompts 40 us (window 16).
-  const int64_t waves = 16 * int64_t(kda::device_cus()), each = 2 * int64_t(HKV);
+  // page.  Windows grow until two items are left for a wave, up to 16 tokens.
+  // From one item to its next a wave passes an odd number of windows: runs begin
+  // a page apart, and an even step would give all of them to the same few waves
+  // (one sequence of 35000 tokens x 8 heads: 58 us with 256 windows, 36 with 255).
+  const int64_t each = 2 * int64_t(HKV), most = 16 * int64_t(kda::device_cus());
+  const int64_t step = most / each < 3 ? 1 : (most / each - 1) | 1;
   int wshift = 0;
-  while (wshift < 4 && (int64_t(T) >> wshift) * each > 2 * waves) ++wshift;
+  while (wshift < 4 && (int64_t(T) >> wshift) * each > 2 * most) ++wshift;
   const int64_t items = ((int64_t(T) + (1 << wshift) - 1) >> wshift) * each;
   if (items > 0x7fffffff) return KDA_ERR_SHAPE;
+  const int64_t waves = items < step * each ? items : step * each;
   const StoreParams p{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_stride, v_stride, slots,
-                      T, HKV, page_size, __builtin_ctz(page_size), wshift, unsigned(items),
+                      T, HKV, page_size, __builtin_ctz(page_size), wshift, unsigned(items), unsigned(waves),
                       int64_t(num_pages) * page_size, page_stride,
                       static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale};
-  const int64_t blocks = ((items < waves ? items : waves) + kStoreWaves - 1) / kStoreWaves;
+  const int64_t blocks = (waves + kStoreWaves - 1) / kStoreWaves;
   hipLaunchKernelGGL(attn_cache_store_kernel, dim3(unsigned(blocks)), dim3(64 * kStoreWaves), 0,
                      kda::as_stream(stream), p);
   return kda::launch_status();
