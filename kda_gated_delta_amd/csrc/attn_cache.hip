@@ -140,7 +140,7 @@ __device__ __forceinline__ void store_run(const uint16_t* rows, int64_t stride, 
 // Memory bounds it where there is much to store: 35000 tokens x 8 heads, 215 MB,
 // take 36 us (6 TB/s, keys and values fresh in the last cache level), 54 of
 // prompts over three caches in turn, which no cache level holds.  256 single
-// tokens x 8 heads take 5.5 us, the latency of slots, rows, scale and codes one
+// tokens x 8 heads take 5 us, the latency of slots, rows, scale and codes one
 // after another.  With a branch for each four rows, and loads that waited for
 // them, one page took 13 us instead of 5.
 __global__ __launch_bounds__(64 * kStoreWaves, 4) void attn_cache_store_kernel(StoreParams p) {

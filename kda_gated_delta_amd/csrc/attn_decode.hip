@@ -28,8 +28,8 @@
 // lane.  Weights are rounded to bfloat16 (times the page's scale of the values, a
 // power of two where the store made it); maximum, sum and output are float32.
 //
-// 64 sequences of up to 16384 tokens, 32 heads on 8: 1.03 GB of codes in 187 us,
-// 5.5 TB/s, and 5 to 7 us of joining; three or four waves per SIMD, or twice as
+// 64 sequences of up to 16384 tokens, 32 heads on 8: 1.03 GB of codes in 165 us,
+// 6.2 TB/s, and 5 us of joining; three or four waves per SIMD, or twice as
 // many pieces, are slower.  2 sequences of up to 131072 tokens, 4 queries of 16
 // heads on 2: 68 MB in 22.5 us and 10 of joining.  There, and the more for one
 // sequence of 1000 tokens (10.7 us in one launch), the chain lengths -> table ->
@@ -160,9 +160,11 @@ struct Pages {
 
 // kAlone: a workgroup of eight waves takes a segment alone, an eighth of its
 // units each, and finishes it: no parts, no second launch (alone says when).
-template <int NT, bool kAlone>
+// kStream: codes are loaded past the last cache level (streams says when).
+template <int NT, bool kAlone, bool kStream>
 __global__ __launch_bounds__(kAlone ? 64 * kAloneWaves : kThreads, 2) void attn_decode_kernel(Params p) {
   constexpr int kGroup = kAlone ? kAloneWaves : kWaves;
+  constexpr int kHint = kStream ? 2 : 0;     // non-temporal
   const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
   __shared__ __align__(16) float merged[kGroup][16 * NT][D + 4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -245,7 +247,7 @@ __global__ __launch_bounds__(kAlone ? 64 * kAloneWaves : kThreads, 2) void attn_
       for (int j = 0; j < 4; ++j) {
         const auto tile = tile_at(args.k_cache, x, unit, from, j);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) kr[j][i] = __builtin_amdgcn_raw_buffer_load_b128(tile, k_off + 16 * i, 0, 0);
+        for (int i = 0; i < 2; ++i) kr[j][i] = __builtin_amdgcn_raw_buffer_load_b128(tile, k_off + 16 * i, 0, kHint);
       }
     };
     auto load_v = [&](const Pages& x, int unit, int from) {
@@ -253,7 +255,7 @@ __global__ __launch_bounds__(kAlone ? 64 * kAloneWaves : kThreads, 2) void attn_
       for (int j = 0; j < 4; ++j) {
         const auto tile = tile_at(args.v_cache, x, unit, from, j);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vr[j][i] = __builtin_amdgcn_raw_buffer_load_b64(tile, v_off + i * D, 0, 0);
+        for (int i = 0; i < 4; ++i) vr[j][i] = __builtin_amdgcn_raw_buffer_load_b64(tile, v_off + i * D, 0, kHint);
       }
     };
 
@@ -697,6 +699,18 @@ bool alone(int64_t segments, int64_t tokens) {
   return tokens <= 24 * kUnit || (tokens <= 64 * kUnit && 4 * segments >= 3 * cus);
 }
 
+// Whether a call may read so many codes that little of them is left in the last
+// cache level (256 MB) when it comes again, after other layers': then loading
+// past it is faster.  What fits should stay there.  Through it against past it,
+// us, by the bytes read, three caches in turn (32 heads on 8; the 68 MB: 4
+// queries of 16 heads on 2):
+//   1029 MB 198 and 175, 500 MB 117 and 105, 200 MB 46.6 and 41.3, 134 MB 44.3 and 41.8, 107 MB 39.7 and 38.0,
+//   68 MB 33.3 and 35.1, 61 MB 21.9 and 22.5, 35 MB 22.5 and 24.7
+bool streams(int64_t N, int64_t table_width, int64_t num_pages, int64_t page_size, int64_t HKV) {
+  const int64_t pages = N * table_width < num_pages ? N * table_width : num_pages;
+  return pages * page_size * HKV * 2 * D > int64_t(96) << 20;
+}
+
 int sizes(int32_t N, int32_t Q, int32_t HQ, int32_t HKV, int32_t Dh) {
   const int e = kda::attn_heads(HQ, HKV, Dh);
   if (e != KDA_OK) return e;
@@ -750,16 +764,21 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
   if (alone(x.segments, int64_t(table_width) * page_size)) {
     const dim3 grid(unsigned(x.segments));
     if (x.tile_rows == 16)
-      hipLaunchKernelGGL((attn_decode_kernel<1, true>), grid, dim3(64 * kAloneWaves), 0, st, p);
+      hipLaunchKernelGGL((attn_decode_kernel<1, true, false>), grid, dim3(64 * kAloneWaves), 0, st, p);
     else
-      hipLaunchKernelGGL((attn_decode_kernel<2, true>), grid, dim3(64 * kAloneWaves), 0, st, p);
+      hipLaunchKernelGGL((attn_decode_kernel<2, true, false>), grid, dim3(64 * kAloneWaves), 0, st, p);
     return kda::launch_status();
   }
   const dim3 grid(unsigned(x.waves / kWaves));
-  if (x.tile_rows == 16)
-    hipLaunchKernelGGL((attn_decode_kernel<1, false>), grid, dim3(kThreads), 0, st, p);
+  const bool stream_past = streams(N, table_width, num_pages, page_size, HKV);
+  if (x.tile_rows == 16 && stream_past)
+    hipLaunchKernelGGL((attn_decode_kernel<1, false, true>), grid, dim3(kThreads), 0, st, p);
+  else if (x.tile_rows == 16)
+    hipLaunchKernelGGL((attn_decode_kernel<1, false, false>), grid, dim3(kThreads), 0, st, p);
+  else if (stream_past)
+    hipLaunchKernelGGL((attn_decode_kernel<2, false, true>), grid, dim3(kThreads), 0, st, p);
   else
-    hipLaunchKernelGGL((attn_decode_kernel<2, false>), grid, dim3(kThreads), 0, st, p);
+    hipLaunchKernelGGL((attn_decode_kernel<2, false, false>), grid, dim3(kThreads), 0, st, p);
   const dim3 joins(unsigned(x.segments * ((tile + join_rows - 1) / join_rows)));
   if (many)
     hipLaunchKernelGGL(attn_decode_join_kernel<1024>, joins, dim3(1024), 0, st, p);

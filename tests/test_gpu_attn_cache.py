@@ -556,3 +556,20 @@ def test_decode_alone_and_cut(gpu_lib, N, longest):
 def test_steps_with_wide_tables(gpu_lib):
     test_prompts_then_steps(Wide(gpu_lib))
     test_captured_steps(Wide(gpu_lib))
+
+
+@pytest.mark.parametrize("HQ", [2, 20])
+def test_decode_large_caches(gpu_lib, HQ):
+    """A cache of more than a hundred megabytes, which is loaded another way: the same bits as from a small one."""
+    lens, P, HKV = [3000, 1, 0, 9000], 64, 1
+    table, pages = tables_for(lens, P, seed=23)
+    table = np.concatenate([table, np.full((len(lens), 3000), -1)], 1)
+    cache = usual_cache(64, pages, HKV, P)
+    q = rand(65, len(lens), 1, HQ, D).to(DEV)
+    o, lse = gpu_lib.attn_decode(q, *cache, ints(table), ints(lens))
+    check_decode(o, lse, q, cache, table, lens)
+    more = 7000 - pages
+    large = [torch.cat([c.view(torch.uint8), torch.full((more, HKV, P, D), 0x7f, dtype=torch.uint8, device=DEV)]).view(E4M3)
+             for c in cache[:2]] + [torch.cat([s, s.new_full((more, HKV), float("nan"))]) for s in cache[2:]]
+    o2, lse2 = gpu_lib.attn_decode(q, *large, ints(table), ints(lens))
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
