@@ -55,7 +55,7 @@ struct Params {
 
 // kSplit = 2: a second set of four waves takes every other key tile, as in the
 // forward (attn_split says when).
-template <typename Out, int kSplit>
+template <typename Out, int kSplit, bool kBoth>
 __global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p) {
   constexpr int kHalf = 4 * kTileBytes;    // two buffers of K and V
   __shared__ __align__(1024) unsigned char all[kSplit * kHalf];
@@ -179,6 +179,11 @@ __global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p)
         const bf16x8 b = pack8(x);
 #pragma unroll
         for (int d = 0; d < 4; ++d) dq[d] = mfma32(read_columns(kt, 32 * w, k, 32 * d, lane), b, dq[d]);
+        if constexpr (kBoth) {
+          const bf16x8 rest = pack8_rest(x, b);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) dq[d] = mfma32(read_columns(kt, 32 * w, k, 32 * d, lane), rest, dq[d]);
+        }
       }
     }
   }
@@ -206,7 +211,7 @@ __global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p)
 
 // ---------------------------------------------------------------- dK and dV
 
-template <typename Out>
+template <typename Out, bool kBoth>
 __global__ __launch_bounds__(kThreads, 2) void attn_dkv_kernel(Params p) {
   constexpr int kBuffer = 2 * kTileBytes + 512;            // Q, dO, lse2, delta
   __shared__ __align__(1024) unsigned char lds[2 * kBuffer];
@@ -301,6 +306,13 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dkv_kernel(Params p) {
         for (int d = 0; d < 4; ++d) dv[d] = mfma32(read_columns(ut, 32 * w, k, 32 * d, lane), pb, dv[d]);
 #pragma unroll
         for (int d = 0; d < 4; ++d) dk[d] = mfma32(read_columns(qt, 32 * w, k, 32 * d, lane), gb, dk[d]);
+        if constexpr (kBoth) {
+          const bf16x8 pr = pack8_rest(x, pb), gr = pack8_rest(y, gb);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) dv[d] = mfma32(read_columns(ut, 32 * w, k, 32 * d, lane), pr, dv[d]);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) dk[d] = mfma32(read_columns(qt, 32 * w, k, 32 * d, lane), gr, dk[d]);
+        }
       }
     }
   }
@@ -361,21 +373,42 @@ int64_t slots_for(int B, int T, int num_seqs) {
 
 size_t stat_floats(int64_t B, int64_t T, int64_t HQ) { return size_t((B * T * HQ + 3) / 4 * 4); }
 
-template <typename Out>
-int launch(const Params& p, hipStream_t stream) {
-  const int64_t blocks = head_blocks(p.slots, p.HQ, p.HKV);
-  if (kda::attn_split(blocks, p.T, p.N, p.cu != nullptr))
-    hipLaunchKernelGGL((attn_dq_kernel<Out, 2>), dim3(unsigned(blocks)), dim3(2 * kThreads), 0, stream, p);
-  else
-    hipLaunchKernelGGL((attn_dq_kernel<Out, 1>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, p);
-  const dim3 grid(unsigned(p.slots * p.HKV * p.parts));
+// Whether weights and score gradients are carried as two bfloat16 terms.  One
+// rounding of each adds as much error to a gradient as rounding the gradient
+// itself, and where there are few of them, by chance more.  There the launch's
+// time is latency, and a second product with what the rounding left costs next to
+// nothing (10 sequences of 3 tokens, 2 heads: dQ and dK off by 0.0028 of their
+// norm with one term, 0.0017 with two, as rounded exact ones are; FIGB).  With
+// more of them chance is averaged out, and the products are what bounds the walk.
+bool both_terms(int64_t rows, int64_t len) { return rows * len <= 1 << 15; }
+
+template <typename Out, bool kBoth>
+void launch_dkv(const Params& p, dim3 grid, hipStream_t stream) {
   if (p.parts == 1) {
-    hipLaunchKernelGGL(attn_dkv_kernel<Out>, grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((attn_dkv_kernel<Out, kBoth>), grid, dim3(kThreads), 0, stream, p);
   } else {
-    hipLaunchKernelGGL(attn_dkv_kernel<float>, grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((attn_dkv_kernel<float, kBoth>), grid, dim3(kThreads), 0, stream, p);
     const int64_t quads = int64_t(p.B) * p.T * p.HKV * (D / 4);
     hipLaunchKernelGGL(attn_sum_kernel<Out>, dim3(unsigned((quads + 255) / 256), 2), dim3(256), 0, stream, p);
   }
+}
+
+template <typename Out>
+int launch(const Params& p, hipStream_t stream) {
+  const int64_t blocks = head_blocks(p.slots, p.HQ, p.HKV);
+  const bool packed = p.cu != nullptr;
+  const bool both = both_terms(int64_t(p.B) * p.T * p.HQ, kda::attn_typical(p.T, p.N, packed));
+  if (kda::attn_split(blocks, p.T, p.N, packed))
+    hipLaunchKernelGGL((attn_dq_kernel<Out, 2, false>), dim3(unsigned(blocks)), dim3(2 * kThreads), 0, stream, p);
+  else if (both)
+    hipLaunchKernelGGL((attn_dq_kernel<Out, 1, true>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((attn_dq_kernel<Out, 1, false>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, p);
+  const dim3 grid(unsigned(p.slots * p.HKV * p.parts));
+  if (both)
+    launch_dkv<Out, true>(p, grid, stream);
+  else
+    launch_dkv<Out, false>(p, grid, stream);
   return kda::launch_status();
 }
 

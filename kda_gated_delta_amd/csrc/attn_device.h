@@ -55,6 +55,14 @@ __device__ __forceinline__ bf16x8 pack8(const float* x) {
   const u32x4 v = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
   return as_bf16x8(v);
 }
+// What rounding to x's bfloat16 values left of them, rounded in turn: the two
+// together hold 16 bits of each.
+__device__ __forceinline__ bf16x8 pack8_rest(const float (&x)[8], const bf16x8& b) {
+  float rest[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rest[i] = x[i] - float(b[i]);
+  return pack8(rest);
+}
 
 // ---------------------------------------------------------------- packed sequences
 

@@ -323,3 +323,18 @@ def test_later_values_in_long_walks(gpu_lib, at, bad):
     keep = (~seen).cpu().numpy()
     assert (np.abs(f64(o) - want)[0][keep] <= tol[0][keep]).all()
     check_prompt(clean, lse, q, k, v)
+
+
+FEW = [(1, 3, 2, 2, None), (4, 2, 8, 2, None), (1, 64, 6, 2, None), (1, 30, 2, 1, [0, 3, 6, 6, 7, 30]), (1, 120, 2, 2, None)]
+
+
+@pytest.mark.parametrize("B,T,HQ,HKV,cu", FEW)
+def test_few_gradients_are_nearly_float32(gpu_lib, B, T, HQ, HKV, cu):
+    """Small calls carry weights and score gradients as two bf16 terms, which leave 2^-16 of each."""
+    q, k, v, up, c = case(B, T, HQ, HKV, cu, seed=250)
+    o, lse = gpu_lib.attn_prefill(q, k, v, cu_seqlens=c)
+    grads = gpu_lib.attn_backward(q, k, v, o, lse, up, cu_seqlens=c, grad_dtype="float32")
+    want, moved = ref.attn_backward(f64(q), f64(k), f64(v), f64(up), cu)
+    ew = 2.0 ** -16 + 4.2 * eps(f64(q), f64(k), T) + 2 * 128 * 2.0 ** -24
+    for got, w, m, name in zip(grads, want, moved, ("dq", "dk", "dv")):
+        check(got, w, 2 * ew * m * 1.01 + 1e-30, name)
