@@ -497,8 +497,9 @@ size_t kda_chunk_backward_workspace_size(int32_t B, int32_t T, int32_t H, int32_
  *     q, k and v may be slices of one projection's rows.
  *   - scale multiplies every score: positive and below 1e30 (128^-1/2 is usual).
  *   - softmax statistics and all sums are float32; the weights (and, in the
- *     backward, the scores' gradients) are rounded once to bf16 as operands of
- *     the second matrix product, outputs once when they are stored.
+ *     backward, the scores' gradients) are rounded to bf16 as operands of the
+ *     second matrix product -- once, or in small calls to two terms of bf16 --
+ *     outputs once when they are stored.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -25,8 +25,11 @@
 // moves between lanes: K's columns as a lane loads 32 bytes of a row, V's rows
 // in the order in which the accumulator of S^T holds the keys, and V's 8-byte
 // loads (one key, 8 columns) turned into 8 operands by byte permutes inside the
-// lane.  Weights are rounded to bfloat16 (times the page's scale of the values, a
-// power of two where the store made it); maximum, sum and output are float32.
+// lane.  Weights (times the page's scale of the values) are rounded to bfloat16;
+// of up to 16 rows what that left is a second term, in products of its own: the
+// roundings of few rows do not average out, and there the matrix unit has time
+// (64 sequences of up to 16384 tokens 174.5 and 174.7 us without and with it; with
+// 32 rows it would cost 15%).  Maximum, sum and output are float32.
 //
 // 64 sequences of up to 16384 tokens, 32 heads on 8: 1.03 GB of codes in 165 us,
 // 6.2 TB/s, and 5 us of joining; three or four waves per SIMD, or twice as
@@ -372,13 +375,14 @@ __global__ __launch_bounds__(kAlone ? 64 * kAloneWaves : kThreads, 2) void attn_
       }
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
-        bf16x8 pb[NT];
+        bf16x8 pb[NT], rest;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           float x[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) x[e] = s[t][j][e], x[4 + e] = s[t][j + 1][e];
           pb[t] = pack8(x);
+          if constexpr (NT == 1) rest = pack8_rest(x, pb[t]);
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b)          // columns 8 l16 + 4 b + 0 .. 3
@@ -403,6 +407,10 @@ __global__ __launch_bounds__(kAlone ? 64 * kAloneWaves : kThreads, 2) void attn_
             for (int t = 0; t < NT; ++t) {
               o[t][4 * b + d] = mfma16(a0, pb[t], o[t][4 * b + d]);
               o[t][4 * b + d + 1] = mfma16(a1, pb[t], o[t][4 * b + d + 1]);
+            }
+            if constexpr (NT == 1) {
+              o[0][4 * b + d] = mfma16(a0, rest, o[0][4 * b + d]);
+              o[0][4 * b + d + 1] = mfma16(a1, rest, o[0][4 * b + d + 1]);
             }
           }
       }

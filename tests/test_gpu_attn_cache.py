@@ -573,3 +573,16 @@ def test_decode_large_caches(gpu_lib, HQ):
              for c in cache[:2]] + [torch.cat([s, s.new_full((more, HKV), float("nan"))]) for s in cache[2:]]
     o2, lse2 = gpu_lib.attn_decode(q, *large, ints(table), ints(lens))
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("lens,HQ,HKV,wide", [([40], 1, 1, False), ([900, 3], 16, 1, False), ([900, 3], 8, 2, True)])
+def test_decode_few_rows_are_nearly_float32(gpu_lib, lens, HQ, HKV, wide):
+    """Up to 16 rows carry weights as two bf16 terms, which leave 2^-16 of each: the result's own rounding is all there is."""
+    table, pages = tables_for(lens, 64, seed=24)
+    cache = usual_cache(66, pages, HKV, 64)
+    q = rand(67, len(lens), 1, HQ, D).to(DEV)
+    o, _ = (Wide(gpu_lib) if wide else gpu_lib).attn_decode(q, *cache, ints(table), ints(lens))
+    codes = [codes_of(c) for c in cache[:2]]
+    want, _, o_abs = ref.attn_decode(f64(q), *codes, f64(cache[2]), f64(cache[3]), table, lens)
+    ez = eps(f64(q), ref.e4m3_table()[codes[0]] * f64(cache[2])[..., None, None], max(lens))
+    check(o, want, ((2.0 ** -16 + 2.1 * ez) * o_abs + U * np.abs(want)) * 1.01 + 1e-30, "o")
