@@ -427,8 +427,9 @@ __global__ __launch_bounds__(kAlone ? 64 * kAloneWaves : kThreads, 2) void attn_
       for (int key = max(unit * kUnit, max(len - args.Q + 1, 0)); key < min((unit + 1) * kUnit, len); ++key) {
         const int id = table[key >> args.shift];
         if (id < 0 || id >= args.num_pages) continue;
-        const float ks = args.k_scale[int64_t(id) * args.HKV + hkv] * c, vs = args.v_scale[int64_t(id) * args.HKV + hkv];
-        const int64_t at = int64_t(id) * args.page_stride + ((int64_t(hkv) << args.shift) + (key & ((1 << args.shift) - 1))) * D;
+        const int64_t scale = int64_t(id) * args.HKV + hkv, inside = key & ((1 << args.shift) - 1);
+        const float ks = args.k_scale[scale] * c, vs = args.v_scale[scale];
+        const int64_t at = int64_t(id) * args.page_stride + ((int64_t(hkv) << args.shift) + inside) * D;
         const u32x4* kp = reinterpret_cast<const u32x4*>(args.k_cache + at + 32 * g4);
         const u32x4* vp = reinterpret_cast<const u32x4*>(args.v_cache + at + 32 * g4);
         float kx[32], vx[32];
