@@ -5,28 +5,27 @@
 //     dQ = scale dS K,   dK = scale dS^T Q,
 // dK and dV summed over the query heads that share a key/value head.
 //
-// attn_dq_kernel gives a wave 32 query rows and walks the keys as the forward
-// does; it also writes, per row, lse in powers of two and delta for the next
-// kernel.  attn_dkv_kernel gives a wave 32 keys and walks the query rows at and
-// after them, head after head of the group, so a key's sums have one order.
-// Where there are too few (key tile, head) units to fill the device, several
-// workgroups share one: each takes an equal part of its query tiles and writes
-// float32 parts that attn_sum_kernel adds in order.  P is formed twice (seven
-// products instead of five): the alternative, adding dQ with atomics, would
-// make the result depend on the order of workgroups.
+// attn_stats_kernel writes, per row, lse in powers of two and delta.  In
+// attn_grads_kernel workgroups of 128 query rows walk the keys as the forward
+// does, for dQ, and workgroups of 128 keys walk the query rows at and after them,
+// head after head of the group, for dK and dV, so every sum has one order.  Where
+// there are too few (key tile, head) units to fill the device, several workgroups
+// share one: each takes an equal part of its query tiles and writes float32 parts
+// that attn_sum_kernel adds in order.  P is formed twice (seven products instead
+// of five): the alternative, adding dQ with atomics, would make the result depend
+// on the order of workgroups.
 //
 // Every product takes its left operand from LDS (rows, or columns through
 // transposing reads) and its right one from registers; P and dS go from the
 // accumulator of one product into the operand of the next without leaving the
 // lane, rounded once to bfloat16.  Sums are float32 throughout.
 //
-// Matrix unit and power bound both walks, as in the forward.  8192 tokens, 16
-// query heads on 4: dQ 374 us (three products, 1100 TFLOP/s), dK and dV 580 us
-// (four, 950; 256 registers, of which 20 live in scratch: with one wave per SIMD
-// and none there it is 5% slower), the parts' sum 22 us (4.8 TB/s), and 275 us of
-// forward before them.  7 packed sequences of up to 2011 tokens, 12 heads on 4:
-// 93, 167, 27 and 69 us: there the longest sequence's first keys are the chain
-// that the others wait for.
+// Matrix unit and power bound the walks, as in the forward.  8192 tokens, 16
+// query heads on 4: 17 us of statistics, 955 of gradients (seven products, 1010
+// TFLOP/s; dK and dV's 256 registers leave some 25 in scratch: with one wave per
+// SIMD and none there they are 5% slower), the parts' sum 22 us (4.8 TB/s).  7
+// packed sequences of up to 2011 tokens, 12 heads on 4: 18, 240 and 21 us: there
+// the longest sequence's first keys are the chain that the others wait for.
 #include "attn_device.h"
 #include "kda_host.h"
 
@@ -49,22 +48,20 @@ struct Params {
   float *lse2, *delta;       // workspace, [B, HQ, T] each
   int parts;                 // workgroups that share a key tile
   float *dk_part, *dv_part;  // workspace, [parts, B, T, HKV, D] each, if parts > 1
+  unsigned key_blocks;       // workgroups of dK and dV
+  bool keys_first;           // in the launch, before dQ's
 };
 
 // ---------------------------------------------------------------- dQ
 
-// kSplit = 2: a second set of four waves takes every other key tile, as in the
-// forward (attn_split says when).
-template <typename Out, int kSplit, bool kBoth>
-__global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p) {
-  constexpr int kHalf = 4 * kTileBytes;    // two buffers of K and V
-  __shared__ __align__(1024) unsigned char all[kSplit * kHalf];
-  const int id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int half = kSplit == 1 ? 0 : id / kWaves, wave = id - half * kWaves;
-  unsigned char* lds = all + half * kHalf;
+// What a workgroup of 128 query rows does.  kStats: it writes lse2 and delta, for
+// all that follow; otherwise it reads them and makes dQ.
+template <typename Out, bool kBoth, bool kStats>
+__device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsigned char* lds) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, h = lane >> 5;
   int slot, hkv, hq;
-  if (!find_head(blockIdx.x, p.slots, p.HQ, p.HKV, slot, hkv, hq)) return;
+  if (!find_head(block, p.slots, p.HQ, p.HKV, slot, hkv, hq)) return;
   const Rows rows = find_rows<false>(p.cu, p.N, p.T, slot, p.slots, BM);
   if (rows.row0 >= rows.len) return;
 
@@ -81,7 +78,7 @@ __global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p)
     }
   }
   const int64_t stat = (int64_t(rows.b) * p.HQ + hq) * p.T + rows.start + r;
-  const float lse2 = p.lse[stat] * kLog2e;
+  const float lse2 = kStats ? p.lse[stat] * kLog2e : p.lse2[stat];
   const float c = p.scale * kLog2e;
   f32x16 dq[4];
 #pragma unroll
@@ -123,7 +120,10 @@ __global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p)
   // make a third of the error of dQ and dK.  There (two tiles of keys at most)
   // delta is made as sum_j P_ij (dO V^T)_ij, to which it is equal.
   float delta = 0.0f;
-  if (rows.row0 == 0) {
+  if constexpr (!kStats) {
+    issue(0, 0);
+    delta = p.delta[stat];
+  } else if (rows.row0 == 0) {
     issue(0, 0);
     for (int t = 0; t < tiles; ++t) {
       __builtin_amdgcn_s_waitcnt(kWaitLoads);
@@ -138,10 +138,7 @@ __global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p)
         for (int e = 0; e < 16; ++e) delta = __builtin_fmaf(s[e], g[e], delta);
       }
     }
-    kda::lds_barrier();
-    if (half < tiles) issue(half, 0);
   } else {
-    if (half < tiles) issue(half, 0);
     const uint16_t* os = p.o + ((rows.first + r) * p.HQ + hq) * D + 8 * h;
 #pragma unroll
     for (int s = 0; s < 8; ++s) {
@@ -150,19 +147,20 @@ __global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p)
       for (int j = 0; j < 8; ++j) delta = __builtin_fmaf(float(x[j]), float(u[s][j]), delta);
     }
   }
-  delta = half_sum(delta);
-  if (r0 + l32 < rows.len && h == 0 && half == 0) {
-    p.lse2[stat] = lse2;
-    p.delta[stat] = delta;
+  if constexpr (kStats) {
+    delta = half_sum(delta);
+    if (r0 + l32 < rows.len && h == 0) {
+      p.lse2[stat] = lse2;
+      p.delta[stat] = delta;
+    }
+    return;
   }
 
-  for (int i = 0; i * kSplit < tiles; ++i) {               // as often for both halves: they share the barrier
-    const int t = i * kSplit + half;
+  for (int t = 0; t < tiles; ++t) {
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     kda::lds_barrier();
-    const unsigned char* kt = lds + (i & 1) * 2 * kTileBytes;
-    if (t + kSplit < tiles) issue(t + kSplit, (i + 1) & 1);
-    if (t >= tiles) continue;
+    const unsigned char* kt = lds + (t & 1) * 2 * kTileBytes;
+    if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const int key0 = t * kTile + 32 * w;
@@ -187,37 +185,26 @@ __global__ __launch_bounds__(kThreads * kSplit, 2) void attn_dq_kernel(Params p)
       }
     }
   }
-  if constexpr (kSplit == 2) {                             // the second half's sums through LDS
-    kda::lds_barrier();
-    float* place = reinterpret_cast<float*>(all) + wave * 64 * 64 + lane;
-    if (half == 1) {
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) place[(16 * d + e) * 64] = dq[d][e];
-    }
-    kda::lds_barrier();
-    if (half == 1) return;
-#pragma unroll
-    for (int d = 0; d < 4; ++d)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) dq[d][e] += place[(16 * d + e) * 64];
-  }
   if (r0 + l32 >= rows.len) return;
   Out* dst = static_cast<Out*>(p.dq) + ((rows.first + r) * p.HQ + hq) * D;
 #pragma unroll
   for (int d = 0; d < 4; ++d) store_row32(dst + 32 * d, dq[d], p.scale, h);
 }
 
+__global__ __launch_bounds__(kThreads, 2) void attn_stats_kernel(Params p) {
+  __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];
+  rows_of_dq<float, false, true>(p, blockIdx.x, lds);
+}
+
 // ---------------------------------------------------------------- dK and dV
 
+constexpr int kBuffer = 2 * kTileBytes + 512;              // Q, dO, lse2, delta
+
 template <typename Out, bool kBoth>
-__global__ __launch_bounds__(kThreads, 2) void attn_dkv_kernel(Params p) {
-  constexpr int kBuffer = 2 * kTileBytes + 512;            // Q, dO, lse2, delta
-  __shared__ __align__(1024) unsigned char lds[2 * kBuffer];
+__device__ __forceinline__ void keys_of_dkv(const Params& p, unsigned id, unsigned char* lds) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, h = lane >> 5;
-  const unsigned id = blockIdx.x, kv_heads = p.HKV;
+  const unsigned kv_heads = p.HKV;
   const int G = p.HQ / p.HKV;
   const int hkv = int(id % kv_heads);
   const int part = int((id / kv_heads) % unsigned(p.parts));
@@ -328,6 +315,20 @@ __global__ __launch_bounds__(kThreads, 2) void attn_dkv_kernel(Params p) {
   }
 }
 
+// All gradients in one launch: what is left open behind the longest walks of the
+// ones fills up with the others.
+template <typename Out, typename Part, bool kBoth>
+__global__ __launch_bounds__(kThreads, 2) void attn_grads_kernel(Params p) {
+  __shared__ __align__(1024) unsigned char lds[2 * kBuffer];
+  const unsigned second = p.keys_first ? p.key_blocks : gridDim.x - p.key_blocks;
+  const bool first = blockIdx.x < second;
+  const unsigned block = first ? blockIdx.x : blockIdx.x - second;
+  if (first == p.keys_first)
+    keys_of_dkv<Part, kBoth>(p, block, lds);
+  else
+    rows_of_dq<Out, kBoth, false>(p, block, lds);
+}
+
 // ---------------------------------------------------------------- the parts' sum
 
 __device__ __forceinline__ void store4(float* dst, f32x4 x) { *reinterpret_cast<f32x4*>(dst) = x; }
@@ -350,15 +351,23 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(Params p) {
   store4(static_cast<Out*>(blockIdx.y ? p.dv : p.dk) + at, sum);
 }
 
-// Workgroups that share a key tile.  A unit is one (key tile, key/value head);
-// two workgroups fit a compute unit, and units of early keys have many times
-// the work of late ones, so the device wants about four per compute unit
-// (measured at 8192 tokens, 16 query and 4 key/value heads: 1, 2, 3, 4, 6 parts
-// take 2.44, 1.65, 1.43, 1.33, 1.35 ms for the training pass).  A part should
-// still walk two query tiles: with one the parts' sum costs more than the walk
-// (2000 tokens, 4 heads: 127 us with two, 148 with one, 150 with eight).
+// Workgroups that share a key tile, and which gradients come first.  A unit is
+// one (key tile, key/value head); two workgroups fit a compute unit, and units of
+// early keys have many times the work of late ones, so the device wants three or
+// four per compute unit.  With sequences of different lengths the first keys of
+// the longest make the longest walk, and come first; with one length both kinds
+// have many long walks, dQ's of a length that no parts shorten, and come first.
+// Training pass in us, in two launches / dK and dV first, 3 per unit / dQ first, 4:
+//   8192 tokens, 16 heads on 4    1300  1325  1294      7 of up to 2011, 12 on 4   360  350  361
+//   4096 tokens, 16 on 2           416   408   395      8 of up to 2000, 16 on 2   423  410  429
+//   1500 tokens, 8 on 1            115    94    89      3 of up to 1000, 64 on 8   289  268  293
+//   700 tokens, 8 on 2              68    55    55      20 of up to 500, 12 on 4   143  128  142
+// A part should still walk two query tiles: with one the parts' sum costs more
+// than the walk (2000 tokens, 4 heads: 127 us with two, 148 with one, 150 with
+// eight).
+bool one_length(int N, bool packed) { return !packed || N == 1; }
 int parts_for(int64_t slots, int T, int N, bool packed, int HQ, int HKV) {
-  const int64_t units = slots * HKV, want = 4 * int64_t(kda::device_cus());
+  const int64_t units = slots * HKV, cus = kda::device_cus(), want = (one_length(N, packed) ? 4 : 3) * cus;
   if (units >= want) return 1;
   const int64_t len = kda::attn_typical(T, N, packed);
   const int64_t walk = (len / kTile / 2 + 1) * (HQ / HKV);
@@ -384,11 +393,12 @@ size_t stat_floats(int64_t B, int64_t T, int64_t HQ) { return size_t((B * T * HQ
 bool both_terms(int64_t rows, int64_t len) { return rows * len <= 1 << 15; }
 
 template <typename Out, bool kBoth>
-void launch_dkv(const Params& p, dim3 grid, hipStream_t stream) {
+void launch_grads(const Params& p, unsigned blocks, hipStream_t stream) {
+  const dim3 grid(p.key_blocks + blocks);
   if (p.parts == 1) {
-    hipLaunchKernelGGL((attn_dkv_kernel<Out, kBoth>), grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((attn_grads_kernel<Out, Out, kBoth>), grid, dim3(kThreads), 0, stream, p);
   } else {
-    hipLaunchKernelGGL((attn_dkv_kernel<float, kBoth>), grid, dim3(kThreads), 0, stream, p);
+    hipLaunchKernelGGL((attn_grads_kernel<Out, float, kBoth>), grid, dim3(kThreads), 0, stream, p);
     const int64_t quads = int64_t(p.B) * p.T * p.HKV * (D / 4);
     hipLaunchKernelGGL(attn_sum_kernel<Out>, dim3(unsigned((quads + 255) / 256), 2), dim3(256), 0, stream, p);
   }
@@ -396,20 +406,12 @@ void launch_dkv(const Params& p, dim3 grid, hipStream_t stream) {
 
 template <typename Out>
 int launch(const Params& p, hipStream_t stream) {
-  const int64_t blocks = head_blocks(p.slots, p.HQ, p.HKV);
-  const bool packed = p.cu != nullptr;
-  const bool both = both_terms(int64_t(p.B) * p.T * p.HQ, kda::attn_typical(p.T, p.N, packed));
-  if (kda::attn_split(blocks, p.T, p.N, packed))
-    hipLaunchKernelGGL((attn_dq_kernel<Out, 2, false>), dim3(unsigned(blocks)), dim3(2 * kThreads), 0, stream, p);
-  else if (both)
-    hipLaunchKernelGGL((attn_dq_kernel<Out, 1, true>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, p);
+  const unsigned blocks = unsigned(head_blocks(p.slots, p.HQ, p.HKV));
+  hipLaunchKernelGGL(attn_stats_kernel, dim3(blocks), dim3(kThreads), 0, stream, p);
+  if (both_terms(int64_t(p.B) * p.T * p.HQ, kda::attn_typical(p.T, p.N, p.cu != nullptr)))
+    launch_grads<Out, true>(p, blocks, stream);
   else
-    hipLaunchKernelGGL((attn_dq_kernel<Out, 1, false>), dim3(unsigned(blocks)), dim3(kThreads), 0, stream, p);
-  const dim3 grid(unsigned(p.slots * p.HKV * p.parts));
-  if (both)
-    launch_dkv<Out, true>(p, grid, stream);
-  else
-    launch_dkv<Out, false>(p, grid, stream);
+    launch_grads<Out, false>(p, blocks, stream);
   return kda::launch_status();
 }
 
@@ -443,14 +445,15 @@ extern "C" int kda_attn_backward(const void* q, const void* k, const void* v, in
   const int64_t slots = slots_for(B, T, seqs);
   const int parts = parts_for(slots, T, N, seqs > 0, HQ, HKV);
   const int64_t quads = int64_t(B) * T * HKV * (D / 4);
-  if (head_blocks(slots, HQ, HKV) > 0x7fffffff || slots * HKV * parts > 0x7fffffff || (quads + 255) / 256 > 0x7fffffff)
+  if (head_blocks(slots, HQ, HKV) > 0x7fffffff || head_blocks(slots, HQ, HKV) + slots * HKV * parts > 0x7fffffff || (quads + 255) / 256 > 0x7fffffff)
     return KDA_ERR_SHAPE;
   float* ws = static_cast<float*>(workspace);
   const size_t stats = stat_floats(B, T, HQ), grads = size_t(parts) * B * T * HKV * D;
   const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                  static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_out), q_stride, k_stride, v_stride,
                  lse, cu_seqlens, N, B, T, HQ, HKV, int(slots), scale, dq, dk, dv,
-                 ws, ws + stats, parts, ws + 2 * stats, ws + 2 * stats + grads};
+                 ws, ws + stats, parts, ws + 2 * stats, ws + 2 * stats + grads,
+                 unsigned(slots * HKV * parts), !one_length(N, seqs > 0)};
   return grad_dtype == KDA_GRAD_FLOAT32 ? launch<float>(p, kda::as_stream(stream))
                                         : launch<uint16_t>(p, kda::as_stream(stream));
 }

@@ -72,16 +72,15 @@ inline int attn_check(const int32_t* cu, int32_t num_seqs, int32_t B, int32_t T,
 
 // Length of a typical sequence of a prompt call.
 inline int64_t attn_typical(int T, int num_seqs, bool packed) { return packed ? T / num_seqs : T; }
-// Whether a row tile's keys are walked by two sets of waves, which halves the
-// chain that the longest walk is but costs a join and, with an odd number of
+// Whether the forward walks a row tile's keys with two sets of waves, which halves
+// the chain that the longest walk is but costs a join and, with an odd number of
 // tiles, a pause.  It pays where one workgroup per compute unit leaves half of
 // the wave slots empty, or where two of them are all there are, so that nothing
 // is left to fill the device behind the longest.  One set against two, us:
-//   one workgroup per unit (8 heads on 2; 400, 600, 1000, 2000 tokens): forward 11.2, 14.8, 21.7, 37.6
-//     and 11.3, 13.8, 18.9, 31.7; training pass 51.1, 64.5, 82.6, 145 and 52.7, 63.3, 77.3, 130
-//   two (2000 x 32 heads, 2500 x 24, 4096 x 16, 8192 x 8): forward 47.5, 55.5, 88.4, 170 and 48.7, 52.2,
-//     79, 143
-//   three (12000 x 8): forward 284 and 303
+//   one workgroup per unit (8 heads on 2; 400, 600, 1000, 2000 tokens): 11.2, 14.8, 21.7, 37.6 and 11.3,
+//     13.8, 18.9, 31.7
+//   two (2000 x 32 heads, 2500 x 24, 4096 x 16, 8192 x 8): 47.5, 55.5, 88.4, 170 and 48.7, 52.2, 79, 143
+//   three (12000 x 8): 284 and 303
 inline bool attn_split(int64_t blocks, int T, int num_seqs, bool packed) {
   const int64_t len = attn_typical(T, num_seqs, packed), cus = device_cus();
   return (blocks <= cus && len >= 512) || (blocks <= 2 * cus && len >= 2048);
