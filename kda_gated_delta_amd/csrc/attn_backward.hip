@@ -21,10 +21,10 @@
 // lane, rounded once to bfloat16.  Sums are float32 throughout.
 //
 // Matrix unit and power bound the walks, as in the forward.  8192 tokens, 16
-// query heads on 4: 17 us of statistics, 955 of gradients (seven products, 1010
+// query heads on 4: 14 us of statistics, 950 of gradients (seven products, 1010
 // TFLOP/s; dK and dV's 256 registers leave some 25 in scratch: with one wave per
 // SIMD and none there they are 5% slower), the parts' sum 22 us (4.8 TB/s).  7
-// packed sequences of up to 2011 tokens, 12 heads on 4: 18, 240 and 21 us: there
+// packed sequences of up to 2011 tokens, 12 heads on 4: 16, 240 and 21 us: there
 // the longest sequence's first keys are the chain that the others wait for.
 #include "attn_device.h"
 #include "kda_host.h"
@@ -62,7 +62,7 @@ __device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsi
   const int l32 = lane & 31, h = lane >> 5;
   int slot, hkv, hq;
   if (!find_head(block, p.slots, p.HQ, p.HKV, slot, hkv, hq)) return;
-  const Rows rows = find_rows<false>(p.cu, p.N, p.T, slot, p.slots, BM);
+  const Rows rows = find_rows<kStats>(p.cu, p.N, p.T, slot, p.slots, BM);   // a sequence's first take longest there
   if (rows.row0 >= rows.len) return;
 
   const int r0 = rows.row0 + wave * 32;
@@ -124,16 +124,16 @@ __device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsi
     issue(0, 0);
     delta = p.delta[stat];
   } else if (rows.row0 == 0) {
-    issue(0, 0);
-    for (int t = 0; t < tiles; ++t) {
+    for (int t = 0; t < tiles; ++t) {                      // one buffer: two tiles at most, and more workgroups
+      if (t > 0) kda::lds_barrier();
+      issue(t, 0);
       __builtin_amdgcn_s_waitcnt(kWaitLoads);
       kda::lds_barrier();
-      if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
       for (int w = 0; w < 2; ++w) {
         const int key0 = t * kTile + 32 * w;
         if (key0 > r0 + 31) break;
         f32x16 s, g;
-        scores(lds + (t & 1) * 2 * kTileBytes, w, key0, s, g);
+        scores(lds, w, key0, s, g);
 #pragma unroll
         for (int e = 0; e < 16; ++e) delta = __builtin_fmaf(s[e], g[e], delta);
       }
@@ -191,8 +191,9 @@ __device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsi
   for (int d = 0; d < 4; ++d) store_row32(dst + 32 * d, dq[d], p.scale, h);
 }
 
-__global__ __launch_bounds__(kThreads, 2) void attn_stats_kernel(Params p) {
-  __shared__ __align__(1024) unsigned char lds[4 * kTileBytes];
+// Memory bounds it (o and dO once); three workgroups to a compute unit.
+__global__ __launch_bounds__(kThreads, 3) void attn_stats_kernel(Params p) {
+  __shared__ __align__(1024) unsigned char lds[2 * kTileBytes];
   rows_of_dq<float, false, true>(p, blockIdx.x, lds);
 }
 
