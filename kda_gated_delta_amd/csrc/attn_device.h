@@ -78,6 +78,9 @@ struct Rows {
   int row0;        // the tile's first row within it; >= len: no such tile
 };
 
+// Offset n, whatever cu holds: differences of two then fit 32 bits.
+__device__ __forceinline__ int offset_of(const int32_t* cu, int n, int T) { return min(max(cu[n], 0), T); }
+
 // Largest n in [0, N) with floor(cu[n] / BM) + n <= slot (0 if none): the
 // whole wave looks at 64 places at once.  cu need not be valid: it is read
 // within its N + 1 entries only.
@@ -87,7 +90,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int T, in
   while (hi - lo > 1) {
     const int step = (hi - lo + 63) / 64;
     const int at = lo + lane * step;
-    const bool ok = at < hi && min(max(cu[at], 0), T) / BM <= slot - at;
+    const bool ok = at < hi && offset_of(cu, at, T) / BM <= slot - at;
     const uint64_t m = __ballot(ok);
     const int k = m ? 63 - __builtin_clzll(m) : 0;
     lo += k * step;
@@ -162,19 +165,16 @@ __device__ __forceinline__ Rows find_rows(const int32_t* cu, int N, int T, int s
   if (N <= 64) {
     const int lane = threadIdx.x & 63;
     int own = 0;
-    if (lane < N) {
-      const int c0 = min(max(cu[lane], 0), T), c1 = min(cu[lane + 1], T);
-      own = max(c1 - c0 + BM - 1, 0) / BM;
-    }
+    if (lane < N) own = max(offset_of(cu, lane + 1, T) - offset_of(cu, lane, T) + BM - 1, 0) / BM;
     n = find_ranked(own, N, T / BM + 1, slot, t);
     if (n >= 0 && kEarly) t = __builtin_amdgcn_readlane(own, n) - 1 - t;
     n = max(n, 0);
   } else {
     const int at = kEarly ? slot : slots - 1 - slot;
     n = find_sequence(cu, N, T, at, BM);
-    t = at - min(max(cu[n], 0), T) / BM - n;
+    t = at - offset_of(cu, n, T) / BM - n;
   }
-  const int c0 = min(max(cu[n], 0), T), c1 = min(cu[n + 1], T);
+  const int c0 = offset_of(cu, n, T), c1 = offset_of(cu, n + 1, T);
   r.b = 0;
   r.first = r.start = c0;
   r.len = max(c1 - c0, 0);
