@@ -337,15 +337,31 @@ __device__ __forceinline__ void store4(uint16_t* dst, f32x4 x) {
   *reinterpret_cast<u32x2*>(dst) = (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
 }
 
+// Whether row t, the same for the whole wave, lies in a sequence: the wave looks
+// at 64 of them at a time.
+__device__ __forceinline__ bool in_sequence(const int32_t* cu, int N, int t) {
+  bool in = false;
+  for (int n = threadIdx.x & 63; n < N; n += 64) in |= t >= cu[n] && t < cu[n + 1];
+  return __any(in);
+}
+
 // Four elements of dK or dV (blockIdx.y) per thread.
 template <typename Out>
 __global__ __launch_bounds__(256) void attn_sum_kernel(Params p) {
   const int64_t size = int64_t(p.B) * p.T * p.HKV * D, at = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (at >= size) return;
   if (p.cu) {                                              // rows outside the sequences are left as they are
-    const int64_t t = at / (int64_t(p.HKV) * D);
-    if (t < p.cu[0] || t >= p.cu[p.N]) return;
+    // From the first offset to the last one every row is passed by some sequence;
+    // other rows lie in one only where offsets decrease.
+    const int row = int(at / (int64_t(p.HKV) * D));
+    bool in = row >= p.cu[0] && row < p.cu[p.N];
+    if (!__all(in)) {                                      // a wave's 256 elements lie in one row or two
+      const int t = __builtin_amdgcn_readfirstlane(row);
+      const bool here = in_sequence(p.cu, p.N, t), next = in_sequence(p.cu, p.N, t + 1);
+      in = row == t ? here : next;
+    }
+    if (!in) return;
   }
+  if (at >= size) return;
   const float* src = (blockIdx.y ? p.dv_part : p.dk_part) + at;
   f32x4 sum = *reinterpret_cast<const f32x4*>(src);
   for (int i = 1; i < p.parts; ++i) sum += *reinterpret_cast<const f32x4*>(src + i * size);

@@ -59,3 +59,14 @@ def test_offsets_outside_the_batch(gpu_lib, cu):
     HQ, HKV = 4, 2
     assert gpu_lib.attn_backward_workspace_size(1, 200, HQ, HKV, len(cu) - 1) == 2 * 200 * HQ * 4   # no parts
     check_all(gpu_lib, 200, HQ, HKV, cu, seed=300)
+
+
+@pytest.mark.parametrize("HQ,HKV", [(8, 1), (8, 2), (12, 3)])
+@pytest.mark.parametrize("cu", [[0, 100, 90], [50, 20, 80], [200, 331, 0, 179, 180, 150], [399, 3, 2, LEAST],
+                                [350, 400] + [300] * 45 + [0, 251]])
+def test_offsets_that_decrease(gpu_lib, cu, HQ, HKV):
+    """A sequence that would end before it starts is empty; the others count wherever they lie, also where several
+    workgroups share a key tile (float32 parts and their sum)."""
+    T = 400
+    assert gpu_lib.attn_backward_workspace_size(1, T, HQ, HKV, len(cu) - 1) > 2 * T * HQ * 4         # parts
+    check_all(gpu_lib, T, HQ, HKV, cu, seed=310)
