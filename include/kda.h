@@ -510,12 +510,12 @@ size_t kda_chunk_backward_workspace_size(int32_t B, int32_t T, int32_t H, int32_
  *     o_i = sum_j exp(z_j - lse_i) v_j.
  *   q           bf16 [B, T, HQ, 128], k, v bf16 [B, T, HKV, 128], at q_stride,
  *               k_stride, v_stride
- *   cu_seqlens, num_seqs   as for kda_chunk_prefill, except that the last
- *               offset may be less than T and the first more than 0: tokens
- *               outside the sequences are neither read nor written.  An offset
- *               is taken as min(max(offset, 0), T), a sequence that would end
- *               before it starts as empty; sequences that overlap give
- *               undefined outputs.
+ *   cu_seqlens, num_seqs   packed sequences [cu[n], cu[n+1]) as for
+ *               kda_chunk_prefill, but in any order and anywhere in the batch:
+ *               tokens outside the sequences are neither read nor written, an
+ *               offset is taken as min(max(offset, 0), T), and a sequence that
+ *               would end before it starts as empty.  Sequences that overlap
+ *               give undefined outputs.
  *   o           bf16 [B, T, HQ, 128], dense
  *   lse         fp32 [B, HQ, T], dense, or NULL
  * A token reaches the outputs of its own sequence from its own row on and no

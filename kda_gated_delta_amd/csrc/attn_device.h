@@ -68,9 +68,9 @@ __device__ __forceinline__ bf16x8 pack8_rest(const float (&x)[8], const bf16x8& 
 
 // A launch covers the rows of every sequence in tiles of BM tokens.  With
 // equal sequences tile and sequence follow from the index.  With packed ones
-// tile t of sequence n has index floor(cu[n] / BM) + n + t: a sequence of L
-// tokens has at most floor(L / BM) + 1 tiles, so indices never meet, and there
-// are at most floor(T / BM) + N of them.
+// they are looked up in the offsets, which may come in any order: sequences that
+// do not overlap have at most floor(T / BM) + N tiles.  No lookup reads past the
+// N + 1 offsets, whatever they hold.
 struct Rows {
   int64_t first;   // the sequence's first token, counted over the whole batch
   int b, start;    // the same as batch row and place in it
@@ -81,22 +81,24 @@ struct Rows {
 // Offset n, whatever cu holds: differences of two then fit 32 bits.
 __device__ __forceinline__ int offset_of(const int32_t* cu, int n, int T) { return min(max(cu[n], 0), T); }
 
-// Largest n in [0, N) with floor(cu[n] / BM) + n <= slot (0 if none): the
-// whole wave looks at 64 places at once.  cu need not be valid: it is read
-// within its N + 1 entries only.
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int N, int T, int slot, int BM) {
-  int lo = 0, hi = N;                         // the answer is in [lo, hi)
+// The sequence that holds row `row` and begins before it, -1 if there is none:
+// the wave looks at 256 sequences at a time.
+__device__ __forceinline__ int find_holder(const int32_t* cu, int N, int row) {
   const int lane = threadIdx.x & 63;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 63) / 64;
-    const int at = lo + lane * step;
-    const bool ok = at < hi && offset_of(cu, at, T) / BM <= slot - at;
-    const uint64_t m = __ballot(ok);
-    const int k = m ? 63 - __builtin_clzll(m) : 0;
-    lo += k * step;
-    hi = min(hi, lo + step);
+  for (int n0 = 0; n0 < N; n0 += 256) {
+    bool in[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = min(n0 + 64 * i + lane, N);
+      in[i] = cu[n] < row && row < cu[min(n + 1, N)];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t m = __ballot(in[i]);
+      if (m) return n0 + 64 * i + __builtin_ctzll(m);
+    }
   }
-  return __builtin_amdgcn_readfirstlane(lo);
+  return -1;
 }
 
 // Tile `rank` of all packed sequences' tiles, those with the largest index first
@@ -148,7 +150,8 @@ __device__ __forceinline__ bool find_head(unsigned id, int slots, int HQ, int HK
 // The rows of workgroup `slot` (of slots) of a launch.  kEarly: the tiles that
 // have most work are a sequence's first (backward's keys), else its last; they
 // come first in the launch, so that the short ones fill the end.  With up to 64
-// packed sequences that holds over all of them, otherwise within each.
+// packed sequences that holds over all of them; with more, they come as the
+// sequences do.
 template <bool kEarly>
 __device__ __forceinline__ Rows find_rows(const int32_t* cu, int N, int T, int slot, int slots, int BM) {
   Rows r;
@@ -170,9 +173,34 @@ __device__ __forceinline__ Rows find_rows(const int32_t* cu, int N, int T, int s
     if (n >= 0 && kEarly) t = __builtin_amdgcn_readlane(own, n) - 1 - t;
     n = max(n, 0);
   } else {
-    const int at = kEarly ? slot : slots - 1 - slot;
-    n = find_sequence(cu, N, T, at, BM);
-    t = at - offset_of(cu, n, T) / BM - n;
+    // N slots for the sequences' first tiles, and floor(T / BM) for the others: of
+    // the rows behind a tile's first up to the next tile's, one is a multiple of
+    // BM.  It leads from slot to tile, however the offsets are ordered, and only
+    // these slots look at all sequences.  Where first tiles have most work the two
+    // kinds are mixed evenly, so that most tiles of a sequence stay near one
+    // another, else the others come first (backward in us, so and with the kinds
+    // apart: 150 sequences of up to 700 tokens, 16 heads on 4, 721 and 752; forward,
+    // so and mixed: 65 of up to 100, 8 on 2, 10.7 and 12.2).
+    bool first;
+    int other;                                           // of the slots for others
+    if constexpr (kEarly) {
+      const uint64_t at = uint64_t(unsigned(slot)) * unsigned(N);
+      n = int(at / unsigned(slots));                     // first tiles before this slot
+      first = at - uint64_t(n) * unsigned(slots) + unsigned(N) >= unsigned(slots);
+      other = slot - n;
+    } else {
+      n = slot - (slots - N);
+      first = n >= 0;
+      other = -1 - n;
+    }
+    if (first) {
+      t = 0;
+    } else {
+      const int row = (other + 1) * BM;
+      n = find_holder(cu, N, row);
+      if (n >= 0) t = (row - offset_of(cu, n, T) + BM - 1) / BM;
+      n = max(n, 0);
+    }
   }
   const int c0 = offset_of(cu, n, T), c1 = offset_of(cu, n + 1, T);
   r.b = 0;

@@ -4,6 +4,8 @@ they start.  Results against the float64 oracle (tolerances as in
 test_gpu_attn_prompt.py); rows outside the sequences stay as they were.
 """
 
+import random
+
 import pytest
 import torch
 
@@ -70,3 +72,35 @@ def test_offsets_that_decrease(gpu_lib, cu, HQ, HKV):
     T = 400
     assert gpu_lib.attn_backward_workspace_size(1, T, HQ, HKV, len(cu) - 1) > 2 * T * HQ * 4         # parts
     check_all(gpu_lib, T, HQ, HKV, cu, seed=310)
+
+
+def mixed(N, seed, lengths=(0, 1, 127, 128, 129, 256, 300, 700), most=6000, front=0):
+    """Offsets of N sequences of these lengths, each among them, those past `most` tokens empty."""
+    rng = random.Random(seed)
+    cu = [front]
+    some = list(lengths) + [rng.choice(lengths) for _ in range(N - len(lengths))]
+    rng.shuffle(some)
+    for n in some:
+        cu.append(cu[-1] + (n if cu[-1] + n <= most else 0))
+    return cu
+
+
+MANY = [  # tokens, heads, offsets, whether several workgroups share a key tile
+    (6100, 4, 1, mixed(65, 1), True),
+    (6100, 2, 2, mixed(65, 2, front=37), False),
+    (6100, 16, 2, mixed(150, 3, front=5), True),
+    (2000, 4, 2, mixed(300, 4, (0, 0, 1, 2, 5, 128, 130), 1990), False),      # more than 256
+    (3000, 4, 1, [2900] * 256 + [3000, 0, 700] + [700] * 10 + [2000], True),
+    (1000, 2, 1, [0, 1000] + [0] * 64, False),
+    (1000, 1, 1, [0] * 70 + [1000], False),
+    (900, 4, 2, [3 * n for n in range(300, -1, -1)], False),                  # nothing but ends before starts
+    (1500, 4, 1, [x for n in range(9, -1, -1) for x in (150 * n, 150 * n + 129 + n)] + [0] * 60, True),
+]
+
+
+@pytest.mark.parametrize("T,HQ,HKV,cu,parts", MANY)
+def test_more_than_64_sequences(gpu_lib, T, HQ, HKV, cu, parts):
+    """Sequences of several row tiles among empty ones, beyond those that one wave ranks, in order and not."""
+    N = len(cu) - 1
+    assert N > 64 and (gpu_lib.attn_backward_workspace_size(1, T, HQ, HKV, N) > 2 * T * HQ * 4 + 12) == parts
+    check_all(gpu_lib, T, HQ, HKV, cu, seed=320 + N)
