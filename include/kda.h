@@ -519,7 +519,8 @@ size_t kda_chunk_backward_workspace_size(int32_t B, int32_t T, int32_t H, int32_
  *   o           bf16 [B, T, HQ, 128], dense
  *   lse         fp32 [B, HQ, T], dense, or NULL
  * A token reaches the outputs of its own sequence from its own row on and no
- * others, also where it holds infinities or NaN.
+ * others, also where it holds infinities or NaN.  A score of -inf is a weight of
+ * zero; a row without any other gives o = 0 and lse = -inf.
  * Sizes: B >= 1, T >= 0 (0 enqueues nothing), 1 <= HQ <= 65535.  o and lse must
  * not alias inputs.  Deterministic.
  */

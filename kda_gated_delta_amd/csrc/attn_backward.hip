@@ -78,7 +78,8 @@ __device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsi
     }
   }
   const int64_t stat = (int64_t(rows.b) * p.HQ + hq) * p.T + rows.start + r;
-  const float lse2 = kStats ? p.lse[stat] * kLog2e : p.lse2[stat];
+  float lse2 = kStats ? p.lse[stat] * kLog2e : p.lse2[stat];
+  if (kStats && lse2 == -INFINITY) lse2 = INFINITY;        // all scores -inf: weights of zero
   const float c = p.scale * kLog2e;
   f32x16 dq[4];
 #pragma unroll

@@ -51,6 +51,10 @@ struct Params {
 // float32 and bfloat16, and most tiles skip the 64 multiplications.
 constexpr float kSlack = 8.0f;
 
+// What weights are taken relative to: a row whose scores so far are all -inf
+// (keys that hold it, or sums that overflow) has no maximum, and weights of zero.
+__device__ __forceinline__ float base(float m) { return m == -INFINITY ? 0.0f : m; }
+
 // Whether any row of a tile's first half, or two, holds an infinity or NaN.
 __device__ __forceinline__ bool any_not_finite(const unsigned char* tile, int halves, int lane) {
   typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -135,13 +139,13 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void attn_prefill_kernel(P
     mx = half_max(mx);
     if (__any((mx - m) * c > kSlack)) {
       const float now = fmaxf(m, mx);
-      const float f = __builtin_amdgcn_exp2f((m - now) * c);
+      const float f = __builtin_amdgcn_exp2f((m - base(now)) * c);
       m = now;
       l *= f;
 #pragma unroll
       for (int d = 0; d < 4; ++d) o[d] *= f;
     }
-    const float b = m * c;
+    const float b = base(m) * c;
     float sum = 0.0f;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -210,7 +214,7 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void attn_prefill_kernel(P
 #pragma unroll
         for (int j = 0; j < 8; ++j) x = __builtin_fmaf(float(q[s][j]), float(y[j]), x);
       }
-      x = __builtin_amdgcn_exp2f(__builtin_fmaf(half_sum(x), c, -m * c));
+      x = __builtin_amdgcn_exp2f(__builtin_fmaf(half_sum(x), c, -base(m) * c));
       if (key > r0 + l32) continue;
 #pragma unroll
       for (int d = 0; d < 4; ++d)
@@ -242,7 +246,7 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void attn_prefill_kernel(P
     kda::lds_barrier();
     if (half == 1) return;
     const float m2 = place[64 * 64], top = fmaxf(m, m2);
-    const float f1 = __builtin_amdgcn_exp2f((m - top) * c), f2 = __builtin_amdgcn_exp2f((m2 - top) * c);
+    const float f1 = __builtin_amdgcn_exp2f((m - base(top)) * c), f2 = __builtin_amdgcn_exp2f((m2 - base(top)) * c);
     total = total * f1 + place[65 * 64] * f2;
     m = top;
 #pragma unroll
@@ -251,7 +255,7 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void attn_prefill_kernel(P
       for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * f1 + place[(16 * d + e) * 64] * f2;
   }
   if (r0 + l32 >= rows.len) return;                       // both lanes of a pair alike
-  const float f = 1.0f / total;
+  const float f = total == 0.0f ? 0.0f : 1.0f / total;
   uint16_t* dst = p.o + ((rows.first + r) * p.HQ + hq) * D;
 #pragma unroll
   for (int d = 0; d < 4; ++d) store_row32(dst + 32 * d, o[d], f, h);
