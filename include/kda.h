@@ -521,8 +521,10 @@ size_t kda_chunk_backward_workspace_size(int32_t B, int32_t T, int32_t H, int32_
  * A token reaches the outputs of its own sequence from its own row on and no
  * others, also where it holds infinities or NaN.  A score of -inf is a weight of
  * zero; a row without any other gives o = 0 and lse = -inf.
- * Sizes: B >= 1, T >= 0 (0 enqueues nothing), 1 <= HQ <= 65535.  o and lse must
- * not alias inputs.  Deterministic.
+ * Sizes: B >= 1, T >= 0 (0 enqueues nothing), 1 <= HQ <= 65535, and fewer than
+ * 2^24 workgroups: HQ for each of the B * ceil(T / 128) row tiles, or of the
+ * T / 128 + num_seqs that packed sequences may have (the backward: HQ + HKV).  o
+ * and lse must not alias inputs.  Deterministic.
  */
 int kda_attn_prefill(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                      int64_t v_stride, const int32_t* cu_seqlens, int32_t num_seqs, int32_t B, int32_t T,
@@ -648,7 +650,7 @@ int kda_attn_cache_store(const void* k, const void* v, int64_t k_stride, int64_t
  * waves depends on all sequences of the call, so the last bits of a row may
  * differ from batch to batch; the same call gives the same bits.
  * Sizes: N >= 0 (0 enqueues nothing), 1 <= Q <= 1024, num_pages >= 1,
- * N * Q * HQ <= 2^26, table_width * page_size <= 2^30.
+ * N * Q * HQ <= 2^26, N * HKV < 2^24, table_width * page_size <= 2^30.
  */
 int kda_attn_decode(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
                     const float* k_scale, const float* v_scale, int32_t page_size, int64_t page_stride,

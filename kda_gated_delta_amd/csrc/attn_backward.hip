@@ -398,6 +398,11 @@ int64_t slots_for(int B, int T, int num_seqs) {
   return num_seqs ? int64_t(T) / BM + num_seqs : int64_t(B) * ((T + BM - 1) / BM);
 }
 
+// Whether a launch takes the workgroups.  (The parts' sum, of few units, has fewer.)
+bool fits(int64_t slots, int parts, int HQ, int HKV) {
+  return head_blocks(slots, HQ, HKV) + slots * HKV * parts <= kda::kMostBlocks;
+}
+
 size_t stat_floats(int64_t B, int64_t T, int64_t HQ) { return size_t((B * T * HQ + 3) / 4 * 4); }
 
 // Whether weights and score gradients are carried as two bfloat16 terms.  One
@@ -439,7 +444,9 @@ extern "C" size_t kda_attn_backward_workspace_size(int32_t B, int32_t T, int32_t
                                                    int32_t num_seqs) {
   if (B < 1 || T < 0 || num_seqs < 0 || (num_seqs && B != 1) || kda::attn_heads(HQ, HKV, Dh) != KDA_OK) return 0;
   if (T == 0) return 0;
-  const int parts = parts_for(slots_for(B, T, num_seqs), T, num_seqs ? num_seqs : B, num_seqs > 0, HQ, HKV);
+  const int64_t slots = slots_for(B, T, num_seqs);
+  const int parts = parts_for(slots, T, num_seqs ? num_seqs : B, num_seqs > 0, HQ, HKV);
+  if (!fits(slots, parts, HQ, HKV)) return 0;
   const size_t sums = parts > 1 ? size_t(parts) * 2 * B * T * HKV * D : 0;
   return (2 * stat_floats(B, T, HQ) + sums) * sizeof(float);
 }
@@ -459,12 +466,10 @@ extern "C" int kda_attn_backward(const void* q, const void* k, const void* v, in
                         static_cast<const void*>(workspace)})
     if (!kda::aligned16(x)) return KDA_ERR_ALIGN;
   const int seqs = cu_seqlens ? num_seqs : 0, N = cu_seqlens ? num_seqs : B;
-  if (workspace_bytes < kda_attn_backward_workspace_size(B, T, HQ, HKV, Dh, seqs)) return KDA_ERR_WORKSPACE;
   const int64_t slots = slots_for(B, T, seqs);
   const int parts = parts_for(slots, T, N, seqs > 0, HQ, HKV);
-  const int64_t quads = int64_t(B) * T * HKV * (D / 4);
-  if (head_blocks(slots, HQ, HKV) > 0x7fffffff || head_blocks(slots, HQ, HKV) + slots * HKV * parts > 0x7fffffff || (quads + 255) / 256 > 0x7fffffff)
-    return KDA_ERR_SHAPE;
+  if (!fits(slots, parts, HQ, HKV)) return KDA_ERR_SHAPE;
+  if (workspace_bytes < kda_attn_backward_workspace_size(B, T, HQ, HKV, Dh, seqs)) return KDA_ERR_WORKSPACE;
   float* ws = static_cast<float*>(workspace);
   const size_t stats = stat_floats(B, T, HQ), grads = size_t(parts) * B * T * HKV * D;
   const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),

@@ -724,6 +724,7 @@ int sizes(int32_t N, int32_t Q, int32_t HQ, int32_t HKV, int32_t Dh) {
   const int e = kda::attn_heads(HQ, HKV, Dh);
   if (e != KDA_OK) return e;
   if (N < 0 || Q < 1 || Q > 1024 || int64_t(N) * HKV * Q * (HQ / HKV) > (1 << 26)) return KDA_ERR_SHAPE;
+  if (int64_t(N) * HKV > kda::kMostBlocks) return KDA_ERR_SHAPE;   // joining workgroups: with more rows there are fewer
   return KDA_OK;
 }
 
@@ -753,7 +754,6 @@ extern "C" int kda_attn_decode(const void* q, int64_t q_stride, const void* k_ca
     if (!kda::aligned16(x)) return KDA_ERR_ALIGN;
   const Plan x = plan_for(N, Q, HQ, HKV);
   if (workspace_bytes < x.bytes) return KDA_ERR_WORKSPACE;
-  if (x.segments * x.tile_rows > 0x7fffffff) return KDA_ERR_SHAPE;
   // Rows of a joining workgroup: one where segments are few and have many parts
   // each, four (a wave each) otherwise, and more where there would be over 4096
   // workgroups: most segments of a large batch are finished by one wave, and a

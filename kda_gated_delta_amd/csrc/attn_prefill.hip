@@ -276,11 +276,11 @@ extern "C" int kda_attn_prefill(const void* q, const void* k, const void* v, int
   for (const void* x : {q, k, v, static_cast<const void*>(o), static_cast<const void*>(lse)})
     if (!kda::aligned16(x)) return KDA_ERR_ALIGN;            // no lse: a null pointer passes
   const int64_t slots = cu_seqlens ? int64_t(T) / BM + num_seqs : int64_t(B) * ((T + BM - 1) / BM);
-  if (head_blocks(slots, HQ, HKV) > 0x7fffffff) return KDA_ERR_SHAPE;
+  const int64_t blocks = head_blocks(slots, HQ, HKV);
+  if (blocks > kda::kMostBlocks) return KDA_ERR_SHAPE;
   const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                  q_stride, k_stride, v_stride, cu_seqlens, cu_seqlens ? num_seqs : B, T, HQ, HKV, int(slots), scale,
                  static_cast<uint16_t*>(o), lse};
-  const int64_t blocks = head_blocks(slots, HQ, HKV);
   if (kda::attn_split(blocks, T, p.N, cu_seqlens != nullptr))
     hipLaunchKernelGGL(attn_prefill_kernel<2>, dim3(unsigned(blocks)), dim3(128 * kWaves), 0,
                        kda::as_stream(stream), p);

@@ -47,6 +47,9 @@ inline int attn_stride(int64_t stride, int32_t heads) {
   if (stride < int64_t(heads) * 128 || stride > (int64_t(1) << 23)) return KDA_ERR_SHAPE;
   return stride % 8 == 0 ? KDA_OK : KDA_ERR_ALIGN;
 }
+// Workgroups (of 256 threads) that a launch takes: the runtime counts its threads
+// in 32 bits.
+constexpr int64_t kMostBlocks = (int64_t(1) << 24) - 1;
 // Pages of 16 to 256 tokens, a power of two; slot numbers (page x page_size +
 // offset) fit int32.
 inline bool attn_page(int32_t page_size) {
