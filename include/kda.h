@@ -500,6 +500,10 @@ size_t kda_chunk_backward_workspace_size(int32_t B, int32_t T, int32_t H, int32_
  *     backward, the scores' gradients) are rounded to bf16 as operands of the
  *     second matrix product -- once, or in small calls to two terms of bf16 --
  *     outputs once when they are stored.
+ *   - the same call gives the same bits.  How the work is cut among workgroups,
+ *     and whether a weight is one term or two, follows the sizes of the whole
+ *     call (and, in decode, all sequences' lengths), so a sequence's last bits may
+ *     differ with what else is in the call.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -616,8 +620,10 @@ int kda_attn_tables(const int32_t* cached_lens, const int32_t* new_lens, int32_t
  * 448 * 2^e >= a: if the first new token stands at offset 0 the scale becomes
  * 2^e (the page is taken over), otherwise max(scale, 2^e), and if that is more
  * than before the codes of the earlier offsets are multiplied by the quotient
- * and rounded again.  New codes are value / scale, rounded to nearest even;
- * infinities and NaN become NaN.  Codes at later offsets are left.
+ * and rounded again.  New codes are value / scale, rounded to nearest even
+ * (under a scale that somebody else put there and that is no power of two,
+ * value * (1 / scale) in float32); infinities and NaN become NaN.  Codes at later
+ * offsets are left.
  * The slots that are stored must differ, and the tokens of one page must stand
  * one after another with successive slots (as kda_attn_tables deals them);
  * otherwise that page's contents are undefined.
@@ -646,9 +652,7 @@ int kda_attn_cache_store(const void* k, const void* v, int64_t k_stride, int64_t
  *               entry do not matter; calls that share one must not overlap
  * What lies in a page behind the sequence's end does not reach the outputs,
  * whatever it is, and a NaN code only the queries that see its token.  The
- * scales of pages that hold tokens are finite.  How a sequence is cut among
- * waves depends on all sequences of the call, so the last bits of a row may
- * differ from batch to batch; the same call gives the same bits.
+ * scales of pages that hold tokens are finite.
  * Sizes: N >= 0 (0 enqueues nothing), 1 <= Q <= 1024, num_pages >= 1,
  * N * Q * HQ <= 2^26, N * HKV < 2^24, table_width * page_size <= 2^30.
  */

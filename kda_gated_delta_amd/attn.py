@@ -125,8 +125,8 @@ def attn_prefill(q, k, v, cu_seqlens=None, scale=None, out=None, lse=None):
     """Causal attention over whole prompts.  q [B,T,HQ,128], k and v
     [B,T,HKV,128] bf16 (tokens may be slices of wider rows); query head h reads
     key/value head h // (HQ // HKV).  cu_seqlens int32 [N+1] (with B == 1):
-    packed sequences; rows outside them are neither read nor written (and hold
-    anything in outputs that are allocated here).  scale
+    packed sequences, in any order; rows outside them are neither read nor
+    written (and hold anything in outputs that are allocated here).  scale
     defaults to 128**-0.5.  Returns (o [B,T,HQ,128] bf16, lse [B,HQ,T] float32,
     the logarithm of each row's sum of exponentials)."""
     dev, B, T, HQ, HKV, (qs, ks, vs), N = _prompt(q, k, v, cu_seqlens)
@@ -266,7 +266,9 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, scal
     [N,Q,HQ,128] bf16 (tokens may be slices of wider rows), the cache as
     attn_cache_store leaves it, page_table int32 [N,W] (rows may be slices of
     wider ones), kv_lens int32 [N]: tokens in the cache, the new ones included.
-    Query i stands at position kv_len - Q + i and sees the tokens up to there.
+    How the work is laid out follows W and the cache's size, which the host knows,
+    not the lengths: a table no wider than the longest sequence needs is fastest
+    for short ones.  Query i stands at position kv_len - Q + i and sees the tokens up to there.
     Returns (o [N,Q,HQ,128] bf16, lse [N,Q,HQ] float32)."""
     dev = _first(q, "q", _BF16, 4)
     N, Q, HQ, _ = q.shape

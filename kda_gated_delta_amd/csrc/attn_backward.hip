@@ -18,12 +18,13 @@
 // Every product takes its left operand from LDS (rows, or columns through
 // transposing reads) and its right one from registers; P and dS go from the
 // accumulator of one product into the operand of the next without leaving the
-// lane, rounded once to bfloat16.  Sums are float32 throughout.
+// lane, rounded once to bfloat16 (in small calls to two terms of it, see
+// both_terms).  Sums are float32 throughout.
 //
 // Matrix unit and power bound the walks, as in the forward.  8192 tokens, 16
 // query heads on 4: 14 us of statistics, 950 of gradients (seven products, 1010
-// TFLOP/s; dK and dV's 256 registers leave some 25 in scratch: with one wave per
-// SIMD and none there they are 5% slower), the parts' sum 22 us (4.8 TB/s).  7
+// TFLOP/s; dK and dV's 256 registers leave 24 in scratch: with one wave per SIMD
+// and none there they are 5% slower), the parts' sum 22 us (151 MB, 6.9 TB/s).  7
 // packed sequences of up to 2011 tokens, 12 heads on 4: 16, 240 and 21 us: there
 // the longest sequence's first keys are the chain that the others wait for.
 #include "attn_device.h"

@@ -696,12 +696,13 @@ Plan plan_for(int64_t N, int64_t Q, int HQ, int HKV) {
 // can hold, not the lengths.  A wave then walks up to an eighth of a segment, at
 // 2.6 us per unit where little else runs; the line balances that, for a second
 // launch and the parts' way through memory.  32 heads on 8, lengths up to the
-// stated one, line and alone in us:
-//   1 sequence: 1000 tokens 15.4 and 13.0, 2000 15.4 and 15.6, 4000 15.2 and 25.8
-//   8: 1500 tokens 15.1 and 13.6, 2000 16.2 and 16.3, 4000 17.9 and 26.8
-//   24: 1000 tokens 16.0 and 12.8, 2000 20.8 and 16.9, 4000 33.2 and 32.6
-//   64: 250 tokens 15.8 and 12.8, 1000 26.3 and 21.6, 4000 70 and 64
-//   128: 60 tokens 15.1 and 18.3 (a workgroup fills a compute unit, and four wait for each)
+// stated one and tables as wide as the longest, line and alone in us:
+//   1 sequence: 1000 tokens 12.5 and 10.8, 2000 12.9 and 16.0, 4096 13.0 and 26.7
+//   16: 1000 tokens 15.1 and 11.5, 1536 15.8 and 14.5, 3000 20.7 and 22.3, 4096 24.2 and 27.9
+//   24: 1000 tokens 15.5 and 11.9, 2000 20.6 and 17.6, 3000 24.5 and 22.9, 4096 29.9 and 31.6
+//   64: 250 tokens 15.9 and 13.2, 1000 23.8 and 22.1, 2000 37.8 and 39.7, 4096 60.0 and 60.7
+//   128: 60 tokens 12.6 and 19.2 (a workgroup fills a compute unit, and four wait for each)
+// From 2000 tokens on the two are near each other; either may be faster by a tenth.
 bool alone(int64_t segments, int64_t tokens) {
   const int64_t cus = kda::device_cus();
   if (segments > 2 * cus) return false;
