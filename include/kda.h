@@ -496,6 +496,8 @@ size_t kda_chunk_backward_workspace_size(int32_t B, int32_t T, int32_t H, int32_
  *     within a row.  Rows of a batch follow one another at that stride, so
  *     q, k and v may be slices of one projection's rows.
  *   - scale multiplies every score: positive and below 1e30 (128^-1/2 is usual).
+ *   - int32 tables, lengths and offsets, and the cache's scales, may begin at any
+ *     multiple of 4 bytes (kda_attn_tables' outputs can be one allocation).
  *   - softmax statistics and all sums are float32; the weights (and, in the
  *     backward, the scores' gradients) are rounded to bf16 as operands of the
  *     second matrix product -- once, or in small calls to two terms of bf16 --
