@@ -6,7 +6,8 @@
  * and "Mathematical definition") and, for single-token decode, on the page
  * "flashinfer.kda_decode.packed_kda_decode" (section "Parameters"), plus
  * the prefill's optional backward (kda_chunk_backward) and, for the layers of
- * a hybrid model that attend over all tokens, attention (kda_attn_*).
+ * a hybrid model that attend over all tokens, attention (kda_attn_*) and latent
+ * attention (kda_latent_*).
  *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers owned by the caller.  The
@@ -671,6 +672,173 @@ int kda_attn_decode(const void* q, int64_t q_stride, const void* k_cache, const 
  * head, 32 rows).
  */
 size_t kda_attn_decode_workspace_size(int32_t N, int32_t Q, int32_t HQ, int32_t HKV, int32_t Dh);
+
+/* ------------------------------------------------------------------------
+ * Latent attention: full-attention layers whose keys and values all come from
+ * one vector of 512 per token, the latent c, and a key part s of 64 that all
+ * heads share.  Head h has the key [W_k,h c, s] (128 + 64) and the value W_v,h c
+ * (128).  A prompt and a training step run the expanded form, over keys and
+ * values that the caller's projection made of the latents; a serving step runs
+ * the absorbed form, over the latents themselves, with queries [W_k,h^T q_h, q_s]
+ * (512 + 64), so that a token's cache is 644 bytes for all heads together.
+ * The conventions are those of full attention above, and:
+ *   - k and v have a stride from token to token (128 to 2^23, the shared part's
+ *     from 64) and one from head to head (0 to 2^40), in elements, multiples of 8:
+ *     they may be the halves of one projection's rows.
+ *   - the usual scale is 192^-1/2, of both forms.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * kda_latent_prefill -- causal attention in the expanded form.
+ *
+ * A sequence has Tq queries, its last tokens, and Tk keys.  For query i and each
+ * head, over the keys j <= i + Tk - Tq:
+ *     z_j = scale (q_i[0:128] . k_j + q_i[128:192] . k_shared_j),
+ *     lse_i = log sum_j exp(z_j),  o_i = sum_j exp(z_j - lse_i) v_j.
+ *   q           bf16 [B, T, H, 192] at q_stride, heads compact
+ *   k, v        bf16 [B, T_kv, H, 128] at their strides
+ *   k_shared    bf16 [B, T_kv, 64] at s_stride
+ *   cu_seqlens, cu_seqlens_kv, num_seqs   packed sequences, as for
+ *               kda_attn_prefill: sequence n has queries [cu[n], cu[n+1]) and keys
+ *               [cu_kv[n], cu_kv[n+1]).  Both or neither are NULL; with NULL Tq = T
+ *               and Tk = T_kv.  The two may be the same array.
+ *   o           bf16 [B, T, H, 128], dense
+ *   lse         fp32 [B, H, T], dense, or NULL
+ * Queries without keys (the first Tq - Tk, where there are more queries) give
+ * o = 0 and lse = -inf.  As for kda_attn_prefill: a token reaches its own
+ * sequence's outputs from its own row on and no others, also where it holds
+ * infinities or NaN; a score of -inf is a weight of zero; rows outside the
+ * sequences are neither read nor written.
+ * Sizes: B >= 1, T, T_kv >= 0, 1 <= H <= 65535, fewer than 2^24 workgroups: H for
+ * each of the B * ceil(T / 128) row tiles, or of the T / 128 + num_seqs that packed
+ * sequences may have.  o and lse must not alias inputs.  Deterministic.
+ */
+int kda_latent_prefill(const void* q, const void* k, const void* k_shared, const void* v, int64_t q_stride,
+                       int64_t k_stride, int64_t k_head, int64_t s_stride, int64_t v_stride, int64_t v_head,
+                       const int32_t* cu_seqlens, const int32_t* cu_seqlens_kv, int32_t num_seqs, int32_t B,
+                       int32_t T, int32_t T_kv, int32_t H, float scale, void* o, float* lse, void* stream);
+
+/*
+ * kda_latent_backward -- gradients of kda_latent_prefill: of sum(o * d_out) with
+ * respect to q, k, k_shared and v.
+ *
+ *   q .. scale  as for kda_latent_prefill, and its outputs o and lse
+ *   d_out       bf16 [B, T, H, 128], dense
+ *   dq          [B, T, H, 192], dense
+ *   d_kv        [B, T_kv, H, 256], dense: a head's dk (128) and dv (128), the
+ *               layout of the projection's rows that both come from
+ *   dk_shared   [B, T_kv, 64], dense, summed over all heads
+ *               all three bf16 (KDA_GRAD_INPUT_DTYPE) or float32
+ *               (KDA_GRAD_FLOAT32).  Tokens outside the sequences are left as they
+ *               were; keys that no query sees have gradients of zero.
+ *   workspace   at least kda_latent_backward_workspace_size(...) bytes; contents on
+ *               entry do not matter; calls that share one must not overlap
+ * What is not finite reaches what it does in kda_attn_backward.  Sizes as for
+ * kda_latent_prefill, workgroups counted for queries and keys together.
+ * Deterministic: no atomics, one order of every sum.
+ */
+int kda_latent_backward(const void* q, const void* k, const void* k_shared, const void* v, int64_t q_stride,
+                        int64_t k_stride, int64_t k_head, int64_t s_stride, int64_t v_stride, int64_t v_head,
+                        const void* o, const float* lse, const void* d_out, const int32_t* cu_seqlens,
+                        const int32_t* cu_seqlens_kv, int32_t num_seqs, int32_t B, int32_t T, int32_t T_kv, int32_t H,
+                        float scale, void* dq, void* d_kv, void* dk_shared, int32_t grad_dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/*
+ * kda_latent_backward_workspace_size -- bytes of workspace kda_latent_backward
+ * needs on the current device (num_seqs: 0 when cu_seqlens is NULL); 0 for sizes it
+ * rejects and where there is nothing to do.  8 bytes per query and head, and 256
+ * per key and head; where there are too few key tiles to fill the device the latter
+ * for each of up to 16 parts, and 1 KB per key, head and part.
+ */
+size_t kda_latent_backward_workspace_size(int32_t B, int32_t T, int32_t T_kv, int32_t H, int32_t num_seqs);
+
+/*
+ * The paged cache of latents, addressed as the cache above (kda_attn_tables deals
+ * its slots too).  Page p holds page_size successive tokens of one sequence, in
+ * three arrays, each with a stride from page to page in elements:
+ *   c_cache     e4m3 [page_size][512]        at c_page      (a multiple of 16)
+ *   c_scale     uint8 [page_size][4]         at scale_page  (a multiple of 4)
+ *   k_cache     bf16 [page_size][64]         at k_page      (a multiple of 8)
+ * Value i of a latent is code i * 2^(scale[i / 128] - 127), the shared key part is
+ * as it was stored.  page_size: 16, 32, 64, 128 or 256 (others
+ * KDA_ERR_UNSUPPORTED); strides of at least a page and at most 2^32 (k_page 2^31);
+ * num_pages * page_size < 2^31.  c_cache and k_cache begin at multiples of 16
+ * bytes, c_scale of 4.
+ */
+
+/*
+ * kda_latent_cache_store -- new tokens into the paged cache.
+ *
+ *   c           bf16 [T, 512] at c_stride, k_shared bf16 [T, 64] at s_stride
+ *   slots       int32 [T]  each token's slot; outside [0, num_pages * page_size)
+ *               -- -1 among them -- it is not stored
+ * Per token and 128 values of the latent, with a the largest finite magnitude among
+ * them and 2^e the least power of two, -64 <= e <= 119, with 448 * 2^e >= a: the
+ * scale is e + 127 and a code is value / 2^e, rounded to nearest even; infinities
+ * and NaN become NaN.  (Values above 448 * 2^119, which only the last 3% of
+ * bfloat16's largest binade are, become that.)  Other tokens are left as they are.
+ * The slots that are stored must differ.  T < 2^29.
+ */
+int kda_latent_cache_store(const void* c, const void* k_shared, int64_t c_stride, int64_t s_stride,
+                           const int32_t* slots, int32_t T, void* c_cache, void* c_scale, void* k_cache,
+                           int32_t page_size, int64_t c_page, int64_t scale_page, int64_t k_page, int32_t num_pages,
+                           void* stream);
+
+/*
+ * kda_latent_cache_load -- cached tokens back to bf16, the sequences packed: what
+ * the next part of a prompt expands into keys and values.
+ *
+ *   page_table  int32, row n at page_table + n * table_stride, table_width entries
+ *   cu_seqlens  int32 [num_seqs + 1]  row t of the outputs, cu[n] <= t < cu[n+1], is
+ *               token t - cu[n] of sequence n.  Offsets do not decrease (where they
+ *               do, the rows of sequences that they cross are undefined).
+ *   c           bf16 [num_tokens, 512], dense
+ *   k_shared    bf16 [num_tokens, 64], dense
+ * Values are exact.  A token without a page (its entry outside [0, num_pages), or
+ * past table_width) gives zeros; rows outside the sequences are left as they were.
+ * Sizes: num_seqs, num_pages, table_width >= 1, 0 <= num_tokens < 2^29 (0 enqueues
+ * nothing).
+ */
+int kda_latent_cache_load(const void* c_cache, const void* c_scale, const void* k_cache, int32_t page_size,
+                          int64_t c_page, int64_t scale_page, int64_t k_page, int32_t num_pages,
+                          const int32_t* page_table, int64_t table_stride, int32_t table_width,
+                          const int32_t* cu_seqlens, int32_t num_seqs, int32_t num_tokens, void* c, void* k_shared,
+                          void* stream);
+
+/*
+ * kda_latent_decode -- attention of the last Q tokens of every sequence over the
+ * paged cache (which holds them already), in the absorbed form.
+ *
+ * Query i of sequence n stands at position kv_lens[n] - Q + i; for each head, over
+ * the tokens j up to there:
+ *     z_j = scale (q[0:512] . c_j + q[512:576] . k_shared_j),
+ *     o = sum_j softmax(z)_j c_j,  lse = log sum_j exp(z_j).
+ *   q           bf16 [N, Q, H, 576] at q_stride from token to token (H * 576 to 2^31)
+ *   page_table, kv_lens   as for kda_attn_decode
+ *   o           bf16 [N, Q, H, 512], dense
+ *   lse         fp32 [N, Q, H], dense, or NULL
+ *   workspace   at least kda_latent_decode_workspace_size(...) bytes; contents on
+ *               entry do not matter; calls that share one must not overlap
+ * As for kda_attn_decode: missing pages hold no tokens, a query without tokens gives
+ * o = 0 and lse = -inf, what lies behind a sequence's end does not reach the outputs,
+ * and what is not finite only the queries that see its token.  Scales of tokens are
+ * 1 to 246.
+ * Sizes: N >= 0 (0 enqueues nothing), 1 <= Q <= 1024, num_pages >= 1,
+ * N * Q * H <= 2^24, table_width * page_size <= 2^30.
+ */
+int kda_latent_decode(const void* q, int64_t q_stride, const void* c_cache, const void* c_scale, const void* k_cache,
+                      int32_t page_size, int64_t c_page, int64_t scale_page, int64_t k_page, int32_t num_pages,
+                      const int32_t* page_table, int64_t table_stride, int32_t table_width, const int32_t* kv_lens,
+                      int32_t N, int32_t Q, int32_t H, float scale, void* o, float* lse, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * kda_latent_decode_workspace_size -- bytes of workspace kda_latent_decode needs on
+ * the current device; 0 for sizes it rejects.  About 1 MB for each 32 rows (Q * H,
+ * up to 128) and 8 compute units, and 8 bytes per (sequence, 128 rows).
+ */
+size_t kda_latent_decode_workspace_size(int32_t N, int32_t Q, int32_t H);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,13 @@ and for the full-attention layers of a hybrid stack (attn.py):
                                                   -> (cu_seqlens, slots, kv_lens, next_head)
   attn_cache_store(k, v, k_cache, v_cache, k_scale, v_scale, slots)
   attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens) -> (o, lse)
+and where those layers are latent attention (latent.py):
+  latent_prefill(q, k, k_shared, v, cu_seqlens=None, cu_seqlens_kv=None)  -> (o, lse)
+  latent_backward(q, k, k_shared, v, o, lse, d_out, ...)  -> (dq, dk, dk_shared, dv)
+  latent_cache_store(c, k_shared, c_cache, c_scale, k_cache, slots)
+  latent_cache_load(c_cache, c_scale, k_cache, page_table, cu_seqlens, num_tokens)
+                                                  -> (c, k_shared)
+  latent_decode(q, c_cache, c_scale, k_cache, page_table, kv_lens)        -> (o, lse)
 """
 
 import ctypes
@@ -42,7 +49,9 @@ EXPORTS = ("kda_status_string", "kda_build_id", "kda_qk_l2norm", "kda_chunk_pref
            "kda_chunk_prefill_workspace_size", "kda_prefill_overlap_wait_limit", "kda_decode", "kda_packed_decode",
            "kda_state_to_pool", "kda_chunk_backward", "kda_chunk_backward_workspace_size", "kda_attn_prefill",
            "kda_attn_backward", "kda_attn_backward_workspace_size", "kda_attn_tables", "kda_attn_cache_store",
-           "kda_attn_decode", "kda_attn_decode_workspace_size")
+           "kda_attn_decode", "kda_attn_decode_workspace_size", "kda_latent_prefill", "kda_latent_backward",
+           "kda_latent_backward_workspace_size", "kda_latent_cache_store", "kda_latent_cache_load",
+           "kda_latent_decode", "kda_latent_decode_workspace_size")
 
 _lib = None
 
@@ -121,6 +130,24 @@ def load():
                                     _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _size, _vp]
     lib.kda_attn_decode_workspace_size.restype = _size
     lib.kda_attn_decode_workspace_size.argtypes = [_i32, _i32, _i32, _i32, _i32]
+    prompt = [_vp] * 4 + [_i64] * 6
+    lib.kda_latent_prefill.restype = ctypes.c_int
+    lib.kda_latent_prefill.argtypes = prompt + [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp]
+    lib.kda_latent_backward.restype = ctypes.c_int
+    lib.kda_latent_backward.argtypes = prompt + [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32,
+                                                 _vp, _vp, _vp, _i32, _vp, _size, _vp]
+    lib.kda_latent_backward_workspace_size.restype = _size
+    lib.kda_latent_backward_workspace_size.argtypes = [_i32, _i32, _i32, _i32, _i32]
+    cache = [_vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32]
+    lib.kda_latent_cache_store.restype = ctypes.c_int
+    lib.kda_latent_cache_store.argtypes = [_vp, _vp, _i64, _i64, _vp, _i32, *cache, _vp]
+    lib.kda_latent_cache_load.restype = ctypes.c_int
+    lib.kda_latent_cache_load.argtypes = [*cache, _vp, _i64, _i32, _vp, _i32, _i32, _vp, _vp, _vp]
+    lib.kda_latent_decode.restype = ctypes.c_int
+    lib.kda_latent_decode.argtypes = [_vp, _i64, *cache, _vp, _i64, _i32, _vp, _i32, _i32, _i32, _f32, _vp, _vp,
+                                      _vp, _size, _vp]
+    lib.kda_latent_decode_workspace_size.restype = _size
+    lib.kda_latent_decode_workspace_size.argtypes = [_i32, _i32, _i32]
     _lib = lib
     return lib
 
@@ -479,3 +506,5 @@ def packed_decode(mixed_qkv, raw_gate, raw_beta, A_log, dt_bias, state_pool, sta
 
 from .attn import (attn_backward, attn_backward_workspace_size, attn_cache_store, attn_decode,  # noqa: E402,F401
                    attn_decode_workspace_size, attn_prefill, attn_tables)
+from .latent import (latent_backward, latent_backward_workspace_size, latent_cache_load,  # noqa: E402,F401
+                     latent_cache_store, latent_decode, latent_decode_workspace_size, latent_prefill)

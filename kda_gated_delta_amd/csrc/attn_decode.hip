@@ -37,18 +37,20 @@
 // heads on 2: 68 MB in 22.5 us and 10 of joining.  There, and the more for one
 // sequence of 1000 tokens (10.7 us in one launch), the chain lengths -> table ->
 // scales and codes -> products is what it takes, not the bytes.
-#include "attn_device.h"
+#include "attn_line.h"
 #include "kda_host.h"
 
 namespace {
 
 using namespace kda::attn;
+using kda::line::Piece;
+using kda::line::length;
+using kda::line::units_of;
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kAloneWaves = 8;               // of a workgroup that takes a segment alone
 constexpr int kUnit = 64;                    // tokens
-constexpr float kSlack = 8.0f;               // see attn_prefill.hip: rescale only when the maximum grew this much
 
 struct Params {
   const uint16_t* q;
@@ -68,80 +70,6 @@ struct Params {
   float* parts;                              // [waves + segments][tile_rows][D + 4]: output, maximum, sum
   int *owner, *last_owner;                   // [segments]: first and last wave of those cut, -1 for the others
 };
-
-// ---------------------------------------------------------------- who does what
-
-template <typename P>
-__device__ __forceinline__ int length(P& p, int n) { return min(max(p.lens[n], 0), p.width << p.shift); }
-// An empty sequence has one unit too: somebody writes its zeros.
-__device__ __forceinline__ int units_of(int len) { return max((len + kUnit - 1) / kUnit, 1); }
-
-// A lane's value for the whole wave, in scalar registers.
-__device__ __forceinline__ int64_t lane_value(int64_t x, int lane) {
-  const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(uint64_t(x)), lane);
-  const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(uint64_t(x) >> 32), lane);
-  return int64_t(uint64_t(hi) << 32 | lo);
-}
-
-// Where a wave's piece of the line begins.
-struct Piece {
-  int w;             // the wave's place in the line
-  int64_t from, to;  // its units
-  int64_t lo, hi;    // its workgroup's units, if all its waves have some; else empty
-  int n, len;        // the sequence that holds the first, and its length
-  int64_t before;    // units of the sequences before it
-};
-
-// The line has U = per x (units of all sequences) units, per = heads x row
-// tiles; place w of W = min(waves, U) takes floor(U w / W) .. floor(U (w + 1) / W) - 1.
-// A 64-way search: each lane sums a stretch of sequences, the wave adds up and
-// picks the stretch that holds the unit, down to one sequence.
-__device__ __forceinline__ Piece find_piece(const Params& p, int wave, int per) {
-  const int lane = threadIdx.x & 63;
-  Piece x{};
-  int lo = 0, hi = p.N;
-  bool top = true;
-  do {
-    const int step = (hi - lo + 63) / 64;
-    const int a = min(lo + lane * step, hi), b = min(a + step, hi);
-    int64_t own = 0;
-    int len = 0;
-#pragma unroll 8
-    for (int n = a; n < b; ++n) len = length(p, n), own += units_of(len);
-    own *= per;
-    int64_t end = own;                       // inclusive sum over the lanes
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int64_t y = __shfl_up(end, d, 64);
-      if (lane >= d) end += y;
-    }
-    if (top) {
-      const int64_t total = lane_value(end, 63), waves = min(total, int64_t(p.waves));
-      // floor(total i / waves) without a long division for each i
-      const unsigned parts = unsigned(waves);
-      const int64_t each = total <= 0x7fffffff ? int64_t(unsigned(total) / parts) : total / waves;
-      const unsigned left = unsigned(total - each * waves);
-      auto cut = [&](int i) { return each * i + int64_t(left * unsigned(i) / parts); };
-      x.w = int(blockIdx.x) * kWaves + wave;
-      if (x.w >= waves) return x;            // nothing for this wave
-      if (x.w - wave + kWaves <= waves) {
-        x.lo = cut(x.w - wave);
-        x.hi = cut(x.w - wave + kWaves);
-      }
-      x.from = cut(x.w);
-      x.to = cut(x.w + 1);
-      top = false;
-    }
-    const uint64_t upto = __ballot(x.before + end <= x.from);   // lanes whose sequences all end before it
-    const int k = min(int(__builtin_popcountll(upto)), (hi - lo + step - 1) / step - 1);
-    x.before += lane_value(end - own, k);
-    x.len = __builtin_amdgcn_readlane(len, k);     // in the last round a stretch is one sequence
-    lo += k * step;
-    hi = min(lo + step, hi);
-  } while (hi - lo > 1);
-  x.n = lo;
-  return x;
-}
 
 // ---------------------------------------------------------------- codes to operands
 
@@ -179,15 +107,15 @@ __global__ __launch_bounds__(kAlone ? 64 * kAloneWaves : kThreads, 2) void attn_
     n = int(blockIdx.x / unsigned(per));
     seg = int(blockIdx.x - unsigned(n) * unsigned(per));
     len = length(p, n);
-    units = units_of(len);
+    units = units_of<kUnit>(len);
     first = units * wave / kGroup;
   } else {
-    const Piece piece = find_piece(p, wave, per);
+    const Piece piece = kda::line::find_piece<kUnit, kWaves>(p, wave, per);
     w = piece.w;
     left = piece.to - piece.from;
     n = piece.n;
     len = piece.len;
-    units = units_of(len);
+    units = units_of<kUnit>(len);
     const int64_t inside = piece.from - piece.before;
     seg = int(inside <= 0x7fffffff ? int64_t(unsigned(inside) / unsigned(units)) : inside / units);
     first = int(inside - int64_t(seg) * units);
@@ -539,7 +467,7 @@ __global__ __launch_bounds__(kAlone ? 64 * kAloneWaves : kThreads, 2) void attn_
     first = 0;
     if (++seg == per) {
       seg = 0;
-      if (++n < args.N) len = length(args, n), units = units_of(len);
+      if (++n < args.N) len = length(args, n), units = units_of<kUnit>(len);
     }
   }
 }

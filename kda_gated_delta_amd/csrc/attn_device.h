@@ -64,6 +64,17 @@ __device__ __forceinline__ bf16x8 pack8_rest(const float (&x)[8], const bf16x8& 
   return pack8(rest);
 }
 
+// ---------------------------------------------------------------- running softmax
+
+// How far (in powers of two) a row's maximum may grow before its sum and
+// output are brought to the new one: weights stay below 2^8, far inside
+// float32 and bfloat16, and most tiles skip the 64 multiplications.
+constexpr float kSlack = 8.0f;
+
+// What weights are taken relative to: a row whose scores so far are all -inf
+// (keys that hold it, or sums that overflow) has no maximum, and weights of zero.
+__device__ __forceinline__ float base(float m) { return m == -INFINITY ? 0.0f : m; }
+
 // ---------------------------------------------------------------- packed sequences
 
 // A launch covers the rows of every sequence in tiles of BM tokens.  With
@@ -76,6 +87,7 @@ struct Rows {
   int b, start;    // the same as batch row and place in it
   int len;         // its tokens
   int row0;        // the tile's first row within it; >= len: no such tile
+  int n;           // the sequence
 };
 
 // Offset n, whatever cu holds: differences of two then fit 32 bits.
@@ -157,7 +169,7 @@ __device__ __forceinline__ Rows find_rows(const int32_t* cu, int N, int T, int s
   Rows r;
   if (!cu) {
     const int tiles = slots / unsigned(N), t = int(slot / unsigned(N));
-    r.b = slot % unsigned(N);
+    r.b = r.n = slot % unsigned(N);
     r.start = 0;
     r.first = int64_t(r.b) * T;
     r.len = T;
@@ -204,6 +216,7 @@ __device__ __forceinline__ Rows find_rows(const int32_t* cu, int N, int T, int s
   }
   const int c0 = offset_of(cu, n, T), c1 = offset_of(cu, n + 1, T);
   r.b = 0;
+  r.n = n;
   r.first = r.start = c0;
   r.len = max(c1 - c0, 0);
   r.row0 = t < 0 || t > r.len / BM ? r.len : t * BM;
@@ -281,6 +294,19 @@ __device__ __forceinline__ bf16x8 read_columns(const unsigned char* tile, int r,
   typedef short s16x8 __attribute__((ext_vector_type(8)));
   const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   return __builtin_bit_cast(bf16x8, v);
+}
+
+// Whether any row of a tile's first half, or two, holds an infinity or NaN.
+__device__ __forceinline__ bool any_not_finite(const unsigned char* tile, int halves, int lane) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 top = {0, 0};
+#pragma unroll 8
+  for (int i = 0; i < 8 * halves; ++i) {
+    const u32x4 x = *reinterpret_cast<const u32x4*>(tile + i * 1024 + lane * 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[j] & 0x7fff7fffu));
+  }
+  return __any(top[0] >= 0x7f80 || top[1] >= 0x7f80);
 }
 
 // Row stores of a transposed accumulator (columns = rows of the output): the

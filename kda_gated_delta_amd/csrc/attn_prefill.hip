@@ -46,28 +46,6 @@ struct Params {
   float* lse;
 };
 
-// How far (in powers of two) a row's maximum may grow before its sum and
-// output are brought to the new one: weights stay below 2^8, far inside
-// float32 and bfloat16, and most tiles skip the 64 multiplications.
-constexpr float kSlack = 8.0f;
-
-// What weights are taken relative to: a row whose scores so far are all -inf
-// (keys that hold it, or sums that overflow) has no maximum, and weights of zero.
-__device__ __forceinline__ float base(float m) { return m == -INFINITY ? 0.0f : m; }
-
-// Whether any row of a tile's first half, or two, holds an infinity or NaN.
-__device__ __forceinline__ bool any_not_finite(const unsigned char* tile, int halves, int lane) {
-  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
-  u16x2 top = {0, 0};
-#pragma unroll 8
-  for (int i = 0; i < 8 * halves; ++i) {
-    const u32x4 x = *reinterpret_cast<const u32x4*>(tile + i * 1024 + lane * 16);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, x[j] & 0x7fff7fffu));
-  }
-  return __any(top[0] >= 0x7f80 || top[1] >= 0x7f80);
-}
-
 // kSplit = 2: a second set of four waves takes every other key tile of the same
 // rows, and the two halves of a row are joined at the end (attn_split says when):
 // the walk over the keys is a chain, and two waves per SIMD halve it.

@@ -89,4 +89,48 @@ inline bool attn_split(int64_t blocks, int T, int num_seqs, bool packed) {
   return (blocks <= cus && len >= 512) || (blocks <= 2 * cus && len >= 2048);
 }
 
+// Sizes shared by the latent-attention entry points.  Keys and values are read
+// through a token's and a head's stride (heads may be slices of one projection's
+// rows, or the outer axis); strides keep every row 16-byte aligned and a 64-row
+// tile's offsets within 31 bits.
+struct LatentLayout {
+  int64_t q_stride, k_stride, k_head, s_stride, v_stride, v_head;
+};
+inline int latent_stride(int64_t stride, int64_t least) {
+  if (stride < least || stride > (int64_t(1) << 23)) return KDA_ERR_SHAPE;
+  return stride % 8 == 0 ? KDA_OK : KDA_ERR_ALIGN;
+}
+inline int latent_head(int64_t stride) {
+  if (stride < 0 || stride > (int64_t(1) << 40)) return KDA_ERR_SHAPE;
+  return stride % 8 == 0 ? KDA_OK : KDA_ERR_ALIGN;
+}
+inline int latent_check(const LatentLayout& x, const int32_t* cu, const int32_t* cu_kv, int32_t num_seqs, int32_t B,
+                        int32_t T, int32_t T_kv, int32_t H, float scale) {
+  if (B < 1 || T < 0 || T_kv < 0 || (!cu) != (!cu_kv) || (cu && (B != 1 || num_seqs < 1))) return KDA_ERR_SHAPE;
+  if (H < 1 || H > 65535) return KDA_ERR_SHAPE;
+  int e = attn_scale(scale);
+  if (e == KDA_OK) e = latent_stride(x.q_stride, int64_t(H) * 192);
+  if (e == KDA_OK) e = latent_stride(x.k_stride, 128);
+  if (e == KDA_OK) e = latent_stride(x.v_stride, 128);
+  if (e == KDA_OK) e = latent_stride(x.s_stride, 64);
+  if (e == KDA_OK) e = latent_head(x.k_head);
+  if (e == KDA_OK) e = latent_head(x.v_head);
+  return e;
+}
+// The latent cache: pages as the attention cache's, each of its three parts with a
+// page stride of its own (in elements), of which a row keeps its alignment.
+struct LatentCache {
+  int32_t page_size, num_pages;
+  int64_t c_stride, scale_stride, s_stride;
+};
+inline int latent_cache(const LatentCache& x) {
+  if (!attn_page(x.page_size)) return KDA_ERR_UNSUPPORTED;
+  if (x.num_pages < 0 || int64_t(x.num_pages) * x.page_size > 0x7fffffff) return KDA_ERR_SHAPE;
+  if (x.c_stride < int64_t(x.page_size) * 512 || x.c_stride > (int64_t(1) << 32)) return KDA_ERR_SHAPE;
+  if (x.scale_stride < int64_t(x.page_size) * 4 || x.scale_stride > (int64_t(1) << 32)) return KDA_ERR_SHAPE;
+  if (x.s_stride < int64_t(x.page_size) * 64 || x.s_stride > (int64_t(1) << 31)) return KDA_ERR_SHAPE;
+  return x.c_stride % 16 == 0 && x.scale_stride % 4 == 0 && x.s_stride % 8 == 0 ? KDA_OK : KDA_ERR_ALIGN;
+}
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 }  // namespace kda

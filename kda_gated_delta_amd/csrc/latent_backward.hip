@@ -1,0 +1,509 @@
+// Gradients of latent attention's expanded form (export kda_latent_backward).
+//
+// With k_j = [kn_j s_j] (192 wide), P_ij = exp(scale q_i . k_j - lse_i) for
+// j <= i + Tk - Tq, delta_i = do_i . o_i, per head:
+//     dV = P^T dO,   dS = P o (dO V^T - delta),
+//     dQ = scale dS K,   [dKn dS_shared] = scale dS^T Q,
+// the shared part's summed over all heads.
+//
+// The walks are attn_backward.hip's: statistics first (lse in powers of two and
+// delta), then in one launch workgroups of 128 query rows, which walk the keys for
+// dQ, and workgroups of 128 keys, which walk the query rows for dK and dV.  Every
+// head has keys of its own, so a walk belongs to one head; only the shared part's
+// gradient crosses heads.  Its terms are written in float32 per head and added in
+// order by latent_sum_kernel, as the parts of a key tile that several workgroups
+// share are.
+#include "kda_host.h"
+#include "latent_device.h"
+
+namespace {
+
+using namespace kda::latent;
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int BM = 32 * kWaves;
+
+struct Params {
+  const uint16_t *q, *k, *v, *s, *o, *d_out;
+  int64_t q_stride, k_stride, v_stride, s_stride, k_head, v_head;
+  const float* lse;
+  const int32_t *cu, *cu_kv;
+  int N, B, T, K, H, slots, key_slots;
+  float scale;
+  void *dq, *dkv, *ds;       // dkv: [B, K, H, 256], a head's dK and dV
+  float *lse2, *delta;       // workspace, [B, H, T] each
+  int parts;                 // workgroups that share a key tile
+  float* dkv_part;           // workspace, [parts, B, K, H, 256], if parts > 1
+  float* ds_part;            // workspace, [H, parts, B, K, 64]
+  unsigned key_blocks;       // workgroups of dK and dV
+  bool keys_first;           // in the launch, before dQ's
+};
+
+// ---------------------------------------------------------------- dQ
+
+constexpr int kKeyBuffer = 2 * kTileBytes + kThinBytes;    // K, V, the shared part
+
+// What a workgroup of 128 query rows does.  kStats: it writes lse2 and delta, for
+// all that follow; otherwise it reads them and makes dQ.
+template <typename Out, bool kBoth, bool kStats>
+__device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsigned char* lds) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l32 = lane & 31, h = lane >> 5;
+  const int slot = int(block / unsigned(p.H)), head = int(block % unsigned(p.H));
+  const Rows rows = find_rows<kStats>(p.cu, p.N, p.T, slot, p.slots, BM);   // a sequence's first take longest there
+  if (rows.row0 >= rows.len) return;
+  const Keys keys = find_keys(p.cu_kv, p.K, rows.n, rows.len);
+
+  const int r0 = rows.row0 + wave * 32;
+  const int r = min(r0 + l32, rows.len - 1);
+  bf16x8 q[12], u[8];                                      // rows of Q and dO as B operands
+  {
+    const uint16_t* qs = p.q + (rows.first + r) * p.q_stride + head * DQ + 8 * h;
+    const uint16_t* us = p.d_out + ((rows.first + r) * p.H + head) * D + 8 * h;
+#pragma unroll
+    for (int s = 0; s < 12; ++s) q[s] = *reinterpret_cast<const bf16x8*>(qs + 16 * s);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) u[s] = *reinterpret_cast<const bf16x8*>(us + 16 * s);
+  }
+  const int64_t stat = (int64_t(rows.b) * p.H + head) * p.T + rows.start + r;
+  float lse2 = kStats ? p.lse[stat] * kLog2e : p.lse2[stat];
+  if (kStats && lse2 == -INFINITY) lse2 = INFINITY;        // all scores -inf, or no keys: weights of zero
+  const float c = p.scale * kLog2e;
+  f32x16 dq[6];
+#pragma unroll
+  for (int d = 0; d < 6; ++d) dq[d] = (f32x16)(0.0f);
+
+  const int see0 = r0 + keys.shift;                        // the last key that the wave's first row sees
+  const int seen = min(rows.row0 + BM, rows.len) + keys.shift;
+  const int tiles = max(seen + kTile - 1, 0) / kTile;
+  TileLoad<kWaves> kload, vload;
+  ThinLoad<kWaves> sload;
+  kload.init(wave, lane, p.k_stride);
+  vload.init(wave, lane, p.v_stride);
+  sload.init(wave, lane, p.s_stride);
+  const uint16_t* kb = p.k + keys.first * p.k_stride + head * p.k_head;
+  const uint16_t* vb = p.v + keys.first * p.v_stride + head * p.v_head;
+  const uint16_t* sb = p.s + keys.first * p.s_stride;
+  auto issue = [&](int t, int at_buf) {
+    unsigned char* buf = lds + at_buf * kKeyBuffer;
+    const int64_t at = int64_t(t) * kTile;
+    kload.issue(kb + at * p.k_stride, p.k_stride, keys.len - int(at), buf, wave);
+    vload.issue(vb + at * p.v_stride, p.v_stride, keys.len - int(at), buf + kTileBytes, wave);
+    sload.issue(sb + at * p.s_stride, p.s_stride, keys.len - int(at), buf + 2 * kTileBytes, wave);
+  };
+  // P^T and (dO V^T)^T (rows = keys) of 32 keys from key0; P is zero after the diagonal.
+  auto scores = [&](const unsigned char* kt, int w, int key0, f32x16& s, f32x16& g) {
+    s = g = (f32x16)(0.0f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = mfma32(read_rows(kt, 32 * w, l32, h, k), q[k], s);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s = mfma32(rows_of<2 * S>(kt + 2 * kTileBytes, 32 * w, l32, h, k), q[8 + k], s);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g = mfma32(read_rows(kt + kTileBytes, 32 * w, l32, h, k), u[k], g);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -lse2));
+    if (key0 + 31 > see0) {
+      const int last = see0 + l32 - key0;
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (8 * (e >> 2) + 4 * h + (e & 3) > last) s[e] = g[e] = 0.0f;
+    }
+  };
+
+  // delta.  The rounding of o to bfloat16 enters it, and with it every score's
+  // gradient of the row (see attn_backward.hip).  Of rows that see few keys (two
+  // tiles at most) it is made as sum_j P_ij (dO V^T)_ij, to which it is equal.
+  float delta = 0.0f;
+  if constexpr (!kStats) {
+    if (tiles > 0) issue(0, 0);
+    delta = p.delta[stat];
+  } else if (tiles <= 2) {
+    for (int t = 0; t < tiles; ++t) {                      // one buffer, and more workgroups
+      if (t > 0) kda::lds_barrier();
+      issue(t, 0);
+      __builtin_amdgcn_s_waitcnt(kWaitLoads);
+      kda::lds_barrier();
+      for (int w = 0; w < 2; ++w) {
+        const int key0 = t * kTile + 32 * w;
+        if (key0 > see0 + 31) break;
+        f32x16 s, g;
+        scores(lds, w, key0, s, g);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) delta = __builtin_fmaf(s[e], g[e], delta);
+      }
+    }
+  } else {
+    const uint16_t* os = p.o + ((rows.first + r) * p.H + head) * D + 8 * h;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const bf16x8 x = *reinterpret_cast<const bf16x8*>(os + 16 * s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) delta = __builtin_fmaf(float(x[j]), float(u[s][j]), delta);
+    }
+  }
+  if constexpr (kStats) {
+    delta = half_sum(delta);
+    if (r0 + l32 < rows.len && h == 0) {
+      p.lse2[stat] = lse2;
+      p.delta[stat] = delta;
+    }
+    return;
+  }
+
+  for (int t = 0; t < tiles; ++t) {
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    kda::lds_barrier();
+    const unsigned char* kt = lds + (t & 1) * kKeyBuffer;
+    const unsigned char* st = kt + 2 * kTileBytes;
+    if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int key0 = t * kTile + 32 * w;
+      if (key0 > see0 + 31) continue;
+      f32x16 s, g;
+      scores(kt, w, key0, s, g);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] *= g[e] - delta;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = s[8 * k + j];
+        const bf16x8 b = pack8(x);
+        bf16x8 rest;
+        if constexpr (kBoth) rest = pack8_rest(x, b);
+#pragma unroll
+        for (int d = 0; d < 6; ++d) {
+          const bf16x8 a = d < 4 ? read_columns(kt, 32 * w, k, 32 * d, lane)
+                                 : columns_of<2 * S>(st, 32 * w, k, 32 * (d - 4), lane);
+          dq[d] = mfma32(a, b, dq[d]);
+          if constexpr (kBoth) dq[d] = mfma32(a, rest, dq[d]);
+        }
+      }
+    }
+  }
+  if (r0 + l32 >= rows.len) return;
+  Out* dst = static_cast<Out*>(p.dq) + ((rows.first + r) * p.H + head) * DQ;
+#pragma unroll
+  for (int d = 0; d < 6; ++d) store_row32(dst + 32 * d, dq[d], p.scale, h);
+}
+
+__global__ __launch_bounds__(kThreads, 3) void latent_stats_kernel(Params p) {
+  __shared__ __align__(1024) unsigned char lds[kKeyBuffer];
+  rows_of_dq<float, false, true>(p, blockIdx.x, lds);
+}
+
+// ---------------------------------------------------------------- dK and dV
+
+constexpr int kRowBuffer = kTileBytes + kThinBytes + kTileBytes + 512;     // Q (128 and 64 wide), dO, lse2, delta
+
+template <typename Out, bool kBoth>
+__device__ __forceinline__ void keys_of_dkv(const Params& p, unsigned id, unsigned char* lds) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l32 = lane & 31, h = lane >> 5;
+  const unsigned heads = p.H;
+  const int head = int(id % heads);
+  const int part = int((id / heads) % unsigned(p.parts));
+  const Rows keys = find_rows<true>(p.cu_kv, p.N, p.K, int(id / (heads * p.parts)), p.key_slots, BM);
+  if (keys.row0 >= keys.len) return;
+  const Keys rows = find_keys(p.cu, p.T, keys.n, 0);       // the sequence's query rows
+  const int shift = keys.len - rows.len;                   // key j is seen from row j - shift on
+
+  const int k0 = keys.row0 + wave * 32;                    // this wave's first key
+  const int key = min(k0 + l32, keys.len - 1);
+  bf16x8 kk[12], vv[8];                                    // rows of [K s] and V as B operands
+  {
+    const uint16_t* ks = p.k + (keys.first + key) * p.k_stride + head * p.k_head + 8 * h;
+    const uint16_t* ss = p.s + (keys.first + key) * p.s_stride + 8 * h;
+    const uint16_t* vs = p.v + (keys.first + key) * p.v_stride + head * p.v_head + 8 * h;
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      kk[s] = *reinterpret_cast<const bf16x8*>(ks + 16 * s);
+      vv[s] = *reinterpret_cast<const bf16x8*>(vs + 16 * s);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) kk[8 + s] = *reinterpret_cast<const bf16x8*>(ss + 16 * s);
+  }
+  const float c = p.scale * kLog2e;
+  f32x16 dk[6], dv[4];
+#pragma unroll
+  for (int d = 0; d < 6; ++d) dk[d] = (f32x16)(0.0f);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) dv[d] = (f32x16)(0.0f);
+
+  // Query tiles from the one that holds the first row that sees the first key.
+  const int t0 = max(keys.row0 - shift, 0) / kTile, walk = max((rows.len + kTile - 1) / kTile - t0, 0);
+  const int begin = t0 + int(int64_t(walk) * part / p.parts), end = t0 + int(int64_t(walk) * (part + 1) / p.parts);
+  TileLoad<kWaves> qload, uload;
+  ThinLoad<kWaves> q2load;
+  const int64_t u_stride = int64_t(p.H) * D;
+  qload.init(wave, lane, p.q_stride);
+  q2load.init(wave, lane, p.q_stride);
+  uload.init(wave, lane, u_stride);
+  const uint16_t* qb = p.q + rows.first * p.q_stride + head * DQ;
+  const uint16_t* ub = p.d_out + rows.first * u_stride + head * D;
+  const int64_t b = p.cu ? 0 : keys.n, start = rows.first - b * p.T;
+  const int64_t stat0 = (b * p.H + head) * p.T + start;
+  auto issue = [&](int t, unsigned char* buf) {
+    const int row = t * kTile;
+    const int64_t at = row;
+    qload.issue(qb + at * p.q_stride, p.q_stride, rows.len - row, buf, wave);
+    q2load.issue(qb + at * p.q_stride + D, p.q_stride, rows.len - row, buf + kTileBytes, wave);
+    uload.issue(ub + at * u_stride, u_stride, rows.len - row, buf + kTileBytes + kThinBytes, wave);
+    if (wave == 0) load_floats(p.lse2 + stat0 + at, rows.len - row, buf + 2 * kTileBytes + kThinBytes, lane);
+    if (wave == 1) load_floats(p.delta + stat0 + at, rows.len - row, buf + 2 * kTileBytes + kThinBytes + 256, lane);
+  };
+  if (begin < end) issue(begin, lds);
+
+  for (int t = begin; t < end; ++t) {
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    kda::lds_barrier();
+    const unsigned char* qt = lds + ((t - begin) & 1) * kRowBuffer;
+    const unsigned char *q2t = qt + kTileBytes, *ut = q2t + kThinBytes;
+    const float* stats = reinterpret_cast<const float*>(ut + kTileBytes);
+    if (t + 1 < end) issue(t + 1, lds + ((t + 1 - begin) & 1) * kRowBuffer);
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+      const int row0 = t * kTile + 32 * w;
+      if (row0 + 31 < k0 - shift) continue;                // none of the rows sees this wave's keys
+      f32x16 s = (f32x16)(0.0f), g = (f32x16)(0.0f);       // S and dO V^T, rows = query rows
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s = mfma32(read_rows(qt, 32 * w, l32, h, k), kk[k], s);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s = mfma32(rows_of<2 * S>(q2t, 32 * w, l32, h, k), kk[8 + k], s);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) g = mfma32(read_rows(ut, 32 * w, l32, h, k), vv[k], g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(stats + 32 * w + 8 * i + 4 * h);
+        const f32x4 d = *reinterpret_cast<const f32x4*>(stats + 64 + 32 * w + 8 * i + 4 * h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * i + j], c, -a[j]));
+          s[4 * i + j] = x;
+          g[4 * i + j] = x * (g[4 * i + j] - d[j]);
+        }
+      }
+      if (row0 + shift < k0 + 31 || row0 + 32 > rows.len) { // pairs behind the diagonal, rows behind the end
+        const int first = k0 + l32 - shift - row0, behind = rows.len - row0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int row = 8 * (e >> 2) + 4 * h + (e & 3);
+          if (row < first || row >= behind) s[e] = g[e] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float x[8], y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = s[8 * k + j], y[j] = g[8 * k + j];
+        const bf16x8 pb = pack8(x), gb = pack8(y);
+        bf16x8 pr, gr;
+        if constexpr (kBoth) pr = pack8_rest(x, pb), gr = pack8_rest(y, gb);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const bf16x8 a = read_columns(ut, 32 * w, k, 32 * d, lane);
+          dv[d] = mfma32(a, pb, dv[d]);
+          if constexpr (kBoth) dv[d] = mfma32(a, pr, dv[d]);
+        }
+#pragma unroll
+        for (int d = 0; d < 6; ++d) {
+          const bf16x8 a = d < 4 ? read_columns(qt, 32 * w, k, 32 * d, lane)
+                                 : columns_of<2 * S>(q2t, 32 * w, k, 32 * (d - 4), lane);
+          dk[d] = mfma32(a, gb, dk[d]);
+          if constexpr (kBoth) dk[d] = mfma32(a, gr, dk[d]);
+        }
+      }
+    }
+  }
+  if (k0 + l32 >= keys.len) return;
+  // (with parts, Out is float and dkv is the parts' buffer)
+  const int64_t all = int64_t(p.B) * p.K, at = keys.first + key;
+  Out* dst = static_cast<Out*>(p.parts > 1 ? p.dkv_part : p.dkv) + ((part * all + at) * p.H + head) * (2 * D);
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    store_row32(dst + 32 * d, dk[d], p.scale, h);
+    store_row32(dst + D + 32 * d, dv[d], 1.0f, h);
+  }
+  float* ds = p.ds_part + ((int64_t(head) * p.parts + part) * all + at) * S;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) store_row32(ds + 32 * d, dk[4 + d], p.scale, h);
+}
+
+// All gradients in one launch: what is left open behind the longest walks of the
+// ones fills up with the others.
+template <typename Out, typename Part, bool kBoth>
+__global__ __launch_bounds__(kThreads, 1) void latent_grads_kernel(Params p) {
+  __shared__ __align__(1024) unsigned char lds[2 * kRowBuffer];
+  const unsigned second = p.keys_first ? p.key_blocks : gridDim.x - p.key_blocks;
+  const bool first = blockIdx.x < second;
+  const unsigned block = first ? blockIdx.x : blockIdx.x - second;
+  if (first == p.keys_first)
+    keys_of_dkv<Part, kBoth>(p, block, lds);
+  else
+    rows_of_dq<Out, kBoth, false>(p, block, lds);
+}
+
+// ---------------------------------------------------------------- the parts' sums
+
+__device__ __forceinline__ void store4(float* dst, f32x4 x) { *reinterpret_cast<f32x4*>(dst) = x; }
+__device__ __forceinline__ void store4(uint16_t* dst, f32x4 x) {
+  *reinterpret_cast<u32x2*>(dst) = (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
+}
+
+// Whether row t, the same for the whole wave, lies in a sequence: the wave looks
+// at 64 of them at a time.
+__device__ __forceinline__ bool in_sequence(const int32_t* cu, int N, int t) {
+  bool in = false;
+  for (int n = threadIdx.x & 63; n < N; n += 64) in |= t >= cu[n] && t < cu[n + 1];
+  return __any(in);
+}
+
+// `parts` arrays of rows of WIDTH floats added up in order, four elements per
+// thread.  Rows outside the sequences are left as they are.
+template <typename Out>
+__device__ __forceinline__ void sum_parts(const float* src, int64_t rows, int64_t width, int parts, Out* dst,
+                                          const int32_t* cu, int N, int64_t at) {
+  const int64_t size = rows * width;
+  if (cu) {
+    // From the first offset to the last one every row is passed by some sequence;
+    // other rows lie in one only where offsets decrease.
+    const int row = int(min(at, size - 1) / width);
+    bool in = row >= cu[0] && row < cu[N];
+    uint64_t open = __ballot(!in);
+    while (open) {                                         // a wave's 256 elements lie in four rows at most
+      const int t = __builtin_amdgcn_readlane(row, __builtin_ctzll(open));
+      if (in_sequence(cu, N, t)) in |= row == t;
+      open &= ~__ballot(row == t);
+    }
+    if (!in) return;
+  }
+  if (at >= size) return;
+  f32x4 sum = *reinterpret_cast<const f32x4*>(src + at);
+#pragma unroll 4
+  for (int i = 1; i < parts; ++i) sum += *reinterpret_cast<const f32x4*>(src + i * size + at);
+  store4(dst + at, sum);
+}
+
+template <typename Out>
+__global__ __launch_bounds__(256) void latent_sum_kernel(Params p, unsigned shared_blocks) {
+  const int64_t rows = int64_t(p.B) * p.K;
+  if (blockIdx.x < shared_blocks)
+    sum_parts<Out>(p.ds_part, rows, S, p.H * p.parts, static_cast<Out*>(p.ds), p.cu_kv, p.N,
+                       (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4);
+  else
+    sum_parts<Out>(p.dkv_part, rows, int64_t(p.H) * 2 * D, p.parts, static_cast<Out*>(p.dkv), p.cu_kv, p.N,
+                       (int64_t(blockIdx.x - shared_blocks) * 256 + threadIdx.x) * 4);
+}
+
+// Workgroups that share a key tile, and which gradients come first: see
+// attn_backward.hip.
+bool one_length(int N, bool packed) { return !packed || N == 1; }
+int parts_for(int64_t key_slots, int T, int N, bool packed, int H) {
+  const int64_t units = key_slots * H, cus = kda::device_cus(), want = (one_length(N, packed) ? 4 : 3) * cus;
+  if (units >= want) return 1;
+  const int64_t walk = kda::attn_typical(T, N, packed) / kTile / 2 + 1;
+  const int64_t most = walk / 2 < 1 ? 1 : (walk / 2 > 16 ? 16 : walk / 2);
+  const int64_t parts = (want + units - 1) / units;
+  return int(parts < most ? parts : most);
+}
+
+int64_t slots_for(int B, int T, int num_seqs) {
+  return num_seqs ? int64_t(T) / BM + num_seqs : int64_t(B) * ((T + BM - 1) / BM);
+}
+
+size_t stat_floats(int64_t B, int64_t T, int64_t H) { return size_t((B * T * H + 3) / 4 * 4); }
+
+// Whether weights and score gradients are carried as two bfloat16 terms: see
+// attn_backward.hip.
+bool both_terms(int64_t rows, int64_t len) { return rows * len <= 1 << 15; }
+
+struct Plan {
+  int64_t slots, key_slots;
+  int parts;
+  size_t stats, dkv, ds;     // floats
+  int64_t sums, shared;      // workgroups of the sums
+  bool fits;
+  size_t bytes() const { return (2 * stats + dkv + ds) * sizeof(float); }
+};
+Plan plan_for(int64_t B, int T, int T_kv, int H, int num_seqs) {
+  Plan x;
+  x.slots = slots_for(int(B), T, num_seqs);
+  x.key_slots = slots_for(int(B), T_kv, num_seqs);
+  x.parts = parts_for(x.key_slots, T, num_seqs ? num_seqs : int(B), num_seqs > 0, H);
+  x.stats = stat_floats(B, T, H);
+  const int64_t rows = B * T_kv;
+  x.dkv = x.parts > 1 ? size_t(x.parts) * rows * H * 2 * D : 0;
+  x.ds = size_t(x.parts) * H * rows * S;
+  x.shared = (rows * S / 4 + 255) / 256;
+  x.sums = x.shared + (x.parts > 1 ? (rows * H * 2 * D / 4 + 255) / 256 : 0);
+  x.fits = (x.slots + x.key_slots * x.parts) * H <= kda::kMostBlocks && x.sums <= kda::kMostBlocks;
+  return x;
+}
+
+template <typename Out, bool kBoth>
+void launch_grads(const Params& p, unsigned blocks, hipStream_t stream) {
+  const dim3 grid(p.key_blocks + blocks);
+  if (p.parts == 1)
+    hipLaunchKernelGGL((latent_grads_kernel<Out, Out, kBoth>), grid, dim3(kThreads), 0, stream, p);
+  else
+    hipLaunchKernelGGL((latent_grads_kernel<Out, float, kBoth>), grid, dim3(kThreads), 0, stream, p);
+}
+
+template <typename Out>
+int launch(const Params& p, const Plan& x, hipStream_t stream) {
+  const unsigned blocks = unsigned(x.slots * p.H);
+  if (blocks) hipLaunchKernelGGL(latent_stats_kernel, dim3(blocks), dim3(kThreads), 0, stream, p);
+  if (both_terms(int64_t(p.B) * p.T * p.H, kda::attn_typical(p.K, p.N, p.cu != nullptr)))
+    launch_grads<Out, true>(p, blocks, stream);
+  else
+    launch_grads<Out, false>(p, blocks, stream);
+  if (x.sums)
+    hipLaunchKernelGGL(latent_sum_kernel<Out>, dim3(unsigned(x.sums)), dim3(256), 0, stream, p, unsigned(x.shared));
+  return kda::launch_status();
+}
+
+}  // namespace
+
+extern "C" size_t kda_latent_backward_workspace_size(int32_t B, int32_t T, int32_t T_kv, int32_t H, int32_t num_seqs) {
+  if (B < 1 || T < 0 || T_kv < 0 || H < 1 || H > 65535 || num_seqs < 0 || (num_seqs && B != 1)) return 0;
+  if (T == 0 && T_kv == 0) return 0;
+  const Plan x = plan_for(B, T, T_kv, H, num_seqs);
+  return x.fits ? x.bytes() : 0;
+}
+
+extern "C" int kda_latent_backward(const void* q, const void* k, const void* k_shared, const void* v, int64_t q_stride,
+                                   int64_t k_stride, int64_t k_head, int64_t s_stride, int64_t v_stride,
+                                   int64_t v_head, const void* o, const float* lse, const void* d_out,
+                                   const int32_t* cu_seqlens, const int32_t* cu_seqlens_kv, int32_t num_seqs,
+                                   int32_t B, int32_t T, int32_t T_kv, int32_t H, float scale, void* dq, void* d_kv,
+                                   void* dk_shared, int32_t grad_dtype, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  const kda::LatentLayout l{q_stride, k_stride, k_head, s_stride, v_stride, v_head};
+  const int e = kda::latent_check(l, cu_seqlens, cu_seqlens_kv, num_seqs, B, T, T_kv, H, scale);
+  if (e != KDA_OK) return e;
+  if (grad_dtype != KDA_GRAD_FLOAT32 && grad_dtype != KDA_GRAD_INPUT_DTYPE) return KDA_ERR_UNSUPPORTED;
+  if (T == 0 && T_kv == 0) return KDA_OK;
+  if ((T && (!q || !o || !lse || !d_out || !dq)) || (T_kv && (!k || !k_shared || !v || !d_kv || !dk_shared)) ||
+      !workspace)
+    return KDA_ERR_NULL;
+  for (const void* y : {q, k, k_shared, v, o, static_cast<const void*>(lse), d_out, static_cast<const void*>(dq),
+                        static_cast<const void*>(d_kv), static_cast<const void*>(dk_shared),
+                        static_cast<const void*>(workspace)})
+    if (!kda::aligned16(y)) return KDA_ERR_ALIGN;
+  const int seqs = cu_seqlens ? num_seqs : 0;
+  const Plan x = plan_for(B, T, T_kv, H, seqs);
+  if (!x.fits) return KDA_ERR_SHAPE;
+  if (workspace_bytes < x.bytes()) return KDA_ERR_WORKSPACE;
+  float* ws = static_cast<float*>(workspace);
+  const int N = cu_seqlens ? num_seqs : B;
+  const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+                 static_cast<const uint16_t*>(k_shared), static_cast<const uint16_t*>(o),
+                 static_cast<const uint16_t*>(d_out), q_stride, k_stride, v_stride, s_stride, k_head, v_head, lse,
+                 cu_seqlens, cu_seqlens_kv, N, B, T, T_kv, H, int(x.slots), int(x.key_slots), scale, dq, d_kv,
+                 dk_shared, ws, ws + x.stats, x.parts, ws + 2 * x.stats, ws + 2 * x.stats + x.dkv,
+                 unsigned(x.key_slots * H * x.parts), !one_length(N, seqs > 0)};
+  return grad_dtype == KDA_GRAD_FLOAT32 ? launch<float>(p, x, kda::as_stream(stream))
+                                        : launch<uint16_t>(p, x, kda::as_stream(stream));
+}
