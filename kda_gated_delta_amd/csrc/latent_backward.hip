@@ -402,7 +402,7 @@ __global__ __launch_bounds__(256) void latent_sum_kernel(Params p, unsigned shar
 bool one_length(int N, bool packed) { return !packed || N == 1; }
 int parts_for(int64_t key_slots, int T, int N, bool packed, int H) {
   const int64_t units = key_slots * H, cus = kda::device_cus(), want = (one_length(N, packed) ? 4 : 3) * cus;
-  if (units >= want) return 1;
+  if (units == 0 || units >= want) return 1;
   const int64_t walk = kda::attn_typical(T, N, packed) / kTile / 2 + 1;
   const int64_t most = walk / 2 < 1 ? 1 : (walk / 2 > 16 ? 16 : walk / 2);
   const int64_t parts = (want + units - 1) / units;

@@ -33,6 +33,7 @@ using kda::line::units_of;
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kLine = 2 * (R + S);           // bytes of a token in LDS
+constexpr int kMostRows = 96;                // of a row tile: the output of 96 is 192 of a wave's registers
 constexpr int kPart = R + 4;                 // floats of a part's row: output, maximum, sum
 
 struct Params {
@@ -62,26 +63,68 @@ __device__ __forceinline__ u32x2 widen(uint32_t w, float f) {
   return (u32x2){__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
 }
 
-template <int NT>
-constexpr int unit_tokens() { return NT == 1 ? 128 : 64; }
+constexpr int kUnit = 64;                    // tokens of a unit
+constexpr int kOwn = kUnit / kWaves;         // of which a wave brings 16, all in one page
+constexpr int kSteps = (R + S) / 32;         // matrix instructions along a key
 
-// NT: row tiles of 32.
+// As they come from the cache, 16 tokens of a wave: codes, shared parts, exponents.
+constexpr int kRawShared = kOwn * R, kRawScale = kRawShared + kOwn * 2 * S, kRaw = kRawScale + 256;
+
+// The order of a line's pieces of 16 bytes, as latent_device.h's turn, for reads of 16
+// lines (16 different places, whatever the order of these bits) and of 16 columns:
+// of 8 successive lines 32 bytes each, in the eight places that there are.
+__device__ __forceinline__ int turn16(int line) {
+  return ((line & 2) << 1) | ((line >> 1) & 2) | ((line >> 3) & 1);
+}
+// Where lane (l16, g4) reads lines 0 .. 15 as an operand of a 16 x 16 product,
+// contraction indices 32 s + 8 g4 .. + 7 for s = 0; further ones are 64 bytes (s odd)
+// beside that in the turned order, and 128 for each two on.
+__device__ __forceinline__ int key_place(int l16, int g4) { return l16 * kLine + (g4 ^ turn16(l16)) * 16; }
+__device__ __forceinline__ bf16x8 keys_at(const unsigned char* tile, int place, int r, int s) {
+  return *reinterpret_cast<const bf16x8*>(tile + (place ^ (s & 1) * 64) + r * kLine + (s >> 1) * 128);
+}
+// Where lane (l16, g4) reads the transpose of lines 0 .. 31 at columns 0 .. 15: it takes
+// column l16 at lines 16 (j / 4) + 4 g4 + j % 4 for j = 0 .. 7, which is the order in
+// which the accumulators of two 16 x 16 products hold their rows.  Further columns are
+// 32 bytes for each 16 beside that in the turned order, and 128 for each 64.
+__device__ __forceinline__ int column_place(int l16, int g4) {
+  const int line = 4 * g4 + (l16 >> 2);
+  return line * kLine + (((l16 >> 1) & 1) ^ turn16(line)) * 16 + (l16 & 1) * 8;
+}
+__device__ __forceinline__ bf16x8 columns_at(const unsigned char* tile, int place, int r, int c) {
+  const unsigned char* p = tile + (place ^ (c >> 4 & 3) * 32) + r * kLine + (c >> 6) * 128;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * kLine));
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// Nothing moves across: operands are fetched in groups, one group ahead of the
+// products that use the other.  (Left alone, the compiler reads each operand right
+// before its product, and the one wave of a SIMD waits for every one of them.)
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// Sum and maximum over the four lanes that hold a row.
+__device__ __forceinline__ float quarter_max(float x) { return half_max(fmaxf(x, __shfl_xor(x, 16, 64))); }
+__device__ __forceinline__ float quarter_sum(float x) { return half_sum(x + __shfl_xor(x, 16, 64)); }
+
+// NT: row tiles of 16, in groups of two.
 template <int NT>
 __global__ __launch_bounds__(kThreads, 1) void latent_decode_kernel(Params p) {
-  constexpr int kUnit = unit_tokens<NT>();
-  constexpr int kShare = NT == 1 ? 4 : NT == 2 ? 2 : 1;    // waves that split the keys of 32 rows
-  constexpr int kKeys = kUnit / kShare / 32;               // blocks of 32 keys for each of them
-  constexpr int kOwn = kUnit / kWaves;                     // tokens that a wave brings
-  constexpr int kGroups = kOwn / 16;                       // the same in groups of 16, each within a page
+  constexpr int kShare = NT == 2 ? 4 : NT == 4 ? 2 : 1;    // waves that split the keys of a group's rows
+  constexpr int kKeys = kUnit / 16 / kShare;               // key tiles of 16 for each of them
+  constexpr int kAhead = kKeys == 1 ? 6 : kKeys == 2 ? 2 : 1;   // steps of which operands are fetched together
   __shared__ __align__(1024) unsigned char tile[kUnit * kLine];
-  __shared__ __align__(16) unsigned char weights[NT * (kUnit / 32) * 2048];
-  __shared__ float top[kShare][32 * NT], sums[kShare][32 * NT];
-  __shared__ int there[kUnit / 16];                        // whether a group's page exists
-  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  __shared__ __align__(1024) unsigned char raw[kWaves][kRaw];
+  __shared__ __align__(16) unsigned char weights[NT * 2048];
+  __shared__ float top[kShare][16 * NT], sums[kShare][16 * NT];
+  __shared__ int there[kUnit / 16];                        // pages of the key tiles, -1: none
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = NT == 1 ? 0 : NT == 2 ? (wave & 1) : wave; // the wave's 32 rows
-  const int share = NT == 1 ? wave : NT == 2 ? (wave >> 1) : 0;
-  const bool scores = g < NT;                              // of three row tiles the fourth wave has none
+  const int g = NT == 2 ? 0 : NT == 4 ? (wave & 1) : wave; // the wave's 32 rows
+  const int share = NT == 2 ? wave : NT == 4 ? (wave >> 1) : 0;
+  const bool scores = 2 * g < NT;                          // of three groups the fourth wave has none
 
   const Piece piece = kda::line::find_piece<kUnit, 1>(p, 0, p.row_tiles);
   int64_t left = piece.to - piece.from;
@@ -95,195 +138,252 @@ __global__ __launch_bounds__(kThreads, 1) void latent_decode_kernel(Params p) {
     // -------- one segment: sequence n, rows row0 .. row0 + tile_rows - 1
     const int row0 = seg * p.tile_rows;
     const int last = int(min(int64_t(units), first + left));
-    const int rows = min(min(p.rows - row0, p.tile_rows), 32 * NT);
+    const int rows = min(min(p.rows - row0, p.tile_rows), 16 * NT);
 
-    f32x16 o[NT][4];
-    float m[NT], l = 0.0f;                                 // m: of all rows; l: own rows and keys
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      m[t] = -INFINITY;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) o[t][d] = (f32x16)(0.0f);
-    }
-
-    // Pages of this wave's next groups, one per lane; -1: no tokens there.
+    // Pages of this wave's tokens in 64 units, one per lane; -1: no tokens there.
     const int32_t* table = p.table + n * p.table_stride;
-    int pages = -1, pages_from = 0;
+    int pages = -1, pages_from = 0, id = -1;
     auto look = [&](int unit) {
       pages_from = unit;
       pages = -1;
-      const int64_t token = int64_t(unit + lane / kGroups) * kUnit + wave * kOwn + lane % kGroups * 16;
+      const int64_t token = int64_t(unit + lane) * kUnit + wave * kOwn;
       if (token < len) {
-        const int id = table[token >> p.shift];
-        if (id >= 0 && id < p.num_pages) pages = id;
+        const int x = table[token >> p.shift];
+        if (x >= 0 && x < p.num_pages) pages = x;
       }
     };
-    // A group's 16 tokens as buffers that end behind the sequence, or are empty:
-    // what is not there reads as zero.
-    u32x4 code[kGroups][8], part[kGroups][2];
-    uint32_t exponent[kGroups];
-    int ids[kGroups];
+    // This wave's 16 tokens of a unit as buffers that end behind the sequence, or
+    // are empty: what is not there is zero in LDS.
     auto load = [&](int unit) {
-      if (unit - pages_from >= 64 / kGroups) look(unit);
+      if (unit - pages_from >= 64) look(unit);
+      id = __builtin_amdgcn_readlane(pages, unit - pages_from);
+      const int token = unit * kUnit + wave * kOwn;
+      const int exist = id < 0 ? 0 : min(len - token, kOwn);
+      const int64_t page = max(id, 0);
+      const int at = token & ((1 << p.shift) - 1);
+      const auto cs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.codes + page * p.c_stride + at * R), 0,
+                                                        exist * R, 0x00020000);
+      const auto ss = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.shared + page * p.s_stride + at * S), 0,
+                                                        exist * 2 * S, 0x00020000);
+      const auto es = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(p.exponents + page * p.scale_stride + at * kBlocks), 0, exist * kBlocks, 0x00020000);
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        ids[i] = __builtin_amdgcn_readlane(pages, (unit - pages_from) * kGroups + i);
-        const int token = unit * kUnit + wave * kOwn + 16 * i;
-        const int exist = ids[i] < 0 ? 0 : min(len - token, 16);
-        const int64_t page = max(ids[i], 0);
-        const int at = token & ((1 << p.shift) - 1);
-        const auto cs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(p.codes + page * p.c_stride + at * R), 0, exist * R, 0x00020000);
-        const auto ss = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint16_t*>(p.shared + page * p.s_stride + at * S), 0, exist * 2 * S, 0x00020000);
-        const auto es = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(p.exponents + page * p.scale_stride + at * kBlocks), 0, exist * kBlocks, 0x00020000);
+      for (int j = 0; j < 8; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(cs, (lds_ptr*)(raw[wave] + j * 1024), 16, lane * 16, j * 1024, 0, 0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) code[i][j] = __builtin_amdgcn_raw_buffer_load_b128(cs, lane * 16 + j * 1024, 0, 0);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) part[i][j] = __builtin_amdgcn_raw_buffer_load_b128(ss, lane * 16 + j * 1024, 0, 0);
-        exponent[i] = __builtin_amdgcn_raw_buffer_load_b32(es, lane * 4, 0, 0);
-      }
-    };
-    // What was loaded, to LDS.  Lanes of 16 codes: 32 are a token's.  A token that
-    // only some of the queries see may hold codes of NaN, which a weight of zero would
-    // not keep out of the others' products: its latent becomes zero and its shared part
-    // NaN, which gives the same to those that see it (their scores are NaN) and
-    // nothing to the others.
-    auto stage = [&](int unit, bool check) {
-#pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const int line0 = wave * kOwn + 16 * i;
-        uint32_t bad = 0;                                  // one bit for each token
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t e0 = __builtin_amdgcn_readlane(exponent[i], 2 * j);
-          const uint32_t e1 = __builtin_amdgcn_readlane(exponent[i], 2 * j + 1);
-          const float f = __uint_as_float(((h ? e1 : e0) >> (l32 & 24) & 255u) << 23);
-          if (check) {
-            uint32_t nan = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) nan |= (code[i][j][k] & 0x7f7f7f7fu) + 0x01010101u;
-            const uint64_t any = __ballot(nan & 0x80808080u);
-            const bool lo = uint32_t(any) != 0, hi = uint32_t(any >> 32) != 0;
-            bad |= uint32_t(lo) << (2 * j) | uint32_t(hi) << (2 * j + 1);
-            if (h ? hi : lo) code[i][j] = (u32x4)(0u);
-          }
-          unsigned char* line = tile + (line0 + 2 * j + h) * kLine;
-          const int turned = turn(2 * j);                  // of both lines
-          const u32x2 a = widen(code[i][j][0], f), b = widen(code[i][j][1], f);
-          const u32x2 x = widen(code[i][j][2], f), y = widen(code[i][j][3], f);
-          *reinterpret_cast<u32x4*>(line + ((2 * l32) ^ turned) * 16) = (u32x4){a[0], a[1], b[0], b[1]};
-          *reinterpret_cast<u32x4*>(line + ((2 * l32 + 1) ^ turned) * 16) = (u32x4){x[0], x[1], y[0], y[1]};
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int row = 8 * j + (lane >> 3);
-          u32x4 x = part[i][j];
-          if (check && (bad >> row & 1)) x = (u32x4)(0x7fc07fc0u);
-          *reinterpret_cast<u32x4*>(tile + (line0 + row) * kLine + ((2 * R / 16 + (lane & 7)) ^ turn(row)) * 16) = x;
-        }
-        if (lane == 0) there[line0 / 16] = ids[i];
-      }
+      for (int j = 0; j < 2; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ss, (lds_ptr*)(raw[wave] + kRawShared + j * 1024), 16, lane * 16,
+                                                 j * 1024, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(es, (lds_ptr*)(raw[wave] + kRawScale), 4, lane * 4, 0, 0, 0);
     };
 
     look(first);
     load(first);
-    bf16x8 q[2 * (R + S) / 32];
-    int limit = 0;                                         // tokens that the lane's row sees
-    if (scores) {
-      const int r = row0 + min(32 * g + l32, rows - 1), i = r / p.H;
-      const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (r - i * p.H) * (R + S) + 8 * h;
+    bf16x8 q[2][kSteps];
+    int limit[2];                                          // tokens that the lane's rows see
 #pragma unroll
-      for (int s = 0; s < 36; ++s) q[s] = *reinterpret_cast<const bf16x8*>(src + 16 * s);
-      limit = len - p.Q + i + 1;
+    for (int t = 0; t < 2; ++t) {
+      const int r = row0 + min(32 * g + 16 * t + l16, rows - 1), i = r / p.H;
+      const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (r - i * p.H) * (R + S) + 8 * g4;
+      if (scores)
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) q[t][s] = *reinterpret_cast<const bf16x8*>(src + 32 * s);
+      limit[t] = len - p.Q + i + 1;
+    }
+    f32x4 o[NT][8];                                        // column 128 wave + 16 d + 4 g4 + e of row 16 t + l16
+    float m[NT], l[2] = {0.0f, 0.0f};                      // m: of all rows; l: own rows and keys
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t] = -INFINITY;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[t][d] = (f32x4)(0.0f);
     }
 
     for (int unit = first; unit < last; ++unit) {
       const int key0 = unit * kUnit;
       const bool edge = key0 + kUnit > len - p.Q + 1;      // some row does not see some key
-      kda::lds_barrier();                                  // the unit before is used up
-      stage(unit, edge && p.Q > 1);
+
+      // -------- this wave's tokens, from codes to bfloat16
+      // (Places are made anew for every unit: kept, they would take registers that
+      // the queries and the output need.)
+      int place_lane = lane;
+      asm volatile("" : "+v"(place_lane));
+      __builtin_amdgcn_s_waitcnt(kWaitLoads);
+      u32x2 code[kOwn];
+      uint32_t exponent[kOwn];
+      u32x4 part[2];
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        code[i] = *reinterpret_cast<const u32x2*>(raw[wave] + i * R + lane * 8);
+        exponent[i] = raw[wave][kRawScale + i * kBlocks + g4];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        part[j] = *reinterpret_cast<const u32x4*>(raw[wave] + kRawShared + j * 1024 + lane * 16);
+      const int from = id;
+      kda::lds_barrier();                                  // the unit before is used up, and this wave has its tokens
       if (unit + 1 < last) load(unit + 1);
-      kda::lds_barrier();
-      f32x16 s[kKeys];
-      if (scores) {
+      // A token that only some of the queries see may hold codes of NaN, which a
+      // weight of zero would not keep out of the others' products: its latent becomes
+      // zero and its shared part NaN, which gives the same to those that see it (their
+      // scores are NaN) and nothing to the others.
+      if (edge && p.Q > 1) {
+        uint32_t bad = 0;                                  // one bit for each token
 #pragma unroll
-        for (int u = 0; u < kKeys; ++u) {
-          const int line = 32 * (share * kKeys + u);
-          s[u] = (f32x16)(0.0f);
-#pragma unroll
-          for (int k = 0; k < 36; ++k) s[u] = mfma32(rows_of<kLine>(tile, line, l32, h, k), q[k], s[u]);
-          const bool here = there[line / 16] >= 0, next = there[line / 16 + 1] >= 0;
-          if (edge || !here || !next) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (!(e < 8 ? here : next) || key0 + line + 8 * (e >> 2) + 4 * h + (e & 3) >= limit) s[u][e] = -INFINITY;
+        for (int i = 0; i < kOwn; ++i) {
+          const uint32_t nan = ((code[i][0] & 0x7f7f7f7fu) + 0x01010101u) | ((code[i][1] & 0x7f7f7f7fu) + 0x01010101u);
+          if (__any(nan & 0x80808080u)) {
+            bad |= 1u << i;
+            code[i] = (u32x2){0, 0};
           }
         }
-        float mx = s[0][0];
 #pragma unroll
-        for (int u = 0; u < kKeys; ++u)
+        for (int j = 0; j < 2; ++j)
+          if (bad >> (8 * j + (lane >> 3)) & 1) part[j] = (u32x4)(0x7fc07fc0u);
+      }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[u][e]);
-        mx = half_max(mx);
-        if (h == 0) top[share][32 * g + l32] = mx;
+      for (int i = 0; i < kOwn; ++i) {
+        const float f = __uint_as_float(exponent[i] << 23);
+        const u32x2 a = widen(code[i][0], f), b = widen(code[i][1], f);
+        *reinterpret_cast<u32x4*>(tile + (wave * kOwn + i) * kLine + (place_lane ^ turn16(i)) * 16) =
+            (u32x4){a[0], a[1], b[0], b[1]};
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int line = 8 * j + (place_lane >> 3);
+        *reinterpret_cast<u32x4*>(tile + (wave * kOwn + line) * kLine + ((R / 8 + (place_lane & 7)) ^ turn16(line)) * 16) =
+            part[j];
+      }
+      if (lane == 0) there[wave] = from;
+      kda::lds_barrier();
+
+      // -------- scores of two row tiles and kKeys key tiles (rows = keys)
+      f32x4 s[2][kKeys];
+      if (scores) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int k = 0; k < kKeys; ++k) s[t][k] = (f32x4)(0.0f);
+        bf16x8 a[2][kAhead][kKeys];
+        const int place = key_place(place_lane & 15, place_lane >> 4);
+        auto fetch = [&](int group) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k)
+              a[group & 1][i][k] = keys_at(tile, place, 16 * (share * kKeys + k), group * kAhead + i);
+        };
+        fetch(0);
+#pragma unroll
+        for (int group = 0; group < kSteps / kAhead; ++group) {
+          fence();
+          if (group + 1 < kSteps / kAhead) fetch(group + 1);
+          fence();
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int k = 0; k < kKeys; ++k)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) s[t][k] = mfma16(a[group & 1][i][k], q[t][group * kAhead + i], s[t][k]);
+        }
+        fence();
+#pragma unroll
+        for (int k = 0; k < kKeys; ++k) {
+          const bool gone = there[share * kKeys + k] < 0;
+          if (edge || gone) {
+            const int key = key0 + 16 * (share * kKeys + k) + 4 * g4;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (gone || key + e >= limit[t]) s[t][k][e] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          float mx = s[t][0][0];
+#pragma unroll
+          for (int k = 0; k < kKeys; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[t][k][e]);
+          mx = quarter_max(mx);
+          if (g4 == 0) top[share][32 * g + 16 * t + l16] = mx;
+        }
       }
       kda::lds_barrier();
+
+      // -------- the maximum of all rows, the same in all waves; weights of the own ones
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float mx = top[0][32 * t + l32];
+        float mx = top[0][16 * t + l16];
 #pragma unroll
-        for (int i = 1; i < kShare; ++i) mx = fmaxf(mx, top[i][32 * t + l32]);
-        if (__any((mx - m[t]) * c > kSlack)) {             // the same in all waves
+        for (int i = 1; i < kShare; ++i) mx = fmaxf(mx, top[i][16 * t + l16]);
+        if (__any((mx - m[t]) * c > kSlack)) {
           const float now = fmaxf(m[t], mx);
           const float f = __builtin_amdgcn_exp2f((m[t] - base(now)) * c);
           m[t] = now;
-          if (t == g) l *= f;
+          if ((t >> 1) == g) l[t & 1] *= f;
 #pragma unroll
-          for (int d = 0; d < 4; ++d) o[t][d] *= f;
+          for (int d = 0; d < 8; ++d) o[t][d] *= f;
         }
       }
       if (scores) {
-        float b = base(m[0]);
 #pragma unroll
-        for (int t = 1; t < NT; ++t) b = t == g ? base(m[t]) : b;
-        b *= c;
+        for (int t = 0; t < 2; ++t) {
+          float b = base(m[t]);
 #pragma unroll
-        for (int u = 0; u < kKeys; ++u)
+          for (int i = 1; i < NT / 2; ++i) b = i == g ? base(m[2 * i + t]) : b;
+          b *= c;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float x[8];
+          for (int k = 0; k < kKeys; ++k) {
+            float x[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              x[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][8 * k + j], c, -b));
-              l += x[j];
+            for (int e = 0; e < 4; ++e) {
+              x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][k][e], c, -b));
+              l[t] += x[e];
             }
-            *reinterpret_cast<bf16x8*>(weights + (((g * (kUnit / 32) + share * kKeys + u) * 2 + k) * 64 + lane) * 16) =
-                pack8(x);
-          }
-      }
-      kda::lds_barrier();
-#pragma unroll
-      for (int u = 0; u < kUnit / 32; ++u)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          bf16x8 w[NT];
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-            w[t] = *reinterpret_cast<const bf16x8*>(weights + (((t * (kUnit / 32) + u) * 2 + k) * 64 + lane) * 16);
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const bf16x8 a = columns_of<kLine>(tile, 32 * u, k, 128 * wave + 32 * d, lane);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) o[t][d] = mfma32(a, w[t], o[t][d]);
+            const int key = share * kKeys + k;             // tile: half of a product's 32 keys
+            *reinterpret_cast<u32x2*>(weights + (((2 * g + t) * 2 + (key >> 1)) * 64 + lane) * 16 + (key & 1) * 8) =
+                (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
           }
         }
+      }
+      kda::lds_barrier();
+
+      // -------- this wave's 128 columns of all rows
+      bf16x8 w[NT], a[2][4];
+      const int place = column_place(place_lane & 15, place_lane >> 4);
+      auto fetch = [&](int group) {                        // 32 keys, four tiles of 16 columns
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          a[group & 1][d] = columns_at(tile, place, 32 * (group >> 1), 128 * wave + 64 * (group & 1) + 16 * d);
+      };
+      fetch(0);
+#pragma unroll
+      for (int group = 0; group < 4; ++group) {
+        fence();
+        if ((group & 1) == 0) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            w[t] = *reinterpret_cast<const bf16x8*>(weights + ((t * 2 + (group >> 1)) * 64 + lane) * 16);
+        }
+        if (group + 1 < 4) fetch(group + 1);
+        fence();
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) o[t][4 * (group & 1) + d] = mfma16(a[group & 1][d], w[t], o[t][4 * (group & 1) + d]);
+      }
+      fence();
     }
 
     // -------- its rows: finished, or a part
-    l = half_sum(l);
-    if (scores && h == 0) sums[share][32 * g + l32] = l;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      l[t] = quarter_sum(l[t]);
+      if (scores && g4 == 0) sums[share][32 * g + 16 * t + l16] = l[t];
+    }
     kda::lds_barrier();
     const bool whole = first == 0 && last == units;
     const int64_t segment = int64_t(n) * p.row_tiles + seg;
@@ -294,7 +394,7 @@ __global__ __launch_bounds__(kThreads, 1) void latent_decode_kernel(Params p) {
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int r = 32 * t + l32;
+      const int r = 16 * t + l16, col = 128 * wave + 4 * g4;
       float sum = sums[0][r];
 #pragma unroll
       for (int i = 1; i < kShare; ++i) sum += sums[i][r];
@@ -303,13 +403,17 @@ __global__ __launch_bounds__(kThreads, 1) void latent_decode_kernel(Params p) {
         const int64_t out = int64_t(n) * p.rows + row0 + r;
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) store_row32(p.o + out * R + 128 * wave + 32 * d, o[t][d], f, h);
-        if (p.lse && wave == 0 && h == 0) p.lse[out] = m[t] * p.scale + __logf(sum);
+        for (int d = 0; d < 8; ++d) {
+          const f32x4 x = o[t][d] * f;
+          *reinterpret_cast<u32x2*>(p.o + out * R + col + 16 * d) =
+              (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
+        }
+        if (p.lse && wave == 0 && g4 == 0) p.lse[out] = m[t] * p.scale + __logf(sum);
       } else {
         float* to = p.parts + (int64_t(slot) * p.tile_rows + r) * kPart;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) store_row32(to + 128 * wave + 32 * d, o[t][d], 1.0f, h);
-        if (wave == 0 && h == 0) to[R] = m[t], to[R + 1] = sum;
+        for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(to + col + 16 * d) = o[t][d];
+        if (wave == 0 && g4 == 0) to[R] = m[t], to[R + 1] = sum;
       }
     }
     left -= last - first;
@@ -395,11 +499,12 @@ struct Plan {
   size_t parts, bytes;
 };
 
-// Rows in as few tiles of at most 128 as they need, of equal size, in steps of 32.
+// Rows in as few tiles of at most kMostRows as they need, of equal size, in steps of
+// 32.
 Plan plan_for(int64_t N, int64_t Q, int H) {
   Plan x;
   x.rows = int(Q * H);
-  x.row_tiles = (x.rows + 127) / 128;
+  x.row_tiles = (x.rows + kMostRows - 1) / kMostRows;
   x.tile_rows = ((x.rows + x.row_tiles - 1) / x.row_tiles + 31) / 32 * 32;
   x.pieces = kda::device_cus();
   x.segments = N * x.row_tiles;
@@ -461,13 +566,11 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
                  static_cast<float*>(workspace), owner, owner + x.segments};
   const hipStream_t st = kda::as_stream(stream);
   if (x.tile_rows == 32)
-    launch<1>(p, x.pieces, st);
-  else if (x.tile_rows == 64)
     launch<2>(p, x.pieces, st);
-  else if (x.tile_rows == 96)
-    launch<3>(p, x.pieces, st);
-  else
+  else if (x.tile_rows == 64)
     launch<4>(p, x.pieces, st);
+  else
+    launch<6>(p, x.pieces, st);
   const unsigned joins = unsigned(x.segments * ((tile + join_rows - 1) / join_rows));
   hipLaunchKernelGGL(latent_decode_join_kernel, dim3(joins), dim3(256), 0, st, p);
   return kda::launch_status();

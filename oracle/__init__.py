@@ -23,6 +23,7 @@ Modules
   packed_decode  the decode step from packed QKV and raw gate/beta logits
   backward   gradients of the forward by float64 autodiff of the recurrence
   attention  full attention, its gradients, the e4m3 cache and its tables
+  latent     latent attention in both forms, its gradients and its e4m3 cache
 
 Pinning status: every public function here is pinned by tests that do not
 re-type its formula (closed forms, the pages' worked example, invariants,
