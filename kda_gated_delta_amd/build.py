@@ -30,14 +30,6 @@ FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 
-# Flags of single files.
-FILE_FLAGS = {
-    # The output of its rows fills the vector registers' first half, the queries the
-    # second: results of matrix instructions are chosen to stand in either, which
-    # leaves nothing in scratch memory (otherwise 180 registers of 96 rows' kernel).
-    "latent_decode.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-}
-
 
 def source_files():
     """Every file the library is compiled from, in a fixed order."""
@@ -58,7 +50,6 @@ def source_hash():
             h.update(fh.read())
         h.update(b"\0")
     h.update(" ".join(FLAGS).encode())
-    h.update(repr(sorted(FILE_FLAGS.items())).encode())
     return h.hexdigest()[:32]
 
 
@@ -78,7 +69,7 @@ def build(verbose=False, jobs=8):
     stamp = source_hash()
     for src in srcs:
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
-        cmd = [hipcc(), *FLAGS, *FILE_FLAGS.get(os.path.basename(src), []), f'-DKDA_SOURCE_HASH="{stamp}"', "-c", src, "-o", obj]
+        cmd = [hipcc(), *FLAGS, f'-DKDA_SOURCE_HASH="{stamp}"', "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))

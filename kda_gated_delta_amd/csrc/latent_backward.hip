@@ -175,7 +175,7 @@ __device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsi
         if constexpr (kBoth) rest = pack8_rest(x, b);
 #pragma unroll
         for (int d = 0; d < 6; ++d) {
-          const bf16x8 a = d < 4 ? read_columns(kt, 32 * w, k, 32 * d, lane)
+          const bf16x8 a = d < 4 ? columns_of<256>(kt, 32 * w, k, 32 * d, lane)
                                  : columns_of<2 * S>(st, 32 * w, k, 32 * (d - 4), lane);
           dq[d] = mfma32(a, b, dq[d]);
           if constexpr (kBoth) dq[d] = mfma32(a, rest, dq[d]);
@@ -303,13 +303,13 @@ __device__ __forceinline__ void keys_of_dkv(const Params& p, unsigned id, unsign
         if constexpr (kBoth) pr = pack8_rest(x, pb), gr = pack8_rest(y, gb);
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const bf16x8 a = read_columns(ut, 32 * w, k, 32 * d, lane);
+          const bf16x8 a = columns_of<256>(ut, 32 * w, k, 32 * d, lane);
           dv[d] = mfma32(a, pb, dv[d]);
           if constexpr (kBoth) dv[d] = mfma32(a, pr, dv[d]);
         }
 #pragma unroll
         for (int d = 0; d < 6; ++d) {
-          const bf16x8 a = d < 4 ? read_columns(qt, 32 * w, k, 32 * d, lane)
+          const bf16x8 a = d < 4 ? columns_of<256>(qt, 32 * w, k, 32 * d, lane)
                                  : columns_of<2 * S>(q2t, 32 * w, k, 32 * (d - 4), lane);
           dk[d] = mfma32(a, gb, dk[d]);
           if constexpr (kBoth) dk[d] = mfma32(a, gr, dk[d]);

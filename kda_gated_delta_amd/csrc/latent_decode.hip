@@ -11,14 +11,14 @@
 // that is cut into equal pieces, one per workgroup (attn_line.h); a segment that
 // lies in several leaves float32 parts, which latent_decode_join_kernel adds up.
 //
-// A workgroup holds a unit in LDS as bfloat16, codes times their scales (exact),
-// and uses it twice: S^T = [C s] Q^T, with 32 rows of Q in a wave's registers, and
-// O^T += C^T P^T, where each wave has 128 of the 512 columns for all rows, so that
-// a column is read (transposed) by one wave only.  Weights go from the waves that
-// made them to all through LDS, as operands; the running maximum is common to the
-// waves, sum and output are float32.  With up to 32 rows the four waves split a
-// unit's keys, with more they split the rows.  The next unit's bytes are in flight
-// in registers meanwhile.
+// A unit lies in LDS as it came, in codes, and is used twice: S^T = [C s] Q^T, with Q
+// in registers, and O^T += C^T P^T, where each wave has 128 of the 512 columns for all
+// rows, so that a column is read (transposed) by one wave only.  Codes become
+// bfloat16 on their way from LDS into the operands.  A token's 128 values under one
+// scale are one wave's columns: a key's scales enter as it is widened, a value's
+// enter the weights, which go from the waves that made them to all through LDS, as
+// operands, in four versions.  The running maximum is common to the waves, sum and
+// output are float32.  The next units are on their way to LDS meanwhile.
 #include "attn_line.h"
 #include "kda_host.h"
 #include "latent_device.h"
@@ -32,8 +32,6 @@ using kda::line::units_of;
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr int kLine = 2 * (R + S);           // bytes of a token in LDS
-constexpr int kMostRows = 96;                // of a row tile: the output of 96 is 192 of a wave's registers
 constexpr int kPart = R + 4;                 // floats of a part's row: output, maximum, sum
 
 struct Params {
@@ -63,74 +61,89 @@ __device__ __forceinline__ u32x2 widen(uint32_t w, float f) {
   return (u32x2){__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
 }
 
-constexpr int kUnit = 64;                    // tokens of a unit
-constexpr int kOwn = kUnit / kWaves;         // of which a wave brings 16, all in one page
-constexpr int kSteps = (R + S) / 32;         // matrix instructions along a key
+// Eight codes as an operand.
+__device__ __forceinline__ bf16x8 widen(uint32_t x, uint32_t y, float f) {
+  const u32x2 a = widen(x, f), b = widen(y, f);
+  return as_bf16x8((u32x4){a[0], a[1], b[0], b[1]});
+}
 
-// As they come from the cache, 16 tokens of a wave: codes, shared parts, exponents.
-constexpr int kRawShared = kOwn * R, kRawScale = kRawShared + kOwn * 2 * S, kRaw = kRawScale + 256;
+constexpr int kUnit = 32;                    // tokens of a unit
+constexpr int kRing = 3;                     // units in LDS
+constexpr int kPerCu = 2;                    // workgroups of a compute unit
+constexpr int kOwn = kUnit / kWaves;         // tokens that a wave brings, all in one page
+constexpr int kLoads = kOwn / 2 + 2;         // of a wave for a unit
+// A unit in LDS: codes [kUnit][512], shared parts [kUnit][128 bytes], exponents.
+constexpr int kShared = kUnit * R, kScale = kShared + kUnit * 2 * S, kBytes = kScale + kWaves * 256;
 
-// The order of a line's pieces of 16 bytes, as latent_device.h's turn, for reads of 16
-// lines (16 different places, whatever the order of these bits) and of 16 columns:
-// of 8 successive lines 32 bytes each, in the eight places that there are.
-__device__ __forceinline__ int turn16(int line) {
-  return ((line & 2) << 1) | ((line >> 1) & 2) | ((line >> 3) & 1);
-}
-// Where lane (l16, g4) reads lines 0 .. 15 as an operand of a 16 x 16 product,
-// contraction indices 32 s + 8 g4 .. + 7 for s = 0; further ones are 64 bytes (s odd)
-// beside that in the turned order, and 128 for each two on.
-__device__ __forceinline__ int key_place(int l16, int g4) { return l16 * kLine + (g4 ^ turn16(l16)) * 16; }
-__device__ __forceinline__ bf16x8 keys_at(const unsigned char* tile, int place, int r, int s) {
-  return *reinterpret_cast<const bf16x8*>(tile + (place ^ (s & 1) * 64) + r * kLine + (s >> 1) * 128);
-}
-// Where lane (l16, g4) reads the transpose of lines 0 .. 31 at columns 0 .. 15: it takes
-// column l16 at lines 16 (j / 4) + 4 g4 + j % 4 for j = 0 .. 7, which is the order in
-// which the accumulators of two 16 x 16 products hold their rows.  Further columns are
-// 32 bytes for each 16 beside that in the turned order, and 128 for each 64.
-__device__ __forceinline__ int column_place(int l16, int g4) {
-  const int line = 4 * g4 + (l16 >> 2);
-  return line * kLine + (((l16 >> 1) & 1) ^ turn16(line)) * 16 + (l16 & 1) * 8;
-}
-__device__ __forceinline__ bf16x8 columns_at(const unsigned char* tile, int place, int r, int c) {
-  const unsigned char* p = tile + (place ^ (c >> 4 & 3) * 32) + r * kLine + (c >> 6) * 128;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * kLine));
-  typedef short s16x8 __attribute__((ext_vector_type(8)));
-  const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  return __builtin_bit_cast(bf16x8, v);
-}
+// Places of 16-byte pieces in a unit's lines: piece c of line r is at c ^ swirl(r), of
+// the shared parts at c ^ swirl2(r).  Of 16 successive lines one piece is then in 16
+// different places of the banks' 256 bytes, and of the 8 x 4 lines whose columns are
+// read together (r, r + 16) two times 16.
+__device__ __forceinline__ int swirl(int r) { return (r & 15) ^ ((r >> 1) & 8); }
+__device__ __forceinline__ int swirl2(int r) { return (r >> 1) & 7; }
 
 // Nothing moves across: operands are fetched in groups, one group ahead of the
 // products that use the other.  (Left alone, the compiler reads each operand right
-// before its product, and the one wave of a SIMD waits for every one of them.)
+// before its product, and the wave waits for every one of them.)
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// Sum and maximum over the four lanes that hold a row.
-__device__ __forceinline__ float quarter_max(float x) { return half_max(fmaxf(x, __shfl_xor(x, 16, 64))); }
-__device__ __forceinline__ float quarter_sum(float x) { return half_sum(x + __shfl_xor(x, 16, 64)); }
+// The lane, made anew: what is made of it again for every unit takes no register from
+// the queries and the output meanwhile.
+__device__ __forceinline__ int lane_now() {
+  int x;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
+  return x;
+}
 
-// NT: row tiles of 16, in groups of two.
+// Sum and maximum over the four lanes that hold a row.
+__device__ __forceinline__ u32x2 quarters(float x) {       // rows 0 and 1, or 2 and 3, of 16 lanes
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return (u32x2){r[0], r[1]};
+}
+__device__ __forceinline__ float quarter_max(float x) {
+  const u32x2 r = quarters(x);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float quarter_sum(float x) {
+  const u32x2 r = quarters(x);
+  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+// At most n loads are left, nothing else.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt(kWaitLoads | (n & 15) | (n >> 4) << 14);
+}
+
+// NT: row tiles of 16.
 template <int NT>
-__global__ __launch_bounds__(kThreads, 1) void latent_decode_kernel(Params p) {
-  constexpr int kShare = NT == 2 ? 4 : NT == 4 ? 2 : 1;    // waves that split the keys of a group's rows
-  constexpr int kKeys = kUnit / 16 / kShare;               // key tiles of 16 for each of them
-  constexpr int kAhead = kKeys == 1 ? 6 : kKeys == 2 ? 2 : 1;   // steps of which operands are fetched together
-  __shared__ __align__(1024) unsigned char tile[kUnit * kLine];
-  __shared__ __align__(1024) unsigned char raw[kWaves][kRaw];
-  __shared__ __align__(16) unsigned char weights[NT * 2048];
-  __shared__ float top[kShare][16 * NT], sums[kShare][16 * NT];
-  __shared__ int there[kUnit / 16];                        // pages of the key tiles, -1: none
+__global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params p) {
+  constexpr int kShare = kWaves / NT, kKeys = 2 / kShare;  // waves that split a row's keys; key tiles of 16 for each
+  // (One object: between two the compiler tells apart what loads to LDS write, and
+  // has reads wait for all those that are on their way to the same one.)
+  __shared__ __align__(1024) struct {
+    unsigned char ring[kRing][kBytes];
+    unsigned char weights[kBlocks][NT][1024];
+    float scales[kUnit][kBlocks];
+    float top[kShare][16 * NT];                            // maxima of a unit, and in the end sums
+    int there[kRing][kWaves];                              // whether a wave's tokens have a page
+  } lds;
+  auto &ring = lds.ring;
+  auto &weights = lds.weights;
+  auto &scales = lds.scales;
+  auto &top = lds.top;
+  auto &there = lds.there;
   const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = NT == 2 ? 0 : NT == 4 ? (wave & 1) : wave; // the wave's 32 rows
-  const int share = NT == 2 ? wave : NT == 4 ? (wave >> 1) : 0;
-  const bool scores = 2 * g < NT;                          // of three groups the fourth wave has none
+  const int share = wave % kShare, mine = wave / kShare;   // the wave's keys, and its row tile
 
   const Piece piece = kda::line::find_piece<kUnit, 1>(p, 0, p.row_tiles);
   int64_t left = piece.to - piece.from;
   int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
   const int64_t inside = piece.from - piece.before;
-  int seg = int(inside / units), first = int(inside - int64_t(seg) * units);
+  int seg = __builtin_amdgcn_readfirstlane(int(inside / units));
+  int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * units));
   bool begun = false;                                      // the piece's first segment is done
   const float c = p.scale * kLog2e;
 
@@ -140,58 +153,72 @@ __global__ __launch_bounds__(kThreads, 1) void latent_decode_kernel(Params p) {
     const int last = int(min(int64_t(units), first + left));
     const int rows = min(min(p.rows - row0, p.tile_rows), 16 * NT);
 
-    // Pages of this wave's tokens in 64 units, one per lane; -1: no tokens there.
+    // The slots of this wave's first tokens in 64 units, one to a lane; -1: no page.
     const int32_t* table = p.table + n * p.table_stride;
-    int pages = -1, pages_from = 0, id = -1;
+    int from = 0, slots = -1;
     auto look = [&](int unit) {
-      pages_from = unit;
-      pages = -1;
-      const int64_t token = int64_t(unit + lane) * kUnit + wave * kOwn;
+      from = unit;
+      slots = -1;
+      const int64_t token = int64_t(unit + lane_now()) * kUnit + wave * kOwn;
       if (token < len) {
-        const int x = table[token >> p.shift];
-        if (x >= 0 && x < p.num_pages) pages = x;
+        const int id = table[token >> p.shift];
+        if (id >= 0 && id < p.num_pages) slots = (id << p.shift) + (int(token) & ((1 << p.shift) - 1));
       }
     };
-    // This wave's 16 tokens of a unit as buffers that end behind the sequence, or
-    // are empty: what is not there is zero in LDS.
+    // They come as buffers that end behind the sequence, or are empty: what is not
+    // there is zero in LDS.
     auto load = [&](int unit) {
-      if (unit - pages_from >= 64) look(unit);
-      id = __builtin_amdgcn_readlane(pages, unit - pages_from);
-      const int token = unit * kUnit + wave * kOwn;
-      const int exist = id < 0 ? 0 : min(len - token, kOwn);
-      const int64_t page = max(id, 0);
-      const int at = token & ((1 << p.shift) - 1);
+      if (unit - from >= 64) look(unit);
+      const int slot = __builtin_amdgcn_readlane(slots, unit - from);
+      const int some = slot < 0 ? 0 : min(len - (unit * kUnit + wave * kOwn), kOwn);
+      const int64_t page = max(slot, 0) >> p.shift;
+      const int at = max(slot, 0) & ((1 << p.shift) - 1);
       const auto cs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.codes + page * p.c_stride + at * R), 0,
-                                                        exist * R, 0x00020000);
+                                                        some * R, 0x00020000);
       const auto ss = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.shared + page * p.s_stride + at * S), 0,
-                                                        exist * 2 * S, 0x00020000);
+                                                        some * 2 * S, 0x00020000);
       const auto es = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint8_t*>(p.exponents + page * p.scale_stride + at * kBlocks), 0, exist * kBlocks, 0x00020000);
+          const_cast<uint8_t*>(p.exponents + page * p.scale_stride + at * kBlocks), 0, some * kBlocks, 0x00020000);
+      const int lane = lane_now();
+      if (lane == 0) there[unit % kRing][wave] = some;
+      unsigned char* to = ring[unit % kRing];
+      const int r0 = wave * kOwn;
+      const int piece0 = (lane & 31) ^ swirl(r0) ^ (lane >> 5);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(cs, (lds_ptr*)(raw[wave] + j * 1024), 16, lane * 16, j * 1024, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ss, (lds_ptr*)(raw[wave] + kRawShared + j * 1024), 16, lane * 16,
-                                                 j * 1024, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(es, (lds_ptr*)(raw[wave] + kRawScale), 4, lane * 4, 0, 0, 0);
+      for (int j = 0; j < kOwn / 2; ++j)                   // two lines each
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(cs, (lds_ptr*)(to + r0 * R + j * 1024), 16,
+                                                 (lane >> 5) * R + (piece0 ^ 2 * j) * 16, j * 1024, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(            // eight lines
+          ss, (lds_ptr*)(to + kShared + r0 * 2 * S), 16,
+          (lane >> 3) * 2 * S + ((lane & 7) ^ swirl2(r0 + (lane >> 3))) * 16, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(es, (lds_ptr*)(to + kScale + wave * 256), 4, lane * 4, 0, 0, 0);
     };
 
+    if (begun) wait_loads<0>();                            // (stores, that would count among the loads)
     look(first);
-    load(first);
-    bf16x8 q[2][kSteps];
-    int limit[2];                                          // tokens that the lane's rows see
+    // Rows of Q as operands.  Along a key the order is what lanes of 16 codes make it:
+    // steps 2 i and 2 i + 1 are the first and second 8 of lane group g4's 16.
+    bf16x8 q[18];
+    int limit;                                             // tokens that the lane's row sees
+    {
+      const int r = row0 + min(16 * mine + l16, rows - 1), i = r / p.H;
+      const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (r - i * p.H) * (R + S);
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int r = row0 + min(32 * g + 16 * t + l16, rows - 1), i = r / p.H;
-      const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (r - i * p.H) * (R + S) + 8 * g4;
-      if (scores)
+      for (int s = 0; s < 16; ++s)
+        q[s] = *reinterpret_cast<const bf16x8*>(src + 64 * (s >> 1) + 16 * g4 + 8 * (s & 1));
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) q[t][s] = *reinterpret_cast<const bf16x8*>(src + 32 * s);
-      limit[t] = len - p.Q + i + 1;
+      for (int s = 0; s < 2; ++s) q[16 + s] = *reinterpret_cast<const bf16x8*>(src + R + 32 * s + 8 * g4);
+      limit = len - p.Q + i + 1;
     }
+    fence();
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i)
+      if (first + i < last) load(first + i);
+    // The queries are waited for before the first unit: left to the compiler they would
+    // be in every unit, and with them the loads behind them.
+    wait_loads<0>();
     f32x4 o[NT][8];                                        // column 128 wave + 16 d + 4 g4 + e of row 16 t + l16
-    float m[NT], l[2] = {0.0f, 0.0f};                      // m: of all rows; l: own rows and keys
+    float m[NT], l = 0.0f;                                 // m: of all rows; l: own row tile and keys
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       m[t] = -INFINITY;
@@ -202,188 +229,183 @@ __global__ __launch_bounds__(kThreads, 1) void latent_decode_kernel(Params p) {
     for (int unit = first; unit < last; ++unit) {
       const int key0 = unit * kUnit;
       const bool edge = key0 + kUnit > len - p.Q + 1;      // some row does not see some key
+      unsigned char* tile = ring[unit % kRing];
+      const int place_lane = lane_now();
+      const int p16 = place_lane & 15, p4 = place_lane >> 4;
 
-      // -------- this wave's tokens, from codes to bfloat16
-      // (Places are made anew for every unit: kept, they would take registers that
-      // the queries and the output need.)
-      int place_lane = lane;
-      asm volatile("" : "+v"(place_lane));
-      __builtin_amdgcn_s_waitcnt(kWaitLoads);
-      u32x2 code[kOwn];
-      uint32_t exponent[kOwn];
-      u32x4 part[2];
+      // -------- this wave's tokens are there; their scales as factors
+      if (unit + 1 < last)
+        wait_loads<kLoads>();
+      else
+        wait_loads<0>();
       __atomic_signal_fence(__ATOMIC_SEQ_CST);
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        code[i] = *reinterpret_cast<const u32x2*>(raw[wave] + i * R + lane * 8);
-        exponent[i] = raw[wave][kRawScale + i * kBlocks + g4];
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        part[j] = *reinterpret_cast<const u32x4*>(raw[wave] + kRawShared + j * 1024 + lane * 16);
-      const int from = id;
-      kda::lds_barrier();                                  // the unit before is used up, and this wave has its tokens
-      if (unit + 1 < last) load(unit + 1);
+      if (place_lane < kOwn * kBlocks)
+        scales[wave * kOwn + (place_lane >> 2)][place_lane & 3] =
+            __uint_as_float(uint32_t(tile[kScale + wave * 256 + place_lane]) << 23);
       // A token that only some of the queries see may hold codes of NaN, which a
       // weight of zero would not keep out of the others' products: its latent becomes
       // zero and its shared part NaN, which gives the same to those that see it (their
       // scores are NaN) and nothing to the others.
       if (edge && p.Q > 1) {
-        uint32_t bad = 0;                                  // one bit for each token
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < kOwn; ++i) {
-          const uint32_t nan = ((code[i][0] & 0x7f7f7f7fu) + 0x01010101u) | ((code[i][1] & 0x7f7f7f7fu) + 0x01010101u);
-          if (__any(nan & 0x80808080u)) {
-            bad |= 1u << i;
-            code[i] = (u32x2){0, 0};
-          }
+          u32x2* code = reinterpret_cast<u32x2*>(tile + (wave * kOwn + i) * R) + place_lane;
+          const u32x2 x = *code;
+          const uint32_t nan = ((x[0] & 0x7f7f7f7fu) + 0x01010101u) | ((x[1] & 0x7f7f7f7fu) + 0x01010101u);
+          if (!__any(nan & 0x80808080u)) continue;
+          *code = (u32x2){0, 0};
+          if (place_lane < 32)
+            reinterpret_cast<uint32_t*>(tile + kShared + (wave * kOwn + i) * 2 * S)[place_lane] = 0x7fc07fc0u;
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (bad >> (8 * j + (lane >> 3)) & 1) part[j] = (u32x4)(0x7fc07fc0u);
       }
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        const float f = __uint_as_float(exponent[i] << 23);
-        const u32x2 a = widen(code[i][0], f), b = widen(code[i][1], f);
-        *reinterpret_cast<u32x4*>(tile + (wave * kOwn + i) * kLine + (place_lane ^ turn16(i)) * 16) =
-            (u32x4){a[0], a[1], b[0], b[1]};
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int line = 8 * j + (place_lane >> 3);
-        *reinterpret_cast<u32x4*>(tile + (wave * kOwn + line) * kLine + ((R / 8 + (place_lane & 7)) ^ turn16(line)) * 16) =
-            part[j];
-      }
-      if (lane == 0) there[wave] = from;
-      kda::lds_barrier();
+      kda::lds_barrier();                                  // everybody's; and the unit before is used up
+      if (unit + kRing - 1 < last) load(unit + kRing - 1);
 
-      // -------- scores of two row tiles and kKeys key tiles (rows = keys)
-      f32x4 s[2][kKeys];
-      if (scores) {
+      // -------- scores of the row tile and kKeys key tiles (rows = keys)
+      f32x4 s[kKeys];
+      {
+        float f[2][kKeys];                                 // the scales of a block, and of the next
+        auto fetch_scale = [&](int block) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+          for (int k = 0; k < kKeys; ++k) f[block & 1][k] = scales[16 * (share * kKeys + k) + p16][block];
+        };
+        fetch_scale(0);
 #pragma unroll
-          for (int k = 0; k < kKeys; ++k) s[t][k] = (f32x4)(0.0f);
-        bf16x8 a[2][kAhead][kKeys];
-        const int place = key_place(place_lane & 15, place_lane >> 4);
-        auto fetch = [&](int group) {
+        for (int k = 0; k < kKeys; ++k) s[k] = (f32x4)(0.0f);
+        // Rounds of kAhead pieces of 16 bytes: eight of codes, two steps each, and two of
+        // the shared part.
+        constexpr int kAhead = 2 / kKeys, kRounds = 10 / kAhead;
+        u32x4 a[2][kAhead][kKeys];
+        auto fetch = [&](int round) {
 #pragma unroll
           for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k)
-              a[group & 1][i][k] = keys_at(tile, place, 16 * (share * kKeys + k), group * kAhead + i);
+            for (int k = 0; k < kKeys; ++k) {
+              const int at = round * kAhead + i, key = 16 * (share * kKeys + k) + p16;
+              const unsigned char* from =
+                  at < 8 ? tile + key * R + ((p4 ^ p16 ^ (share * kKeys + k) * 8) * 16 ^ at * 64)
+                         : tile + kShared + key * 2 * S + ((4 * (at - 8) + p4) ^ swirl2(p16)) * 16;
+              a[round & 1][i][k] = *reinterpret_cast<const u32x4*>(from);
+            }
         };
         fetch(0);
 #pragma unroll
-        for (int group = 0; group < kSteps / kAhead; ++group) {
+        for (int round = 0; round < kRounds; ++round) {
           fence();
-          if (group + 1 < kSteps / kAhead) fetch(group + 1);
+          if (round + 1 < kRounds) fetch(round + 1);
+          if (round * kAhead % 2 == 0 && round * kAhead < 6) fetch_scale(round * kAhead / 2 + 1);
           fence();
 #pragma unroll
           for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-            for (int k = 0; k < kKeys; ++k)
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-              for (int t = 0; t < 2; ++t) s[t][k] = mfma16(a[group & 1][i][k], q[t][group * kAhead + i], s[t][k]);
+              for (int k = 0; k < kKeys; ++k) {
+                const int at = round * kAhead + i;
+                const u32x4 x = a[round & 1][i][k];
+                if (at < 8)
+                  s[k] = mfma16(widen(x[2 * half], x[2 * half + 1], f[at >> 1 & 1][k]), q[2 * at + half], s[k]);
+                else if (half == 0)
+                  s[k] = mfma16(as_bf16x8(x), q[at + 8], s[k]);
+              }
         }
         fence();
 #pragma unroll
         for (int k = 0; k < kKeys; ++k) {
-          const bool gone = there[share * kKeys + k] < 0;
-          if (edge || gone) {
-            const int key = key0 + 16 * (share * kKeys + k) + 4 * g4;
+          const int key = 16 * (share * kKeys + k) + 4 * p4;
+          const bool gone = there[unit % kRing][key / kOwn] == 0;
+          if (edge || __any(gone)) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (gone || key + e >= limit[t]) s[t][k][e] = -INFINITY;
+            for (int e = 0; e < 4; ++e)
+              if (gone || key0 + key + e >= limit) s[k][e] = -INFINITY;
           }
         }
+        float mx = s[0][0];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float mx = s[t][0][0];
+        for (int k = 0; k < kKeys; ++k)
 #pragma unroll
-          for (int k = 0; k < kKeys; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[t][k][e]);
-          mx = quarter_max(mx);
-          if (g4 == 0) top[share][32 * g + 16 * t + l16] = mx;
-        }
+          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[k][e]);
+        mx = quarter_max(mx);
+        if (p4 == 0) top[share][16 * mine + p16] = mx;
       }
       kda::lds_barrier();
 
       // -------- the maximum of all rows, the same in all waves; weights of the own ones
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float mx = top[0][16 * t + l16];
+        float mx = top[0][16 * t + p16];
 #pragma unroll
-        for (int i = 1; i < kShare; ++i) mx = fmaxf(mx, top[i][16 * t + l16]);
+        for (int i = 1; i < kShare; ++i) mx = fmaxf(mx, top[i][16 * t + p16]);
         if (__any((mx - m[t]) * c > kSlack)) {
           const float now = fmaxf(m[t], mx);
           const float f = __builtin_amdgcn_exp2f((m[t] - base(now)) * c);
           m[t] = now;
-          if ((t >> 1) == g) l[t & 1] *= f;
+          if (t == mine) l *= f;
 #pragma unroll
           for (int d = 0; d < 8; ++d) o[t][d] *= f;
         }
       }
-      if (scores) {
+      {
+        float b = base(m[0]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          float b = base(m[t]);
+        for (int t = 1; t < NT; ++t) b = t == mine ? base(m[t]) : b;
+        b *= c;
 #pragma unroll
-          for (int i = 1; i < NT / 2; ++i) b = i == g ? base(m[2 * i + t]) : b;
-          b *= c;
+        for (int k = 0; k < kKeys; ++k) {
+          const int key = share * kKeys + k;               // tile: half of a product's 32 keys
+          f32x4 f[4];                                      // of four keys: their blocks' scales
 #pragma unroll
-          for (int k = 0; k < kKeys; ++k) {
-            float x[4];
+          for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const f32x4*>(scales[16 * key + 4 * p4 + e]);
+          float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][k][e], c, -b));
-              l[t] += x[e];
-            }
-            const int key = share * kKeys + k;             // tile: half of a product's 32 keys
-            *reinterpret_cast<u32x2*>(weights + (((2 * g + t) * 2 + (key >> 1)) * 64 + lane) * 16 + (key & 1) * 8) =
-                (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
+          for (int e = 0; e < 4; ++e) {
+            x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][e], c, -b));
+            l += x[e];
           }
+#pragma unroll
+          for (int d = 0; d < kBlocks; ++d)
+            *reinterpret_cast<u32x2*>(weights[d][mine] + place_lane * 16 + key * 8) =
+                (u32x2){kda::pack_bf16(x[0] * f[0][d], x[1] * f[1][d]), kda::pack_bf16(x[2] * f[2][d], x[3] * f[3][d])};
         }
       }
       kda::lds_barrier();
 
-      // -------- this wave's 128 columns of all rows
-      bf16x8 w[NT], a[2][4];
-      const int place = column_place(place_lane & 15, place_lane >> 4);
-      auto fetch = [&](int group) {                        // 32 keys, four tiles of 16 columns
+      // -------- this wave's 128 columns of all rows: lane l16 takes column l16 of 16 at
+      // keys 16 (j / 4) + 4 g4 + j % 4 for j = 0 .. 7, the order in which two key tiles'
+      // scores made their weights.  (A transposing read gathers, in every 16 lanes, byte
+      // i & 7 of the 8-byte pieces addressed by lanes (i >> 3) + 2 e into byte e of lane i.)
+      bf16x8 w[NT];
+      constexpr int kAhead = 8 / NT;                       // tiles of 16 columns fetched together
+      u32x2 a[2][kAhead];
+      const int line = ((p16 >> 1) & 3) + 4 * p4 + (p16 & 8) * 2;
+      const int place = line * R + ((8 * wave) ^ swirl(line)) * 16 + (p16 & 1) * 8;
+      auto fetch = [&](int round) {
 #pragma unroll
-        for (int d = 0; d < 4; ++d)
-          a[group & 1][d] = columns_at(tile, place, 32 * (group >> 1), 128 * wave + 64 * (group & 1) + 16 * d);
+        for (int d = 0; d < kAhead; ++d)
+          a[round & 1][d] = __builtin_bit_cast(
+              u32x2, transposed((const lds_i32x2*)(tile + (place ^ (kAhead * round + d) * 16))));
       };
       fetch(0);
 #pragma unroll
-      for (int group = 0; group < 4; ++group) {
-        fence();
-        if ((group & 1) == 0) {
+      for (int t = 0; t < NT; ++t) w[t] = *reinterpret_cast<const bf16x8*>(weights[wave][t] + place_lane * 16);
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            w[t] = *reinterpret_cast<const bf16x8*>(weights + ((t * 2 + (group >> 1)) * 64 + lane) * 16);
+      for (int round = 0; round < 8 / kAhead; ++round) {
+        fence();
+        if (round + 1 < 8 / kAhead) fetch(round + 1);
+        fence();
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          const bf16x8 x = widen(a[round & 1][d][0], a[round & 1][d][1], 1.0f);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) o[t][kAhead * round + d] = mfma16(x, w[t], o[t][kAhead * round + d]);
         }
-        if (group + 1 < 4) fetch(group + 1);
-        fence();
-#pragma unroll
-        for (int d = 0; d < 4; ++d)
-#pragma unroll
-          for (int t = 0; t < NT; ++t) o[t][4 * (group & 1) + d] = mfma16(a[group & 1][d], w[t], o[t][4 * (group & 1) + d]);
       }
       fence();
     }
 
     // -------- its rows: finished, or a part
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      l[t] = quarter_sum(l[t]);
-      if (scores && g4 == 0) sums[share][32 * g + 16 * t + l16] = l[t];
-    }
+    l = quarter_sum(l);
+    if (g4 == 0) top[share][16 * mine + l16] = l;
     kda::lds_barrier();
     const bool whole = first == 0 && last == units;
     const int64_t segment = int64_t(n) * p.row_tiles + seg;
@@ -395,9 +417,9 @@ __global__ __launch_bounds__(kThreads, 1) void latent_decode_kernel(Params p) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = 16 * t + l16, col = 128 * wave + 4 * g4;
-      float sum = sums[0][r];
+      float sum = top[0][r];
 #pragma unroll
-      for (int i = 1; i < kShare; ++i) sum += sums[i][r];
+      for (int i = 1; i < kShare; ++i) sum += top[i][r];
       if (r >= rows) continue;
       if (whole) {
         const int64_t out = int64_t(n) * p.rows + row0 + r;
@@ -499,14 +521,13 @@ struct Plan {
   size_t parts, bytes;
 };
 
-// Rows in as few tiles of at most kMostRows as they need, of equal size, in steps of
-// 32.
+// Rows in tiles of 64, or of 32 where that leaves fewer unused.
 Plan plan_for(int64_t N, int64_t Q, int H) {
   Plan x;
   x.rows = int(Q * H);
-  x.row_tiles = (x.rows + kMostRows - 1) / kMostRows;
-  x.tile_rows = ((x.rows + x.row_tiles - 1) / x.row_tiles + 31) / 32 * 32;
-  x.pieces = kda::device_cus();
+  x.tile_rows = (x.rows + 31) / 32 % 2 ? 32 : 64;
+  x.row_tiles = (x.rows + x.tile_rows - 1) / x.tile_rows;
+  x.pieces = kda::device_cus() * kPerCu;
   x.segments = N * x.row_tiles;
   x.parts = size_t(2 * x.pieces) * x.tile_rows * kPart * sizeof(float);
   x.bytes = x.parts + size_t(x.segments) * 2 * sizeof(int);
@@ -567,10 +588,8 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
   const hipStream_t st = kda::as_stream(stream);
   if (x.tile_rows == 32)
     launch<2>(p, x.pieces, st);
-  else if (x.tile_rows == 64)
-    launch<4>(p, x.pieces, st);
   else
-    launch<6>(p, x.pieces, st);
+    launch<4>(p, x.pieces, st);
   const unsigned joins = unsigned(x.segments * ((tile + join_rows - 1) / join_rows));
   hipLaunchKernelGGL(latent_decode_join_kernel, dim3(joins), dim3(256), 0, st, p);
   return kda::launch_status();

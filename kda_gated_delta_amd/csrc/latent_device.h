@@ -28,7 +28,19 @@ __device__ __forceinline__ bf16x8 rows_of(const unsigned char* tile, int r, int 
   return *reinterpret_cast<const bf16x8*>(tile + line * BYTES + (((2 * s + h) ^ turn(line)) * 16));
 }
 
-// As attn_device.h's read_columns, of a tile with lines of BYTES.
+// Transposing reads.  What they read was waited for by whoever calls them: as calls
+// with a pointer of their own (restrict) the compiler does not take them to read what
+// loads to LDS that are still on their way will write, and does not wait for those.
+__device__ __forceinline__ s16x4 transposed(const lds_s16x4* __restrict p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16(const_cast<lds_s16x4*>(p));
+}
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+__device__ __forceinline__ i32x2 transposed(const lds_i32x2* __restrict p) {
+  return __builtin_amdgcn_ds_read_tr8_b64_v2i32(const_cast<lds_i32x2*>(p));
+}
+
+// As attn_device.h's read_columns, of a tile with lines of BYTES in the order `turn`.
 template <int BYTES>
 __device__ __forceinline__ bf16x8 columns_of(const unsigned char* tile, int r, int m, int c, int lane) {
   const int j = lane & 15, h = lane >> 5;
@@ -36,8 +48,9 @@ __device__ __forceinline__ bf16x8 columns_of(const unsigned char* tile, int r, i
   const int col = c + (lane & 16) + 4 * (j & 3);
   const int piece = col >> 3, half = (col & 4) * 2;
   const unsigned char* p = tile + line * BYTES + half;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + (piece ^ turn(line)) * 16));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 8 * BYTES + (piece ^ turn(line + 8)) * 16));
+  auto place = [](int line) { return BYTES == 256 ? swizzle(line) : turn(line); };
+  const s16x4 a = transposed((const lds_s16x4*)(p + (piece ^ place(line)) * 16));
+  const s16x4 b = transposed((const lds_s16x4*)(p + 8 * BYTES + (piece ^ place(line + 8)) * 16));
   typedef short s16x8 __attribute__((ext_vector_type(8)));
   const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   return __builtin_bit_cast(bf16x8, v);

@@ -141,7 +141,7 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
         for (int j = 0; j < 8; ++j) x[j] = s[u][8 * k + j];
         const bf16x8 w = pack8(x);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) o[d] = mfma32(read_columns(vt, 32 * u, k, 32 * d, lane), w, o[d]);
+        for (int d = 0; d < 4; ++d) o[d] = mfma32(columns_of<256>(vt, 32 * u, k, 32 * d, lane), w, o[d]);
       }
     }
   };
