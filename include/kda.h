@@ -762,7 +762,7 @@ size_t kda_latent_backward_workspace_size(int32_t B, int32_t T, int32_t T_kv, in
  *   k_cache     bf16 [page_size][64]         at k_page      (a multiple of 8)
  * Value i of a latent is code i * 2^(scale[i / 128] - 127), the shared key part is
  * as it was stored.  page_size: 16, 32, 64, 128 or 256 (others
- * KDA_ERR_UNSUPPORTED); strides of at least a page and at most 2^32 (k_page 2^31);
+ * KDA_ERR_UNSUPPORTED); strides of at least a page and below 2^32 (k_page 2^31);
  * num_pages * page_size < 2^31.  c_cache and k_cache begin at multiples of 16
  * bytes, c_scale of 4.
  */

@@ -126,9 +126,9 @@ struct LatentCache {
 inline int latent_cache(const LatentCache& x) {
   if (!attn_page(x.page_size)) return KDA_ERR_UNSUPPORTED;
   if (x.num_pages < 0 || int64_t(x.num_pages) * x.page_size > 0x7fffffff) return KDA_ERR_SHAPE;
-  if (x.c_stride < int64_t(x.page_size) * 512 || x.c_stride > (int64_t(1) << 32)) return KDA_ERR_SHAPE;
-  if (x.scale_stride < int64_t(x.page_size) * 4 || x.scale_stride > (int64_t(1) << 32)) return KDA_ERR_SHAPE;
-  if (x.s_stride < int64_t(x.page_size) * 64 || x.s_stride > (int64_t(1) << 31)) return KDA_ERR_SHAPE;
+  if (x.c_stride < int64_t(x.page_size) * 512 || x.c_stride >= (int64_t(1) << 32)) return KDA_ERR_SHAPE;
+  if (x.scale_stride < int64_t(x.page_size) * 4 || x.scale_stride >= (int64_t(1) << 32)) return KDA_ERR_SHAPE;
+  if (x.s_stride < int64_t(x.page_size) * 64 || x.s_stride >= (int64_t(1) << 31)) return KDA_ERR_SHAPE;
   return x.c_stride % 16 == 0 && x.scale_stride % 4 == 0 && x.s_stride % 8 == 0 ? KDA_OK : KDA_ERR_ALIGN;
 }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

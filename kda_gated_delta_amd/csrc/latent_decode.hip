@@ -110,6 +110,16 @@ __device__ __forceinline__ float quarter_sum(float x) {
   return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
+// Each lane's WIDE bytes at offset + more of `bytes` bytes, to WIDE * lane behind `to`.
+template <int WIDE>                          // 16 or 4
+__device__ __forceinline__ void load_lds(const void* from, int bytes, unsigned char* to, int offset, int more) {
+  const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(from), 0, bytes, 0x00020000);
+  if (WIDE == 16)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr*)to, 16, offset, more, 0, 0);
+  else
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr*)to, 4, offset, more, 0, 0);
+}
+
 // At most n loads are left, nothing else.
 template <int n>
 __device__ __forceinline__ void wait_loads() {
@@ -337,7 +347,8 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
 #pragma unroll
         for (int i = 1; i < kShare; ++i) mx = fmaxf(mx, top[i][16 * t + p16]);
         if (__any((mx - m[t]) * c > kSlack)) {
-          const float now = fmaxf(m[t], mx);
+          // (row by row: what a row sees does not change how another one is rounded)
+          const float now = (mx - m[t]) * c > kSlack ? mx : m[t];
           const float f = __builtin_amdgcn_exp2f((m[t] - base(now)) * c);
           m[t] = now;
           if (t == mine) l *= f;
@@ -448,6 +459,374 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
   }
 }
 
+// ---------------------------------------------------------------- over 32 rows
+
+// Eight waves, in pairs of one that makes weights and one that uses them (a unit
+// later), one of each kind on every SIMD: of the scores a wave has all 32 keys of one
+// or two row tiles, so that maxima and sums are its own, of the output 128 columns of
+// all row tiles, which are one block of every token's scales.  The output's waves also
+// bring the tokens.
+constexpr int kWideThreads = 512;
+
+// A scale: byte `block` of a token's four exponents, as a factor.
+__device__ __forceinline__ float scale_of(uint32_t exponents, int block) {
+  return __uint_as_float((exponents >> (8 * block) & 255u) << 23);
+}
+
+// NT: row tiles of 16.
+template <int NT>
+__global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Params p) {
+  constexpr int kOwnRows = NT <= 4 ? 1 : 2;                // row tiles of a wave's scores
+  constexpr int kWideRing = 4;                             // units in LDS
+  constexpr int kWideBytes = kScale + kUnit * kBlocks;
+  __shared__ __align__(1024) struct {
+    unsigned char ring[kWideRing][kWideBytes];
+    unsigned char weights[2][kBlocks][NT][1024];
+    float factor[2][16 * NT];                              // of the output so far
+    int grown[2][kWaves];                                  // whether a wave has factors that are not 1
+    float sum[16 * NT], top[16 * NT];
+    int there[kWideRing][kWaves];                          // whether a wave's tokens have a page
+  } lds;
+  auto &ring = lds.ring;
+  auto &weights = lds.weights;
+  auto &there = lds.there;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int role = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
+
+  const Piece piece = kda::line::find_piece<kUnit, 1>(p, 0, p.row_tiles);
+  int64_t left = piece.to - piece.from;
+  int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
+  const int64_t inside = piece.from - piece.before;
+  int seg = __builtin_amdgcn_readfirstlane(int(inside / units));
+  int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * units));
+  bool begun = false;                                      // the piece's first segment is done
+  const float c = p.scale * kLog2e;
+
+  while (left > 0) {
+    // -------- one segment: sequence n, rows row0 .. row0 + tile_rows - 1
+    const int row0 = seg * p.tile_rows;
+    const int last = int(min(int64_t(units), first + left));
+    const int rows = min(p.rows - row0, p.tile_rows);
+    const bool whole = first == 0 && last == units;
+    const int64_t segment = int64_t(n) * p.row_tiles + seg;
+    const int slot = 2 * piece.w + int(begun);
+
+    if (role == 0) {
+      // ======== weights of row tiles mine ..
+      const int mine = wave * kOwnRows;
+      const bool busy = 16 * mine < rows;
+      // Rows of Q as operands.  Along a key the order is what lanes of 16 codes make it:
+      // steps 2 i and 2 i + 1 are the first and second 8 of lane group g4's 16.
+      bf16x8 q[kOwnRows][18];
+      int limit[kOwnRows];                                 // tokens that the lane's row sees
+#pragma unroll
+      for (int t = 0; t < kOwnRows; ++t) {
+        const int r = row0 + min(16 * (mine + t) + l16, rows - 1), i = r / p.H;
+        const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (r - i * p.H) * (R + S);
+#pragma unroll
+        for (int s = 0; s < 16; ++s)
+          q[t][s] = *reinterpret_cast<const bf16x8*>(src + 64 * (s >> 1) + 16 * g4 + 8 * (s & 1));
+#pragma unroll
+        for (int s = 0; s < 2; ++s) q[t][16 + s] = *reinterpret_cast<const bf16x8*>(src + R + 32 * s + 8 * g4);
+        limit[t] = len - p.Q + i + 1;
+      }
+      wait_loads<0>();
+      float m[kOwnRows], l[kOwnRows];                      // l: of this lane's keys only, until the end
+#pragma unroll
+      for (int t = 0; t < kOwnRows; ++t) m[t] = -INFINITY, l[t] = 0.0f;
+
+      for (int unit = first; unit < last; ++unit) {
+        kda::lds_barrier();                                // the unit is there
+        if (!busy) {
+          if (lane == 0) lds.grown[unit & 1][wave] = 0;
+          continue;
+        }
+        unsigned char* tile = ring[unit % kWideRing];
+        const int key0 = unit * kUnit;
+        const bool edge = key0 + kUnit > len - p.Q + 1;    // some row does not see some key
+        const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
+        f32x4 s[2][kOwnRows];
+        u32x4 own[2];                                      // the exponents of this lane's keys, 16 k + 4 g4 + e
+        {
+          // Of a key's 20 pieces of 16 bytes (eight of codes, two steps each, and two of the
+          // shared part) kAhead are on their way.
+          constexpr int kAhead = 4;
+          u32x4 a[kAhead];
+          uint32_t scales[2];
+          const int key_at = l16 * R + ((g4 ^ swirl(l16)) * 16);
+          const int shared_at = kShared + l16 * 2 * S + ((g4 ^ swirl2(l16)) * 16);
+          auto fetch = [&](int i) {
+            const int k = i & 1, at = i >> 1;
+            int x = at < 8 ? key_at : shared_at;
+            asm("" : "+v"(x));                             // (its variants are not worth a register each)
+            a[i % kAhead] = *reinterpret_cast<const u32x4*>(  // (swirl(16 + l16) = swirl(l16) ^ 8)
+                at < 8 ? tile + k * 16 * R + (x ^ at * 64 ^ k * 128) : tile + k * 32 * S + (x ^ (at - 8) * 64));
+          };
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            scales[k] = *reinterpret_cast<const uint32_t*>(tile + kScale + (16 * k + l16) * kBlocks);
+#pragma unroll
+          for (int i = 0; i < kAhead - 1; ++i) fetch(i);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int t = 0; t < kOwnRows; ++t) s[k][t] = (f32x4)(0.0f);
+#pragma unroll
+          for (int i = 0; i < 20; ++i) {
+            const int k = i & 1, at = i >> 1;
+            fence();
+            if (i + kAhead - 1 < 20) fetch(i + kAhead - 1);
+            if (i >= 18) own[k] = *reinterpret_cast<const u32x4*>(tile + kScale + (16 * k + 4 * g4) * kBlocks);
+            fence();
+            const u32x4 x = a[i % kAhead];
+            if (at < 8) {
+              const float f = scale_of(scales[k], at >> 1);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const bf16x8 y = widen(x[2 * half], x[2 * half + 1], f);
+#pragma unroll
+                for (int t = 0; t < kOwnRows; ++t) s[k][t] = mfma16(y, q[t][2 * at + half], s[k][t]);
+              }
+            } else {
+#pragma unroll
+              for (int t = 0; t < kOwnRows; ++t) s[k][t] = mfma16(as_bf16x8(x), q[t][at + 8], s[k][t]);
+            }
+          }
+          fence();
+        }
+        bool gone[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) gone[k] = there[unit % kWideRing][2 * k + (g4 >> 1)] == 0;
+        if (edge || __any(gone[0] || gone[1])) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int t = 0; t < kOwnRows; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (gone[k] || key0 + 16 * k + 4 * g4 + e >= limit[t]) s[k][t][e] = -INFINITY;
+        }
+        bool grown = false;
+#pragma unroll
+        for (int t = 0; t < kOwnRows; ++t) {
+          float mx = s[0][t][0];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[k][t][e]);
+          mx = quarter_max(mx);
+          // (row by row: what a row sees does not change how another one is rounded)
+          const float now = (mx - m[t]) * c > kSlack ? mx : m[t];
+          const float f = __builtin_amdgcn_exp2f((m[t] - base(now)) * c);
+          grown |= now != m[t];
+          m[t] = now;
+          l[t] *= f;
+          if (g4 == 0) lds.factor[unit & 1][16 * (mine + t) + l16] = f;
+          const float b = base(now) * c;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[k][t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][t][e], c, -b));
+              l[t] += s[k][t][e];
+            }
+        }
+        grown = __any(grown);
+        if (lane == 0) lds.grown[unit & 1][wave] = grown;
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d) {                // as operands, times each block's scales
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[4 * k + e] = scale_of(own[k][e], d);
+#pragma unroll
+          for (int t = 0; t < kOwnRows; ++t) {
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[4 * k + e] = s[k][t][e] * f[4 * k + e];
+            *reinterpret_cast<bf16x8*>(weights[unit & 1][d][mine + t] + lane * 16) = pack8(x);
+          }
+        }
+      }
+      kda::lds_barrier();                                  // the last weights are there
+      if (busy) {
+#pragma unroll
+        for (int t = 0; t < kOwnRows; ++t) {
+          l[t] = quarter_sum(l[t]);
+          if (g4 == 0) {
+            lds.sum[16 * (mine + t) + l16] = l[t];
+            lds.top[16 * (mine + t) + l16] = m[t];
+          }
+        }
+      }
+      kda::lds_barrier();                                  // and sums and maxima
+      if (threadIdx.x == 0) {
+        if (first == 0) p.owner[segment] = whole ? -1 : slot;
+        if (first != 0 && last == units) p.last_owner[segment] = piece.w;
+      }
+    } else {
+      // ======== columns 128 wave ..
+      // The slots of this wave's first tokens in 64 units, one to a lane; -1: no page.
+      const int32_t* table = p.table + n * p.table_stride;
+      int from = 0, slots = -1;
+      auto look = [&](int unit) {
+        from = unit;
+        slots = -1;
+        const int64_t token = int64_t(unit + lane_now()) * kUnit + wave * kOwn;
+        if (token < len) {
+          const int id = table[token >> p.shift];
+          if (id >= 0 && id < p.num_pages) slots = (id << p.shift) + (int(token) & ((1 << p.shift) - 1));
+        }
+      };
+      // They come as buffers that end behind the sequence, or are empty: what is not
+      // there is zero in LDS.  (Behind the last unit nothing comes.)
+      auto load = [&](int unit) {
+        if (unit - from >= 64) look(unit);
+        const int slot = __builtin_amdgcn_readlane(slots, unit - from);
+        const int some = slot < 0 ? 0 : min(len - (unit * kUnit + wave * kOwn), kOwn);
+        const int64_t page = max(slot, 0) >> p.shift;
+        const int at = max(slot, 0) & ((1 << p.shift) - 1);
+        const int lane = lane_now();
+        if (lane == 0) there[unit % kWideRing][wave] = some;
+        unsigned char* to = ring[unit % kWideRing];
+        const int r0 = wave * kOwn;
+        const int piece0 = (lane & 31) ^ swirl(r0) ^ (lane >> 5);
+#pragma unroll
+        for (int j = 0; j < kOwn / 2; ++j)                 // two lines each
+          load_lds<16>(p.codes + page * p.c_stride + at * R, some * R, to + r0 * R + j * 1024,
+                       (lane >> 5) * R + (piece0 ^ 2 * j) * 16, j * 1024);
+        load_lds<16>(p.shared + page * p.s_stride + at * S, some * 2 * S, to + kShared + r0 * 2 * S,  // eight lines
+                     (lane >> 3) * 2 * S + ((lane & 7) ^ swirl2(r0 + (lane >> 3))) * 16, 0);
+        if (lane < kOwn)
+          load_lds<4>(p.exponents + page * p.scale_stride + at * kBlocks, some * kBlocks, to + kScale + r0 * kBlocks,
+                      lane * 4, 0);
+      };
+      if (begun) wait_loads<0>();                          // (stores, that would count among the loads)
+      look(first);
+#pragma unroll
+      for (int i = 0; i < kWideRing - 2; ++i) load(first + i);
+      f32x4 o[NT][8];                                      // column 128 wave + 16 d + 4 g4 + e of row 16 t + l16
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[t][d] = (f32x4)(0.0f);
+
+      for (int unit = first; unit <= last; ++unit) {
+        // this wave's tokens of the unit are there
+        wait_loads<(kWideRing - 3) * kLoads>();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        // A token that only some of the queries see may hold codes of NaN, which a
+        // weight of zero would not keep out of the others' products: its latent becomes
+        // zero and its shared part NaN, which gives the same to those that see it (their
+        // scores are NaN) and nothing to the others.
+        if (p.Q > 1 && unit < last && unit * kUnit + kUnit > len - p.Q + 1) {
+          unsigned char* tile = ring[unit % kWideRing];
+          const int lane = lane_now();
+#pragma unroll 1
+          for (int i = wave * kOwn; i < wave * kOwn + kOwn; ++i) {
+            u32x2* code = reinterpret_cast<u32x2*>(tile + i * R) + lane;
+            const u32x2 x = *code;
+            const uint32_t nan = ((x[0] & 0x7f7f7f7fu) + 0x01010101u) | ((x[1] & 0x7f7f7f7fu) + 0x01010101u);
+            if (!__any(nan & 0x80808080u)) continue;
+            *code = (u32x2){0, 0};
+            if (lane < 32) reinterpret_cast<uint32_t*>(tile + kShared + i * 2 * S)[lane] = 0x7fc07fc0u;
+          }
+        }
+        kda::lds_barrier();                                // and the weights of the unit before
+        if (unit < last) load(unit + kWideRing - 2);
+        if (unit == first) continue;
+
+        // -------- the unit before: lane l16 takes column l16 of 16 at keys 16 (j / 4) + 4 g4 +
+        // j % 4 for j = 0 .. 7, the order in which the scores hold them.  (A transposing
+        // read gathers, in every 16 lanes, byte i & 7 of the 8-byte pieces addressed by
+        // lanes (i >> 3) + 2 e into byte e of lane i.)
+        const int before = unit - 1;
+        unsigned char* tile = ring[before % kWideRing];
+        const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
+        const int line = ((l16 >> 1) & 3) + 4 * g4 + (l16 & 8) * 2;
+        const int place = line * R + ((8 * wave) ^ swirl(line)) * 16 + (l16 & 1) * 8;
+        constexpr int kTiles = 4, kAhead = 3;              // tiles of 16 columns at once; row tiles ahead
+        bf16x8 w[kAhead], x[kTiles];
+        u32x2 a[kTiles];
+        auto fetch = [&](int group) {
+#pragma unroll
+          for (int d = 0; d < kTiles; ++d)
+            a[d] = __builtin_bit_cast(u32x2,
+                                      transposed((const lds_i32x2*)(tile + (place ^ (kTiles * group + d) * 16))));
+        };
+        auto fetch_weights = [&](int i) {
+          w[i % kAhead] = *reinterpret_cast<const bf16x8*>(weights[before & 1][wave][i % NT] + lane * 16);
+        };
+        const u32x4 grown = *reinterpret_cast<const u32x4*>(lds.grown[before & 1]);
+        fetch(0);
+        if (__builtin_amdgcn_readfirstlane(grown[0] | grown[1] | grown[2] | grown[3])) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float f = lds.factor[before & 1][16 * t + l16];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[t][d] *= f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead - 1; ++i) fetch_weights(i);
+#pragma unroll
+        for (int group = 0; group < 8 / kTiles; ++group) {
+#pragma unroll
+          for (int d = 0; d < kTiles; ++d) x[d] = widen(a[d][0], a[d][1], 1.0f);
+          fence();
+          if (group + 1 < 8 / kTiles) fetch(group + 1);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const int i = group * NT + t;
+            if (i + kAhead - 1 < 8 / kTiles * NT) fetch_weights(i + kAhead - 1);
+            fence();
+#pragma unroll
+            for (int d = 0; d < kTiles; ++d)
+              o[t][kTiles * group + d] = mfma16(x[d], w[i % kAhead], o[t][kTiles * group + d]);
+            fence();
+          }
+        }
+      }
+
+      // -------- its rows: finished, or a part
+      wait_loads<0>();                                     // (those that brought nothing, too)
+      kda::lds_barrier();
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int r = 16 * t + l16, col = 128 * wave + 4 * g4;
+        if (r >= rows) continue;
+        if (whole) {
+          const int64_t out = int64_t(n) * p.rows + row0 + r;
+          const float sum = lds.sum[r], f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            const f32x4 x = o[t][d] * f;
+            *reinterpret_cast<u32x2*>(p.o + out * R + col + 16 * d) =
+                (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
+          }
+          if (p.lse && wave == 0 && g4 == 0) p.lse[out] = lds.top[r] * p.scale + __logf(sum);
+        } else {
+          float* to = p.parts + (int64_t(slot) * p.tile_rows + r) * kPart;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(to + col + 16 * d) = o[t][d];
+          if (wave == 0 && g4 == 0) to[R] = lds.top[r], to[R + 1] = lds.sum[r];
+        }
+      }
+    }
+    left -= last - first;
+    first = 0;
+    begun = true;
+    if (++seg == p.row_tiles) {
+      seg = 0;
+      if (++n < p.N) len = length(p, n), units = units_of<kUnit>(len);
+    }
+  }
+}
+
 // ---------------------------------------------------------------- joining the parts
 
 // A workgroup takes join_rows rows of a segment, one after another: two streams of
@@ -521,13 +900,14 @@ struct Plan {
   size_t parts, bytes;
 };
 
-// Rows in tiles of 64, or of 32 where that leaves fewer unused.
+// Up to 32 rows go to the kernel of four waves, more, in equal tiles of up to 128, to
+// the one of eight.
 Plan plan_for(int64_t N, int64_t Q, int H) {
   Plan x;
   x.rows = int(Q * H);
-  x.tile_rows = (x.rows + 31) / 32 % 2 ? 32 : 64;
-  x.row_tiles = (x.rows + x.tile_rows - 1) / x.tile_rows;
-  x.pieces = kda::device_cus() * kPerCu;
+  x.row_tiles = (x.rows + 95) / 96;
+  x.tile_rows = ((x.rows + x.row_tiles - 1) / x.row_tiles + 15) / 16 * 16;
+  x.pieces = kda::device_cus() * (x.tile_rows <= 32 ? kPerCu : 1);
   x.segments = N * x.row_tiles;
   x.parts = size_t(2 * x.pieces) * x.tile_rows * kPart * sizeof(float);
   x.bytes = x.parts + size_t(x.segments) * 2 * sizeof(int);
@@ -537,11 +917,6 @@ Plan plan_for(int64_t N, int64_t Q, int H) {
 int sizes(int32_t N, int32_t Q, int32_t H) {
   if (N < 0 || Q < 1 || Q > 1024 || H < 1 || H > 65535) return KDA_ERR_SHAPE;
   return int64_t(N) * Q * H > (1 << 24) ? KDA_ERR_SHAPE : KDA_OK;
-}
-
-template <int NT>
-void launch(const Params& p, int pieces, hipStream_t stream) {
-  hipLaunchKernelGGL(latent_decode_kernel<NT>, dim3(unsigned(pieces)), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace
@@ -586,10 +961,13 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
                  scale, static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, join_rows, x.pieces,
                  static_cast<float*>(workspace), owner, owner + x.segments};
   const hipStream_t st = kda::as_stream(stream);
-  if (x.tile_rows == 32)
-    launch<2>(p, x.pieces, st);
+  const dim3 grid(unsigned(x.pieces));
+  if (x.tile_rows <= 32)
+    hipLaunchKernelGGL(latent_decode_kernel<2>, grid, dim3(kThreads), 0, st, p);
+  else if (x.tile_rows <= 64)
+    hipLaunchKernelGGL(latent_decode_wide_kernel<4>, grid, dim3(kWideThreads), 0, st, p);
   else
-    launch<4>(p, x.pieces, st);
+    hipLaunchKernelGGL(latent_decode_wide_kernel<6>, grid, dim3(kWideThreads), 0, st, p);
   const unsigned joins = unsigned(x.segments * ((tile + join_rows - 1) / join_rows));
   hipLaunchKernelGGL(latent_decode_join_kernel, dim3(joins), dim3(256), 0, st, p);
   return kda::launch_status();

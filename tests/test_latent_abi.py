@@ -106,9 +106,9 @@ def decode(**kw):
 def test_cache_layout(call):
     for P in (0, 8, 100, 512):
         assert call(P=P, cp=1 << 20, sp=1 << 20, kp=1 << 20) == E_UNSUPPORTED
-    assert call(cp=64 * 512 - 16) == E_SHAPE and call(cp=64 * 512 + 8) == E_ALIGN and call(cp=(1 << 32) + 16) == E_SHAPE
-    assert call(sp=64 * 4 - 4) == E_SHAPE and call(sp=64 * 4 + 2) == E_ALIGN and call(sp=(1 << 32) + 4) == E_SHAPE
-    assert call(kp=64 * 64 - 8) == E_SHAPE and call(kp=64 * 64 + 4) == E_ALIGN and call(kp=(1 << 31) + 8) == E_SHAPE
+    assert call(cp=64 * 512 - 16) == E_SHAPE and call(cp=64 * 512 + 8) == E_ALIGN and call(cp=1 << 32) == E_SHAPE
+    assert call(sp=64 * 4 - 4) == E_SHAPE and call(sp=64 * 4 + 2) == E_ALIGN and call(sp=1 << 32) == E_SHAPE
+    assert call(kp=64 * 64 - 8) == E_SHAPE and call(kp=64 * 64 + 4) == E_ALIGN and call(kp=1 << 31) == E_SHAPE
     assert call(pages=-1) == E_SHAPE and call(pages=1 << 25) == E_SHAPE
     for name in ("cc", "cs", "kc"):
         assert call(**{name: NULL}) == E_NULL
