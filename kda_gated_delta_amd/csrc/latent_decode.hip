@@ -5,20 +5,35 @@
 // latent, 512 wide, the same for all heads.  For query token i of Q (its position is
 // len - Q + i) and head h, over the tokens j <= len - Q + i of the sequence:
 //     z_j = scale q . [c_j s_j],   o = sum_j softmax(z)_j c_j.
-// The Q queries of all heads are rows of one matrix, in tiles of at most 128.
+// The Q queries of all heads are rows of one matrix, in tiles of at most 96.
 //
-// All (sequence, row tile) segments in order, in units of tokens, form one line
+// All (sequence, row tile) segments in order, in units of 32 tokens, form one line
 // that is cut into equal pieces, one per workgroup (attn_line.h); a segment that
 // lies in several leaves float32 parts, which latent_decode_join_kernel adds up.
 //
 // A unit lies in LDS as it came, in codes, and is used twice: S^T = [C s] Q^T, with Q
 // in registers, and O^T += C^T P^T, where each wave has 128 of the 512 columns for all
 // rows, so that a column is read (transposed) by one wave only.  Codes become
-// bfloat16 on their way from LDS into the operands.  A token's 128 values under one
-// scale are one wave's columns: a key's scales enter as it is widened, a value's
-// enter the weights, which go from the waves that made them to all through LDS, as
-// operands, in four versions.  The running maximum is common to the waves, sum and
-// output are float32.  The next units are on their way to LDS meanwhile.
+// bfloat16 (exactly) on their way from LDS into the operands.  A token's 128 values
+// under one scale are one wave's columns: a key's scales enter as it is widened, a
+// value's enter the weights, which go from the waves that made them to all through
+// LDS, as operands.  The one rounding on the way is the weights', to bfloat16; scores,
+// maximum, sum and output are float32.  The next units are on their way to LDS
+// meanwhile.
+//
+// What bounds it: up to 32 rows the reads of the cache (64 sequences of up to 16384
+// tokens, 32 heads, 327 MB: 96 us; the walk takes 86, of which 66 are spent in units, at
+// 4.9 TB/s, the card's copying rate, and the rest before its first unit and on its
+// parts).  With more rows it is a unit's conversions, products and weights (48
+// sequences of up to 8192 tokens, 96 heads, 41 GFLOP: 94 us; 4100 cycles for a unit's
+// 96 rows, of which products 1900, and twice 12 us for 50 MB of parts).
+//
+// Tried and left: units widened once, as bfloat16 in LDS, which then cannot feed the
+// products (115 and 101 us); for 32 rows one workgroup of eight waves per compute unit
+// with the keys split over four pairs of waves (111) or all waves at one unit of 64
+// tokens (104), which pause together where two workgroups fill each other's pauses;
+// for 96 rows waves that hold 16 rows and all columns (118), and waves that go through
+// scores, weights and output together (115).
 #include "attn_line.h"
 #include "kda_host.h"
 #include "latent_device.h"
@@ -30,9 +45,14 @@ using kda::line::Piece;
 using kda::line::length;
 using kda::line::units_of;
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kPart = R + 4;                 // floats of a part's row: output, maximum, sum
+constexpr int kWaves = 4;                    // that bring a unit, and have its columns
+// A part: output, as the waves hold it ([row tile of 16][32 tiles of 16 columns][64
+// lanes][4], lane l16 + 16 g4 with columns 4 g4 + e of row l16), then each row's
+// maximum and sum.  Every store and load of a wave is then 1 KB in one piece.
+constexpr int kPart = R + 2;                 // floats for a row
+__device__ __forceinline__ int64_t in_part(int row_tile, int column_tile, int lane) {
+  return ((int64_t(row_tile) * (R / 16) + column_tile) * 64 + lane) * 4;
+}
 
 struct Params {
   const uint16_t* q;
@@ -47,9 +67,9 @@ struct Params {
   float scale;
   uint16_t* o;
   float* lse;
-  int rows, tile_rows, row_tiles, join_rows; // Q x H; rows of one tile; tiles; rows of a joining workgroup
+  int rows, tile_rows, row_tiles;         // Q x H; rows of one tile (a multiple of 16); tiles
   int waves;                                 // pieces
-  float* parts;                              // [2 x pieces][tile_rows][kPart]: a piece has one of its first segment, one of its last
+  float* parts;                              // [2 x pieces][tile_rows x kPart]: a piece has one of its first segment, one of its last
   int *owner, *last_owner;                   // [segments]: first part and last piece of those cut, -1 for the others
 };
 
@@ -68,11 +88,10 @@ __device__ __forceinline__ bf16x8 widen(uint32_t x, uint32_t y, float f) {
 }
 
 constexpr int kUnit = 32;                    // tokens of a unit
-constexpr int kRing = 3;                     // units in LDS
-constexpr int kPerCu = 2;                    // workgroups of a compute unit
 constexpr int kOwn = kUnit / kWaves;         // tokens that a wave brings, all in one page
 constexpr int kLoads = kOwn / 2 + 2;         // of a wave for a unit
-// A unit in LDS: codes [kUnit][512], shared parts [kUnit][128 bytes], exponents.
+// A unit in LDS: codes [kUnit][512], shared parts [kUnit][128 bytes], exponents (of
+// kOwn tokens in 256 bytes).
 constexpr int kShared = kUnit * R, kScale = kShared + kUnit * 2 * S, kBytes = kScale + kWaves * 256;
 
 // Places of 16-byte pieces in a unit's lines: piece c of line r is at c ^ swirl(r), of
@@ -126,17 +145,95 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt(kWaitLoads | (n & 15) | (n >> 4) << 14);
 }
 
-// NT: row tiles of 16.
-template <int NT>
+// A scale: byte `block` of a token's four exponents, as a factor.
+__device__ __forceinline__ float scale_of(uint32_t exponents, int block) {
+  return __uint_as_float((exponents >> (8 * block) & 255u) << 23);
+}
+// A key's four exponents in a unit, and those of four successive keys.
+__device__ __forceinline__ const unsigned char* exponents_of(const unsigned char* tile, int key) {
+  return tile + kScale + key / kOwn * 256 + key % kOwn * kBlocks;
+}
+
+// How a wave brings its kOwn tokens of a segment's units.
+struct Tokens {
+  const int32_t* table;
+  int len, wave;
+  int from, slots;         // the slots of the first tokens in 64 units, one to a lane; -1: no page
+
+  struct Source {
+    const uint8_t* codes;
+    const uint16_t* shared;
+    const uint8_t* exponents;
+    int some;              // tokens
+    unsigned char* tile;
+  };
+
+  __device__ __forceinline__ void look(const Params& p, int unit) {
+    from = unit;
+    slots = -1;
+    const int64_t token = int64_t(unit + lane_now()) * kUnit + wave * kOwn;
+    if (token < len) {
+      const int id = table[token >> p.shift];
+      if (id >= 0 && id < p.num_pages) slots = (id << p.shift) + (int(token) & ((1 << p.shift) - 1));
+    }
+  }
+  // There: whether the wave's tokens have a page.
+  __device__ __forceinline__ Source source(const Params& p, int unit, unsigned char* tile, int* there) {
+    if (unit - from >= 64) look(p, unit);
+    const int slot = __builtin_amdgcn_readlane(slots, unit - from);
+    const int some = slot < 0 ? 0 : min(len - (unit * kUnit + wave * kOwn), kOwn);
+    const int64_t page = max(slot, 0) >> p.shift;
+    const int at = max(slot, 0) & ((1 << p.shift) - 1);
+    if (lane_now() == 0) there[wave] = some;
+    return Source{p.codes + page * p.c_stride + at * R, p.shared + page * p.s_stride + at * S,
+                  p.exponents + page * p.scale_stride + at * kBlocks, some, tile};
+  }
+  // Load i of kLoads.  They come as buffers that end behind the sequence, or are empty:
+  // what is not there is zero in LDS.
+  __device__ __forceinline__ void load(const Source& x, int i) const {
+    const int lane = lane_now(), r0 = wave * kOwn;
+    if (i < kOwn / 2)                                      // two lines
+      load_lds<16>(x.codes, x.some * R, x.tile + r0 * R + i * 1024,
+                   (lane >> 5) * R + (((lane & 31) ^ swirl(r0) ^ (lane >> 5)) ^ 2 * i) * 16, i * 1024);
+    else if (i == kOwn / 2)                                // eight lines
+      load_lds<16>(x.shared, x.some * 2 * S, x.tile + kShared + r0 * 2 * S,
+                   (lane >> 3) * 2 * S + ((lane & 7) ^ swirl2(r0 + (lane >> 3))) * 16, 0);
+    else
+      load_lds<4>(x.exponents, x.some * kBlocks, x.tile + kScale + wave * 256, lane * 4, 0);
+  }
+  // A token that only some of the queries see may hold codes of NaN, which a weight of
+  // zero would not keep out of the others' products: its latent becomes zero and its
+  // shared part NaN, which gives the same to those that see it (their scores are NaN)
+  // and nothing to the others.
+  __device__ __forceinline__ void without_nan(unsigned char* tile) const {
+    const int lane = lane_now();
+#pragma unroll 1
+    for (int i = wave * kOwn; i < wave * kOwn + kOwn; ++i) {
+      u32x2* code = reinterpret_cast<u32x2*>(tile + i * R) + lane;
+      const u32x2 x = *code;
+      const uint32_t nan = ((x[0] & 0x7f7f7f7fu) + 0x01010101u) | ((x[1] & 0x7f7f7f7fu) + 0x01010101u);
+      if (!__any(nan & 0x80808080u)) continue;
+      *code = (u32x2){0, 0};
+      if (lane < 32) reinterpret_cast<uint32_t*>(tile + kShared + i * 2 * S)[lane] = 0x7fc07fc0u;
+    }
+  }
+};
+
+// ---------------------------------------------------------------- up to 32 rows
+
+// Four waves; of a unit's scores a wave has 16 keys and 16 rows.  Two workgroups on a
+// compute unit: one has its pauses while the other computes.
+constexpr int kThreads = 64 * kWaves, kPerCu = 2, kRing = 3;
+constexpr int kRowTiles = 2;
+
 __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params p) {
-  constexpr int kShare = kWaves / NT, kKeys = 2 / kShare;  // waves that split a row's keys; key tiles of 16 for each
   // (One object: between two the compiler tells apart what loads to LDS write, and
   // has reads wait for all those that are on their way to the same one.)
   __shared__ __align__(1024) struct {
     unsigned char ring[kRing][kBytes];
-    unsigned char weights[kBlocks][NT][1024];
+    unsigned char weights[kBlocks][kRowTiles][1024];
     float scales[kUnit][kBlocks];
-    float top[kShare][16 * NT];                            // maxima of a unit, and in the end sums
+    float top[2][16 * kRowTiles];                          // maxima of a unit, and in the end sums
     int there[kRing][kWaves];                              // whether a wave's tokens have a page
   } lds;
   auto &ring = lds.ring;
@@ -146,7 +243,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
   auto &there = lds.there;
   const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int share = wave % kShare, mine = wave / kShare;   // the wave's keys, and its row tile
+  const int half = wave & 1, mine = wave >> 1;             // the wave's key tile, and its row tile
 
   const Piece piece = kda::line::find_piece<kUnit, 1>(p, 0, p.row_tiles);
   int64_t left = piece.to - piece.from;
@@ -161,51 +258,16 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
     // -------- one segment: sequence n, rows row0 .. row0 + tile_rows - 1
     const int row0 = seg * p.tile_rows;
     const int last = int(min(int64_t(units), first + left));
-    const int rows = min(min(p.rows - row0, p.tile_rows), 16 * NT);
+    const int rows = min(p.rows - row0, p.tile_rows);
 
-    // The slots of this wave's first tokens in 64 units, one to a lane; -1: no page.
-    const int32_t* table = p.table + n * p.table_stride;
-    int from = 0, slots = -1;
-    auto look = [&](int unit) {
-      from = unit;
-      slots = -1;
-      const int64_t token = int64_t(unit + lane_now()) * kUnit + wave * kOwn;
-      if (token < len) {
-        const int id = table[token >> p.shift];
-        if (id >= 0 && id < p.num_pages) slots = (id << p.shift) + (int(token) & ((1 << p.shift) - 1));
-      }
-    };
-    // They come as buffers that end behind the sequence, or are empty: what is not
-    // there is zero in LDS.
+    Tokens tokens{p.table + n * p.table_stride, len, wave, 0, -1};
     auto load = [&](int unit) {
-      if (unit - from >= 64) look(unit);
-      const int slot = __builtin_amdgcn_readlane(slots, unit - from);
-      const int some = slot < 0 ? 0 : min(len - (unit * kUnit + wave * kOwn), kOwn);
-      const int64_t page = max(slot, 0) >> p.shift;
-      const int at = max(slot, 0) & ((1 << p.shift) - 1);
-      const auto cs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.codes + page * p.c_stride + at * R), 0,
-                                                        some * R, 0x00020000);
-      const auto ss = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(p.shared + page * p.s_stride + at * S), 0,
-                                                        some * 2 * S, 0x00020000);
-      const auto es = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint8_t*>(p.exponents + page * p.scale_stride + at * kBlocks), 0, some * kBlocks, 0x00020000);
-      const int lane = lane_now();
-      if (lane == 0) there[unit % kRing][wave] = some;
-      unsigned char* to = ring[unit % kRing];
-      const int r0 = wave * kOwn;
-      const int piece0 = (lane & 31) ^ swirl(r0) ^ (lane >> 5);
+      const auto next = tokens.source(p, unit, ring[unit % kRing], there[unit % kRing]);
 #pragma unroll
-      for (int j = 0; j < kOwn / 2; ++j)                   // two lines each
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(cs, (lds_ptr*)(to + r0 * R + j * 1024), 16,
-                                                 (lane >> 5) * R + (piece0 ^ 2 * j) * 16, j * 1024, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(            // eight lines
-          ss, (lds_ptr*)(to + kShared + r0 * 2 * S), 16,
-          (lane >> 3) * 2 * S + ((lane & 7) ^ swirl2(r0 + (lane >> 3))) * 16, 0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(es, (lds_ptr*)(to + kScale + wave * 256), 4, lane * 4, 0, 0, 0);
+      for (int i = 0; i < kLoads; ++i) tokens.load(next, i);
     };
-
     if (begun) wait_loads<0>();                            // (stores, that would count among the loads)
-    look(first);
+    tokens.look(p, first);
     // Rows of Q as operands.  Along a key the order is what lanes of 16 codes make it:
     // steps 2 i and 2 i + 1 are the first and second 8 of lane group g4's 16.
     bf16x8 q[18];
@@ -227,10 +289,10 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
     // The queries are waited for before the first unit: left to the compiler they would
     // be in every unit, and with them the loads behind them.
     wait_loads<0>();
-    f32x4 o[NT][8];                                        // column 128 wave + 16 d + 4 g4 + e of row 16 t + l16
-    float m[NT], l = 0.0f;                                 // m: of all rows; l: own row tile and keys
+    f32x4 o[kRowTiles][8];                                       // column 128 wave + 16 d + 4 g4 + e of row 16 t + l16
+    float m[kRowTiles], l = 0.0f;                          // m: of all rows; l: own row tile and keys
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < kRowTiles; ++t) {
       m[t] = -INFINITY;
 #pragma unroll
       for (int d = 0; d < 8; ++d) o[t][d] = (f32x4)(0.0f);
@@ -252,100 +314,64 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
       if (place_lane < kOwn * kBlocks)
         scales[wave * kOwn + (place_lane >> 2)][place_lane & 3] =
             __uint_as_float(uint32_t(tile[kScale + wave * 256 + place_lane]) << 23);
-      // A token that only some of the queries see may hold codes of NaN, which a
-      // weight of zero would not keep out of the others' products: its latent becomes
-      // zero and its shared part NaN, which gives the same to those that see it (their
-      // scores are NaN) and nothing to the others.
-      if (edge && p.Q > 1) {
-#pragma unroll 1
-        for (int i = 0; i < kOwn; ++i) {
-          u32x2* code = reinterpret_cast<u32x2*>(tile + (wave * kOwn + i) * R) + place_lane;
-          const u32x2 x = *code;
-          const uint32_t nan = ((x[0] & 0x7f7f7f7fu) + 0x01010101u) | ((x[1] & 0x7f7f7f7fu) + 0x01010101u);
-          if (!__any(nan & 0x80808080u)) continue;
-          *code = (u32x2){0, 0};
-          if (place_lane < 32)
-            reinterpret_cast<uint32_t*>(tile + kShared + (wave * kOwn + i) * 2 * S)[place_lane] = 0x7fc07fc0u;
-        }
-      }
+      if (edge && p.Q > 1) tokens.without_nan(tile);
       kda::lds_barrier();                                  // everybody's; and the unit before is used up
       if (unit + kRing - 1 < last) load(unit + kRing - 1);
 
-      // -------- scores of the row tile and kKeys key tiles (rows = keys)
-      f32x4 s[kKeys];
+      // -------- scores of 16 keys (rows) and 16 rows (columns)
+      f32x4 s = (f32x4)(0.0f);
       {
-        float f[2][kKeys];                                 // the scales of a block, and of the next
-        auto fetch_scale = [&](int block) {
-#pragma unroll
-          for (int k = 0; k < kKeys; ++k) f[block & 1][k] = scales[16 * (share * kKeys + k) + p16][block];
-        };
+        float f[2];                                        // the scale of a block, and of the next
+        auto fetch_scale = [&](int block) { f[block & 1] = scales[16 * half + p16][block]; };
         fetch_scale(0);
-#pragma unroll
-        for (int k = 0; k < kKeys; ++k) s[k] = (f32x4)(0.0f);
-        // Rounds of kAhead pieces of 16 bytes: eight of codes, two steps each, and two of
-        // the shared part.
-        constexpr int kAhead = 2 / kKeys, kRounds = 10 / kAhead;
-        u32x4 a[2][kAhead][kKeys];
+        // Rounds of two pieces of 16 bytes: eight of codes, two steps each, and two of the
+        // shared part.
+        u32x4 a[2][2];
         auto fetch = [&](int round) {
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-            for (int k = 0; k < kKeys; ++k) {
-              const int at = round * kAhead + i, key = 16 * (share * kKeys + k) + p16;
-              const unsigned char* from =
-                  at < 8 ? tile + key * R + ((p4 ^ p16 ^ (share * kKeys + k) * 8) * 16 ^ at * 64)
-                         : tile + kShared + key * 2 * S + ((4 * (at - 8) + p4) ^ swirl2(p16)) * 16;
-              a[round & 1][i][k] = *reinterpret_cast<const u32x4*>(from);
-            }
+          for (int i = 0; i < 2; ++i) {
+            const int at = round * 2 + i, key = 16 * half + p16;
+            a[round & 1][i] = *reinterpret_cast<const u32x4*>(
+                at < 8 ? tile + key * R + ((p4 ^ p16 ^ half * 8) * 16 ^ at * 64)
+                       : tile + kShared + key * 2 * S + ((4 * (at - 8) + p4) ^ swirl2(p16)) * 16);
+          }
         };
         fetch(0);
 #pragma unroll
-        for (int round = 0; round < kRounds; ++round) {
+        for (int round = 0; round < 5; ++round) {
           fence();
-          if (round + 1 < kRounds) fetch(round + 1);
-          if (round * kAhead % 2 == 0 && round * kAhead < 6) fetch_scale(round * kAhead / 2 + 1);
+          if (round + 1 < 5) fetch(round + 1);
+          if (round < 3) fetch_scale(round + 1);
           fence();
 #pragma unroll
-          for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-#pragma unroll
-              for (int k = 0; k < kKeys; ++k) {
-                const int at = round * kAhead + i;
-                const u32x4 x = a[round & 1][i][k];
-                if (at < 8)
-                  s[k] = mfma16(widen(x[2 * half], x[2 * half + 1], f[at >> 1 & 1][k]), q[2 * at + half], s[k]);
-                else if (half == 0)
-                  s[k] = mfma16(as_bf16x8(x), q[at + 8], s[k]);
-              }
-        }
-        fence();
-#pragma unroll
-        for (int k = 0; k < kKeys; ++k) {
-          const int key = 16 * (share * kKeys + k) + 4 * p4;
-          const bool gone = there[unit % kRing][key / kOwn] == 0;
-          if (edge || __any(gone)) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (gone || key0 + key + e >= limit) s[k][e] = -INFINITY;
+          for (int i = 0; i < 2; ++i) {
+            const int at = round * 2 + i;
+            const u32x4 x = a[round & 1][i];
+            if (at < 8) {
+              s = mfma16(widen(x[0], x[1], f[round & 1]), q[2 * at], s);
+              s = mfma16(widen(x[2], x[3], f[round & 1]), q[2 * at + 1], s);
+            } else {
+              s = mfma16(as_bf16x8(x), q[at + 8], s);
+            }
           }
         }
-        float mx = s[0][0];
+        fence();
+        const int key = 16 * half + 4 * p4;
+        const bool gone = there[unit % kRing][key / kOwn] == 0;
+        if (edge || __any(gone)) {
 #pragma unroll
-        for (int k = 0; k < kKeys; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[k][e]);
-        mx = quarter_max(mx);
-        if (p4 == 0) top[share][16 * mine + p16] = mx;
+          for (int e = 0; e < 4; ++e)
+            if (gone || key0 + key + e >= limit) s[e] = -INFINITY;
+        }
+        const float mx = quarter_max(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
+        if (p4 == 0) top[half][16 * mine + p16] = mx;
       }
       kda::lds_barrier();
 
       // -------- the maximum of all rows, the same in all waves; weights of the own ones
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float mx = top[0][16 * t + p16];
-#pragma unroll
-        for (int i = 1; i < kShare; ++i) mx = fmaxf(mx, top[i][16 * t + p16]);
+      for (int t = 0; t < kRowTiles; ++t) {
+        const float mx = fmaxf(top[0][16 * t + p16], top[1][16 * t + p16]);
         if (__any((mx - m[t]) * c > kSlack)) {
           // (row by row: what a row sees does not change how another one is rounded)
           const float now = (mx - m[t]) * c > kSlack ? mx : m[t];
@@ -357,27 +383,21 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
         }
       }
       {
-        float b = base(m[0]);
+        const float b = base(mine == 0 ? m[0] : m[1]) * c;
+        f32x4 f[4];                                        // of four keys: their blocks' scales
 #pragma unroll
-        for (int t = 1; t < NT; ++t) b = t == mine ? base(m[t]) : b;
-        b *= c;
+        for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const f32x4*>(scales[16 * half + 4 * p4 + e]);
+        float x[4];
 #pragma unroll
-        for (int k = 0; k < kKeys; ++k) {
-          const int key = share * kKeys + k;               // tile: half of a product's 32 keys
-          f32x4 f[4];                                      // of four keys: their blocks' scales
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = *reinterpret_cast<const f32x4*>(scales[16 * key + 4 * p4 + e]);
-          float x[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][e], c, -b));
-            l += x[e];
-          }
-#pragma unroll
-          for (int d = 0; d < kBlocks; ++d)
-            *reinterpret_cast<u32x2*>(weights[d][mine] + place_lane * 16 + key * 8) =
-                (u32x2){kda::pack_bf16(x[0] * f[0][d], x[1] * f[1][d]), kda::pack_bf16(x[2] * f[2][d], x[3] * f[3][d])};
+        for (int e = 0; e < 4; ++e) {
+          x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -b));
+          l += x[e];
         }
+        // (a key tile is half of a product's 32 keys)
+#pragma unroll
+        for (int d = 0; d < kBlocks; ++d)
+          *reinterpret_cast<u32x2*>(weights[d][mine] + place_lane * 16 + half * 8) =
+              (u32x2){kda::pack_bf16(x[0] * f[0][d], x[1] * f[1][d]), kda::pack_bf16(x[2] * f[2][d], x[3] * f[3][d])};
       }
       kda::lds_barrier();
 
@@ -385,8 +405,8 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
       // keys 16 (j / 4) + 4 g4 + j % 4 for j = 0 .. 7, the order in which two key tiles'
       // scores made their weights.  (A transposing read gathers, in every 16 lanes, byte
       // i & 7 of the 8-byte pieces addressed by lanes (i >> 3) + 2 e into byte e of lane i.)
-      bf16x8 w[NT];
-      constexpr int kAhead = 8 / NT;                       // tiles of 16 columns fetched together
+      bf16x8 w[kRowTiles];
+      constexpr int kAhead = 4;                            // tiles of 16 columns fetched together
       u32x2 a[2][kAhead];
       const int line = ((p16 >> 1) & 3) + 4 * p4 + (p16 & 8) * 2;
       const int place = line * R + ((8 * wave) ^ swirl(line)) * 16 + (p16 & 1) * 8;
@@ -398,7 +418,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
       };
       fetch(0);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) w[t] = *reinterpret_cast<const bf16x8*>(weights[wave][t] + place_lane * 16);
+      for (int t = 0; t < kRowTiles; ++t) w[t] = *reinterpret_cast<const bf16x8*>(weights[wave][t] + place_lane * 16);
 #pragma unroll
       for (int round = 0; round < 8 / kAhead; ++round) {
         fence();
@@ -408,7 +428,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
         for (int d = 0; d < kAhead; ++d) {
           const bf16x8 x = widen(a[round & 1][d][0], a[round & 1][d][1], 1.0f);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) o[t][kAhead * round + d] = mfma16(x, w[t], o[t][kAhead * round + d]);
+          for (int t = 0; t < kRowTiles; ++t) o[t][kAhead * round + d] = mfma16(x, w[t], o[t][kAhead * round + d]);
         }
       }
       fence();
@@ -416,7 +436,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
 
     // -------- its rows: finished, or a part
     l = quarter_sum(l);
-    if (g4 == 0) top[share][16 * mine + l16] = l;
+    if (g4 == 0) top[half][16 * mine + l16] = l;
     kda::lds_barrier();
     const bool whole = first == 0 && last == units;
     const int64_t segment = int64_t(n) * p.row_tiles + seg;
@@ -425,14 +445,13 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
       if (first == 0) p.owner[segment] = whole ? -1 : slot;
       if (first != 0 && last == units) p.last_owner[segment] = piece.w;
     }
+    float* part = p.parts + int64_t(slot) * p.tile_rows * kPart;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < kRowTiles; ++t) {
       const int r = 16 * t + l16, col = 128 * wave + 4 * g4;
-      float sum = top[0][r];
-#pragma unroll
-      for (int i = 1; i < kShare; ++i) sum += top[i][r];
-      if (r >= rows) continue;
+      const float sum = top[0][r] + top[1][r];
       if (whole) {
+        if (r >= rows) continue;
         const int64_t out = int64_t(n) * p.rows + row0 + r;
         const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -442,11 +461,11 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
               (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
         }
         if (p.lse && wave == 0 && g4 == 0) p.lse[out] = m[t] * p.scale + __logf(sum);
-      } else {
-        float* to = p.parts + (int64_t(slot) * p.tile_rows + r) * kPart;
+      } else if (16 * t < rows) {
 #pragma unroll
-        for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(to + col + 16 * d) = o[t][d];
-        if (wave == 0 && g4 == 0) to[R] = m[t], to[R + 1] = sum;
+        for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(part + in_part(t, 8 * wave + d, lane)) = o[t][d];
+        if (wave == 0 && g4 == 0)
+          *reinterpret_cast<float2*>(part + p.tile_rows * R + 2 * r) = make_float2(m[t], sum);
       }
     }
     left -= last - first;
@@ -468,20 +487,14 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
 // bring the tokens.
 constexpr int kWideThreads = 512;
 
-// A scale: byte `block` of a token's four exponents, as a factor.
-__device__ __forceinline__ float scale_of(uint32_t exponents, int block) {
-  return __uint_as_float((exponents >> (8 * block) & 255u) << 23);
-}
-
 // NT: row tiles of 16.
 template <int NT>
 __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Params p) {
   constexpr int kOwnRows = NT <= 4 ? 1 : 2;                // row tiles of a wave's scores
   constexpr int kWideRing = 4;                             // units in LDS
-  constexpr int kWideBytes = kScale + kUnit * kBlocks;
   __shared__ __align__(1024) struct {
-    unsigned char ring[kWideRing][kWideBytes];
-    unsigned char weights[2][kBlocks][NT][1024];
+    unsigned char ring[kWideRing][kBytes];
+    unsigned char weights[2][NT][1024];
     float factor[2][16 * NT];                              // of the output so far
     int grown[2][kWaves];                                  // whether a wave has factors that are not 1
     float sum[16 * NT], top[16 * NT];
@@ -547,7 +560,6 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
         const bool edge = key0 + kUnit > len - p.Q + 1;    // some row does not see some key
         const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
         f32x4 s[2][kOwnRows];
-        u32x4 own[2];                                      // the exponents of this lane's keys, 16 k + 4 g4 + e
         {
           // Of a key's 20 pieces of 16 bytes (eight of codes, two steps each, and two of the
           // shared part) kAhead are on their way.
@@ -565,7 +577,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
           };
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            scales[k] = *reinterpret_cast<const uint32_t*>(tile + kScale + (16 * k + l16) * kBlocks);
+            scales[k] = *reinterpret_cast<const uint32_t*>(exponents_of(tile, 16 * k + l16));
 #pragma unroll
           for (int i = 0; i < kAhead - 1; ++i) fetch(i);
 #pragma unroll
@@ -577,7 +589,6 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
             const int k = i & 1, at = i >> 1;
             fence();
             if (i + kAhead - 1 < 20) fetch(i + kAhead - 1);
-            if (i >= 18) own[k] = *reinterpret_cast<const u32x4*>(tile + kScale + (16 * k + 4 * g4) * kBlocks);
             fence();
             const u32x4 x = a[i % kAhead];
             if (at < 8) {
@@ -635,21 +646,13 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
         grown = __any(grown);
         if (lane == 0) lds.grown[unit & 1][wave] = grown;
 #pragma unroll
-        for (int d = 0; d < kBlocks; ++d) {                // as operands, times each block's scales
-          float f[8];
+        for (int t = 0; t < kOwnRows; ++t) {
+          float x[8];
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[4 * k + e] = scale_of(own[k][e], d);
-#pragma unroll
-          for (int t = 0; t < kOwnRows; ++t) {
-            float x[8];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) x[4 * k + e] = s[k][t][e] * f[4 * k + e];
-            *reinterpret_cast<bf16x8*>(weights[unit & 1][d][mine + t] + lane * 16) = pack8(x);
-          }
+            for (int e = 0; e < 4; ++e) x[4 * k + e] = s[k][t][e];
+          *reinterpret_cast<bf16x8*>(weights[unit & 1][mine + t] + lane * 16) = pack8(x);
         }
       }
       kda::lds_barrier();                                  // the last weights are there
@@ -670,75 +673,39 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
       }
     } else {
       // ======== columns 128 wave ..
-      // The slots of this wave's first tokens in 64 units, one to a lane; -1: no page.
-      const int32_t* table = p.table + n * p.table_stride;
-      int from = 0, slots = -1;
-      auto look = [&](int unit) {
-        from = unit;
-        slots = -1;
-        const int64_t token = int64_t(unit + lane_now()) * kUnit + wave * kOwn;
-        if (token < len) {
-          const int id = table[token >> p.shift];
-          if (id >= 0 && id < p.num_pages) slots = (id << p.shift) + (int(token) & ((1 << p.shift) - 1));
-        }
-      };
-      // They come as buffers that end behind the sequence, or are empty: what is not
-      // there is zero in LDS.  (Behind the last unit nothing comes.)
-      auto load = [&](int unit) {
-        if (unit - from >= 64) look(unit);
-        const int slot = __builtin_amdgcn_readlane(slots, unit - from);
-        const int some = slot < 0 ? 0 : min(len - (unit * kUnit + wave * kOwn), kOwn);
-        const int64_t page = max(slot, 0) >> p.shift;
-        const int at = max(slot, 0) & ((1 << p.shift) - 1);
-        const int lane = lane_now();
-        if (lane == 0) there[unit % kWideRing][wave] = some;
-        unsigned char* to = ring[unit % kWideRing];
-        const int r0 = wave * kOwn;
-        const int piece0 = (lane & 31) ^ swirl(r0) ^ (lane >> 5);
-#pragma unroll
-        for (int j = 0; j < kOwn / 2; ++j)                 // two lines each
-          load_lds<16>(p.codes + page * p.c_stride + at * R, some * R, to + r0 * R + j * 1024,
-                       (lane >> 5) * R + (piece0 ^ 2 * j) * 16, j * 1024);
-        load_lds<16>(p.shared + page * p.s_stride + at * S, some * 2 * S, to + kShared + r0 * 2 * S,  // eight lines
-                     (lane >> 3) * 2 * S + ((lane & 7) ^ swirl2(r0 + (lane >> 3))) * 16, 0);
-        if (lane < kOwn)
-          load_lds<4>(p.exponents + page * p.scale_stride + at * kBlocks, some * kBlocks, to + kScale + r0 * kBlocks,
-                      lane * 4, 0);
+      Tokens tokens{p.table + n * p.table_stride, len, wave, 0, -1};
+      auto source = [&](int unit) {                        // (behind the last unit nothing comes)
+        return tokens.source(p, unit, ring[unit % kWideRing], there[unit % kWideRing]);
       };
       if (begun) wait_loads<0>();                          // (stores, that would count among the loads)
-      look(first);
+      tokens.look(p, first);
 #pragma unroll
-      for (int i = 0; i < kWideRing - 2; ++i) load(first + i);
+      for (int u = 0; u < kWideRing - 2; ++u) {
+        const auto next = source(first + u);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) tokens.load(next, i);
+      }
       f32x4 o[NT][8];                                      // column 128 wave + 16 d + 4 g4 + e of row 16 t + l16
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int d = 0; d < 8; ++d) o[t][d] = (f32x4)(0.0f);
 
-      for (int unit = first; unit <= last; ++unit) {
-        // this wave's tokens of the unit are there
+      auto arrive = [&](int unit) {                        // this wave's tokens of the unit are there
         wait_loads<(kWideRing - 3) * kLoads>();
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        // A token that only some of the queries see may hold codes of NaN, which a
-        // weight of zero would not keep out of the others' products: its latent becomes
-        // zero and its shared part NaN, which gives the same to those that see it (their
-        // scores are NaN) and nothing to the others.
-        if (p.Q > 1 && unit < last && unit * kUnit + kUnit > len - p.Q + 1) {
-          unsigned char* tile = ring[unit % kWideRing];
-          const int lane = lane_now();
-#pragma unroll 1
-          for (int i = wave * kOwn; i < wave * kOwn + kOwn; ++i) {
-            u32x2* code = reinterpret_cast<u32x2*>(tile + i * R) + lane;
-            const u32x2 x = *code;
-            const uint32_t nan = ((x[0] & 0x7f7f7f7fu) + 0x01010101u) | ((x[1] & 0x7f7f7f7fu) + 0x01010101u);
-            if (!__any(nan & 0x80808080u)) continue;
-            *code = (u32x2){0, 0};
-            if (lane < 32) reinterpret_cast<uint32_t*>(tile + kShared + i * 2 * S)[lane] = 0x7fc07fc0u;
-          }
-        }
+        if (p.Q > 1 && unit < last && unit * kUnit + kUnit > len - p.Q + 1) tokens.without_nan(ring[unit % kWideRing]);
         kda::lds_barrier();                                // and the weights of the unit before
-        if (unit < last) load(unit + kWideRing - 2);
-        if (unit == first) continue;
+      };
+      arrive(first);
+      {
+        const auto next = source(first + kWideRing - 2);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) tokens.load(next, i);
+      }
+      for (int unit = first + 1; unit <= last; ++unit) {
+        arrive(unit);
+        const auto next = source(unit + kWideRing - 2);
 
         // -------- the unit before: lane l16 takes column l16 of 16 at keys 16 (j / 4) + 4 g4 +
         // j % 4 for j = 0 .. 7, the order in which the scores hold them.  (A transposing
@@ -749,20 +716,34 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
         const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
         const int line = ((l16 >> 1) & 3) + 4 * g4 + (l16 & 8) * 2;
         const int place = line * R + ((8 * wave) ^ swirl(line)) * 16 + (l16 & 1) * 8;
-        constexpr int kTiles = 4, kAhead = 3;              // tiles of 16 columns at once; row tiles ahead
-        bf16x8 w[kAhead], x[kTiles];
-        u32x2 a[kTiles];
-        auto fetch = [&](int group) {
-#pragma unroll
-          for (int d = 0; d < kTiles; ++d)
-            a[d] = __builtin_bit_cast(u32x2,
-                                      transposed((const lds_i32x2*)(tile + (place ^ (kTiles * group + d) * 16))));
-        };
+        constexpr int kAhead = 2;                          // row tiles
+        u32x4 w[kAhead];
+        bf16x8 x[8];
+        u32x2 a[8];
         auto fetch_weights = [&](int i) {
-          w[i % kAhead] = *reinterpret_cast<const bf16x8*>(weights[before & 1][wave][i % NT] + lane * 16);
+          w[i % kAhead] = *reinterpret_cast<const u32x4*>(weights[before & 1][i] + lane * 16);
+        };
+        // Scales of the lane's eight keys for these columns, and weights times them: a power
+        // of two, so that nothing is rounded (or only below 2^-126).
+        u32x4 exponents[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          exponents[k] = *reinterpret_cast<const u32x4*>(exponents_of(tile, 16 * k + 4 * g4));
+        float scales[8];
+        auto scaled = [&](const u32x4& w) {
+          u32x4 y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float lo = __uint_as_float(w[i] << 16) * scales[2 * i];
+            const float hi = __uint_as_float(w[i]) * scales[2 * i + 1];  // (the lower half stays below a bfloat16's bits)
+            y[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302);
+          }
+          return as_bf16x8(y);
         };
         const u32x4 grown = *reinterpret_cast<const u32x4*>(lds.grown[before & 1]);
-        fetch(0);
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+          a[d] = __builtin_bit_cast(u32x2, transposed((const lds_i32x2*)(tile + (place ^ d * 16))));
         if (__builtin_amdgcn_readfirstlane(grown[0] | grown[1] | grown[2] | grown[3])) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
@@ -774,32 +755,33 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
 #pragma unroll
         for (int i = 0; i < kAhead - 1; ++i) fetch_weights(i);
 #pragma unroll
-        for (int group = 0; group < 8 / kTiles; ++group) {
+        for (int i = 0; i < 8; ++i) scales[i] = scale_of(exponents[i >> 2][i & 3], wave);
 #pragma unroll
-          for (int d = 0; d < kTiles; ++d) x[d] = widen(a[d][0], a[d][1], 1.0f);
+        for (int d = 0; d < 8; ++d) x[d] = widen(a[d][0], a[d][1], 1.0f);
+        fence();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (t + kAhead - 1 < NT) fetch_weights(t + kAhead - 1);
+          // (at once the loads would wait for one another)
+#pragma unroll
+          for (int i = t * kLoads / NT; i < (t + 1) * kLoads / NT; ++i) tokens.load(next, i);
+          const bf16x8 y = scaled(w[t % kAhead]);
           fence();
-          if (group + 1 < 8 / kTiles) fetch(group + 1);
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const int i = group * NT + t;
-            if (i + kAhead - 1 < 8 / kTiles * NT) fetch_weights(i + kAhead - 1);
-            fence();
-#pragma unroll
-            for (int d = 0; d < kTiles; ++d)
-              o[t][kTiles * group + d] = mfma16(x[d], w[i % kAhead], o[t][kTiles * group + d]);
-            fence();
-          }
+          for (int d = 0; d < 8; ++d) o[t][d] = mfma16(x[d], y, o[t][d]);
+          fence();
         }
       }
 
       // -------- its rows: finished, or a part
       wait_loads<0>();                                     // (those that brought nothing, too)
       kda::lds_barrier();
+      float* part = p.parts + int64_t(slot) * p.tile_rows * kPart;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int r = 16 * t + l16, col = 128 * wave + 4 * g4;
-        if (r >= rows) continue;
         if (whole) {
+          if (r >= rows) continue;
           const int64_t out = int64_t(n) * p.rows + row0 + r;
           const float sum = lds.sum[r], f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -809,11 +791,11 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
                 (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
           }
           if (p.lse && wave == 0 && g4 == 0) p.lse[out] = lds.top[r] * p.scale + __logf(sum);
-        } else {
-          float* to = p.parts + (int64_t(slot) * p.tile_rows + r) * kPart;
+        } else if (16 * t < rows) {
 #pragma unroll
-          for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(to + col + 16 * d) = o[t][d];
-          if (wave == 0 && g4 == 0) to[R] = lds.top[r], to[R + 1] = lds.sum[r];
+          for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(part + in_part(t, 8 * wave + d, lane)) = o[t][d];
+          if (wave == 0 && g4 == 0)
+            *reinterpret_cast<float2*>(part + p.tile_rows * R + 2 * r) = make_float2(lds.top[r], lds.sum[r]);
         }
       }
     }
@@ -829,69 +811,78 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
 
 // ---------------------------------------------------------------- joining the parts
 
-// A workgroup takes join_rows rows of a segment, one after another: two streams of
-// 128 lanes, four columns to a lane.
-__global__ __launch_bounds__(256) void latent_decode_join_kernel(Params p) {
-  __shared__ float weights[256], red[R], stat[4];
-  const int tile = min(p.rows, p.tile_rows), groups = (tile + p.join_rows - 1) / p.join_rows;
-  const int64_t segment = blockIdx.x / unsigned(groups);
+// A wave adds up 16 rows x 32 columns, every lane its own row's.  With STREAMS waves
+// (a workgroup) each takes every STREAMS-th part, and they are brought together in LDS.
+template <int STREAMS>
+__global__ __launch_bounds__(64 * STREAMS) void latent_decode_join_kernel(Params p) {
+  constexpr int kTiles = 2, kAhead = 4;        // column tiles; parts on their way
+  __shared__ f32x4 outputs[STREAMS][kTiles][64];
+  __shared__ float2 stats[STREAMS][16];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned row_tiles = unsigned(p.tile_rows) / 16, per = row_tiles * (R / 16 / kTiles);
+  const int64_t segment = blockIdx.x / per;
+  const unsigned in = blockIdx.x - unsigned(segment) * per;
+  const int row_tile = int(in / (R / 16 / kTiles)), column_tile = int(in % (R / 16 / kTiles)) * kTiles;
   const int slot = p.owner[segment];
-  if (slot < 0) return;                        // finished by its workgroup
-  const int w0 = slot >> 1, count = p.last_owner[segment] - w0 + 1;
   const int64_t n = segment / p.row_tiles;
-  const int row0 = int(segment - n * p.row_tiles) * p.tile_rows;
-  const int from = int(blockIdx.x % unsigned(groups)) * p.join_rows;
-  const int limit = min(min(from + p.join_rows, tile), p.rows - row0);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  auto over_all = [&](float x, bool most) {
+  const int r = 16 * row_tile + l16, row = int(segment - n * p.row_tiles) * p.tile_rows + r;
+  if (slot < 0 || row - l16 >= p.rows) return; // finished by its workgroup; or no row
+  const int w0 = slot >> 1, count = p.last_owner[segment] - w0 + 1;
+  const float c = p.scale * kLog2e;
+  // part i: the first may be its piece's last segment, the others are their pieces' first
+  auto at = [&](int i) { return p.parts + int64_t(i == 0 ? slot : 2 * (w0 + i)) * p.tile_rows * kPart; };
+  f32x4 x[kAhead][kTiles], acc[kTiles];
+  float2 stat[kAhead];
+  float m = -INFINITY, sum = 0.0f;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const float y = __shfl_xor(x, d, 64);
-      x = most ? fmaxf(x, y) : x + y;
-    }
-    __syncthreads();
-    if (lane == 0) stat[wave] = x;
-    __syncthreads();
-    x = stat[0];
+  for (int d = 0; d < kTiles; ++d) acc[d] = (f32x4)(0.0f);
+  auto fetch = [&](int i, int k) {
+    const float* from = at(min(i, count - 1));
 #pragma unroll
-    for (int i = 1; i < 4; ++i) x = most ? fmaxf(x, stat[i]) : x + stat[i];
-    return x;
+    for (int d = 0; d < kTiles; ++d) x[k][d] = *reinterpret_cast<const f32x4*>(from + in_part(row_tile, column_tile + d, lane));
+    stat[k] = *reinterpret_cast<const float2*>(from + p.tile_rows * R + 2 * r);
   };
-  for (int r = from; r < limit; ++r) {
-    // part i: the first may be its piece's last segment, the others are their pieces' first
-    auto at = [&](int i) {
-      return p.parts + (int64_t(i == 0 ? slot : 2 * (w0 + i)) * p.tile_rows + r) * kPart;
-    };
-    float m = -INFINITY;
-    for (int i = tid; i < count; i += 256) m = fmaxf(m, at(i)[R]);
-    m = over_all(m, true);
-    const int stream = tid >> 7, col = (tid & 127) * 4;
-    f32x4 acc = (f32x4)(0.0f);
-    float sum = 0.0f;
-    for (int i0 = 0; i0 < count; i0 += 256) {
-      const int here = min(count - i0, 256);
-      __syncthreads();
-      if (tid < here) {
-        const float f = __builtin_amdgcn_exp2f((at(i0 + tid)[R] - base(m)) * (p.scale * kLog2e));
-        weights[tid] = f;
-        sum += f * at(i0 + tid)[R + 1];
-      }
-      __syncthreads();
-#pragma unroll 4
-      for (int k = stream; k < here; k += 2) acc += *reinterpret_cast<const f32x4*>(at(i0 + k) + col) * weights[k];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) fetch(wave + k * STREAMS, k);
+  for (int i0 = wave; i0 < count; i0 += kAhead * STREAMS)
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (i0 + k * STREAMS >= count) break;
+      const float now = fmaxf(m, stat[k].x);
+      const float f = __builtin_amdgcn_exp2f((m - base(now)) * c), g = __builtin_amdgcn_exp2f((stat[k].x - base(now)) * c);
+      m = now;
+      sum = sum * f + stat[k].y * g;
+#pragma unroll
+      for (int d = 0; d < kTiles; ++d) acc[d] = acc[d] * f + x[k][d] * g;
+      fetch(i0 + (k + kAhead) * STREAMS, k);
     }
-    sum = over_all(sum, false);
-    if (stream == 1) *reinterpret_cast<f32x4*>(&red[col]) = acc;
+  if (STREAMS > 1) {
+#pragma unroll
+    for (int d = 0; d < kTiles; ++d) outputs[wave][d][lane] = acc[d];
+    if (g4 == 0) stats[wave][l16] = make_float2(m, sum);
     __syncthreads();
-    if (stream == 0) {
-      const int64_t out = n * p.rows + row0 + r;
-      acc += *reinterpret_cast<const f32x4*>(&red[col]);
-      acc *= sum == 0.0f ? 0.0f : 1.0f / sum;
-      *reinterpret_cast<u32x2*>(p.o + out * R + col) =
-          (u32x2){kda::pack_bf16(acc[0], acc[1]), kda::pack_bf16(acc[2], acc[3])};
-      if (p.lse && tid == 0) p.lse[out] = m * p.scale + __logf(sum);
+    if (wave != 0) return;
+    for (int i = 1; i < STREAMS; ++i) {
+      const float2 other = stats[i][l16];
+      const float now = fmaxf(m, other.x);
+      const float f = __builtin_amdgcn_exp2f((m - base(now)) * c), g = __builtin_amdgcn_exp2f((other.x - base(now)) * c);
+      m = now;
+      sum = sum * f + other.y * g;
+#pragma unroll
+      for (int d = 0; d < kTiles; ++d) acc[d] = acc[d] * f + outputs[i][d][lane] * g;
     }
   }
+  if (row >= p.rows) return;
+  const int64_t out = n * p.rows + row;
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int d = 0; d < kTiles; ++d) {
+    const f32x4 y = acc[d] * f;
+    *reinterpret_cast<u32x2*>(p.o + out * R + 16 * (column_tile + d) + 4 * g4) =
+        (u32x2){kda::pack_bf16(y[0], y[1]), kda::pack_bf16(y[2], y[3])};
+  }
+  if (p.lse && column_tile == 0 && g4 == 0) p.lse[out] = m * p.scale + __logf(sum);
 }
 
 struct Plan {
@@ -900,8 +891,8 @@ struct Plan {
   size_t parts, bytes;
 };
 
-// Up to 32 rows go to the kernel of four waves, more, in equal tiles of up to 128, to
-// the one of eight.
+// Up to 32 rows go to the kernel of four waves, more, in equal tiles of up to 96, which
+// is what eight waves' registers hold, to the other.
 Plan plan_for(int64_t N, int64_t Q, int H) {
   Plan x;
   x.rows = int(Q * H);
@@ -949,26 +940,28 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
     if (!kda::aligned4(y)) return KDA_ERR_ALIGN;
   const Plan x = plan_for(N, Q, H);
   if (workspace_bytes < x.bytes) return KDA_ERR_WORKSPACE;
-  // Rows of a joining workgroup: one, or more where there would be over 4096
-  // workgroups; one that finds nothing to join is not free.
-  const int tile = x.rows < x.tile_rows ? x.rows : x.tile_rows;
-  const int64_t share = (x.segments * tile + 4095) / 4096;
-  const int join_rows = int(share < tile ? share : tile);
   int* owner = reinterpret_cast<int*>(static_cast<char*>(workspace) + x.parts);
   const Params p{static_cast<const uint16_t*>(q), q_stride, static_cast<const uint8_t*>(c_cache),
                  static_cast<const uint8_t*>(c_scale), static_cast<const uint16_t*>(k_cache), c_page, scale_page,
                  k_page, page_table, table_stride, kv_lens, N, Q, H, table_width, __builtin_ctz(page_size), num_pages,
-                 scale, static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, join_rows, x.pieces,
+                 scale, static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, x.pieces,
                  static_cast<float*>(workspace), owner, owner + x.segments};
   const hipStream_t st = kda::as_stream(stream);
   const dim3 grid(unsigned(x.pieces));
   if (x.tile_rows <= 32)
-    hipLaunchKernelGGL(latent_decode_kernel<2>, grid, dim3(kThreads), 0, st, p);
+    hipLaunchKernelGGL(latent_decode_kernel, grid, dim3(kThreads), 0, st, p);
   else if (x.tile_rows <= 64)
     hipLaunchKernelGGL(latent_decode_wide_kernel<4>, grid, dim3(kWideThreads), 0, st, p);
   else
     hipLaunchKernelGGL(latent_decode_wide_kernel<6>, grid, dim3(kWideThreads), 0, st, p);
-  const unsigned joins = unsigned(x.segments * ((tile + join_rows - 1) / join_rows));
-  hipLaunchKernelGGL(latent_decode_join_kernel, dim3(joins), dim3(256), 0, st, p);
+  // Parts of a segment, about: each in turn takes a microsecond.
+  const unsigned joins = unsigned(x.segments) * unsigned(x.tile_rows) / 16 * (R / 32);
+  const int64_t each = x.pieces / x.segments;
+  if (each <= 16)
+    hipLaunchKernelGGL(latent_decode_join_kernel<1>, dim3(joins), dim3(64), 0, st, p);
+  else if (each <= 64)
+    hipLaunchKernelGGL(latent_decode_join_kernel<4>, dim3(joins), dim3(256), 0, st, p);
+  else
+    hipLaunchKernelGGL(latent_decode_join_kernel<16>, dim3(joins), dim3(1024), 0, st, p);
   return kda::launch_status();
 }
