@@ -194,13 +194,32 @@ __global__ __launch_bounds__(kThreads, 3) void latent_stats_kernel(Params p) {
   rows_of_dq<float, false, true>(p, blockIdx.x, lds);
 }
 
+template <typename Out, bool kBoth>
+__global__ __launch_bounds__(kThreads, 2) void latent_dq_kernel(Params p) {
+  __shared__ __align__(1024) unsigned char lds[2 * kKeyBuffer];
+  rows_of_dq<Out, kBoth, false>(p, blockIdx.x, lds);
+}
+
 // ---------------------------------------------------------------- dK and dV
 
 constexpr int kRowBuffer = kTileBytes + kThinBytes + kTileBytes + 512;     // Q (128 and 64 wide), dO, lse2, delta
 
+// Two waves to 32 keys: one makes P and dS of 32 query rows, the other adds the
+// products with those of the 32 rows before them to dK and dV.  Each has 20 of the 40
+// products; together they are what a SIMD's registers hold, and while one computes
+// weights the other's products go on.
 template <typename Out, bool kBoth>
-__device__ __forceinline__ void keys_of_dkv(const Params& p, unsigned id, unsigned char* lds) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+__global__ __launch_bounds__(2 * kThreads, 2) void latent_dkv_kernel(Params p) {
+  constexpr int kLoadWaves = 2 * kWaves, kRing = kBoth ? 2 : 3, kTerms = kBoth ? 4 : 2;
+  __shared__ __align__(1024) struct {
+    unsigned char ring[kRing][kRowBuffer];
+    unsigned char terms[2][kWaves][kTerms][2][1024];       // P, dS (and what their rounding left) as operands
+  } lds;
+  auto &ring = lds.ring;
+  auto &terms = lds.terms;
+  const unsigned id = blockIdx.x;
+  const int all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wave = all_waves & (kWaves - 1), role = all_waves / kWaves;
   const int l32 = lane & 31, h = lane >> 5;
   const unsigned heads = p.H;
   const int head = int(id % heads);
@@ -212,6 +231,43 @@ __device__ __forceinline__ void keys_of_dkv(const Params& p, unsigned id, unsign
 
   const int k0 = keys.row0 + wave * 32;                    // this wave's first key
   const int key = min(k0 + l32, keys.len - 1);
+  // Query tiles from the one that holds the first row that sees the first key.
+  const int t0 = max(keys.row0 - shift, 0) / kTile, walk = max((rows.len + kTile - 1) / kTile - t0, 0);
+  const int begin = t0 + int(int64_t(walk) * part / p.parts), end = t0 + int(int64_t(walk) * (part + 1) / p.parts);
+  const int steps = 2 * max(end - begin, 0);               // of 32 rows
+  TileLoad<kLoadWaves> qload, uload;
+  ThinLoad<kLoadWaves> q2load;
+  const int64_t u_stride = int64_t(p.H) * D;
+  qload.init(all_waves, lane, p.q_stride);
+  q2load.init(all_waves, lane, p.q_stride);
+  uload.init(all_waves, lane, u_stride);
+  const uint16_t* qb = p.q + rows.first * p.q_stride + head * DQ;
+  const uint16_t* ub = p.d_out + rows.first * u_stride + head * D;
+  const int64_t b = p.cu ? 0 : keys.n, start = rows.first - b * p.T;
+  const int64_t stat0 = (b * p.H + head) * p.T + start;
+  constexpr int kLoads = 5;                                // of a wave for a tile (two have one more)
+  auto issue = [&](int i) {                                // tile begin + i; behind the last nothing comes
+    const int row = min(begin + i, end) * kTile, left = begin + i < end ? rows.len - row : 0;
+    const int64_t at = row;
+    unsigned char* buf = ring[i % kRing];
+    qload.issue(qb + at * p.q_stride, p.q_stride, left, buf, all_waves);
+    q2load.issue(qb + at * p.q_stride + D, p.q_stride, left, buf + kTileBytes, all_waves);
+    uload.issue(ub + at * u_stride, u_stride, left, buf + kTileBytes + kThinBytes, all_waves);
+    if (all_waves == 0) load_floats(p.lse2 + stat0 + at, left, buf + 2 * kTileBytes + kThinBytes, lane);
+    if (all_waves == 1) load_floats(p.delta + stat0 + at, left, buf + 2 * kTileBytes + kThinBytes + 256, lane);
+  };
+  // Before step i: its rows are there, and the terms of the step before.
+  auto arrive = [&](int i) {
+    if (i % 2 == 0) __builtin_amdgcn_s_waitcnt(kWaitLoads | (kRing == 3 ? kLoads : 0));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    kda::lds_barrier();
+    if (i % 2 == 1) issue(i / 2 + kRing - 1);              // (the tile in its place was used a step before)
+  };
+  auto skipped = [&](int i) {                              // none of the rows sees this wave's keys
+    return begin * kTile + 32 * i + 31 < k0 - shift;
+  };
+
+  if (role == 0) {
   bf16x8 kk[12], vv[8];                                    // rows of [K s] and V as B operands
   {
     const uint16_t* ks = p.k + (keys.first + key) * p.k_stride + head * p.k_head + 8 * h;
@@ -226,47 +282,20 @@ __device__ __forceinline__ void keys_of_dkv(const Params& p, unsigned id, unsign
     for (int s = 0; s < 4; ++s) kk[8 + s] = *reinterpret_cast<const bf16x8*>(ss + 16 * s);
   }
   const float c = p.scale * kLog2e;
-  f32x16 dk[6], dv[4];
+    if (steps > 0) {
 #pragma unroll
-  for (int d = 0; d < 6; ++d) dk[d] = (f32x16)(0.0f);
-#pragma unroll
-  for (int d = 0; d < 4; ++d) dv[d] = (f32x16)(0.0f);
-
-  // Query tiles from the one that holds the first row that sees the first key.
-  const int t0 = max(keys.row0 - shift, 0) / kTile, walk = max((rows.len + kTile - 1) / kTile - t0, 0);
-  const int begin = t0 + int(int64_t(walk) * part / p.parts), end = t0 + int(int64_t(walk) * (part + 1) / p.parts);
-  TileLoad<kWaves> qload, uload;
-  ThinLoad<kWaves> q2load;
-  const int64_t u_stride = int64_t(p.H) * D;
-  qload.init(wave, lane, p.q_stride);
-  q2load.init(wave, lane, p.q_stride);
-  uload.init(wave, lane, u_stride);
-  const uint16_t* qb = p.q + rows.first * p.q_stride + head * DQ;
-  const uint16_t* ub = p.d_out + rows.first * u_stride + head * D;
-  const int64_t b = p.cu ? 0 : keys.n, start = rows.first - b * p.T;
-  const int64_t stat0 = (b * p.H + head) * p.T + start;
-  auto issue = [&](int t, unsigned char* buf) {
-    const int row = t * kTile;
-    const int64_t at = row;
-    qload.issue(qb + at * p.q_stride, p.q_stride, rows.len - row, buf, wave);
-    q2load.issue(qb + at * p.q_stride + D, p.q_stride, rows.len - row, buf + kTileBytes, wave);
-    uload.issue(ub + at * u_stride, u_stride, rows.len - row, buf + kTileBytes + kThinBytes, wave);
-    if (wave == 0) load_floats(p.lse2 + stat0 + at, rows.len - row, buf + 2 * kTileBytes + kThinBytes, lane);
-    if (wave == 1) load_floats(p.delta + stat0 + at, rows.len - row, buf + 2 * kTileBytes + kThinBytes + 256, lane);
-  };
-  if (begin < end) issue(begin, lds);
-
-  for (int t = begin; t < end; ++t) {
+      for (int i = 0; i < kRing - 1; ++i) issue(i);
+    }
+    // The keys are waited for before the first step: left to the compiler they would be
+    // in every step, and with them the loads behind them.
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
-    kda::lds_barrier();
-    const unsigned char* qt = lds + ((t - begin) & 1) * kRowBuffer;
-    const unsigned char *q2t = qt + kTileBytes, *ut = q2t + kThinBytes;
-    const float* stats = reinterpret_cast<const float*>(ut + kTileBytes);
-    if (t + 1 < end) issue(t + 1, lds + ((t + 1 - begin) & 1) * kRowBuffer);
-#pragma unroll 1
-    for (int w = 0; w < 2; ++w) {
-      const int row0 = t * kTile + 32 * w;
-      if (row0 + 31 < k0 - shift) continue;                // none of the rows sees this wave's keys
+    for (int i = 0; i < steps; ++i) {
+      arrive(i);
+      if (skipped(i)) continue;
+      const unsigned char* qt = ring[i / 2 % kRing];
+      const unsigned char *q2t = qt + kTileBytes, *ut = q2t + kThinBytes;
+      const float* stats = reinterpret_cast<const float*>(ut + kTileBytes);
+      const int w = i & 1, row0 = begin * kTile + 32 * i;
       f32x16 s = (f32x16)(0.0f), g = (f32x16)(0.0f);       // S and dO V^T, rows = query rows
 #pragma unroll
       for (int k = 0; k < 8; ++k) s = mfma32(read_rows(qt, 32 * w, l32, h, k), kk[k], s);
@@ -298,25 +327,59 @@ __device__ __forceinline__ void keys_of_dkv(const Params& p, unsigned id, unsign
         float x[8], y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] = s[8 * k + j], y[j] = g[8 * k + j];
+        auto put = [&](int term, bf16x8 z) {
+          *reinterpret_cast<bf16x8*>(terms[i & 1][wave][term][k] + lane * 16) = z;
+        };
         const bf16x8 pb = pack8(x), gb = pack8(y);
-        bf16x8 pr, gr;
-        if constexpr (kBoth) pr = pack8_rest(x, pb), gr = pack8_rest(y, gb);
+        put(0, pb);
+        put(1, gb);
+        if constexpr (kBoth) put(2, pack8_rest(x, pb)), put(3, pack8_rest(y, gb));
+      }
+    }
+    if (steps > 0) arrive(steps);
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);                // (those that brought nothing)
+    return;
+  }
+
+  f32x16 dk[6], dv[4];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const bf16x8 a = columns_of<256>(ut, 32 * w, k, 32 * d, lane);
-          dv[d] = mfma32(a, pb, dv[d]);
-          if constexpr (kBoth) dv[d] = mfma32(a, pr, dv[d]);
-        }
+  for (int d = 0; d < 6; ++d) dk[d] = (f32x16)(0.0f);
 #pragma unroll
-        for (int d = 0; d < 6; ++d) {
-          const bf16x8 a = d < 4 ? columns_of<256>(qt, 32 * w, k, 32 * d, lane)
-                                 : columns_of<2 * S>(q2t, 32 * w, k, 32 * (d - 4), lane);
-          dk[d] = mfma32(a, gb, dk[d]);
-          if constexpr (kBoth) dk[d] = mfma32(a, gr, dk[d]);
-        }
+  for (int d = 0; d < 4; ++d) dv[d] = (f32x16)(0.0f);
+  if (steps > 0) {
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) issue(i);
+    arrive(0);
+  }
+  for (int i = 1; i <= steps; ++i) {
+    arrive(i);
+    const int before = i - 1;
+    if (skipped(before)) continue;
+    const unsigned char* qt = ring[before / 2 % kRing];
+    const unsigned char *q2t = qt + kTileBytes, *ut = q2t + kThinBytes;
+    const int w = before & 1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      auto get = [&](int term) { return *reinterpret_cast<const bf16x8*>(terms[before & 1][wave][term][k] + lane * 16); };
+      const bf16x8 pb = get(0), gb = get(1);
+      bf16x8 pr, gr;
+      if constexpr (kBoth) pr = get(2), gr = get(3);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const bf16x8 a = columns_of<256>(ut, 32 * w, k, 32 * d, lane);
+        dv[d] = mfma32(a, pb, dv[d]);
+        if constexpr (kBoth) dv[d] = mfma32(a, pr, dv[d]);
+      }
+#pragma unroll
+      for (int d = 0; d < 6; ++d) {
+        const bf16x8 a = d < 4 ? columns_of<256>(qt, 32 * w, k, 32 * d, lane)
+                               : columns_of<2 * S>(q2t, 32 * w, k, 32 * (d - 4), lane);
+        dk[d] = mfma32(a, gb, dk[d]);
+        if constexpr (kBoth) dk[d] = mfma32(a, gr, dk[d]);
       }
     }
   }
+  __builtin_amdgcn_s_waitcnt(kWaitLoads);                  // (those that brought nothing)
   if (k0 + l32 >= keys.len) return;
   // (with parts, Out is float and dkv is the parts' buffer)
   const int64_t all = int64_t(p.B) * p.K, at = keys.first + key;
@@ -329,20 +392,6 @@ __device__ __forceinline__ void keys_of_dkv(const Params& p, unsigned id, unsign
   float* ds = p.ds_part + ((int64_t(head) * p.parts + part) * all + at) * S;
 #pragma unroll
   for (int d = 0; d < 2; ++d) store_row32(ds + 32 * d, dk[4 + d], p.scale, h);
-}
-
-// All gradients in one launch: what is left open behind the longest walks of the
-// ones fills up with the others.
-template <typename Out, typename Part, bool kBoth>
-__global__ __launch_bounds__(kThreads, 1) void latent_grads_kernel(Params p) {
-  __shared__ __align__(1024) unsigned char lds[2 * kRowBuffer];
-  const unsigned second = p.keys_first ? p.key_blocks : gridDim.x - p.key_blocks;
-  const bool first = blockIdx.x < second;
-  const unsigned block = first ? blockIdx.x : blockIdx.x - second;
-  if (first == p.keys_first)
-    keys_of_dkv<Part, kBoth>(p, block, lds);
-  else
-    rows_of_dq<Out, kBoth, false>(p, block, lds);
 }
 
 // ---------------------------------------------------------------- the parts' sums
@@ -444,11 +493,12 @@ Plan plan_for(int64_t B, int T, int T_kv, int H, int num_seqs) {
 
 template <typename Out, bool kBoth>
 void launch_grads(const Params& p, unsigned blocks, hipStream_t stream) {
-  const dim3 grid(p.key_blocks + blocks);
-  if (p.parts == 1)
-    hipLaunchKernelGGL((latent_grads_kernel<Out, Out, kBoth>), grid, dim3(kThreads), 0, stream, p);
-  else
-    hipLaunchKernelGGL((latent_grads_kernel<Out, float, kBoth>), grid, dim3(kThreads), 0, stream, p);
+  const dim3 keys(p.key_blocks);
+  if (p.key_blocks && p.parts == 1)
+    hipLaunchKernelGGL((latent_dkv_kernel<Out, kBoth>), keys, dim3(2 * kThreads), 0, stream, p);
+  else if (p.key_blocks)
+    hipLaunchKernelGGL((latent_dkv_kernel<float, kBoth>), keys, dim3(2 * kThreads), 0, stream, p);
+  if (blocks) hipLaunchKernelGGL((latent_dq_kernel<Out, kBoth>), dim3(blocks), dim3(kThreads), 0, stream, p);
 }
 
 template <typename Out>
