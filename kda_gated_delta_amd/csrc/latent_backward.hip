@@ -6,13 +6,21 @@
 //     dQ = scale dS K,   [dKn dS_shared] = scale dS^T Q,
 // the shared part's summed over all heads.
 //
-// The walks are attn_backward.hip's: statistics first (lse in powers of two and
-// delta), then in one launch workgroups of 128 query rows, which walk the keys for
-// dQ, and workgroups of 128 keys, which walk the query rows for dK and dV.  Every
-// head has keys of its own, so a walk belongs to one head; only the shared part's
-// gradient crosses heads.  Its terms are written in float32 per head and added in
-// order by latent_sum_kernel, as the parts of a key tile that several workgroups
-// share are.
+// Statistics first (lse in powers of two and delta); then workgroups of 128 keys,
+// which walk the query rows for dK and dV, and workgroups of 128 query rows, which
+// walk the keys for dQ.  Every head has keys of its own, so a walk belongs to one head;
+// only the shared part's gradient crosses heads.  Its terms are written in float32
+// per head and added in order by latent_sum_kernel, as the parts of a key tile that
+// several workgroups share are.
+//
+// Weights and score gradients are made in both walks, 320 of the 1152 products per
+// pair that are made and 320 of the 832 that the formulas have (the other way, dQ in
+// parts or with atomics, would write and read 768 bytes of float32 per pair of tiles'
+// rows).  What bounds the walks are the products.  8192 tokens x 16 heads: dK and dV
+// 709 us, 0.69 TFLOP, 970 TFLOP/s; dQ 491 us, 0.55 TFLOP, 1120; statistics 14, sum 7
+// (a large matrix product reaches 1224 on this card).  With all of a walk in one wave, and
+// both walks in one launch of one workgroup to a compute unit, dK, dV and dQ took
+// 1422 us together: nothing ran while the one wave of a SIMD made weights.
 #include "kda_host.h"
 #include "latent_device.h"
 
@@ -36,8 +44,6 @@ struct Params {
   int parts;                 // workgroups that share a key tile
   float* dkv_part;           // workspace, [parts, B, K, H, 256], if parts > 1
   float* ds_part;            // workspace, [H, parts, B, K, 64]
-  unsigned key_blocks;       // workgroups of dK and dV
-  bool keys_first;           // in the launch, before dQ's
 };
 
 // ---------------------------------------------------------------- dQ
@@ -446,13 +452,17 @@ __global__ __launch_bounds__(256) void latent_sum_kernel(Params p, unsigned shar
                        (int64_t(blockIdx.x - shared_blocks) * 256 + threadIdx.x) * 4);
 }
 
-// Workgroups that share a key tile, and which gradients come first: see
-// attn_backward.hip.
-bool one_length(int N, bool packed) { return !packed || N == 1; }
+// Workgroups that share a key tile: enough for every compute unit to have one, or two
+// where all walks but the longest are shorter (one length, from the diagonal on) and long
+// enough to be cut.  For one and for two, a training pass in us:
+//   one length: 8 heads x 4096 tokens 367 and 347, 4 x 8192 695 and 636, 16 x 2048 204 and 205,
+//     16 x 1000 111 and 123
+//   packed: 8 heads x 8 of up to 1000 134 and 169, 4 x 5 of 2000 196 and 214, 12 x 6 of 1200 150 and 194
 int parts_for(int64_t key_slots, int T, int N, bool packed, int H) {
-  const int64_t units = key_slots * H, cus = kda::device_cus(), want = (one_length(N, packed) ? 4 : 3) * cus;
+  const int64_t len = kda::attn_typical(T, N, packed), cus = kda::device_cus();
+  const int64_t units = key_slots * H, want = (!packed || N == 1) && len > 2048 ? 2 * cus : cus;
   if (units == 0 || units >= want) return 1;
-  const int64_t walk = kda::attn_typical(T, N, packed) / kTile / 2 + 1;
+  const int64_t walk = len / kTile / 2 + 1;
   const int64_t most = walk / 2 < 1 ? 1 : (walk / 2 > 16 ? 16 : walk / 2);
   const int64_t parts = (want + units - 1) / units;
   return int(parts < most ? parts : most);
@@ -492,23 +502,23 @@ Plan plan_for(int64_t B, int T, int T_kv, int H, int num_seqs) {
 }
 
 template <typename Out, bool kBoth>
-void launch_grads(const Params& p, unsigned blocks, hipStream_t stream) {
-  const dim3 keys(p.key_blocks);
-  if (p.key_blocks && p.parts == 1)
+void launch_grads(const Params& p, unsigned key_blocks, unsigned blocks, hipStream_t stream) {
+  const dim3 keys(key_blocks);
+  if (key_blocks && p.parts == 1)
     hipLaunchKernelGGL((latent_dkv_kernel<Out, kBoth>), keys, dim3(2 * kThreads), 0, stream, p);
-  else if (p.key_blocks)
+  else if (key_blocks)
     hipLaunchKernelGGL((latent_dkv_kernel<float, kBoth>), keys, dim3(2 * kThreads), 0, stream, p);
   if (blocks) hipLaunchKernelGGL((latent_dq_kernel<Out, kBoth>), dim3(blocks), dim3(kThreads), 0, stream, p);
 }
 
 template <typename Out>
 int launch(const Params& p, const Plan& x, hipStream_t stream) {
-  const unsigned blocks = unsigned(x.slots * p.H);
+  const unsigned blocks = unsigned(x.slots * p.H), key_blocks = unsigned(x.key_slots * p.H * p.parts);
   if (blocks) hipLaunchKernelGGL(latent_stats_kernel, dim3(blocks), dim3(kThreads), 0, stream, p);
   if (both_terms(int64_t(p.B) * p.T * p.H, kda::attn_typical(p.K, p.N, p.cu != nullptr)))
-    launch_grads<Out, true>(p, blocks, stream);
+    launch_grads<Out, true>(p, key_blocks, blocks, stream);
   else
-    launch_grads<Out, false>(p, blocks, stream);
+    launch_grads<Out, false>(p, key_blocks, blocks, stream);
   if (x.sums)
     hipLaunchKernelGGL(latent_sum_kernel<Out>, dim3(unsigned(x.sums)), dim3(256), 0, stream, p, unsigned(x.shared));
   return kda::launch_status();
@@ -552,8 +562,7 @@ extern "C" int kda_latent_backward(const void* q, const void* k, const void* k_s
                  static_cast<const uint16_t*>(k_shared), static_cast<const uint16_t*>(o),
                  static_cast<const uint16_t*>(d_out), q_stride, k_stride, v_stride, s_stride, k_head, v_head, lse,
                  cu_seqlens, cu_seqlens_kv, N, B, T, T_kv, H, int(x.slots), int(x.key_slots), scale, dq, d_kv,
-                 dk_shared, ws, ws + x.stats, x.parts, ws + 2 * x.stats, ws + 2 * x.stats + x.dkv,
-                 unsigned(x.key_slots * H * x.parts), !one_length(N, seqs > 0)};
+                 dk_shared, ws, ws + x.stats, x.parts, ws + 2 * x.stats, ws + 2 * x.stats + x.dkv};
   return grad_dtype == KDA_GRAD_FLOAT32 ? launch<float>(p, x, kda::as_stream(stream))
                                         : launch<uint16_t>(p, x, kda::as_stream(stream));
 }
