@@ -42,17 +42,19 @@ def _even(t, name, lead, inner):
 def _rows(t, name, dev, shape):
     """Elements from token to token of bf16 t, of this shape, whose last axes past the tokens' (all but the last, or the
     last two of q) are compact."""
-    _gpu(t, name, _BF16, dev, shape)
-    width = 1
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.get_device() == dev and t.shape == shape):
+        _gpu(t, name, _BF16, dev, shape)
+    width = shape[-1] if len(shape) < 4 else shape[2] * shape[3]
     if t.is_contiguous():
-        for n in shape[2 if len(shape) > 2 else 1:]:
-            width *= n
         return width
-    inner = len(shape) - (2 if len(shape) == 4 else 1)
-    for n, stride in zip(reversed(shape[inner:]), reversed(t.stride()[inner:])):
-        if n > 1 and stride != width:
+    stride = t.stride()
+    if len(shape) == 2 and stride[1] == 1:
+        return stride[0] if shape[0] > 1 else width
+    inner, compact = len(shape) - (2 if len(shape) == 4 else 1), 1
+    for n, step in zip(reversed(shape[inner:]), reversed(stride[inner:])):
+        if n > 1 and step != compact:
             raise ValueError(f"{name}: the axes behind the tokens must be compact")
-        width *= n
+        compact *= n
     return _even(t, name, shape[:inner], width)
 
 
@@ -166,17 +168,21 @@ def latent_backward(q, k, k_shared, v, o, lse, d_out, cu_seqlens=None, cu_seqlen
 def _cache(c_cache, c_scale, k_cache, dev):
     """The arguments that a checked cache makes: pointers, page size, strides, pages."""
     _gpu(c_cache, "c_cache", _E4M3, dev)
-    if c_cache.dim() != 3 or c_cache.shape[2] != R:
-        raise ValueError(f"c_cache must be [pages, page_size, {R}], got {list(c_cache.shape)}")
-    pages, size, _ = c_cache.shape
-    strides = []
-    for t, name, dtype, width in ((c_cache, "c_cache", _E4M3, R), (c_scale, "c_scale", _U8, R // BLOCK),
-                                  (k_cache, "k_cache", _BF16, S)):
-        _gpu(t, name, dtype, dev, (pages, size, width))
-        if pages and t.stride()[1:] != (width, 1):
-            raise ValueError(f"{name}: pages must be compact inside")
-        strides.append(t.stride(0) if pages > 1 else size * width)
-    return (c_cache.data_ptr(), c_scale.data_ptr(), k_cache.data_ptr(), size, *strides, pages)
+    shape = c_cache.shape
+    if len(shape) != 3 or shape[2] != R:
+        raise ValueError(f"c_cache must be [pages, page_size, {R}], got {list(shape)}")
+    pages, size, _ = shape
+    _gpu(c_scale, "c_scale", _U8, dev, (pages, size, R // BLOCK))
+    _gpu(k_cache, "k_cache", _BF16, dev, (pages, size, S))
+    c, e, s = c_cache.stride(), c_scale.stride(), k_cache.stride()
+    if pages > 1:
+        if c[1:] != (R, 1) or e[1:] != (R // BLOCK, 1) or s[1:] != (S, 1):
+            raise ValueError("c_cache, c_scale, k_cache: pages must be compact inside")
+        return (c_cache.data_ptr(), c_scale.data_ptr(), k_cache.data_ptr(), size, c[0], e[0], s[0], pages)
+    if pages and not (c_cache.is_contiguous() and c_scale.is_contiguous() and k_cache.is_contiguous()):
+        raise ValueError("c_cache, c_scale, k_cache: pages must be compact inside")
+    return (c_cache.data_ptr(), c_scale.data_ptr(), k_cache.data_ptr(), size, size * R, size * (R // BLOCK), size * S,
+            pages)
 
 
 def latent_cache_store(c, k_shared, c_cache, c_scale, k_cache, slots):
