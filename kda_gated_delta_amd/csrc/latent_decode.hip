@@ -71,6 +71,8 @@ struct Params {
   int waves;                                 // pieces
   float* parts;                              // [2 x pieces][tile_rows x kPart]: a piece has one of its first segment, one of its last
   int *owner, *last_owner;                   // [segments]: first part and last piece of those cut, -1 for the others
+  int* cut;                                  // [pieces]: the segment that is cut behind the piece and begins in it, or -1
+  bool by_piece;                             // pieces, of which few are followed by a cut, are fewer than segments
 };
 
 // A word of four codes, times a power of two, as bfloat16 pairs.
@@ -246,6 +248,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
   const int half = wave & 1, mine = wave >> 1;             // the wave's key tile, and its row tile
 
   const Piece piece = kda::line::find_piece<kUnit, 1>(p, 0, p.row_tiles);
+  if (threadIdx.x == 0) p.cut[blockIdx.x] = -1;
   int64_t left = piece.to - piece.from;
   int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
   const int64_t inside = piece.from - piece.before;
@@ -444,6 +447,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
     if (threadIdx.x == 0) {
       if (first == 0) p.owner[segment] = whole ? -1 : slot;
       if (first != 0 && last == units) p.last_owner[segment] = piece.w;
+      if (first == 0 && !whole) p.cut[piece.w] = int(segment);
     }
     float* part = p.parts + int64_t(slot) * p.tile_rows * kPart;
 #pragma unroll
@@ -508,6 +512,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
   const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
 
   const Piece piece = kda::line::find_piece<kUnit, 1>(p, 0, p.row_tiles);
+  if (threadIdx.x == 0) p.cut[blockIdx.x] = -1;
   int64_t left = piece.to - piece.from;
   int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
   const int64_t inside = piece.from - piece.before;
@@ -670,6 +675,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
       if (threadIdx.x == 0) {
         if (first == 0) p.owner[segment] = whole ? -1 : slot;
         if (first != 0 && last == units) p.last_owner[segment] = piece.w;
+        if (first == 0 && !whole) p.cut[piece.w] = int(segment);
       }
     } else {
       // ======== columns 128 wave ..
@@ -821,8 +827,9 @@ __global__ __launch_bounds__(64 * STREAMS) void latent_decode_join_kernel(Params
   const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned row_tiles = unsigned(p.tile_rows) / 16, per = row_tiles * (R / 16 / kTiles);
-  const int64_t segment = blockIdx.x / per;
-  const unsigned in = blockIdx.x - unsigned(segment) * per;
+  const unsigned which = blockIdx.x / per, in = blockIdx.x - which * per;
+  const int64_t segment = p.by_piece ? p.cut[which] : int(which);
+  if (segment < 0) return;
   const int row_tile = int(in / (R / 16 / kTiles)), column_tile = int(in % (R / 16 / kTiles)) * kTiles;
   const int slot = p.owner[segment];
   const int64_t n = segment / p.row_tiles;
@@ -901,7 +908,7 @@ Plan plan_for(int64_t N, int64_t Q, int H) {
   x.pieces = kda::device_cus() * (x.tile_rows <= 32 ? kPerCu : 1);
   x.segments = N * x.row_tiles;
   x.parts = size_t(2 * x.pieces) * x.tile_rows * kPart * sizeof(float);
-  x.bytes = x.parts + size_t(x.segments) * 2 * sizeof(int);
+  x.bytes = x.parts + (size_t(x.segments) * 2 + x.pieces) * sizeof(int);
   return x;
 }
 
@@ -945,7 +952,7 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
                  static_cast<const uint8_t*>(c_scale), static_cast<const uint16_t*>(k_cache), c_page, scale_page,
                  k_page, page_table, table_stride, kv_lens, N, Q, H, table_width, __builtin_ctz(page_size), num_pages,
                  scale, static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, x.pieces,
-                 static_cast<float*>(workspace), owner, owner + x.segments};
+                 static_cast<float*>(workspace), owner, owner + x.segments, owner + 2 * x.segments, x.segments > x.pieces};
   const hipStream_t st = kda::as_stream(stream);
   const dim3 grid(unsigned(x.pieces));
   if (x.tile_rows <= 32)
@@ -955,7 +962,7 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
   else
     hipLaunchKernelGGL(latent_decode_wide_kernel<6>, grid, dim3(kWideThreads), 0, st, p);
   // Parts of a segment, about: each in turn takes a microsecond.
-  const unsigned joins = unsigned(x.segments) * unsigned(x.tile_rows) / 16 * (R / 32);
+  const unsigned joins = unsigned(p.by_piece ? x.pieces : x.segments) * unsigned(x.tile_rows / 16) * (R / 32);
   const int64_t each = x.pieces / x.segments;
   if (each <= 16)
     hipLaunchKernelGGL(latent_decode_join_kernel<1>, dim3(joins), dim3(64), 0, st, p);

@@ -210,6 +210,17 @@ def test_decode_many_sequences(gpu_lib):
     check_decode(o, lse, q, cache, table, lens)
 
 
+@pytest.mark.parametrize("H", [40, 70, 130])
+def test_decode_many_sequences_of_many_heads(gpu_lib, H):
+    """More sequences, or row tiles of them, than pieces, with some much longer than the others."""
+    lens = [int(x) for x in np.random.default_rng(H).integers(0, 40, 270)]
+    lens[100] = 900
+    lens[269] = 300
+    q, cache, table, _ = make_decode(6, lens, 1, H, 16)
+    o, lse = gpu_lib.latent_decode(q, *cache, ints(table), ints(lens))
+    check_decode(o, lse, q, cache, table, lens)
+
+
 def test_decode_tables(gpu_lib):
     """Missing pages in the middle, ids out of range, lengths past the table, wide tables, slices of wider rows."""
     lens = [300, 500, -4, 10 ** 9, 64]
