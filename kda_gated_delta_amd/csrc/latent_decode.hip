@@ -159,7 +159,7 @@ __device__ __forceinline__ const unsigned char* exponents_of(const unsigned char
 // How a wave brings its kOwn tokens of a segment's units.
 struct Tokens {
   const int32_t* table;
-  int len, wave;
+  int end, wave;           // tokens from `end` on are not brought
   int from, slots;         // the slots of the first tokens in 64 units, one to a lane; -1: no page
 
   struct Source {
@@ -174,7 +174,7 @@ struct Tokens {
     from = unit;
     slots = -1;
     const int64_t token = int64_t(unit + lane_now()) * kUnit + wave * kOwn;
-    if (token < len) {
+    if (token < end) {
       const int id = table[token >> p.shift];
       if (id >= 0 && id < p.num_pages) slots = (id << p.shift) + (int(token) & ((1 << p.shift) - 1));
     }
@@ -183,7 +183,7 @@ struct Tokens {
   __device__ __forceinline__ Source source(const Params& p, int unit, unsigned char* tile, int* there) {
     if (unit - from >= 64) look(p, unit);
     const int slot = __builtin_amdgcn_readlane(slots, unit - from);
-    const int some = slot < 0 ? 0 : min(len - (unit * kUnit + wave * kOwn), kOwn);
+    const int some = slot < 0 ? 0 : min(end - (unit * kUnit + wave * kOwn), kOwn);
     const int64_t page = max(slot, 0) >> p.shift;
     const int at = max(slot, 0) & ((1 << p.shift) - 1);
     if (lane_now() == 0) there[wave] = some;
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
     const int last = int(min(int64_t(units), first + left));
     const int rows = min(p.rows - row0, p.tile_rows);
 
-    Tokens tokens{p.table + n * p.table_stride, len, wave, 0, -1};
+    Tokens tokens{p.table + n * p.table_stride, min(len, last * kUnit), wave, 0, -1};
     auto load = [&](int unit) {
       const auto next = tokens.source(p, unit, ring[unit % kRing], there[unit % kRing]);
 #pragma unroll
@@ -679,7 +679,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
       }
     } else {
       // ======== columns 128 wave ..
-      Tokens tokens{p.table + n * p.table_stride, len, wave, 0, -1};
+      Tokens tokens{p.table + n * p.table_stride, min(len, last * kUnit), wave, 0, -1};
       auto source = [&](int unit) {                        // (behind the last unit nothing comes)
         return tokens.source(p, unit, ring[unit % kWideRing], there[unit % kWideRing]);
       };
