@@ -295,6 +295,34 @@ def test_decode_later_nan(gpu_lib, H):
                 assert torch.isnan(a[:, Q - back:]).all() and torch.isnan(b[:, Q - back:]).all()
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("H", [8, 40, 70, 100])
+def test_decode_query_that_is_not_finite(gpu_lib, H, bad):
+    """It gives its own row NaN, and the others what they were."""
+    lens = [300, 40]
+    q, cache, table, _ = make_decode(14, lens, 2, H, 16)
+    o, lse = gpu_lib.latent_decode(q, *cache, ints(table), ints(lens))
+    hit = torch.zeros(2, 2, H, dtype=torch.bool)
+    hit[0, 0, 3] = hit[0, 1, H - 1] = hit[1, 1, 0] = True
+    other = q.clone()
+    other[hit.to(DEV)] = bad
+    a, b = gpu_lib.latent_decode(other, *cache, ints(table), ints(lens))
+    hit = hit.to(DEV)
+    assert torch.isnan(a[hit]).all()
+    assert torch.equal(a[~hit], o[~hit]) and torch.equal(b[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("H", [16, 48, 96])
+def test_decode_beside_large_scales(gpu_lib, H):
+    """Latents whose scales are far apart, between tokens and between the blocks of one."""
+    lens = [90, 33]
+    q, cache, table, _ = make_decode(15, lens, 1, H, 16)
+    rng = np.random.default_rng(16)
+    cache[1].copy_(torch.from_numpy((127 + rng.integers(-40, 1, cache[1].shape)).astype(np.uint8)))
+    o, lse = gpu_lib.latent_decode(q, *cache, ints(table), ints(lens))
+    check_decode(o, lse, q, cache, table, lens)
+
+
 def test_decode_past_32_bits(gpu_lib):
     """Pages 2^27 codes apart, 40 of them: offsets past 2^32 in all three parts."""
     pages, P = 40, 16
@@ -339,6 +367,33 @@ def test_decodes_share_nothing_but_what_is_said(gpu_lib):
     for (args, want), one in zip(sets, got):
         again = kda.latent_decode(*args, workspace=ws)
         assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(want, one, again))
+
+
+@pytest.mark.parametrize("H", [16, 72])
+def test_two_graphs_of_one_workspace(gpu_lib, H):
+    """Replayed in turn, with eager work between them, on inputs and lengths of their own."""
+    kda = gpu_lib
+    ws = torch.empty(kda.latent_decode_workspace_size(3, 1, H), dtype=torch.uint8, device=DEV)
+    sets = []
+    for seed, lens in ((60, [700, 5, 129]), (61, [64, 0, 1000])):
+        q, cache, table, _ = make_decode(seed, lens, 1, H, 32, W=40)
+        args = [q, *cache, ints(table), ints(lens)]
+        kda.latent_decode(*args, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = kda.latent_decode(*args, workspace=ws)
+        sets.append((graph, args, out, lens))
+    for turn in range(4):
+        for i, (graph, args, out, lens) in enumerate(sets):
+            args[0].copy_(rand(70 + 2 * turn + i, *args[0].shape))
+            args[5].copy_(ints([max(n - 31 * turn, 0) for n in lens]))
+            ws.fill_(255)
+            graph.replay()
+            got = [t.clone() for t in out]
+            want = kda.latent_decode(*args)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 # ---------------------------------------------------------------- together

@@ -59,7 +59,7 @@ def check_grads(grads, q, k, s, v, up, cu=None, cu_kv=None, scale=ref.SCALE, rou
 CASES = [  # B, T, K, H, offsets of queries, of keys
     (1, 1, 1, 1, None, None), (1, 2, 2, 3, None, None), (2, 31, 31, 5, None, None), (1, 32, 32, 2, None, None),
     (3, 63, 63, 4, None, None), (1, 65, 65, 3, None, None), (2, 127, 127, 1, None, None), (1, 129, 129, 9, None, None),
-    (1, 517, 517, 3, None, None),
+    (1, 517, 517, 3, None, None), (1, 450, 450, 70, None, None),
     (1, 1, 200, 2, None, None), (2, 3, 66, 3, None, None), (1, 33, 97, 2, None, None), (1, 100, 333, 2, None, None),
     (1, 130, 700, 1, None, None),
     (1, 5, 3, 2, None, None), (2, 200, 70, 2, None, None), (1, 300, 1, 1, None, None), (1, 9, 0, 2, None, None),
