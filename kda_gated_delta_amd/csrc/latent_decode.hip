@@ -507,7 +507,6 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
   auto &ring = lds.ring;
   auto &weights = lds.weights;
   auto &there = lds.there;
-  const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
   const int role = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
 
@@ -536,6 +535,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
       const bool busy = 16 * mine < rows;
       // Rows of Q as operands.  Along a key the order is what lanes of 16 codes make it:
       // steps 2 i and 2 i + 1 are the first and second 8 of lane group g4's 16.
+      const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
       bf16x8 q[kOwnRows][18];
       int limit[kOwnRows];                                 // tokens that the lane's row sees
 #pragma unroll
@@ -783,6 +783,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
       wait_loads<0>();                                     // (those that brought nothing, too)
       kda::lds_barrier();
       float* part = p.parts + int64_t(slot) * p.tile_rows * kPart;
+      const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int r = 16 * t + l16, col = 128 * wave + 4 * g4;
