@@ -210,6 +210,9 @@ __global__ __launch_bounds__(kThreads, 2) void latent_dq_kernel(Params p) {
 
 constexpr int kRowBuffer = kTileBytes + kThinBytes + kTileBytes + 512;     // Q (128 and 64 wide), dO, lse2, delta
 
+// Nothing moves across.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
 // Two waves to 32 keys: one makes P and dS of 32 query rows, the other adds the
 // products with those of the 32 rows before them to dK and dV.  Each has 20 of the 40
 // products; together they are what a SIMD's registers hold, and while one computes
@@ -303,22 +306,39 @@ __global__ __launch_bounds__(2 * kThreads, 2) void latent_dkv_kernel(Params p) {
       const float* stats = reinterpret_cast<const float*>(ut + kTileBytes);
       const int w = i & 1, row0 = begin * kTile + 32 * i;
       f32x16 s = (f32x16)(0.0f), g = (f32x16)(0.0f);       // S and dO V^T, rows = query rows
+      // Operands are read kAhead products before they are used, and what follows from S
+      // is made while the products of dO V^T go on.
+      constexpr int kAhead = 4;
+      bf16x8 a[kAhead];
+      f32x4 stat[4];
+      auto fetch = [&](int j) {
+        a[j % kAhead] = j < 8    ? read_rows(qt, 32 * w, l32, h, j)
+                        : j < 12 ? rows_of<2 * S>(q2t, 32 * w, l32, h, j - 8)
+                                 : read_rows(ut, 32 * w, l32, h, j - 12);
+      };
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s = mfma32(read_rows(qt, 32 * w, l32, h, k), kk[k], s);
+      for (int j = 0; j < kAhead - 1; ++j) fetch(j);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s = mfma32(rows_of<2 * S>(q2t, 32 * w, l32, h, k), kk[8 + k], s);
+      for (int j = 0; j < 20; ++j) {
+        fence();
+        if (j + kAhead - 1 < 20) fetch(j + kAhead - 1);
+        if (j >= 6 && j < 10) stat[j - 6] = *reinterpret_cast<const f32x4*>(stats + 32 * w + 8 * (j - 6) + 4 * h);
+        fence();
+        if (j < 12) {
+          s = mfma32(a[j % kAhead], kk[j], s);
+        } else {
+          g = mfma32(a[j % kAhead], vv[j - 12], g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) g = mfma32(read_rows(ut, 32 * w, l32, h, k), vv[k], g);
+          for (int e = 2 * (j - 12); e < 2 * (j - 12) + 2; ++e)
+            s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -stat[e >> 2][e & 3]));
+        }
+      }
+      fence();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(stats + 32 * w + 8 * i + 4 * h);
         const f32x4 d = *reinterpret_cast<const f32x4*>(stats + 64 + 32 * w + 8 * i + 4 * h);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * i + j], c, -a[j]));
-          s[4 * i + j] = x;
-          g[4 * i + j] = x * (g[4 * i + j] - d[j]);
-        }
+        for (int j = 0; j < 4; ++j) g[4 * i + j] = s[4 * i + j] * (g[4 * i + j] - d[j]);
       }
       if (row0 + shift < k0 + 31 || row0 + 32 > rows.len) { // pairs behind the diagonal, rows behind the end
         const int first = k0 + l32 - shift - row0, behind = rows.len - row0;
@@ -364,26 +384,33 @@ __global__ __launch_bounds__(2 * kThreads, 2) void latent_dkv_kernel(Params p) {
     const unsigned char* qt = ring[before / 2 % kRing];
     const unsigned char *q2t = qt + kTileBytes, *ut = q2t + kThinBytes;
     const int w = before & 1;
+    bf16x8 term[2][kTerms];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      auto get = [&](int term) { return *reinterpret_cast<const bf16x8*>(terms[before & 1][wave][term][k] + lane * 16); };
-      const bf16x8 pb = get(0), gb = get(1);
-      bf16x8 pr, gr;
-      if constexpr (kBoth) pr = get(2), gr = get(3);
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        const bf16x8 a = columns_of<256>(ut, 32 * w, k, 32 * d, lane);
-        dv[d] = mfma32(a, pb, dv[d]);
-        if constexpr (kBoth) dv[d] = mfma32(a, pr, dv[d]);
-      }
+      for (int x = 0; x < kTerms; ++x)
+        term[k][x] = *reinterpret_cast<const bf16x8*>(terms[before & 1][wave][x][k] + lane * 16);
+    constexpr int kAhead = 3;                              // as above
+    bf16x8 a[kAhead];
+    auto fetch = [&](int j) {
+      const int k = j / 10, d = j % 10;
+      a[j % kAhead] = d < 4   ? columns_of<256>(ut, 32 * w, k, 32 * d, lane)
+                      : d < 8 ? columns_of<256>(qt, 32 * w, k, 32 * (d - 4), lane)
+                              : columns_of<2 * S>(q2t, 32 * w, k, 32 * (d - 8), lane);
+    };
 #pragma unroll
-      for (int d = 0; d < 6; ++d) {
-        const bf16x8 a = d < 4 ? columns_of<256>(qt, 32 * w, k, 32 * d, lane)
-                               : columns_of<2 * S>(q2t, 32 * w, k, 32 * (d - 4), lane);
-        dk[d] = mfma32(a, gb, dk[d]);
-        if constexpr (kBoth) dk[d] = mfma32(a, gr, dk[d]);
-      }
+    for (int j = 0; j < kAhead - 1; ++j) fetch(j);
+#pragma unroll
+    for (int j = 0; j < 20; ++j) {
+      const int k = j / 10, d = j % 10, x = d < 4 ? 0 : 1;
+      fence();
+      if (j + kAhead - 1 < 20) fetch(j + kAhead - 1);
+      fence();
+      f32x16& sum = d < 4 ? dv[d & 3] : dk[d < 4 ? 0 : d - 4];
+      sum = mfma32(a[j % kAhead], term[k][x], sum);
+      if constexpr (kBoth) sum = mfma32(a[j % kAhead], term[k][x + 2], sum);
     }
+    fence();
   }
   __builtin_amdgcn_s_waitcnt(kWaitLoads);                  // (those that brought nothing)
   if (k0 + l32 >= keys.len) return;
