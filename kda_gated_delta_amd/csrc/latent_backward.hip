@@ -277,20 +277,20 @@ __global__ __launch_bounds__(2 * kThreads, 2) void latent_dkv_kernel(Params p) {
   };
 
   if (role == 0) {
-  bf16x8 kk[12], vv[8];                                    // rows of [K s] and V as B operands
-  {
-    const uint16_t* ks = p.k + (keys.first + key) * p.k_stride + head * p.k_head + 8 * h;
-    const uint16_t* ss = p.s + (keys.first + key) * p.s_stride + 8 * h;
-    const uint16_t* vs = p.v + (keys.first + key) * p.v_stride + head * p.v_head + 8 * h;
+    bf16x8 kk[12], vv[8];                                    // rows of [K s] and V as B operands
+    {
+      const uint16_t* ks = p.k + (keys.first + key) * p.k_stride + head * p.k_head + 8 * h;
+      const uint16_t* ss = p.s + (keys.first + key) * p.s_stride + 8 * h;
+      const uint16_t* vs = p.v + (keys.first + key) * p.v_stride + head * p.v_head + 8 * h;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      kk[s] = *reinterpret_cast<const bf16x8*>(ks + 16 * s);
-      vv[s] = *reinterpret_cast<const bf16x8*>(vs + 16 * s);
+      for (int s = 0; s < 8; ++s) {
+        kk[s] = *reinterpret_cast<const bf16x8*>(ks + 16 * s);
+        vv[s] = *reinterpret_cast<const bf16x8*>(vs + 16 * s);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) kk[8 + s] = *reinterpret_cast<const bf16x8*>(ss + 16 * s);
     }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) kk[8 + s] = *reinterpret_cast<const bf16x8*>(ss + 16 * s);
-  }
-  const float c = p.scale * kLog2e;
+    const float c = p.scale * kLog2e;
     if (steps > 0) {
 #pragma unroll
       for (int i = 0; i < kRing - 1; ++i) issue(i);
@@ -310,7 +310,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void latent_dkv_kernel(Params p) {
       // is made while the products of dO V^T go on.
       constexpr int kAhead = 4;
       bf16x8 a[kAhead];
-      f32x4 stat[4];
+      f32x4 stat[4], del[4];
       auto fetch = [&](int j) {
         a[j % kAhead] = j < 8    ? read_rows(qt, 32 * w, l32, h, j)
                         : j < 12 ? rows_of<2 * S>(q2t, 32 * w, l32, h, j - 8)
@@ -323,6 +323,7 @@ __global__ __launch_bounds__(2 * kThreads, 2) void latent_dkv_kernel(Params p) {
         fence();
         if (j + kAhead - 1 < 20) fetch(j + kAhead - 1);
         if (j >= 6 && j < 10) stat[j - 6] = *reinterpret_cast<const f32x4*>(stats + 32 * w + 8 * (j - 6) + 4 * h);
+        if (j >= 14 && j < 18) del[j - 14] = *reinterpret_cast<const f32x4*>(stats + 64 + 32 * w + 8 * (j - 14) + 4 * h);
         fence();
         if (j < 12) {
           s = mfma32(a[j % kAhead], kk[j], s);
@@ -335,12 +336,9 @@ __global__ __launch_bounds__(2 * kThreads, 2) void latent_dkv_kernel(Params p) {
       }
       fence();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x4 d = *reinterpret_cast<const f32x4*>(stats + 64 + 32 * w + 8 * i + 4 * h);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) g[4 * i + j] = s[4 * i + j] * (g[4 * i + j] - d[j]);
-      }
+      for (int e = 0; e < 16; ++e) g[e] = s[e] * (g[e] - del[e >> 2][e & 3]);
       if (row0 + shift < k0 + 31 || row0 + 32 > rows.len) { // pairs behind the diagonal, rows behind the end
+        fence();                                           // (or it is done for all pairs, with selects)
         const int first = k0 + l32 - shift - row0, behind = rows.len - row0;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
