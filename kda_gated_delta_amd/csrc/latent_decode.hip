@@ -832,11 +832,11 @@ __global__ __launch_bounds__(64 * STREAMS) void latent_decode_join_kernel(Params
   const int64_t segment = p.by_piece ? p.cut[which] : int(which);
   if (segment < 0) return;
   const int row_tile = int(in / (R / 16 / kTiles)), column_tile = int(in % (R / 16 / kTiles)) * kTiles;
-  const int slot = p.owner[segment];
+  const int slot = p.owner[segment], last = p.last_owner[segment];
   const int64_t n = segment / p.row_tiles;
   const int r = 16 * row_tile + l16, row = int(segment - n * p.row_tiles) * p.tile_rows + r;
   if (slot < 0 || row - l16 >= p.rows) return; // finished by its workgroup; or no row
-  const int w0 = slot >> 1, count = p.last_owner[segment] - w0 + 1;
+  const int w0 = slot >> 1, count = last - w0 + 1;
   const float c = p.scale * kLog2e;
   // part i: the first may be its piece's last segment, the others are their pieces' first
   auto at = [&](int i) { return p.parts + int64_t(i == 0 ? slot : 2 * (w0 + i)) * p.tile_rows * kPart; };
@@ -871,15 +871,22 @@ __global__ __launch_bounds__(64 * STREAMS) void latent_decode_join_kernel(Params
     if (g4 == 0) stats[wave][l16] = make_float2(m, sum);
     __syncthreads();
     if (wave != 0) return;
-    for (int i = 1; i < STREAMS; ++i) {
-      const float2 other = stats[i][l16];
-      const float now = fmaxf(m, other.x);
-      const float f = __builtin_amdgcn_exp2f((m - base(now)) * c), g = __builtin_amdgcn_exp2f((other.x - base(now)) * c);
-      m = now;
-      sum = sum * f + other.y * g;
+    float part[STREAMS];
 #pragma unroll
-      for (int d = 0; d < kTiles; ++d) acc[d] = acc[d] * f + outputs[i][d][lane] * g;
+    for (int i = 1; i < STREAMS; ++i) m = fmaxf(m, stats[i][l16].x);
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < STREAMS; ++i) {
+      const float2 other = stats[i][l16];
+      part[i] = __builtin_amdgcn_exp2f((other.x - base(m)) * c);
+      sum += other.y * part[i];
     }
+#pragma unroll
+    for (int d = 0; d < kTiles; ++d) acc[d] *= part[0];
+#pragma unroll
+    for (int i = 1; i < STREAMS; ++i)
+#pragma unroll
+      for (int d = 0; d < kTiles; ++d) acc[d] += outputs[i][d][lane] * part[i];
   }
   if (row >= p.rows) return;
   const int64_t out = n * p.rows + row;
@@ -955,7 +962,10 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
                  scale, static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, x.pieces,
                  static_cast<float*>(workspace), owner, owner + x.segments, owner + 2 * x.segments, x.segments > x.pieces};
   const hipStream_t st = kda::as_stream(stream);
-  const dim3 grid(unsigned(x.pieces));
+  // No more pieces than units that the tables could hold.
+  const int64_t most = x.segments * ((int64_t(table_width) * page_size + kUnit - 1) / kUnit);
+  const int pieces = int(x.pieces < most ? x.pieces : most);
+  const dim3 grid{unsigned(pieces)};
   if (x.tile_rows <= 32)
     hipLaunchKernelGGL(latent_decode_kernel, grid, dim3(kThreads), 0, st, p);
   else if (x.tile_rows <= 64)
@@ -963,8 +973,8 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
   else
     hipLaunchKernelGGL(latent_decode_wide_kernel<6>, grid, dim3(kWideThreads), 0, st, p);
   // Parts of a segment, about: each in turn takes a microsecond.
-  const unsigned joins = unsigned(p.by_piece ? x.pieces : x.segments) * unsigned(x.tile_rows / 16) * (R / 32);
-  const int64_t each = x.pieces / x.segments;
+  const unsigned joins = unsigned(p.by_piece ? pieces : x.segments) * unsigned(x.tile_rows / 16) * (R / 32);
+  const int64_t each = pieces / x.segments;
   if (each <= 16)
     hipLaunchKernelGGL(latent_decode_join_kernel<1>, dim3(joins), dim3(64), 0, st, p);
   else if (each <= 64)
