@@ -21,6 +21,24 @@ __device__ __forceinline__ int64_t lane_value(int64_t x, int lane) {
   return int64_t(uint64_t(hi) << 32 | lo);
 }
 
+// x plus what CTRL's lane holds, in the rows of 16 lanes that ROWS names and have one.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t plus_lane(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(uint64_t(x))), CTRL, ROWS, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(uint64_t(x) >> 32)), CTRL, ROWS, 0xf, false);
+  return x + int64_t(uint64_t(hi) << 32 | lo);
+}
+// Sum over the lanes up to each.  (Shuffles through LDS would cost every workgroup half
+// a microsecond of its start.)
+__device__ __forceinline__ int64_t sum_upto(int64_t x) {
+  x = plus_lane<0x111, 0xf>(x);                  // 1, 2, 4, 8 lanes before, within rows
+  x = plus_lane<0x112, 0xf>(x);
+  x = plus_lane<0x114, 0xf>(x);
+  x = plus_lane<0x118, 0xf>(x);
+  x = plus_lane<0x142, 0xa>(x);                  // the row before's last lane
+  return plus_lane<0x143, 0xc>(x);               // lane 31
+}
+
 // Where a piece of the line begins.  WAVES successive pieces belong to a workgroup,
 // one to each wave (or one to all of it, with WAVES = 1).
 struct Piece {
@@ -49,12 +67,7 @@ __device__ __forceinline__ Piece find_piece(const P& p, int wave, int per) {
 #pragma unroll 8
     for (int n = a; n < b; ++n) len = length(p, n), own += units_of<UNIT>(len);
     own *= per;
-    int64_t end = own;                       // inclusive sum over the lanes
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int64_t y = __shfl_up(end, d, 64);
-      if (lane >= d) end += y;
-    }
+    const int64_t end = sum_upto(own);
     if (top) {
       const int64_t total = lane_value(end, 63), waves = min(total, int64_t(p.waves));
       // floor(total i / waves) without a long division for each i

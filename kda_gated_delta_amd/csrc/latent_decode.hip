@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
   int64_t left = piece.to - piece.from;
   int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
   const int64_t inside = piece.from - piece.before;
-  int seg = __builtin_amdgcn_readfirstlane(int(inside / units));
+  int seg = p.row_tiles == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(inside / units));
   int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * units));
   bool begun = false;                                      // the piece's first segment is done
   const float c = p.scale * kLog2e;
@@ -515,7 +515,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
   int64_t left = piece.to - piece.from;
   int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
   const int64_t inside = piece.from - piece.before;
-  int seg = __builtin_amdgcn_readfirstlane(int(inside / units));
+  int seg = p.row_tiles == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(inside / units));
   int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * units));
   bool begun = false;                                      // the piece's first segment is done
   const float c = p.scale * kLog2e;
