@@ -819,10 +819,12 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
 // ---------------------------------------------------------------- joining the parts
 
 // A wave adds up 16 rows x 32 columns, every lane its own row's.  With STREAMS waves
-// (a workgroup) each takes every STREAMS-th part, and they are brought together in LDS.
+// (a workgroup) each takes every STREAMS-th part of 16 columns (32 or 64 are slower: a
+// history of 30000 tokens x 16 heads 25.6, 30.2 and 40.5 us; without streams 16 are: 64
+// sequences 96.8, 95.5 and 95.7), and they are brought together in LDS.
 template <int STREAMS>
 __global__ __launch_bounds__(64 * STREAMS) void latent_decode_join_kernel(Params p) {
-  constexpr int kTiles = 2, kAhead = 4;        // column tiles; parts on their way
+  constexpr int kTiles = STREAMS == 1 ? 2 : 1, kAhead = 4;   // column tiles; parts on their way
   __shared__ f32x4 outputs[STREAMS][kTiles][64];
   __shared__ float2 stats[STREAMS][16];
   const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
@@ -972,12 +974,14 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
     hipLaunchKernelGGL(latent_decode_wide_kernel<4>, grid, dim3(kWideThreads), 0, st, p);
   else
     hipLaunchKernelGGL(latent_decode_wide_kernel<6>, grid, dim3(kWideThreads), 0, st, p);
-  // Parts of a segment, about: each in turn takes a microsecond.
-  const unsigned joins = unsigned(p.by_piece ? pieces : x.segments) * unsigned(x.tile_rows / 16) * (R / 32);
+  // By the parts of a segment, about; 1, 4 and 16 streams in us: with 12 (20 sequences of up to
+  // 8000 tokens, 96 heads) 64.8 and 66.2, with 16 (32 of 16 heads) 39.4 and 37.6, with 64 (8 of
+  // them) 25.4 for 4 and 24.9 for 16, with 128 (4) 24.1 and 19.7.
+  const unsigned joins = unsigned(p.by_piece ? pieces : x.segments) * unsigned(x.tile_rows / 16) * (R / 16);
   const int64_t each = pieces / x.segments;
-  if (each <= 16)
-    hipLaunchKernelGGL(latent_decode_join_kernel<1>, dim3(joins), dim3(64), 0, st, p);
-  else if (each <= 64)
+  if (each < 16)
+    hipLaunchKernelGGL(latent_decode_join_kernel<1>, dim3(joins / 2), dim3(64), 0, st, p);
+  else if (each < 64)
     hipLaunchKernelGGL(latent_decode_join_kernel<4>, dim3(joins), dim3(256), 0, st, p);
   else
     hipLaunchKernelGGL(latent_decode_join_kernel<16>, dim3(joins), dim3(1024), 0, st, p);
