@@ -778,7 +778,7 @@ size_t kda_latent_backward_workspace_size(int32_t B, int32_t T, int32_t T_kv, in
  * scale is e + 127 and a code is value / 2^e, rounded to nearest even; infinities
  * and NaN become NaN.  (Values above 448 * 2^119, which only the last 3% of
  * bfloat16's largest binade are, become that.)  Other tokens are left as they are.
- * The slots that are stored must differ.  T < 2^29.
+ * The slots that are stored must differ.  T < 2^27.
  */
 int kda_latent_cache_store(const void* c, const void* k_shared, int64_t c_stride, int64_t s_stride,
                            const int32_t* slots, int32_t T, void* c_cache, void* c_scale, void* k_cache,

@@ -53,27 +53,29 @@ __device__ __forceinline__ float fit(float x) {
   return __builtin_fabsf(x) < INFINITY ? __builtin_amdgcn_fmed3f(x, -448.0f, 448.0f) : x;
 }
 
-// A wave takes TOKENS successive tokens, all their rows on the way at once: 64 lanes
-// of 8 values are a latent, 16 lanes one block.
-template <int TOKENS>
+// A wave takes kTokens successive tokens, all their rows on the way at once: 64 lanes
+// of 8 values are a latent, 16 lanes one block.  Bound by memory where there are many
+// (75000 tokens, 135 MB, 28.1 us, 4.8 TB/s, the copy's rate; with 1, 4 and 8 tokens
+// to a wave 29.2, 29.3 and 31.2), by the launch where there are few.
+constexpr int kTokens = 2;
 __global__ __launch_bounds__(64 * kWaves) void latent_cache_store_kernel(StoreParams p) {
   const int lane = threadIdx.x & 63;
-  const int t0 = (int(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * TOKENS;
-  const int n = min(p.T - t0, TOKENS);
+  const int t0 = (int(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kTokens;
+  const int n = min(p.T - t0, kTokens);
   if (n <= 0) return;
-  int slot[TOKENS];
-  u32x4 x[TOKENS], s;
+  int slot[kTokens];
+  u32x4 x[kTokens], s;
 #pragma unroll
-  for (int i = 0; i < TOKENS; ++i) {
+  for (int i = 0; i < kTokens; ++i) {
     const int t = t0 + min(i, n - 1);
     slot[i] = i < n ? p.slots[t] : -1;
     x[i] = *reinterpret_cast<const u32x4*>(p.c + t * p.c_stride + 8 * lane);
   }
   const int row = min(lane >> 3, n - 1);                   // the shared parts: eight lanes a token
-  if (lane < 8 * TOKENS) s = *reinterpret_cast<const u32x4*>(p.s + (t0 + row) * p.s_stride + 8 * (lane & 7));
+  if (lane < 8 * kTokens) s = *reinterpret_cast<const u32x4*>(p.s + (t0 + row) * p.s_stride + 8 * (lane & 7));
   int mine = -1;
 #pragma unroll
-  for (int i = 0; i < TOKENS; ++i) {
+  for (int i = 0; i < kTokens; ++i) {
     uint32_t top = finite_top(x[i]);
 #pragma unroll
     for (int d = 1; d < 16; d *= 2) top = max(top, uint32_t(__shfl_xor(int(top), d, 64)));
@@ -117,7 +119,8 @@ struct LoadParams {
 };
 
 // A wave takes kRun successive rows of the output; lane i < kRun finds out where
-// row i comes from.
+// row i comes from.  Bound by memory (131000 tokens, 236 MB: 43 us, 5.4 TB/s, into
+// outputs that the caches hold, 53 into others).
 constexpr int kRun = 8;
 __global__ __launch_bounds__(64 * kWaves) void latent_cache_load_kernel(LoadParams p) {
   const int lane = threadIdx.x & 63;
@@ -193,7 +196,7 @@ extern "C" int kda_latent_cache_store(const void* c, const void* k_shared, int64
   if (e == KDA_OK) e = kda::latent_stride(s_stride, S);
   if (e == KDA_OK && T < 0) e = KDA_ERR_SHAPE;
   if (e != KDA_OK) return e;
-  const int64_t most = int64_t(kda::kMostBlocks) * kWaves * 8;
+  const int64_t most = int64_t(kda::kMostBlocks) * kWaves * kTokens;
   if (T > most) return KDA_ERR_SHAPE;
   if (T == 0 || num_pages == 0) return KDA_OK;
   if (!c || !k_shared || !slots || !c_cache || !c_scale || !k_cache) return KDA_ERR_NULL;
@@ -202,11 +205,8 @@ extern "C" int kda_latent_cache_store(const void* c, const void* k_shared, int64
   if (!kda::aligned4(c_scale) || !kda::aligned4(slots)) return KDA_ERR_ALIGN;
   const StoreParams p{static_cast<const uint16_t*>(c), static_cast<const uint16_t*>(k_shared), c_stride, s_stride,
                       slots, T, as_cache(c_cache, c_scale, k_cache, x)};
-  auto blocks = [&](int tokens) { return dim3(unsigned((int64_t(T) + kWaves * tokens - 1) / (kWaves * tokens))); };
-  if (T <= 4 * kWaves * kda::device_cus())
-    hipLaunchKernelGGL(latent_cache_store_kernel<1>, blocks(1), dim3(64 * kWaves), 0, kda::as_stream(stream), p);
-  else
-    hipLaunchKernelGGL(latent_cache_store_kernel<8>, blocks(8), dim3(64 * kWaves), 0, kda::as_stream(stream), p);
+  const unsigned blocks = unsigned((int64_t(T) + kWaves * kTokens - 1) / (kWaves * kTokens));
+  hipLaunchKernelGGL(latent_cache_store_kernel, dim3(blocks), dim3(64 * kWaves), 0, kda::as_stream(stream), p);
   return kda::launch_status();
 }
 
