@@ -13,14 +13,14 @@
 // per head and added in order by latent_sum_kernel, as the parts of a key tile that
 // several workgroups share are.
 //
-// Weights and score gradients are made in both walks, 320 of the 1152 products per
-// pair that are made and 320 of the 832 that the formulas have (the other way, dQ in
-// parts or with atomics, would write and read 768 bytes of float32 per pair of tiles'
-// rows).  What bounds the walks are the products.  8192 tokens x 16 heads: dK and dV
-// 709 us, 0.69 TFLOP, 970 TFLOP/s; dQ 491 us, 0.55 TFLOP, 1120; statistics 14, sum 7
-// (a large matrix product reaches 1224 on this card).  With all of a walk in one wave, and
-// both walks in one launch of one workgroup to a compute unit, dK, dV and dQ took
-// 1422 us together: nothing ran while the one wave of a SIMD made weights.
+// Weights and score gradients are made in both walks: 1152 products of a pair's numbers
+// where the formulas have 832.  One walk for all would add dQ up across workgroups, in
+// float32 through memory and in order (attn_backward.hip has no such sums either).
+// What bounds the walks are the products, at the power limit (8192 tokens x 16 heads:
+// dK and dV 609 to 646 us, 0.69 TFLOP, 1070 TFLOP/s; dQ 476 to 491 us, 0.55 TFLOP, 1120;
+// statistics 15, sum 8; a large matrix product reaches 1224 on this card).  With all
+// of a walk in one wave and both walks in one launch of one workgroup to a compute
+// unit, dK, dV and dQ took 1422 us: nothing ran while a SIMD's one wave made weights.
 #include "kda_host.h"
 #include "latent_device.h"
 

@@ -21,19 +21,21 @@
 // maximum, sum and output are float32.  The next units are on their way to LDS
 // meanwhile.
 //
-// What bounds it: up to 32 rows the reads of the cache (64 sequences of up to 16384
-// tokens, 32 heads, 327 MB: 96 us; the walk takes 86, of which 66 are spent in units, at
-// 4.9 TB/s, the card's copying rate, and the rest before its first unit and on its
-// parts).  With more rows it is a unit's conversions, products and weights (48
-// sequences of up to 8192 tokens, 96 heads, 41 GFLOP: 94 us; 4100 cycles for a unit's
-// 96 rows, of which products 1900, and twice 12 us for 50 MB of parts).
+// What bounds it: up to 32 rows memory (64 sequences of up to 16384 tokens, 32 heads, 327
+// MB: 96 us; the walk reads 340 MB and writes 38 of parts in 88 us, the join reads those
+// in 12).  With more rows a unit's conversions, products and weights (48 sequences of up
+// to 8192 tokens, 96 heads, 41 GFLOP: 83 us; 4100 cycles for a unit's 96 rows, of which
+// products 1900, and 60 MB of parts written and read).  One short history is two launches.
 //
 // Tried and left: units widened once, as bfloat16 in LDS, which then cannot feed the
-// products (115 and 101 us); for 32 rows one workgroup of eight waves per compute unit
-// with the keys split over four pairs of waves (111) or all waves at one unit of 64
-// tokens (104), which pause together where two workgroups fill each other's pauses;
-// for 96 rows waves that hold 16 rows and all columns (118), and waves that go through
-// scores, weights and output together (115).
+// products (115 and 101 us); scores by the e4m3 instructions, which sum with fewer bits
+// (a score off by 2^-14 of its products' magnitudes); for 32 rows one workgroup of eight
+// waves per compute unit, with the keys split over four pairs of waves (111) or all
+// waves at one unit of 64 tokens (104), which pause together where two workgroups fill
+// each other's pauses, weights by the maxima of the unit before (97), and a next
+// segment's loads before the results are stored (101); for 96 rows waves that hold 16
+// rows and all columns (118), or that go through scores, weights and output together
+// (115).
 #include "attn_line.h"
 #include "kda_host.h"
 #include "latent_device.h"
