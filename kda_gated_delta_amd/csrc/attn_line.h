@@ -51,9 +51,11 @@ struct Piece {
 
 // The line has U = per x (units of all sequences) units, per = heads x row
 // tiles; place w of W = min(waves, U) takes floor(U w / W) .. floor(U (w + 1) / W) - 1.
+// With EXTRA every segment counts as many units more, before its own: what it costs to
+// begin and end one, so that a piece that does so in its middle is shorter.
 // A 64-way search: each lane sums a stretch of sequences, the wave adds up and
 // picks the stretch that holds the unit, down to one sequence.
-template <int UNIT, int WAVES, typename P>
+template <int UNIT, int WAVES, int EXTRA = 0, typename P>
 __device__ __forceinline__ Piece find_piece(const P& p, int wave, int per) {
   const int lane = threadIdx.x & 63;
   Piece x{};
@@ -65,7 +67,7 @@ __device__ __forceinline__ Piece find_piece(const P& p, int wave, int per) {
     int64_t own = 0;
     int len = 0;
 #pragma unroll 8
-    for (int n = a; n < b; ++n) len = length(p, n), own += units_of<UNIT>(len);
+    for (int n = a; n < b; ++n) len = length(p, n), own += units_of<UNIT>(len) + EXTRA;
     own *= per;
     const int64_t end = sum_upto(own);
     if (top) {

@@ -22,7 +22,7 @@
 // meanwhile.
 //
 // What bounds it: up to 32 rows memory (64 sequences of up to 16384 tokens, 32 heads, 327
-// MB: 96 us; the walk reads 340 MB and writes 38 of parts in 88 us, the join reads those
+// MB: 92 us; the walk reads 340 MB and writes 38 of parts in 88 us, the join reads those
 // in 12).  With more rows a unit's conversions, products and weights (48 sequences of up
 // to 8192 tokens, 96 heads, 41 GFLOP: 83 us; 4100 cycles for a unit's 96 rows, of which
 // products 1900, and 60 MB of parts written and read).  One short history is two launches.
@@ -228,6 +228,10 @@ struct Tokens {
 // Four waves; of a unit's scores a wave has 16 keys and 16 rows.  Two workgroups on a
 // compute unit: one has its pauses while the other computes.
 constexpr int kThreads = 64 * kWaves, kPerCu = 2, kRing = 3;
+// Units that a segment costs besides its own.  With 0, 4, 6 and 8, us: 64 sequences of up to
+// 16384 tokens 95.4, 92.4, 91.6, 91.2; 4096 of up to 300 222, 193, 191, 195; 2000 of up to 2000
+// 344, 331, 332, 337.
+constexpr int kExtra = 6;
 constexpr int kRowTiles = 2;
 
 __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params p) {
@@ -249,13 +253,15 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = wave & 1, mine = wave >> 1;             // the wave's key tile, and its row tile
 
-  const Piece piece = kda::line::find_piece<kUnit, 1>(p, 0, p.row_tiles);
+  const Piece piece = kda::line::find_piece<kUnit, 1, kExtra>(p, 0, p.row_tiles);
   if (threadIdx.x == 0) p.cut[blockIdx.x] = -1;
   int64_t left = piece.to - piece.from;
   int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
   const int64_t inside = piece.from - piece.before;
-  int seg = p.row_tiles == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(inside / units));
-  int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * units));
+  int seg = p.row_tiles == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(inside / (units + kExtra)));
+  int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * (units + kExtra)) - kExtra);
+  left += min(first, 0);                                   // (the extra units are before the first)
+  first = max(first, 0);
   bool begun = false;                                      // the piece's first segment is done
   const float c = p.scale * kLog2e;
 
@@ -474,7 +480,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
           *reinterpret_cast<float2*>(part + p.tile_rows * R + 2 * r) = make_float2(m[t], sum);
       }
     }
-    left -= last - first;
+    left -= last - first + kExtra;
     first = 0;
     begun = true;
     if (++seg == p.row_tiles) {
@@ -492,6 +498,9 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
 // all row tiles, which are one block of every token's scales.  The output's waves also
 // bring the tokens.
 constexpr int kWideThreads = 512;
+// As kExtra: 48 sequences of up to 8192 tokens, 96 heads 81.7, 75.6, 75.4, 74.4; 600 of up to 1000
+// 185, 148, 138, 139; 32 of up to 8000, 64 heads 59.2, 46.3, 46.5, 46.3.
+constexpr int kWideExtra = 8;
 
 // NT: row tiles of 16.
 template <int NT>
@@ -512,13 +521,15 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
   const int role = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
   const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
 
-  const Piece piece = kda::line::find_piece<kUnit, 1>(p, 0, p.row_tiles);
+  const Piece piece = kda::line::find_piece<kUnit, 1, kWideExtra>(p, 0, p.row_tiles);
   if (threadIdx.x == 0) p.cut[blockIdx.x] = -1;
   int64_t left = piece.to - piece.from;
   int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
   const int64_t inside = piece.from - piece.before;
-  int seg = p.row_tiles == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(inside / units));
-  int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * units));
+  int seg = p.row_tiles == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(inside / (units + kWideExtra)));
+  int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * (units + kWideExtra)) - kWideExtra);
+  left += min(first, 0);                                   // (the extra units are before the first)
+  first = max(first, 0);
   bool begun = false;                                      // the piece's first segment is done
   const float c = p.scale * kLog2e;
 
@@ -808,7 +819,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
         }
       }
     }
-    left -= last - first;
+    left -= last - first + kWideExtra;
     first = 0;
     begun = true;
     if (++seg == p.row_tiles) {
@@ -967,7 +978,8 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
                  static_cast<float*>(workspace), owner, owner + x.segments, owner + 2 * x.segments, x.segments > x.pieces};
   const hipStream_t st = kda::as_stream(stream);
   // No more pieces than units that the tables could hold.
-  const int64_t most = x.segments * ((int64_t(table_width) * page_size + kUnit - 1) / kUnit);
+  const int extra = x.tile_rows <= 32 ? kExtra : kWideExtra;
+  const int64_t most = x.segments * ((int64_t(table_width) * page_size + kUnit - 1) / kUnit + extra);
   const int pieces = int(x.pieces < most ? x.pieces : most);
   const dim3 grid{unsigned(pieces)};
   if (x.tile_rows <= 32)
