@@ -823,7 +823,8 @@ int kda_latent_cache_load(const void* c_cache, const void* c_scale, const void* 
  * As for kda_attn_decode: missing pages hold no tokens, a query without tokens gives
  * o = 0 and lse = -inf, what lies behind a sequence's end does not reach the outputs,
  * and what is not finite only the queries that see its token.  Scales of tokens are
- * 1 to 246.
+ * 1 to 246.  A query that is not finite gives NaN.  Weights up to 256 times a value are
+ * added in float32: 256 * tokens * |c| below 2^128 gives no infinity.
  * Sizes: N >= 0 (0 enqueues nothing), 1 <= Q <= 1024, num_pages >= 1,
  * N * Q * H <= 2^24, table_width * page_size <= 2^30.
  */

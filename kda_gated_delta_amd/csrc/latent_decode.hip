@@ -754,7 +754,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Par
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float lo = __uint_as_float(w[i] << 16) * scales[2 * i];
-            const float hi = __uint_as_float(w[i]) * scales[2 * i + 1];  // (the lower half stays below a bfloat16's bits)
+            const float hi = __uint_as_float(w[i] & 0xffff0000u) * scales[2 * i + 1];
             y[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302);
           }
           return as_bf16x8(y);

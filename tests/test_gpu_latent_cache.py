@@ -295,6 +295,22 @@ def test_decode_later_nan(gpu_lib, H):
                 assert torch.isnan(a[:, Q - back:]).all() and torch.isnan(b[:, Q - back:]).all()
 
 
+@pytest.mark.parametrize("H", [5, 8, 30, 64])
+def test_decode_later_large(gpu_lib, H):
+    """The newest tokens' latents under the largest scale leave the queries before them as they were, to the bit."""
+    lens, Q = [40, 129, 5, 64], 6
+    q, cache, table, _ = make_decode(17, lens, Q, H, 16)
+    o, lse = gpu_lib.latent_decode(q, *cache, ints(table), ints(lens))
+    for back in range(1, 5):
+        now = [t.clone() for t in cache]
+        for row, n in zip(table, lens):
+            t = n - back
+            now[0].view(torch.uint8)[row[t // 16], t % 16] = 0x7e           # 448
+            now[1][row[t // 16], t % 16] = 246
+        a, b = gpu_lib.latent_decode(q, *now, ints(table), ints(lens))
+        assert torch.equal(a[:, :Q - back], o[:, :Q - back]) and torch.equal(b[:, :Q - back], lse[:, :Q - back])
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("H", [8, 40, 70, 100])
 def test_decode_query_that_is_not_finite(gpu_lib, H, bad):
