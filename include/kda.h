@@ -836,9 +836,9 @@ int kda_latent_decode(const void* q, int64_t q_stride, const void* c_cache, cons
 
 /*
  * kda_latent_decode_workspace_size -- bytes of workspace kda_latent_decode needs on
- * the current device; 0 for sizes it rejects.  Up to 32 rows (Q * H) 8 KB for each row
- * and compute unit, with more 4 KB (96 rows or more: as 96), and 8 bytes per
- * (sequence, 96 rows) and a little.
+ * the current device; 0 for sizes it rejects.  About 4 KB for each row (Q * H, up to
+ * 96) and compute unit (twice that with many sequences of up to 32 rows), and 8
+ * bytes per (sequence, 96 rows).
  */
 size_t kda_latent_decode_workspace_size(int32_t N, int32_t Q, int32_t H);
 

@@ -21,21 +21,22 @@
 // maximum, sum and output are float32.  The next units are on their way to LDS
 // meanwhile.
 //
-// What bounds it: up to 32 rows memory (64 sequences of up to 16384 tokens, 32 heads, 327
-// MB: 92 us; the walk reads 340 MB and writes 38 of parts in 88 us, the join reads those
-// in 12).  With more rows a unit's conversions, products and weights (48 sequences of up
-// to 8192 tokens, 96 heads, 41 GFLOP: 83 us; 4100 cycles for a unit's 96 rows, of which
-// products 1900, and 60 MB of parts written and read).  One short history is two launches.
+// What bounds it: up to 32 rows a step of the output's waves (2500 cycles, of them a
+// quarter waits to send the loads of a next unit), near to what memory allows (64
+// sequences of up to 16384 tokens, 32 heads, 327 MB: 89 us; 79 of them the walk, which
+// reads 4.3 TB/s, 7 the join of 21 MB of parts).  With more rows a unit's conversions,
+// products and weights (48 sequences of up to 8192 tokens, 96 heads, 41 GFLOP: 76 us;
+// 4100 cycles for a unit's 96 rows, of which products 1900, and 60 MB of parts written
+// and read).  One short history is two launches.
 //
 // Tried and left: units widened once, as bfloat16 in LDS, which then cannot feed the
-// products (115 and 101 us); scores by the e4m3 instructions, which sum with fewer bits
-// (a score off by 2^-14 of its products' magnitudes); for 32 rows one workgroup of eight
-// waves per compute unit, with the keys split over four pairs of waves (111) or all
-// waves at one unit of 64 tokens (104), which pause together where two workgroups fill
-// each other's pauses, weights by the maxima of the unit before (97), and a next
-// segment's loads before the results are stored (101); for 96 rows waves that hold 16
-// rows and all columns (118), or that go through scores, weights and output together
-// (115).
+// products (115 us for the first of these, 101 for the second); scores by the e4m3
+// instructions, which sum with fewer bits (a score off by 2^-14 of its products'
+// magnitudes); for 32 rows the keys split over four pairs of waves that have all
+// columns (111) and eight waves at one unit of 64 tokens, all of them through scores,
+// weights and output (104); for 96 rows waves that hold 16 rows and all columns (118), or
+// that go through all together (115); a next segment's loads before the results of the
+// one before are stored (no gain); neighbouring pieces on one XCD (none).
 #include "attn_line.h"
 #include "kda_host.h"
 #include "latent_device.h"
@@ -223,35 +224,41 @@ struct Tokens {
   }
 };
 
-// ---------------------------------------------------------------- up to 32 rows
+// ---------------------------------------------------------------- the walk
 
-// Four waves; of a unit's scores a wave has 16 keys and 16 rows.  Two workgroups on a
-// compute unit: one has its pauses while the other computes.
-constexpr int kThreads = 64 * kWaves, kPerCu = 2, kRing = 3;
-// Units that a segment costs besides its own.  With 0, 4, 6 and 8, us: 64 sequences of up to
-// 16384 tokens 95.4, 92.4, 91.6, 91.2; 4096 of up to 300 222, 193, 191, 195; 2000 of up to 2000
-// 344, 331, 332, 337.
-constexpr int kExtra = 6;
-constexpr int kRowTiles = 2;
+// Eight waves, four that make weights and four that use them a unit or two later, one
+// of each kind on every SIMD.  Of the output a wave has 128 columns of all row tiles,
+// which are one block of every token's scales.  Of the scores it has all 32 keys of one
+// or two row tiles, so that maxima and sums are its own, or, with up to 32 rows, 16 keys
+// of one.  The output's waves also bring the tokens.
+constexpr int kThreads = 512;
+// Units that a segment costs besides its own, for its beginning and end.  With 0, 4, 6 and
+// 8, us: 48 sequences of up to 8192 tokens, 96 heads 81.7, 75.6, 75.4, 74.4; 600 of up to 1000 185,
+// 148, 138, 139; 32 of up to 8000, 64 heads 59.2, 46.3, 46.5, 46.3.
+constexpr int kExtra = 8;
 
-__global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params p) {
-  // (One object: between two the compiler tells apart what loads to LDS write, and
-  // has reads wait for all those that are on their way to the same one.)
+// NT: row tiles of 16.
+template <int NT>
+__global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(Params p) {
+  constexpr int kOwnRows = NT <= 4 ? 1 : 2;                // row tiles of a wave's scores
+  constexpr int kSplit = NT <= 2 ? 2 : 1;                  // waves that share a unit's keys
+  constexpr int kLag = kSplit;                             // from a unit's scores to its output
+  constexpr int kRing = kSplit == 2 ? 6 : 4;               // units in LDS
+  constexpr int kAheadUnits = kRing - 1 - kLag;            // on their way
   __shared__ __align__(1024) struct {
     unsigned char ring[kRing][kBytes];
-    unsigned char weights[kBlocks][kRowTiles][1024];
-    float scales[kUnit][kBlocks];
-    float top[2][16 * kRowTiles];                          // maxima of a unit, and in the end sums
-    int there[kRing][kWaves];                              // whether a wave's tokens have a page
+    unsigned char weights[2][NT][1024];
+    float factor[2][16 * NT];                              // of the output so far
+    int grown[2][kWaves];                                  // whether a wave has factors that are not 1
+    float most[2][2][16 * NT];                             // of a unit, with kSplit = 2
+    float sum[kSplit][16 * NT], top[16 * NT];
+    int there[kRing][kWaves];                          // whether a wave's tokens have a page
   } lds;
   auto &ring = lds.ring;
   auto &weights = lds.weights;
-  auto &scales = lds.scales;
-  auto &top = lds.top;
   auto &there = lds.there;
-  const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int half = wave & 1, mine = wave >> 1;             // the wave's key tile, and its row tile
+  const int role = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
 
   const Piece piece = kda::line::find_piece<kUnit, 1, kExtra>(p, 0, p.row_tiles);
   if (threadIdx.x == 0) p.cut[blockIdx.x] = -1;
@@ -270,10 +277,430 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
     const int row0 = seg * p.tile_rows;
     const int last = int(min(int64_t(units), first + left));
     const int rows = min(p.rows - row0, p.tile_rows);
+    const bool whole = first == 0 && last == units;
+    const int64_t segment = int64_t(n) * p.row_tiles + seg;
+    const int slot = 2 * piece.w + int(begun);
+
+    if (role == 0) {
+      // ======== weights of row tiles mine ..
+      const int mine = wave / kSplit * kOwnRows, half = wave % kSplit;
+      const bool busy = 16 * mine < rows;
+      // Rows of Q as operands.  Along a key the order is what lanes of 16 codes make it:
+      // steps 2 i and 2 i + 1 are the first and second 8 of lane group g4's 16.
+      const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
+      bf16x8 q[kOwnRows][18];
+      int limit[kOwnRows];                                 // tokens that the lane's row sees
+#pragma unroll
+      for (int t = 0; t < kOwnRows; ++t) {
+        const int r = row0 + min(16 * (mine + t) + l16, rows - 1), i = r / p.H;
+        const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (r - i * p.H) * (R + S);
+#pragma unroll
+        for (int s = 0; s < 16; ++s)
+          q[t][s] = *reinterpret_cast<const bf16x8*>(src + 64 * (s >> 1) + 16 * g4 + 8 * (s & 1));
+#pragma unroll
+        for (int s = 0; s < 2; ++s) q[t][16 + s] = *reinterpret_cast<const bf16x8*>(src + R + 32 * s + 8 * g4);
+        limit[t] = len - p.Q + i + 1;
+      }
+      wait_loads<0>();
+      float m[kOwnRows], l[kOwnRows];                      // l: of this lane's keys only, until the end
+#pragma unroll
+      for (int t = 0; t < kOwnRows; ++t) m[t] = -INFINITY, l[t] = 0.0f;
+
+      // Of half a unit's keys first the scores are made, and their maxima known to both
+      // waves; a step later, beside the next unit's scores, the weights.
+      f32x4 scores = (f32x4)(0.0f);
+      for (int unit = first; kSplit == 2 && unit <= last; ++unit) {
+        kda::lds_barrier();                                // the unit is there, and the maxima of the one before
+        const int odd = (unit - 1) & 1;                    // (of the unit before)
+        if (!busy) {
+          if (lane == 0) lds.grown[odd][wave] = 0;
+          continue;
+        }
+        unsigned char* tile = ring[unit % kRing];
+        const int key0 = unit * kUnit;
+        const bool edge = key0 + kUnit > len - p.Q + 1;    // some row does not see some key
+        const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4, row = 16 * mine + l16;
+        const f32x4 before = scores;
+        const float mx0 = lds.most[odd][0][row], mx1 = lds.most[odd][1][row];
+        if (unit < last) {
+          f32x4 s = (f32x4)(0.0f);
+          constexpr int kAhead = 3;                        // as below
+          u32x4 a[kAhead];
+          const int key = 16 * half + l16;
+          const int key_at = key * R + ((g4 ^ swirl(key)) * 16);
+          const int shared_at = kShared + key * 2 * S + ((g4 ^ swirl2(key)) * 16);
+          auto fetch = [&](int i) {
+            a[i % kAhead] = *reinterpret_cast<const u32x4*>(tile + (i < 8 ? key_at ^ i * 64 : shared_at ^ (i - 8) * 64));
+          };
+          const uint32_t scales = *reinterpret_cast<const uint32_t*>(exponents_of(tile, key));
+#pragma unroll
+          for (int i = 0; i < kAhead - 1; ++i) fetch(i);
+#pragma unroll
+          for (int i = 0; i < 10; ++i) {
+            fence();
+            if (i + kAhead - 1 < 10) fetch(i + kAhead - 1);
+            fence();
+            const u32x4 x = a[i % kAhead];
+            if (i < 8) {
+              const float f = scale_of(scales, i >> 1);
+              s = mfma16(widen(x[0], x[1], f), q[0][2 * i], s);
+              s = mfma16(widen(x[2], x[3], f), q[0][2 * i + 1], s);
+            } else {
+              s = mfma16(as_bf16x8(x), q[0][i + 8], s);
+            }
+          }
+          fence();
+          const bool gone = there[unit % kRing][2 * half + (g4 >> 1)] == 0;
+          if (edge || __any(gone)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (gone || key0 + 16 * half + 4 * g4 + e >= limit[0]) s[e] = -INFINITY;
+          }
+          const float mx = quarter_max(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
+          if (g4 == 0) lds.most[unit & 1][half][row] = mx;
+          scores = s;
+        }
+        if (unit > first) {
+          const float mx = fmaxf(mx0, mx1);
+          // (row by row: what a row sees does not change how another one is rounded)
+          const float now = (mx - m[0]) * c > kSlack ? mx : m[0];
+          const float f = __builtin_amdgcn_exp2f((m[0] - base(now)) * c);
+          const bool grown = __any(now != m[0]);
+          m[0] = now;
+          l[0] *= f;
+          if (g4 == 0 && half == 0) lds.factor[odd][row] = f;
+          if (lane == 0) lds.grown[odd][wave] = grown;
+          const float b = base(now) * c;
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(before[e], c, -b));
+            l[0] += x[e];
+          }
+          *reinterpret_cast<u32x2*>(weights[odd][mine] + lane * 16 + half * 8) =
+              (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
+        }
+      }
+      for (int unit = first; kSplit == 1 && unit < last; ++unit) {
+        kda::lds_barrier();                                // the unit is there
+        if (!busy) {
+          if (lane == 0) lds.grown[unit & 1][wave] = 0;
+          continue;
+        }
+        unsigned char* tile = ring[unit % kRing];
+        const int key0 = unit * kUnit;
+        const bool edge = key0 + kUnit > len - p.Q + 1;    // some row does not see some key
+        const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
+        f32x4 s[2][kOwnRows];
+        {
+          // Of a key's 20 pieces of 16 bytes (eight of codes, two steps each, and two of the
+          // shared part) kAhead are on their way.
+          constexpr int kAhead = 4;
+          u32x4 a[kAhead];
+          uint32_t scales[2];
+          const int key_at = l16 * R + ((g4 ^ swirl(l16)) * 16);
+          const int shared_at = kShared + l16 * 2 * S + ((g4 ^ swirl2(l16)) * 16);
+          auto fetch = [&](int i) {
+            const int k = i & 1, at = i >> 1;
+            int x = at < 8 ? key_at : shared_at;
+            asm("" : "+v"(x));                             // (its variants are not worth a register each)
+            a[i % kAhead] = *reinterpret_cast<const u32x4*>(  // (swirl(16 + l16) = swirl(l16) ^ 8)
+                at < 8 ? tile + k * 16 * R + (x ^ at * 64 ^ k * 128) : tile + k * 32 * S + (x ^ (at - 8) * 64));
+          };
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            scales[k] = *reinterpret_cast<const uint32_t*>(exponents_of(tile, 16 * k + l16));
+#pragma unroll
+          for (int i = 0; i < kAhead - 1; ++i) fetch(i);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int t = 0; t < kOwnRows; ++t) s[k][t] = (f32x4)(0.0f);
+#pragma unroll
+          for (int i = 0; i < 20; ++i) {
+            const int k = i & 1, at = i >> 1;
+            fence();
+            if (i + kAhead - 1 < 20) fetch(i + kAhead - 1);
+            fence();
+            const u32x4 x = a[i % kAhead];
+            if (at < 8) {
+              const float f = scale_of(scales[k], at >> 1);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const bf16x8 y = widen(x[2 * half], x[2 * half + 1], f);
+#pragma unroll
+                for (int t = 0; t < kOwnRows; ++t) s[k][t] = mfma16(y, q[t][2 * at + half], s[k][t]);
+              }
+            } else {
+#pragma unroll
+              for (int t = 0; t < kOwnRows; ++t) s[k][t] = mfma16(as_bf16x8(x), q[t][at + 8], s[k][t]);
+            }
+          }
+          fence();
+        }
+        bool gone[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) gone[k] = there[unit % kRing][2 * k + (g4 >> 1)] == 0;
+        if (edge || __any(gone[0] || gone[1])) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int t = 0; t < kOwnRows; ++t)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (gone[k] || key0 + 16 * k + 4 * g4 + e >= limit[t]) s[k][t][e] = -INFINITY;
+        }
+        bool grown = false;
+#pragma unroll
+        for (int t = 0; t < kOwnRows; ++t) {
+          float mx = s[0][t][0];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[k][t][e]);
+          mx = quarter_max(mx);
+          // (row by row: what a row sees does not change how another one is rounded)
+          const float now = (mx - m[t]) * c > kSlack ? mx : m[t];
+          const float f = __builtin_amdgcn_exp2f((m[t] - base(now)) * c);
+          grown |= now != m[t];
+          m[t] = now;
+          l[t] *= f;
+          if (g4 == 0) lds.factor[unit & 1][16 * (mine + t) + l16] = f;
+          const float b = base(now) * c;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              s[k][t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][t][e], c, -b));
+              l[t] += s[k][t][e];
+            }
+        }
+        grown = __any(grown);
+        if (lane == 0) lds.grown[unit & 1][wave] = grown;
+#pragma unroll
+        for (int t = 0; t < kOwnRows; ++t) {
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * k + e] = s[k][t][e];
+          *reinterpret_cast<bf16x8*>(weights[unit & 1][mine + t] + lane * 16) = pack8(x);
+        }
+      }
+      kda::lds_barrier();                                  // the last weights are there
+      if (busy) {
+#pragma unroll
+        for (int t = 0; t < kOwnRows; ++t) {
+          l[t] = quarter_sum(l[t]);
+          if (g4 == 0) {
+            lds.sum[half][16 * (mine + t) + l16] = l[t];
+            lds.top[16 * (mine + t) + l16] = m[t];
+          }
+        }
+      }
+      kda::lds_barrier();                                  // and sums and maxima
+      if (threadIdx.x == 0) {
+        if (first == 0) p.owner[segment] = whole ? -1 : slot;
+        if (first != 0 && last == units) p.last_owner[segment] = piece.w;
+        if (first == 0 && !whole) p.cut[piece.w] = int(segment);
+      }
+    } else {
+      // ======== columns 128 wave ..
+      Tokens tokens{p.table + n * p.table_stride, min(len, last * kUnit), wave, 0, -1};
+      auto source = [&](int unit) {                        // (behind the last unit nothing comes)
+        return tokens.source(p, unit, ring[unit % kRing], there[unit % kRing]);
+      };
+      if (begun) wait_loads<0>();                          // (stores, that would count among the loads)
+      tokens.look(p, first);
+#pragma unroll
+      for (int u = 0; u < kAheadUnits; ++u) {
+        const auto next = source(first + u);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) tokens.load(next, i);
+      }
+      f32x4 o[NT][8];                                      // column 128 wave + 16 d + 4 g4 + e of row 16 t + l16
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[t][d] = (f32x4)(0.0f);
+
+      auto arrive = [&](int unit) {                        // this wave's tokens of the unit are there
+        wait_loads<(kAheadUnits - 1) * kLoads>();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        if (p.Q > 1 && unit < last && unit * kUnit + kUnit > len - p.Q + 1) tokens.without_nan(ring[unit % kRing]);
+        kda::lds_barrier();                                // and the weights of the one kLag before
+      };
+#pragma unroll
+      for (int u = 0; u < kLag; ++u) {
+        arrive(first + u);
+        const auto next = source(first + u + kAheadUnits);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) tokens.load(next, i);
+      }
+      for (int unit = first + kLag; unit < last + kLag; ++unit) {
+        arrive(unit);
+
+        // -------- the unit kLag before: lane l16 takes column l16 of 16 at keys 16 (j / 4) + 4 g4 +
+        // j % 4 for j = 0 .. 7, the order in which the scores hold them.  (A transposing
+        // read gathers, in every 16 lanes, byte i & 7 of the 8-byte pieces addressed by
+        // lanes (i >> 3) + 2 e into byte e of lane i.)
+        const int before = unit - kLag;
+        unsigned char* tile = ring[before % kRing];
+        const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
+        const int line = ((l16 >> 1) & 3) + 4 * g4 + (l16 & 8) * 2;
+        const int place = line * R + ((8 * wave) ^ swirl(line)) * 16 + (l16 & 1) * 8;
+        constexpr int kAhead = 2;                          // row tiles
+        u32x4 w[kAhead];
+        bf16x8 x[8];
+        u32x2 a[8];
+        auto fetch_weights = [&](int i) {
+          w[i % kAhead] = *reinterpret_cast<const u32x4*>(weights[before & 1][i] + lane * 16);
+        };
+        u32x4 exponents[2];                                // of the lane's eight keys
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          exponents[k] = *reinterpret_cast<const u32x4*>(exponents_of(tile, 16 * k + 4 * g4));
+        const u32x4 grown = *reinterpret_cast<const u32x4*>(lds.grown[before & 1]);
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+          a[d] = __builtin_bit_cast(u32x2, transposed((const lds_i32x2*)(tile + (place ^ d * 16))));
+#pragma unroll
+        for (int i = 0; i < kAhead - 1; ++i) fetch_weights(i);
+        fence();
+        const auto next = source(unit + kAheadUnits);      // (while these reads go on)
+        fence();
+        // Weights times the keys' scales for these columns: powers of two, so that nothing is
+        // rounded (or only below 2^-126).
+        float scales[8];
+        auto scaled = [&](const u32x4& w) {
+          u32x4 y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float lo = __uint_as_float(w[i] << 16) * scales[2 * i];
+            const float hi = __uint_as_float(w[i] & 0xffff0000u) * scales[2 * i + 1];
+            y[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302);
+          }
+          return as_bf16x8(y);
+        };
+        if (__builtin_amdgcn_readfirstlane(grown[0] | grown[1] | grown[2] | grown[3])) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const float f = lds.factor[before & 1][16 * t + l16];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[t][d] *= f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) scales[i] = scale_of(exponents[i >> 2][i & 3], wave);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[d] = widen(a[d][0], a[d][1], 1.0f);
+        fence();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          if (t + kAhead - 1 < NT) fetch_weights(t + kAhead - 1);
+          // (at once the loads would wait for one another)
+#pragma unroll
+          for (int i = t * kLoads / NT; i < (t + 1) * kLoads / NT; ++i) tokens.load(next, i);
+          const bf16x8 y = scaled(w[t % kAhead]);
+          fence();
+#pragma unroll
+          for (int d = 0; d < 8; ++d) o[t][d] = mfma16(x[d], y, o[t][d]);
+          fence();
+        }
+      }
+
+      // -------- its rows: finished, or a part
+      wait_loads<0>();                                     // (those that brought nothing, too)
+      kda::lds_barrier();
+      float* part = p.parts + int64_t(slot) * p.tile_rows * kPart;
+      auto total = [&](int r) { return kSplit == 2 ? lds.sum[0][r] + lds.sum[kSplit - 1][r] : lds.sum[0][r]; };
+      const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int r = 16 * t + l16, col = 128 * wave + 4 * g4;
+        if (whole) {
+          if (r >= rows) continue;
+          const int64_t out = int64_t(n) * p.rows + row0 + r;
+          const float sum = total(r), f = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            const f32x4 x = o[t][d] * f;
+            *reinterpret_cast<u32x2*>(p.o + out * R + col + 16 * d) =
+                (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
+          }
+          if (p.lse && wave == 0 && g4 == 0) p.lse[out] = lds.top[r] * p.scale + __logf(sum);
+        } else if (16 * t < rows) {
+#pragma unroll
+          for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(part + in_part(t, 8 * wave + d, lane)) = o[t][d];
+          if (wave == 0 && g4 == 0)
+            *reinterpret_cast<float2*>(part + p.tile_rows * R + 2 * r) = make_float2(lds.top[r], total(r));
+        }
+      }
+    }
+    left -= last - first + kExtra;
+    first = 0;
+    begun = true;
+    if (++seg == p.row_tiles) {
+      seg = 0;
+      if (++n < p.N) len = length(p, n), units = units_of<kUnit>(len);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the walk, up to 32 rows of many segments
+
+// Four waves, which go through scores, weights and output together; of a unit's scores
+// a wave has 16 keys and 16 rows.  Two workgroups on a compute unit: one has its pauses,
+// and its segments' beginnings and ends, while the other computes.  With segments this
+// is the faster one from about 512 on (latent_decode_kernel and this one, 16 heads, up to 1000
+// tokens: 300 sequences 45.2 and 44.8 us; 32 heads: 2000 of up to 2000 339 and 329, 4096 of up to 300
+// 228 and 192; and the other way 64 of up to 16384 88 and 91, one of 30000 21 and 26).
+constexpr int kManyThreads = 64 * kWaves, kPerCu = 2, kManyRing = 3;
+// As kExtra: 4096 sequences of up to 300 tokens with 0, 4, 6 and 8 222, 193, 191 and 195 us, 2000 of up
+// to 2000 344, 331, 332 and 337.
+constexpr int kManyExtra = 6;
+constexpr int kRowTiles = 2;
+
+__global__ __launch_bounds__(kManyThreads, kPerCu) void latent_decode_many_kernel(Params p) {
+  // (One object: between two the compiler tells apart what loads to LDS write, and
+  // has reads wait for all those that are on their way to the same one.)
+  __shared__ __align__(1024) struct {
+    unsigned char ring[kManyRing][kBytes];
+    unsigned char weights[kBlocks][kRowTiles][1024];
+    float scales[kUnit][kBlocks];
+    float top[2][16 * kRowTiles];                          // maxima of a unit, and in the end sums
+    int there[kManyRing][kWaves];                              // whether a wave's tokens have a page
+  } lds;
+  auto &ring = lds.ring;
+  auto &weights = lds.weights;
+  auto &scales = lds.scales;
+  auto &top = lds.top;
+  auto &there = lds.there;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave & 1, mine = wave >> 1;             // the wave's key tile, and its row tile
+
+  const Piece piece = kda::line::find_piece<kUnit, 1, kManyExtra>(p, 0, p.row_tiles);
+  if (threadIdx.x == 0) p.cut[blockIdx.x] = -1;
+  int64_t left = piece.to - piece.from;
+  int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
+  const int64_t inside = piece.from - piece.before;
+  int seg = p.row_tiles == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(inside / (units + kManyExtra)));
+  int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * (units + kManyExtra)) - kManyExtra);
+  left += min(first, 0);                                   // (the extra units are before the first)
+  first = max(first, 0);
+  bool begun = false;                                      // the piece's first segment is done
+  const float c = p.scale * kLog2e;
+
+  while (left > 0) {
+    // -------- one segment: sequence n, rows row0 .. row0 + tile_rows - 1
+    const int row0 = seg * p.tile_rows;
+    const int last = int(min(int64_t(units), first + left));
+    const int rows = min(p.rows - row0, p.tile_rows);
 
     Tokens tokens{p.table + n * p.table_stride, min(len, last * kUnit), wave, 0, -1};
     auto load = [&](int unit) {
-      const auto next = tokens.source(p, unit, ring[unit % kRing], there[unit % kRing]);
+      const auto next = tokens.source(p, unit, ring[unit % kManyRing], there[unit % kManyRing]);
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) tokens.load(next, i);
     };
@@ -295,7 +722,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
     }
     fence();
 #pragma unroll
-    for (int i = 0; i < kRing - 1; ++i)
+    for (int i = 0; i < kManyRing - 1; ++i)
       if (first + i < last) load(first + i);
     // The queries are waited for before the first unit: left to the compiler they would
     // be in every unit, and with them the loads behind them.
@@ -312,7 +739,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
     for (int unit = first; unit < last; ++unit) {
       const int key0 = unit * kUnit;
       const bool edge = key0 + kUnit > len - p.Q + 1;      // some row does not see some key
-      unsigned char* tile = ring[unit % kRing];
+      unsigned char* tile = ring[unit % kManyRing];
       const int place_lane = lane_now();
       const int p16 = place_lane & 15, p4 = place_lane >> 4;
 
@@ -327,7 +754,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
             __uint_as_float(uint32_t(tile[kScale + wave * 256 + place_lane]) << 23);
       if (edge && p.Q > 1) tokens.without_nan(tile);
       kda::lds_barrier();                                  // everybody's; and the unit before is used up
-      if (unit + kRing - 1 < last) load(unit + kRing - 1);
+      if (unit + kManyRing - 1 < last) load(unit + kManyRing - 1);
 
       // -------- scores of 16 keys (rows) and 16 rows (columns)
       f32x4 s = (f32x4)(0.0f);
@@ -368,7 +795,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
         }
         fence();
         const int key = 16 * half + 4 * p4;
-        const bool gone = there[unit % kRing][key / kOwn] == 0;
+        const bool gone = there[unit % kManyRing][key / kOwn] == 0;
         if (edge || __any(gone)) {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -480,346 +907,7 @@ __global__ __launch_bounds__(kThreads, kPerCu) void latent_decode_kernel(Params 
           *reinterpret_cast<float2*>(part + p.tile_rows * R + 2 * r) = make_float2(m[t], sum);
       }
     }
-    left -= last - first + kExtra;
-    first = 0;
-    begun = true;
-    if (++seg == p.row_tiles) {
-      seg = 0;
-      if (++n < p.N) len = length(p, n), units = units_of<kUnit>(len);
-    }
-  }
-}
-
-// ---------------------------------------------------------------- over 32 rows
-
-// Eight waves, in pairs of one that makes weights and one that uses them (a unit
-// later), one of each kind on every SIMD: of the scores a wave has all 32 keys of one
-// or two row tiles, so that maxima and sums are its own, of the output 128 columns of
-// all row tiles, which are one block of every token's scales.  The output's waves also
-// bring the tokens.
-constexpr int kWideThreads = 512;
-// As kExtra: 48 sequences of up to 8192 tokens, 96 heads 81.7, 75.6, 75.4, 74.4; 600 of up to 1000
-// 185, 148, 138, 139; 32 of up to 8000, 64 heads 59.2, 46.3, 46.5, 46.3.
-constexpr int kWideExtra = 8;
-
-// NT: row tiles of 16.
-template <int NT>
-__global__ __launch_bounds__(kWideThreads, 2) void latent_decode_wide_kernel(Params p) {
-  constexpr int kOwnRows = NT <= 4 ? 1 : 2;                // row tiles of a wave's scores
-  constexpr int kWideRing = 4;                             // units in LDS
-  __shared__ __align__(1024) struct {
-    unsigned char ring[kWideRing][kBytes];
-    unsigned char weights[2][NT][1024];
-    float factor[2][16 * NT];                              // of the output so far
-    int grown[2][kWaves];                                  // whether a wave has factors that are not 1
-    float sum[16 * NT], top[16 * NT];
-    int there[kWideRing][kWaves];                          // whether a wave's tokens have a page
-  } lds;
-  auto &ring = lds.ring;
-  auto &weights = lds.weights;
-  auto &there = lds.there;
-  const int role = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
-  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);
-
-  const Piece piece = kda::line::find_piece<kUnit, 1, kWideExtra>(p, 0, p.row_tiles);
-  if (threadIdx.x == 0) p.cut[blockIdx.x] = -1;
-  int64_t left = piece.to - piece.from;
-  int n = piece.n, len = piece.len, units = units_of<kUnit>(len);
-  const int64_t inside = piece.from - piece.before;
-  int seg = p.row_tiles == 1 ? 0 : __builtin_amdgcn_readfirstlane(int(inside / (units + kWideExtra)));
-  int first = __builtin_amdgcn_readfirstlane(int(inside - int64_t(seg) * (units + kWideExtra)) - kWideExtra);
-  left += min(first, 0);                                   // (the extra units are before the first)
-  first = max(first, 0);
-  bool begun = false;                                      // the piece's first segment is done
-  const float c = p.scale * kLog2e;
-
-  while (left > 0) {
-    // -------- one segment: sequence n, rows row0 .. row0 + tile_rows - 1
-    const int row0 = seg * p.tile_rows;
-    const int last = int(min(int64_t(units), first + left));
-    const int rows = min(p.rows - row0, p.tile_rows);
-    const bool whole = first == 0 && last == units;
-    const int64_t segment = int64_t(n) * p.row_tiles + seg;
-    const int slot = 2 * piece.w + int(begun);
-
-    if (role == 0) {
-      // ======== weights of row tiles mine ..
-      const int mine = wave * kOwnRows;
-      const bool busy = 16 * mine < rows;
-      // Rows of Q as operands.  Along a key the order is what lanes of 16 codes make it:
-      // steps 2 i and 2 i + 1 are the first and second 8 of lane group g4's 16.
-      const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
-      bf16x8 q[kOwnRows][18];
-      int limit[kOwnRows];                                 // tokens that the lane's row sees
-#pragma unroll
-      for (int t = 0; t < kOwnRows; ++t) {
-        const int r = row0 + min(16 * (mine + t) + l16, rows - 1), i = r / p.H;
-        const uint16_t* src = p.q + (int64_t(n) * p.Q + i) * p.q_stride + (r - i * p.H) * (R + S);
-#pragma unroll
-        for (int s = 0; s < 16; ++s)
-          q[t][s] = *reinterpret_cast<const bf16x8*>(src + 64 * (s >> 1) + 16 * g4 + 8 * (s & 1));
-#pragma unroll
-        for (int s = 0; s < 2; ++s) q[t][16 + s] = *reinterpret_cast<const bf16x8*>(src + R + 32 * s + 8 * g4);
-        limit[t] = len - p.Q + i + 1;
-      }
-      wait_loads<0>();
-      float m[kOwnRows], l[kOwnRows];                      // l: of this lane's keys only, until the end
-#pragma unroll
-      for (int t = 0; t < kOwnRows; ++t) m[t] = -INFINITY, l[t] = 0.0f;
-
-      for (int unit = first; unit < last; ++unit) {
-        kda::lds_barrier();                                // the unit is there
-        if (!busy) {
-          if (lane == 0) lds.grown[unit & 1][wave] = 0;
-          continue;
-        }
-        unsigned char* tile = ring[unit % kWideRing];
-        const int key0 = unit * kUnit;
-        const bool edge = key0 + kUnit > len - p.Q + 1;    // some row does not see some key
-        const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
-        f32x4 s[2][kOwnRows];
-        {
-          // Of a key's 20 pieces of 16 bytes (eight of codes, two steps each, and two of the
-          // shared part) kAhead are on their way.
-          constexpr int kAhead = 4;
-          u32x4 a[kAhead];
-          uint32_t scales[2];
-          const int key_at = l16 * R + ((g4 ^ swirl(l16)) * 16);
-          const int shared_at = kShared + l16 * 2 * S + ((g4 ^ swirl2(l16)) * 16);
-          auto fetch = [&](int i) {
-            const int k = i & 1, at = i >> 1;
-            int x = at < 8 ? key_at : shared_at;
-            asm("" : "+v"(x));                             // (its variants are not worth a register each)
-            a[i % kAhead] = *reinterpret_cast<const u32x4*>(  // (swirl(16 + l16) = swirl(l16) ^ 8)
-                at < 8 ? tile + k * 16 * R + (x ^ at * 64 ^ k * 128) : tile + k * 32 * S + (x ^ (at - 8) * 64));
-          };
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            scales[k] = *reinterpret_cast<const uint32_t*>(exponents_of(tile, 16 * k + l16));
-#pragma unroll
-          for (int i = 0; i < kAhead - 1; ++i) fetch(i);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int t = 0; t < kOwnRows; ++t) s[k][t] = (f32x4)(0.0f);
-#pragma unroll
-          for (int i = 0; i < 20; ++i) {
-            const int k = i & 1, at = i >> 1;
-            fence();
-            if (i + kAhead - 1 < 20) fetch(i + kAhead - 1);
-            fence();
-            const u32x4 x = a[i % kAhead];
-            if (at < 8) {
-              const float f = scale_of(scales[k], at >> 1);
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const bf16x8 y = widen(x[2 * half], x[2 * half + 1], f);
-#pragma unroll
-                for (int t = 0; t < kOwnRows; ++t) s[k][t] = mfma16(y, q[t][2 * at + half], s[k][t]);
-              }
-            } else {
-#pragma unroll
-              for (int t = 0; t < kOwnRows; ++t) s[k][t] = mfma16(as_bf16x8(x), q[t][at + 8], s[k][t]);
-            }
-          }
-          fence();
-        }
-        bool gone[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) gone[k] = there[unit % kWideRing][2 * k + (g4 >> 1)] == 0;
-        if (edge || __any(gone[0] || gone[1])) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int t = 0; t < kOwnRows; ++t)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (gone[k] || key0 + 16 * k + 4 * g4 + e >= limit[t]) s[k][t][e] = -INFINITY;
-        }
-        bool grown = false;
-#pragma unroll
-        for (int t = 0; t < kOwnRows; ++t) {
-          float mx = s[0][t][0];
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[k][t][e]);
-          mx = quarter_max(mx);
-          // (row by row: what a row sees does not change how another one is rounded)
-          const float now = (mx - m[t]) * c > kSlack ? mx : m[t];
-          const float f = __builtin_amdgcn_exp2f((m[t] - base(now)) * c);
-          grown |= now != m[t];
-          m[t] = now;
-          l[t] *= f;
-          if (g4 == 0) lds.factor[unit & 1][16 * (mine + t) + l16] = f;
-          const float b = base(now) * c;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[k][t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][t][e], c, -b));
-              l[t] += s[k][t][e];
-            }
-        }
-        grown = __any(grown);
-        if (lane == 0) lds.grown[unit & 1][wave] = grown;
-#pragma unroll
-        for (int t = 0; t < kOwnRows; ++t) {
-          float x[8];
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[4 * k + e] = s[k][t][e];
-          *reinterpret_cast<bf16x8*>(weights[unit & 1][mine + t] + lane * 16) = pack8(x);
-        }
-      }
-      kda::lds_barrier();                                  // the last weights are there
-      if (busy) {
-#pragma unroll
-        for (int t = 0; t < kOwnRows; ++t) {
-          l[t] = quarter_sum(l[t]);
-          if (g4 == 0) {
-            lds.sum[16 * (mine + t) + l16] = l[t];
-            lds.top[16 * (mine + t) + l16] = m[t];
-          }
-        }
-      }
-      kda::lds_barrier();                                  // and sums and maxima
-      if (threadIdx.x == 0) {
-        if (first == 0) p.owner[segment] = whole ? -1 : slot;
-        if (first != 0 && last == units) p.last_owner[segment] = piece.w;
-        if (first == 0 && !whole) p.cut[piece.w] = int(segment);
-      }
-    } else {
-      // ======== columns 128 wave ..
-      Tokens tokens{p.table + n * p.table_stride, min(len, last * kUnit), wave, 0, -1};
-      auto source = [&](int unit) {                        // (behind the last unit nothing comes)
-        return tokens.source(p, unit, ring[unit % kWideRing], there[unit % kWideRing]);
-      };
-      if (begun) wait_loads<0>();                          // (stores, that would count among the loads)
-      tokens.look(p, first);
-#pragma unroll
-      for (int u = 0; u < kWideRing - 2; ++u) {
-        const auto next = source(first + u);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) tokens.load(next, i);
-      }
-      f32x4 o[NT][8];                                      // column 128 wave + 16 d + 4 g4 + e of row 16 t + l16
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int d = 0; d < 8; ++d) o[t][d] = (f32x4)(0.0f);
-
-      auto arrive = [&](int unit) {                        // this wave's tokens of the unit are there
-        wait_loads<(kWideRing - 3) * kLoads>();
-        __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        if (p.Q > 1 && unit < last && unit * kUnit + kUnit > len - p.Q + 1) tokens.without_nan(ring[unit % kWideRing]);
-        kda::lds_barrier();                                // and the weights of the unit before
-      };
-      arrive(first);
-      {
-        const auto next = source(first + kWideRing - 2);
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) tokens.load(next, i);
-      }
-      for (int unit = first + 1; unit <= last; ++unit) {
-        arrive(unit);
-        const auto next = source(unit + kWideRing - 2);
-
-        // -------- the unit before: lane l16 takes column l16 of 16 at keys 16 (j / 4) + 4 g4 +
-        // j % 4 for j = 0 .. 7, the order in which the scores hold them.  (A transposing
-        // read gathers, in every 16 lanes, byte i & 7 of the 8-byte pieces addressed by
-        // lanes (i >> 3) + 2 e into byte e of lane i.)
-        const int before = unit - 1;
-        unsigned char* tile = ring[before % kWideRing];
-        const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
-        const int line = ((l16 >> 1) & 3) + 4 * g4 + (l16 & 8) * 2;
-        const int place = line * R + ((8 * wave) ^ swirl(line)) * 16 + (l16 & 1) * 8;
-        constexpr int kAhead = 2;                          // row tiles
-        u32x4 w[kAhead];
-        bf16x8 x[8];
-        u32x2 a[8];
-        auto fetch_weights = [&](int i) {
-          w[i % kAhead] = *reinterpret_cast<const u32x4*>(weights[before & 1][i] + lane * 16);
-        };
-        // Scales of the lane's eight keys for these columns, and weights times them: a power
-        // of two, so that nothing is rounded (or only below 2^-126).
-        u32x4 exponents[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          exponents[k] = *reinterpret_cast<const u32x4*>(exponents_of(tile, 16 * k + 4 * g4));
-        float scales[8];
-        auto scaled = [&](const u32x4& w) {
-          u32x4 y;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float lo = __uint_as_float(w[i] << 16) * scales[2 * i];
-            const float hi = __uint_as_float(w[i] & 0xffff0000u) * scales[2 * i + 1];
-            y[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302);
-          }
-          return as_bf16x8(y);
-        };
-        const u32x4 grown = *reinterpret_cast<const u32x4*>(lds.grown[before & 1]);
-#pragma unroll
-        for (int d = 0; d < 8; ++d)
-          a[d] = __builtin_bit_cast(u32x2, transposed((const lds_i32x2*)(tile + (place ^ d * 16))));
-        if (__builtin_amdgcn_readfirstlane(grown[0] | grown[1] | grown[2] | grown[3])) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const float f = lds.factor[before & 1][16 * t + l16];
-#pragma unroll
-            for (int d = 0; d < 8; ++d) o[t][d] *= f;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead - 1; ++i) fetch_weights(i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) scales[i] = scale_of(exponents[i >> 2][i & 3], wave);
-#pragma unroll
-        for (int d = 0; d < 8; ++d) x[d] = widen(a[d][0], a[d][1], 1.0f);
-        fence();
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (t + kAhead - 1 < NT) fetch_weights(t + kAhead - 1);
-          // (at once the loads would wait for one another)
-#pragma unroll
-          for (int i = t * kLoads / NT; i < (t + 1) * kLoads / NT; ++i) tokens.load(next, i);
-          const bf16x8 y = scaled(w[t % kAhead]);
-          fence();
-#pragma unroll
-          for (int d = 0; d < 8; ++d) o[t][d] = mfma16(x[d], y, o[t][d]);
-          fence();
-        }
-      }
-
-      // -------- its rows: finished, or a part
-      wait_loads<0>();                                     // (those that brought nothing, too)
-      kda::lds_barrier();
-      float* part = p.parts + int64_t(slot) * p.tile_rows * kPart;
-      const int lane = lane_now(), l16 = lane & 15, g4 = lane >> 4;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int r = 16 * t + l16, col = 128 * wave + 4 * g4;
-        if (whole) {
-          if (r >= rows) continue;
-          const int64_t out = int64_t(n) * p.rows + row0 + r;
-          const float sum = lds.sum[r], f = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            const f32x4 x = o[t][d] * f;
-            *reinterpret_cast<u32x2*>(p.o + out * R + col + 16 * d) =
-                (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
-          }
-          if (p.lse && wave == 0 && g4 == 0) p.lse[out] = lds.top[r] * p.scale + __logf(sum);
-        } else if (16 * t < rows) {
-#pragma unroll
-          for (int d = 0; d < 8; ++d) *reinterpret_cast<f32x4*>(part + in_part(t, 8 * wave + d, lane)) = o[t][d];
-          if (wave == 0 && g4 == 0)
-            *reinterpret_cast<float2*>(part + p.tile_rows * R + 2 * r) = make_float2(lds.top[r], lds.sum[r]);
-        }
-      }
-    }
-    left -= last - first + kWideExtra;
+    left -= last - first + kManyExtra;
     first = 0;
     begun = true;
     if (++seg == p.row_tiles) {
@@ -918,18 +1006,20 @@ __global__ __launch_bounds__(64 * STREAMS) void latent_decode_join_kernel(Params
 struct Plan {
   int rows, tile_rows, row_tiles, pieces;
   int64_t segments;
+  bool many;
   size_t parts, bytes;
 };
 
-// Up to 32 rows go to the kernel of four waves, more, in equal tiles of up to 96, which
-// is what eight waves' registers hold, to the other.
+// Rows in equal tiles of up to 96, which is what eight waves' registers hold.  Many
+// segments of up to 32 rows go to the kernel of four waves.
 Plan plan_for(int64_t N, int64_t Q, int H) {
   Plan x;
   x.rows = int(Q * H);
   x.row_tiles = (x.rows + 95) / 96;
   x.tile_rows = ((x.rows + x.row_tiles - 1) / x.row_tiles + 15) / 16 * 16;
-  x.pieces = kda::device_cus() * (x.tile_rows <= 32 ? kPerCu : 1);
   x.segments = N * x.row_tiles;
+  x.many = x.tile_rows <= 32 && x.segments > 2 * kda::device_cus();
+  x.pieces = kda::device_cus() * (x.many ? kPerCu : 1);
   x.parts = size_t(2 * x.pieces) * x.tile_rows * kPart * sizeof(float);
   x.bytes = x.parts + (size_t(x.segments) * 2 + x.pieces) * sizeof(int);
   return x;
@@ -978,16 +1068,17 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
                  static_cast<float*>(workspace), owner, owner + x.segments, owner + 2 * x.segments, x.segments > x.pieces};
   const hipStream_t st = kda::as_stream(stream);
   // No more pieces than units that the tables could hold.
-  const int extra = x.tile_rows <= 32 ? kExtra : kWideExtra;
-  const int64_t most = x.segments * ((int64_t(table_width) * page_size + kUnit - 1) / kUnit + extra);
+  const int64_t most = x.segments * ((int64_t(table_width) * page_size + kUnit - 1) / kUnit + (x.many ? kManyExtra : kExtra));
   const int pieces = int(x.pieces < most ? x.pieces : most);
   const dim3 grid{unsigned(pieces)};
-  if (x.tile_rows <= 32)
-    hipLaunchKernelGGL(latent_decode_kernel, grid, dim3(kThreads), 0, st, p);
+  if (x.many)
+    hipLaunchKernelGGL(latent_decode_many_kernel, grid, dim3(kManyThreads), 0, st, p);
+  else if (x.tile_rows <= 32)
+    hipLaunchKernelGGL(latent_decode_kernel<2>, grid, dim3(kThreads), 0, st, p);
   else if (x.tile_rows <= 64)
-    hipLaunchKernelGGL(latent_decode_wide_kernel<4>, grid, dim3(kWideThreads), 0, st, p);
+    hipLaunchKernelGGL(latent_decode_kernel<4>, grid, dim3(kThreads), 0, st, p);
   else
-    hipLaunchKernelGGL(latent_decode_wide_kernel<6>, grid, dim3(kWideThreads), 0, st, p);
+    hipLaunchKernelGGL(latent_decode_kernel<6>, grid, dim3(kThreads), 0, st, p);
   // By the parts of a segment, about; 1, 4 and 16 streams in us: with 12 (20 sequences of up to
   // 8000 tokens, 96 heads) 64.8 and 66.2, with 16 (32 of 16 heads) 39.4 and 37.6, with 64 (8 of
   // them) 25.4 for 4 and 24.9 for 16, with 128 (4) 24.1 and 19.7.

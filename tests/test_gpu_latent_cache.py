@@ -221,6 +221,37 @@ def test_decode_many_sequences_of_many_heads(gpu_lib, H):
     check_decode(o, lse, q, cache, table, lens)
 
 
+@pytest.mark.parametrize("Q,H", [(1, 1), (1, 17), (1, 32), (4, 8), (6, 5)])
+def test_decode_more_sequences_than_workgroups(gpu_lib, Q, H):
+    """600 short histories: missing pages, NaN beside the tokens, and NaN among the newest ones, which the queries
+    before them do not see."""
+    rng = np.random.default_rng(40 + H)
+    lens = [int(x) for x in rng.integers(0, 50, 600)]
+    lens[7], lens[599] = 1500, 400
+    q, cache, table, _ = make_decode(41, lens, Q, H, 16)
+    table[7, 3] = table[20, 0] = -1
+    held = np.zeros(cache[0].shape[:2], bool)
+    for row, n in zip(table, lens):
+        for t in range(n):
+            held[row[t // 16], t % 16] |= row[t // 16] >= 0
+    o, lse = gpu_lib.latent_decode(q, *cache, ints(table), ints(lens))
+    check_decode(o, lse, q, cache, table, lens)
+    free = torch.from_numpy(~held).to(DEV)
+    cache[0].view(torch.uint8)[free] = 0x7f
+    cache[1][free] = 255
+    cache[2][free] = float("nan")
+    a, b = gpu_lib.latent_decode(q, *cache, ints(table), ints(lens))
+    assert torch.equal(a, o) and torch.equal(b, lse)
+    if Q > 1:
+        for row, n in zip(table, lens):
+            if n > 1 and row[(n - 1) // 16] >= 0:
+                cache[0].view(torch.uint8)[row[(n - 1) // 16], (n - 1) % 16, 77] = 0xff
+        a, b = gpu_lib.latent_decode(q, *cache, ints(table), ints(lens))
+        assert torch.equal(a[:, :Q - 1], o[:, :Q - 1]) and torch.equal(b[:, :Q - 1], lse[:, :Q - 1])
+        seen = [n > 1 and row[(n - 1) // 16] >= 0 for row, n in zip(table, lens)]
+        assert torch.isnan(a[:, Q - 1][torch.tensor(seen, device=DEV)]).all()
+
+
 def test_decode_tables(gpu_lib):
     """Missing pages in the middle, ids out of range, lengths past the table, wide tables, slices of wider rows."""
     lens = [300, 500, -4, 10 ** 9, 64]
