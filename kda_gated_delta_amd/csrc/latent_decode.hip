@@ -23,8 +23,8 @@
 //
 // What bounds it: up to 32 rows a step of the output's waves (2500 cycles, of them a
 // quarter waits to send the loads of a next unit), near to what memory allows (64
-// sequences of up to 16384 tokens, 32 heads, 327 MB: 89 us; 79 of them the walk, which
-// reads 4.3 TB/s, 7 the join of 21 MB of parts).  With more rows a unit's conversions,
+// sequences of up to 16384 tokens, 32 heads, 327 MB: 89 us; the walk reads 335 MB and
+// writes 20 of parts, the join takes 6 us of it).  With more rows a unit's conversions,
 // products and weights (48 sequences of up to 8192 tokens, 96 heads, 41 GFLOP: 76 us;
 // 4100 cycles for a unit's 96 rows, of which products 1900, and 60 MB of parts written
 // and read).  One short history is two launches.
