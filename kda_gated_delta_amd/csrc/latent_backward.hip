@@ -6,9 +6,8 @@
 //     dQ = scale dS K,   [dKn dS_shared] = scale dS^T Q,
 // the shared part's summed over all heads.
 //
-// Statistics first (lse in powers of two and delta); then workgroups of 128 keys,
-// which walk the query rows for dK and dV, and workgroups of 128 query rows, which
-// walk the keys for dQ.  Every head has keys of its own, so a walk belongs to one head;
+// Workgroups of 128 query rows walk the keys for dQ (and first make lse in powers of
+// two and delta), then workgroups of 128 keys walk the query rows for dK and dV.  Every head has keys of its own, so a walk belongs to one head;
 // only the shared part's gradient crosses heads.  Its terms are written in float32
 // per head and added in order by latent_sum_kernel, as the parts of a key tile that
 // several workgroups share are.
@@ -18,7 +17,8 @@
 // float32 through memory and in order (attn_backward.hip has no such sums either).
 // What bounds the walks are the products, at the power limit (8192 tokens x 16 heads:
 // dK and dV 609 to 646 us, 0.69 TFLOP, 1070 TFLOP/s; dQ 476 to 491 us, 0.55 TFLOP, 1120;
-// statistics 15, sum 8; a large matrix product reaches 1224 on this card).  With all
+// sum 8; a large matrix product reaches 1224 on this card).  lse2 and delta in a launch of
+// their own cost 7 to 13 us (6 samples of up to 500 tokens x 16 heads 89 to 82).  With all
 // of a walk in one wave and both walks in one launch of one workgroup to a compute
 // unit, dK, dV and dQ took 1422 us: nothing ran while a SIMD's one wave made weights.
 #include "kda_host.h"
@@ -50,14 +50,15 @@ struct Params {
 
 constexpr int kKeyBuffer = 2 * kTileBytes + kThinBytes;    // K, V, the shared part
 
-// What a workgroup of 128 query rows does.  kStats: it writes lse2 and delta, for
-// all that follow; otherwise it reads them and makes dQ.
-template <typename Out, bool kBoth, bool kStats>
-__device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsigned char* lds) {
+// A workgroup has 128 query rows.  It also writes their lse2 and delta, for the walks
+// over query rows that follow.
+template <typename Out, bool kBoth>
+__global__ __launch_bounds__(kThreads, 2) void latent_dq_kernel(Params p) {
+  __shared__ __align__(1024) unsigned char lds[2 * kKeyBuffer];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l32 = lane & 31, h = lane >> 5;
-  const int slot = int(block / unsigned(p.H)), head = int(block % unsigned(p.H));
-  const Rows rows = find_rows<kStats>(p.cu, p.N, p.T, slot, p.slots, BM);   // a sequence's first take longest there
+  const int slot = int(blockIdx.x / unsigned(p.H)), head = int(blockIdx.x % unsigned(p.H));
+  const Rows rows = find_rows<false>(p.cu, p.N, p.T, slot, p.slots, BM);
   if (rows.row0 >= rows.len) return;
   const Keys keys = find_keys(p.cu_kv, p.K, rows.n, rows.len);
 
@@ -73,8 +74,8 @@ __device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsi
     for (int s = 0; s < 8; ++s) u[s] = *reinterpret_cast<const bf16x8*>(us + 16 * s);
   }
   const int64_t stat = (int64_t(rows.b) * p.H + head) * p.T + rows.start + r;
-  float lse2 = kStats ? p.lse[stat] * kLog2e : p.lse2[stat];
-  if (kStats && lse2 == -INFINITY) lse2 = INFINITY;        // all scores -inf, or no keys: weights of zero
+  float lse2 = p.lse[stat] * kLog2e;
+  if (lse2 == -INFINITY) lse2 = INFINITY;                  // all scores -inf, or no keys: weights of zero
   const float c = p.scale * kLog2e;
   f32x16 dq[6];
 #pragma unroll
@@ -121,24 +122,18 @@ __device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsi
   // gradient of the row (see attn_backward.hip).  Of rows that see few keys (two
   // tiles at most) it is made as sum_j P_ij (dO V^T)_ij, to which it is equal.
   float delta = 0.0f;
-  if constexpr (!kStats) {
-    if (tiles > 0) issue(0, 0);
-    delta = p.delta[stat];
-  } else if (tiles <= 2) {
-    for (int t = 0; t < tiles; ++t) {                      // one buffer, and more workgroups
-      if (t > 0) kda::lds_barrier();
-      issue(t, 0);
-      __builtin_amdgcn_s_waitcnt(kWaitLoads);
-      kda::lds_barrier();
-      for (int w = 0; w < 2; ++w) {
-        const int key0 = t * kTile + 32 * w;
-        if (key0 > see0 + 31) break;
-        f32x16 s, g;
-        scores(lds, w, key0, s, g);
+  if (tiles <= 2) {
+    for (int t = 0; t < tiles; ++t) issue(t, t);
+    __builtin_amdgcn_s_waitcnt(kWaitLoads);
+    kda::lds_barrier();
+    for (int w = 0; w < 2 * tiles; ++w) {
+      if (32 * w > see0 + 31) break;
+      f32x16 s, g;
+      scores(lds + w / 2 * kKeyBuffer, w & 1, 32 * w, s, g);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) delta = __builtin_fmaf(s[e], g[e], delta);
-      }
+      for (int e = 0; e < 16; ++e) delta = __builtin_fmaf(s[e], g[e], delta);
     }
+    kda::lds_barrier();
   } else {
     const uint16_t* os = p.o + ((rows.first + r) * p.H + head) * D + 8 * h;
 #pragma unroll
@@ -148,15 +143,13 @@ __device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsi
       for (int j = 0; j < 8; ++j) delta = __builtin_fmaf(float(x[j]), float(u[s][j]), delta);
     }
   }
-  if constexpr (kStats) {
-    delta = half_sum(delta);
-    if (r0 + l32 < rows.len && h == 0) {
-      p.lse2[stat] = lse2;
-      p.delta[stat] = delta;
-    }
-    return;
+  delta = half_sum(delta);
+  if (r0 + l32 < rows.len && h == 0) {
+    p.lse2[stat] = lse2;
+    p.delta[stat] = delta;
   }
 
+  if (tiles > 0) issue(0, 0);
   for (int t = 0; t < tiles; ++t) {
     __builtin_amdgcn_s_waitcnt(kWaitLoads);
     kda::lds_barrier();
@@ -193,17 +186,6 @@ __device__ __forceinline__ void rows_of_dq(const Params& p, unsigned block, unsi
   Out* dst = static_cast<Out*>(p.dq) + ((rows.first + r) * p.H + head) * DQ;
 #pragma unroll
   for (int d = 0; d < 6; ++d) store_row32(dst + 32 * d, dq[d], p.scale, h);
-}
-
-__global__ __launch_bounds__(kThreads, 3) void latent_stats_kernel(Params p) {
-  __shared__ __align__(1024) unsigned char lds[kKeyBuffer];
-  rows_of_dq<float, false, true>(p, blockIdx.x, lds);
-}
-
-template <typename Out, bool kBoth>
-__global__ __launch_bounds__(kThreads, 2) void latent_dq_kernel(Params p) {
-  __shared__ __align__(1024) unsigned char lds[2 * kKeyBuffer];
-  rows_of_dq<Out, kBoth, false>(p, blockIdx.x, lds);
 }
 
 // ---------------------------------------------------------------- dK and dV
@@ -528,18 +510,17 @@ Plan plan_for(int64_t B, int T, int T_kv, int H, int num_seqs) {
 
 template <typename Out, bool kBoth>
 void launch_grads(const Params& p, unsigned key_blocks, unsigned blocks, hipStream_t stream) {
+  if (blocks) hipLaunchKernelGGL((latent_dq_kernel<Out, kBoth>), dim3(blocks), dim3(kThreads), 0, stream, p);
   const dim3 keys(key_blocks);
   if (key_blocks && p.parts == 1)
     hipLaunchKernelGGL((latent_dkv_kernel<Out, kBoth>), keys, dim3(2 * kThreads), 0, stream, p);
   else if (key_blocks)
     hipLaunchKernelGGL((latent_dkv_kernel<float, kBoth>), keys, dim3(2 * kThreads), 0, stream, p);
-  if (blocks) hipLaunchKernelGGL((latent_dq_kernel<Out, kBoth>), dim3(blocks), dim3(kThreads), 0, stream, p);
 }
 
 template <typename Out>
 int launch(const Params& p, const Plan& x, hipStream_t stream) {
   const unsigned blocks = unsigned(x.slots * p.H), key_blocks = unsigned(x.key_slots * p.H * p.parts);
-  if (blocks) hipLaunchKernelGGL(latent_stats_kernel, dim3(blocks), dim3(kThreads), 0, stream, p);
   if (both_terms(int64_t(p.B) * p.T * p.H, kda::attn_typical(p.K, p.N, p.cu != nullptr)))
     launch_grads<Out, true>(p, key_blocks, blocks, stream);
   else

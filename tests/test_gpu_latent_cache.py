@@ -221,13 +221,14 @@ def test_decode_many_sequences_of_many_heads(gpu_lib, H):
     check_decode(o, lse, q, cache, table, lens)
 
 
+@pytest.mark.parametrize("N", [300, 600])
 @pytest.mark.parametrize("Q,H", [(1, 1), (1, 17), (1, 32), (4, 8), (6, 5)])
-def test_decode_more_sequences_than_workgroups(gpu_lib, Q, H):
-    """600 short histories: missing pages, NaN beside the tokens, and NaN among the newest ones, which the queries
+def test_decode_more_sequences_than_workgroups(gpu_lib, N, Q, H):
+    """Many short histories: missing pages, NaN beside the tokens, and NaN among the newest ones, which the queries
     before them do not see."""
     rng = np.random.default_rng(40 + H)
-    lens = [int(x) for x in rng.integers(0, 50, 600)]
-    lens[7], lens[599] = 1500, 400
+    lens = [int(x) for x in rng.integers(0, 50, N)]
+    lens[7], lens[N - 1] = 1500, 400
     q, cache, table, _ = make_decode(41, lens, Q, H, 16)
     table[7, 3] = table[20, 0] = -1
     held = np.zeros(cache[0].shape[:2], bool)
