@@ -119,19 +119,26 @@ __global__ __launch_bounds__(kThreads, 2) void latent_dq_kernel(Params p) {
   };
 
   // delta.  The rounding of o to bfloat16 enters it, and with it every score's
-  // gradient of the row (see attn_backward.hip).  Of rows that see few keys (two
-  // tiles at most) it is made as sum_j P_ij (dO V^T)_ij, to which it is equal.
+  // gradient of the row (see attn_backward.hip).  Of rows that see few keys (four
+  // tiles at most) it is made as sum_j P_ij (dO V^T)_ij, to which it is equal: dQ's error,
+  // in halves of a rounding's, is 1.54 with none or two tiles so, 1.43 with four and 1.42 with
+  // all (4 sequences of up to 690 tokens, 2 heads); four cost 5 us where no row sees more and
+  // nothing elsewhere, eight 15 of 570.
   float delta = 0.0f;
-  if (tiles <= 2) {
-    for (int t = 0; t < tiles; ++t) issue(t, t);
-    __builtin_amdgcn_s_waitcnt(kWaitLoads);
-    kda::lds_barrier();
-    for (int w = 0; w < 2 * tiles; ++w) {
-      if (32 * w > see0 + 31) break;
-      f32x16 s, g;
-      scores(lds + w / 2 * kKeyBuffer, w & 1, 32 * w, s, g);
+  if (tiles <= 4) {
+    if (tiles > 0) issue(0, 0);
+    for (int t = 0; t < tiles; ++t) {
+      __builtin_amdgcn_s_waitcnt(kWaitLoads);
+      kda::lds_barrier();
+      if (t + 1 < tiles) issue(t + 1, (t + 1) & 1);
+      for (int w = 0; w < 2; ++w) {
+        const int key0 = t * kTile + 32 * w;
+        if (key0 > see0 + 31) break;
+        f32x16 s, g;
+        scores(lds + (t & 1) * kKeyBuffer, w, key0, s, g);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) delta = __builtin_fmaf(s[e], g[e], delta);
+        for (int e = 0; e < 16; ++e) delta = __builtin_fmaf(s[e], g[e], delta);
+      }
     }
     kda::lds_barrier();
   } else {
@@ -481,9 +488,11 @@ int64_t slots_for(int B, int T, int num_seqs) {
 
 size_t stat_floats(int64_t B, int64_t T, int64_t H) { return size_t((B * T * H + 3) / 4 * 4); }
 
-// Whether weights and score gradients are carried as two bfloat16 terms: see
-// attn_backward.hip.
-bool both_terms(int64_t rows, int64_t len) { return rows * len <= 1 << 15; }
+// Whether weights and score gradients are carried as two bfloat16 terms, which leaves a
+// gradient the error of its own rounding instead of 1.41 times that (by chance more
+// where there are few of them, 1.46 with 300 rows x 5 heads) and there costs little: 48.5 to
+// 52.5 us for 2 sequences of up to 201 tokens, 5 heads, 53.5 to 57.3 for 4 of up to 228, 12 heads.
+bool both_terms(int64_t rows, int64_t len) { return rows * len <= 1 << 19; }
 
 struct Plan {
   int64_t slots, key_slots;
