@@ -62,7 +62,7 @@ struct Params {
   int64_t q_stride;
   const uint8_t *codes, *exponents;
   const uint16_t* shared;
-  int64_t c_stride, scale_stride, s_stride;
+  uint32_t c_stride, scale_stride, s_stride;
   const int32_t* table;
   int64_t table_stride;
   const int32_t* lens;
@@ -187,7 +187,7 @@ struct Tokens {
     if (unit - from >= 64) look(p, unit);
     const int slot = __builtin_amdgcn_readlane(slots, unit - from);
     const int some = slot < 0 ? 0 : min(end - (unit * kUnit + wave * kOwn), kOwn);
-    const int64_t page = max(slot, 0) >> p.shift;
+    const uint64_t page = uint32_t(max(slot, 0)) >> p.shift;
     const int at = max(slot, 0) & ((1 << p.shift) - 1);
     if (lane_now() == 0) there[wave] = some;
     return Source{p.codes + page * p.c_stride + at * R, p.shared + page * p.s_stride + at * S,
@@ -1062,8 +1062,8 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
   if (workspace_bytes < x.bytes) return KDA_ERR_WORKSPACE;
   int* owner = reinterpret_cast<int*>(static_cast<char*>(workspace) + x.parts);
   const Params p{static_cast<const uint16_t*>(q), q_stride, static_cast<const uint8_t*>(c_cache),
-                 static_cast<const uint8_t*>(c_scale), static_cast<const uint16_t*>(k_cache), c_page, scale_page,
-                 k_page, page_table, table_stride, kv_lens, N, Q, H, table_width, __builtin_ctz(page_size), num_pages,
+                 static_cast<const uint8_t*>(c_scale), static_cast<const uint16_t*>(k_cache), uint32_t(c_page),
+                 uint32_t(scale_page), uint32_t(k_page), page_table, table_stride, kv_lens, N, Q, H, table_width, __builtin_ctz(page_size), num_pages,
                  scale, static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, x.pieces,
                  static_cast<float*>(workspace), owner, owner + x.segments, owner + 2 * x.segments, x.segments > x.pieces};
   const hipStream_t st = kda::as_stream(stream);
