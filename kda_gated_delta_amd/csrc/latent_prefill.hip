@@ -119,7 +119,8 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
       for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[u][e]);
     mx = half_max(mx);
     if (__any((mx - m) * c > kSlack)) {
-      const float now = fmaxf(m, mx);
+      // (row by row: what a row sees does not change how another one is rounded)
+      const float now = (mx - m) * c > kSlack ? mx : m;
       const float f = __builtin_amdgcn_exp2f((m - base(now)) * c);
       m = now;
       l *= f;
