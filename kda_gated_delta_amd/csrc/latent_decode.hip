@@ -111,14 +111,6 @@ __device__ __forceinline__ int swirl2(int r) { return (r >> 1) & 7; }
 // before its product, and the wave waits for every one of them.)
 __device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
 
-// The lane, made anew: what is made of it again for every unit takes no register from
-// the queries and the output meanwhile.
-__device__ __forceinline__ int lane_now() {
-  int x;
-  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
-  return x;
-}
-
 // Sum and maximum over the four lanes that hold a row.
 __device__ __forceinline__ u32x2 quarters(float x) {       // rows 0 and 1, or 2 and 3, of 16 lanes
   const uint32_t u = __float_as_uint(x);

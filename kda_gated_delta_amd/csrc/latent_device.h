@@ -14,6 +14,14 @@ constexpr int S = 64;                    // the key part that all heads share
 constexpr int DQ = D + S;                // an expanded query
 constexpr int kBlocks = R / 128;         // scales of a token
 
+// The lane, made anew: what is made of it again for every unit or tile takes no
+// register from the queries and the output meanwhile.
+__device__ __forceinline__ int lane_now() {
+  int x;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
+  return x;
+}
+
 // Lines of 128 bytes, or of an odd multiple: successive lines begin in the two
 // halves of the banks' 256 bytes by turns.  Piece c (16 bytes) of line r is stored
 // at place c ^ turn(r): 16 successive lines hold one piece in 16 different places,

@@ -43,6 +43,14 @@ struct Params {
   float* lse;
 };
 
+constexpr int kWhole = 0, kDiagonal = 1, kPartly = 2;
+// Eight bfloat16 values, zero for those that are not finite.
+__device__ __forceinline__ bf16x8 finite_or_zero(bf16x8 x) {
+  typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+  const u16x8 b = __builtin_bit_cast(u16x8, x);
+  return __builtin_bit_cast(bf16x8, (b & 0x7f80) == 0x7f80 ? (u16x8)(0) : b);
+}
+
 // kSplit = 2: a second set of four waves takes every other key tile of the same
 // rows, and the two halves of a row are joined at the end (attn_split says when).
 template <int kSplit>
@@ -88,11 +96,14 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
     sload.issue(sb + at * p.s_stride, p.s_stride, keys.len - int(at), to + 2 * kTileBytes, wave);
     vload.issue(vb + at * p.v_stride, p.v_stride, keys.len - int(at), to + kTileBytes, wave);
   };
-  int late = -1;                                          // first key of a tile left for the end
-  auto tile = [&](const unsigned char* kt, int key0, auto diagonal) {
+  int late = -1;                                          // first key of a tile with values left for the end
+  auto tile = [&](const unsigned char* kt, int key0, auto kind_of) {
+    constexpr int kind = decltype(kind_of)::value;
+    // (where the diagonal crosses nothing that follows from the lane is kept from tile to tile)
+    const int lane = kind == kWhole ? int(threadIdx.x & 63) : lane_now(), l32 = lane & 31, h = lane >> 5;
     const unsigned char *vt = kt + kTileBytes, *st = vt + kTileBytes;
     // where no row of the wave sees the tile's second half it is left out
-    const int halves_seen = decltype(diagonal)::value && see0 + 31 < key0 + 32 ? 1 : 2;
+    const int halves_seen = kind != kWhole && see0 + 31 < key0 + 32 ? 1 : 2;
     f32x16 s[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -103,14 +114,13 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
 #pragma unroll
       for (int k = 0; k < 4; ++k) s[u] = mfma32(rows_of<2 * S>(st, 32 * u, l32, h, k), q[8 + k], s[u]);
     }
-    if constexpr (decltype(diagonal)::value) {
+    if constexpr (kind != kWhole) {
       const int last = see0 + l32 - key0;                 // the last key of the tile that the row sees
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (32 * u + 8 * (e >> 2) + 4 * h + (e & 3) > last) s[u][e] = -INFINITY;
-      if (late < 0 && any_not_finite(vt, halves_seen, lane)) late = key0;
     }
     float mx = s[0][0];
 #pragma unroll
@@ -137,7 +147,6 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
         sum += s[u][e];
       }
     l += sum;
-    if (decltype(diagonal)::value && late >= 0) return;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (u >= halves_seen) continue;
@@ -148,7 +157,11 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
         for (int j = 0; j < 8; ++j) x[j] = s[u][8 * k + j];
         const bf16x8 w = pack8(x);
 #pragma unroll
-        for (int d = 0; d < 4; ++d) o[d] = mfma32(columns_of<256>(vt, 32 * u, k, 32 * d, lane), w, o[d]);
+        for (int d = 0; d < 4; ++d) {
+          const bf16x8 v = columns_of<256>(vt, 32 * u, k, 32 * d, lane);
+          o[d] = mfma32(kind == kPartly ? finite_or_zero(v) : v, w, o[d]);
+          if (kind == kPartly) __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   };
@@ -161,7 +174,7 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
     kda::lds_barrier();
     if ((i + 1) * kSplit + half < tiles) issue((i + 1) * kSplit + half, (i + 1) & 1);
   };
-  auto take = [&](int i, auto diagonal) { tile(lds + (i & 1) * kBuffer, (i * kSplit + half) * kTile, diagonal); };
+  auto take = [&](int i, auto kind) { tile(lds + (i & 1) * kBuffer, (i * kSplit + half) * kTile, kind); };
   if (half < tiles) issue(half, 0);
   // Tiles that all rows of the wave see, those that the diagonal crosses (two at
   // most, since 32 rows end within 32 keys; none perhaps, or none of this half's),
@@ -170,19 +183,24 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
   int i = 0;
   for (; i * kSplit + half < whole; ++i) {
     arrive(i);
-    take(i, std::false_type{});
+    take(i, std::integral_constant<int, kWhole>{});
   }
 #pragma unroll 1
   for (; i * kSplit + half < some; ++i) {
     arrive(i);
-    take(i, std::true_type{});
+    const int key0 = (i * kSplit + half) * kTile;
+    if (any_not_finite(lds + (i & 1) * kBuffer + kTileBytes, see0 + 31 < key0 + 32 ? 1 : 2, lane_now())) {
+      if (late < 0) late = key0;
+      take(i, std::integral_constant<int, kPartly>{});
+    } else {
+      take(i, std::integral_constant<int, kDiagonal>{});
+    }
   }
   for (; i < rounds; ++i) arrive(i);
 
-  // A weight of zero does not keep an infinity or NaN of a later row of V out of a
-  // product.  If a tile that the diagonal crosses holds one, its keys (and those of
-  // this half's next such tile) are added here one by one, from memory, each to the
-  // rows that see it.
+  // Those values (and those of this half's next such tile) are added here, from memory,
+  // each to the rows that see it: nothing that is finite is rounded otherwise than
+  // without them.
   if (late >= 0) {
     const int end = min(see0 + 32, keys.len);
 #pragma unroll 1
@@ -204,10 +222,11 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const u32x2 y = *reinterpret_cast<const u32x2*>(vr + 32 * d + 8 * e);
-          o[d][4 * e] = __builtin_fmaf(x, kda::bf16lo(y[0]), o[d][4 * e]);
-          o[d][4 * e + 1] = __builtin_fmaf(x, kda::bf16hi(y[0]), o[d][4 * e + 1]);
-          o[d][4 * e + 2] = __builtin_fmaf(x, kda::bf16lo(y[1]), o[d][4 * e + 2]);
-          o[d][4 * e + 3] = __builtin_fmaf(x, kda::bf16hi(y[1]), o[d][4 * e + 3]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float f = j & 1 ? kda::bf16hi(y[j >> 1]) : kda::bf16lo(y[j >> 1]), sum = o[d][4 * e + j];
+            o[d][4 * e + j] = __builtin_fabsf(f) < INFINITY ? sum : __builtin_fmaf(x, f, sum);
+          }
         }
     }
   }
@@ -237,12 +256,13 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
 #pragma unroll
       for (int e = 0; e < 16; ++e) o[d][e] = o[d][e] * f1 + place[(16 * d + e) * 64] * f2;
   }
-  if (r0 + l32 >= rows.len) return;                       // both lanes of a pair alike
+  const int row = r0 + (lane_now() & 31);
+  if (row >= rows.len) return;                            // both lanes of a pair alike
   const float f = total == 0.0f ? 0.0f : 1.0f / total;
-  uint16_t* dst = p.o + ((rows.first + r) * p.H + head) * D;
+  uint16_t* dst = p.o + ((rows.first + row) * p.H + head) * D;
 #pragma unroll
   for (int d = 0; d < 4; ++d) store_row32(dst + 32 * d, o[d], f, h);
-  if (p.lse && h == 0) p.lse[(int64_t(rows.b) * p.H + head) * p.T + rows.start + r] = m * p.scale + __logf(total);
+  if (p.lse && h == 0) p.lse[(int64_t(rows.b) * p.H + head) * p.T + rows.start + row] = m * p.scale + __logf(total);
 }
 
 }  // namespace
