@@ -734,7 +734,8 @@ int kda_latent_prefill(const void* q, const void* k, const void* k_shared, const
  *   workspace   at least kda_latent_backward_workspace_size(...) bytes; contents on
  *               entry do not matter; calls that share one must not overlap
  * What is not finite reaches what it does in kda_attn_backward.  Sizes as for
- * kda_latent_prefill, workgroups counted for queries and keys together.
+ * kda_latent_prefill, workgroups counted for queries and keys together, and fewer
+ * than 2^23 for keys: H for each row tile of keys (and each part of it, see below).
  * Deterministic: no atomics, one order of every sum.
  */
 int kda_latent_backward(const void* q, const void* k, const void* k_shared, const void* v, int64_t q_stride,

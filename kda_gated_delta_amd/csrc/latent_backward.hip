@@ -513,7 +513,8 @@ Plan plan_for(int64_t B, int T, int T_kv, int H, int num_seqs) {
   x.ds = size_t(x.parts) * H * rows * S;
   x.shared = (rows * S / 4 + 255) / 256;
   x.sums = x.shared + (x.parts > 1 ? (rows * H * 2 * D / 4 + 255) / 256 : 0);
-  x.fits = (x.slots + x.key_slots * x.parts) * H <= kda::kMostBlocks && x.sums <= kda::kMostBlocks;
+  const int64_t keys = x.key_slots * x.parts * H;          // of twice as many threads
+  x.fits = x.slots * H + keys <= kda::kMostBlocks && keys <= kda::kMostBlocks / 2 && x.sums <= kda::kMostBlocks;
   return x;
 }
 
