@@ -483,7 +483,7 @@ int parts_for(int64_t key_slots, int T, int N, bool packed, int H) {
 }
 
 int64_t slots_for(int B, int T, int num_seqs) {
-  return num_seqs ? int64_t(T) / BM + num_seqs : int64_t(B) * ((T + BM - 1) / BM);
+  return num_seqs ? int64_t(T) / BM + num_seqs : int64_t(B) * ((int64_t(T) + BM - 1) / BM);
 }
 
 size_t stat_floats(int64_t B, int64_t T, int64_t H) { return size_t((B * T * H + 3) / 4 * 4); }
@@ -503,9 +503,10 @@ struct Plan {
   size_t bytes() const { return (2 * stats + dkv + ds) * sizeof(float); }
 };
 Plan plan_for(int64_t B, int T, int T_kv, int H, int num_seqs) {
-  Plan x;
+  Plan x{};
   x.slots = slots_for(int(B), T, num_seqs);
   x.key_slots = slots_for(int(B), T_kv, num_seqs);
+  if (x.slots > kda::kMostBlocks || x.key_slots > kda::kMostBlocks) return x;   // (what follows fits 64 bits then)
   x.parts = parts_for(x.key_slots, T, num_seqs ? num_seqs : int(B), num_seqs > 0, H);
   x.stats = stat_floats(B, T, H);
   const int64_t rows = B * T_kv;

@@ -279,9 +279,9 @@ extern "C" int kda_latent_prefill(const void* q, const void* k, const void* k_sh
   if (!q || !o || (T_kv && (!k || !k_shared || !v))) return KDA_ERR_NULL;
   for (const void* y : {q, k, k_shared, v, static_cast<const void*>(o), static_cast<const void*>(lse)})
     if (!kda::aligned16(y)) return KDA_ERR_ALIGN;            // no lse: a null pointer passes
-  const int64_t slots = cu_seqlens ? int64_t(T) / BM + num_seqs : int64_t(B) * ((T + BM - 1) / BM);
+  const int64_t slots = cu_seqlens ? int64_t(T) / BM + num_seqs : int64_t(B) * ((int64_t(T) + BM - 1) / BM);
   const int64_t blocks = slots * H;
-  if (blocks > kda::kMostBlocks) return KDA_ERR_SHAPE;
+  if (slots > kda::kMostBlocks || blocks > kda::kMostBlocks) return KDA_ERR_SHAPE;
   const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                  static_cast<const uint16_t*>(k_shared), q_stride, k_stride, v_stride, s_stride, k_head, v_head,
                  cu_seqlens, cu_seqlens_kv, cu_seqlens ? num_seqs : B, T, T_kv, H, int(slots), scale,

@@ -5,7 +5,7 @@ dK and dV.  Without a GPU; only refused calls are made."""
 import pytest
 
 import kda_gated_delta_amd as kda
-from test_latent_abi import E_SHAPE, FAKE, backward
+from test_latent_abi import E_SHAPE, FAKE, backward, prefill
 
 MOST = (1 << 23) - 1               # of 512 threads
 
@@ -26,3 +26,16 @@ def test_the_most_workgroups():
     # queries and keys together, of one head
     assert kda.latent_backward_workspace_size(MOST, 1, 1, 1) > 0
     assert kda.latent_backward_workspace_size(MOST + 1, 1, 1, 1) == 0
+
+
+def test_the_count_does_not_overflow():
+    """2^53 tiles times 2^11 heads are 0 in 64 bits."""
+    far = dict(B=1 << 30, H=2048, qs=2048 * 192)
+    assert prefill(**far, T=1 << 30, K=1) == E_SHAPE
+    for T, K in ((1 << 30, 1), (1, 1 << 30), (1 << 30, 1 << 30)):
+        assert backward(**far, T=T, K=K) == E_SHAPE
+        assert kda.latent_backward_workspace_size(1 << 30, T, K, 2048) == 0
+    most = 2 ** 31 - 1
+    assert prefill(B=2, T=most, K=1, H=4) == E_SHAPE and prefill(B=1, T=most, K=1, H=43690, qs=43690 * 192) == E_SHAPE
+    for T, K in ((most, 1), (1, most)):
+        assert backward(B=1, T=T, K=K, H=43690, qs=43690 * 192) == E_SHAPE
