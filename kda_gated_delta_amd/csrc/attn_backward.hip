@@ -387,7 +387,7 @@ __global__ __launch_bounds__(256) void attn_sum_kernel(Params p) {
 bool one_length(int N, bool packed) { return !packed || N == 1; }
 int parts_for(int64_t slots, int T, int N, bool packed, int HQ, int HKV) {
   const int64_t units = slots * HKV, cus = kda::device_cus(), want = (one_length(N, packed) ? 4 : 3) * cus;
-  if (units >= want) return 1;
+  if (units >= want || slots > kda::kMostBlocks) return 1;   // (of more slots units may have overflowed)
   const int64_t len = kda::attn_typical(T, N, packed);
   const int64_t walk = (len / kTile / 2 + 1) * (HQ / HKV);
   const int64_t most = walk / 2 < 1 ? 1 : (walk / 2 > 16 ? 16 : walk / 2);
@@ -396,12 +396,12 @@ int parts_for(int64_t slots, int T, int N, bool packed, int HQ, int HKV) {
 }
 
 int64_t slots_for(int B, int T, int num_seqs) {
-  return num_seqs ? int64_t(T) / BM + num_seqs : int64_t(B) * ((T + BM - 1) / BM);
+  return num_seqs ? int64_t(T) / BM + num_seqs : int64_t(B) * ((int64_t(T) + BM - 1) / BM);
 }
 
 // Whether a launch takes the workgroups.  (The parts' sum, of few units, has fewer.)
 bool fits(int64_t slots, int parts, int HQ, int HKV) {
-  return head_blocks(slots, HQ, HKV) + slots * HKV * parts <= kda::kMostBlocks;
+  return slots <= kda::kMostBlocks && head_blocks(slots, HQ, HKV) + slots * HKV * parts <= kda::kMostBlocks;
 }
 
 size_t stat_floats(int64_t B, int64_t T, int64_t HQ) { return size_t((B * T * HQ + 3) / 4 * 4); }
