@@ -709,9 +709,9 @@ size_t kda_attn_decode_workspace_size(int32_t N, int32_t Q, int32_t HQ, int32_t 
  * sequence's outputs from its own row on and no others, also where it holds
  * infinities or NaN; a score of -inf is a weight of zero; rows outside the
  * sequences are neither read nor written.
- * Sizes: B >= 1, T, T_kv >= 0, 1 <= H <= 65535, fewer than 2^24 workgroups: H for
- * each of the B * ceil(T / 128) row tiles, or of the T / 128 + num_seqs that packed
- * sequences may have.  o and lse must not alias inputs.  Deterministic.
+ * Sizes: B >= 1, T, T_kv >= 0, 1 <= H <= 43690 (q_stride is H * 192 to 2^23), fewer
+ * than 2^24 workgroups: H for each of the B * ceil(T / 128) row tiles, or of the
+ * T / 128 + num_seqs that packed sequences may have.  o and lse must not alias inputs.  Deterministic.
  */
 int kda_latent_prefill(const void* q, const void* k, const void* k_shared, const void* v, int64_t q_stride,
                        int64_t k_stride, int64_t k_head, int64_t s_stride, int64_t v_stride, int64_t v_head,

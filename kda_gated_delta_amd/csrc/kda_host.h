@@ -104,10 +104,12 @@ inline int latent_head(int64_t stride) {
   if (stride < 0 || stride > (int64_t(1) << 40)) return KDA_ERR_SHAPE;
   return stride % 8 == 0 ? KDA_OK : KDA_ERR_ALIGN;
 }
+// (a row of queries is heads x 192 of at most 2^23)
+constexpr int32_t kLatentHeads = (1 << 23) / 192;
 inline int latent_check(const LatentLayout& x, const int32_t* cu, const int32_t* cu_kv, int32_t num_seqs, int32_t B,
                         int32_t T, int32_t T_kv, int32_t H, float scale) {
   if (B < 1 || T < 0 || T_kv < 0 || (!cu) != (!cu_kv) || (cu && (B != 1 || num_seqs < 1))) return KDA_ERR_SHAPE;
-  if (H < 1 || H > 65535) return KDA_ERR_SHAPE;
+  if (H < 1 || H > kLatentHeads) return KDA_ERR_SHAPE;
   int e = attn_scale(scale);
   if (e == KDA_OK) e = latent_stride(x.q_stride, int64_t(H) * 192);
   if (e == KDA_OK) e = latent_stride(x.k_stride, 128);

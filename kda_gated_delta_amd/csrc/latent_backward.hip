@@ -544,7 +544,7 @@ int launch(const Params& p, const Plan& x, hipStream_t stream) {
 }  // namespace
 
 extern "C" size_t kda_latent_backward_workspace_size(int32_t B, int32_t T, int32_t T_kv, int32_t H, int32_t num_seqs) {
-  if (B < 1 || T < 0 || T_kv < 0 || H < 1 || H > 65535 || num_seqs < 0 || (num_seqs && B != 1)) return 0;
+  if (B < 1 || T < 0 || T_kv < 0 || H < 1 || H > kda::kLatentHeads || num_seqs < 0 || (num_seqs && B != 1)) return 0;
   if (T == 0 && T_kv == 0) return 0;
   const Plan x = plan_for(B, T, T_kv, H, num_seqs);
   return x.fits ? x.bytes() : 0;

@@ -39,3 +39,17 @@ def test_the_count_does_not_overflow():
     assert prefill(B=2, T=most, K=1, H=4) == E_SHAPE and prefill(B=1, T=most, K=1, H=43690, qs=43690 * 192) == E_SHAPE
     for T, K in ((most, 1), (1, most)):
         assert backward(B=1, T=T, K=K, H=43690, qs=43690 * 192) == E_SHAPE
+
+
+def test_the_most_heads():
+    """A row of queries is 192 H elements of at most 2^23."""
+    most = (1 << 23) // 192
+    assert most == 43690
+    for call in (prefill, backward):
+        assert call(H=most, qs=192 * most, B=1 << 20) == E_SHAPE          # (for its workgroups)
+        assert call(T=0, K=0, H=most, qs=192 * most) == 0
+        for H in (most + 1, 65535):
+            assert call(T=0, K=0, H=H, qs=1 << 23) == E_SHAPE and call(T=0, K=0, H=H, qs=192 * H) == E_SHAPE
+    assert kda.latent_backward_workspace_size(1, 1, 1, most) > 0
+    for H in (most + 1, 65535):
+        assert kda.latent_backward_workspace_size(1, 1, 1, H) == 0
