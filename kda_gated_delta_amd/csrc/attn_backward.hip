@@ -37,6 +37,7 @@ using namespace kda::attn;
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int BM = 32 * kWaves;
+static_assert(BM == kda::kAttnRows);
 
 struct Params {
   const uint16_t *q, *k, *v, *o, *d_out;
@@ -334,19 +335,6 @@ __global__ __launch_bounds__(kThreads, 2) void attn_grads_kernel(Params p) {
 
 // ---------------------------------------------------------------- the parts' sum
 
-__device__ __forceinline__ void store4(float* dst, f32x4 x) { *reinterpret_cast<f32x4*>(dst) = x; }
-__device__ __forceinline__ void store4(uint16_t* dst, f32x4 x) {
-  *reinterpret_cast<u32x2*>(dst) = (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
-}
-
-// Whether row t, the same for the whole wave, lies in a sequence: the wave looks
-// at 64 of them at a time.
-__device__ __forceinline__ bool in_sequence(const int32_t* cu, int N, int t) {
-  bool in = false;
-  for (int n = threadIdx.x & 63; n < N; n += 64) in |= t >= cu[n] && t < cu[n + 1];
-  return __any(in);
-}
-
 // Four elements of dK or dV (blockIdx.y) per thread.
 template <typename Out>
 __global__ __launch_bounds__(256) void attn_sum_kernel(Params p) {
@@ -395,16 +383,10 @@ int parts_for(int64_t slots, int T, int N, bool packed, int HQ, int HKV) {
   return int(parts < most ? parts : most);
 }
 
-int64_t slots_for(int B, int T, int num_seqs) {
-  return num_seqs ? int64_t(T) / BM + num_seqs : int64_t(B) * ((int64_t(T) + BM - 1) / BM);
-}
-
 // Whether a launch takes the workgroups.  (The parts' sum, of few units, has fewer.)
 bool fits(int64_t slots, int parts, int HQ, int HKV) {
   return slots <= kda::kMostBlocks && head_blocks(slots, HQ, HKV) + slots * HKV * parts <= kda::kMostBlocks;
 }
-
-size_t stat_floats(int64_t B, int64_t T, int64_t HQ) { return size_t((B * T * HQ + 3) / 4 * 4); }
 
 // Whether weights and score gradients are carried as two bfloat16 terms.  One
 // rounding of each adds as much error to a gradient as rounding the gradient
@@ -445,11 +427,11 @@ extern "C" size_t kda_attn_backward_workspace_size(int32_t B, int32_t T, int32_t
                                                    int32_t num_seqs) {
   if (B < 1 || T < 0 || num_seqs < 0 || (num_seqs && B != 1) || kda::attn_heads(HQ, HKV, Dh) != KDA_OK) return 0;
   if (T == 0) return 0;
-  const int64_t slots = slots_for(B, T, num_seqs);
+  const int64_t slots = kda::attn_slots(B, T, num_seqs);
   const int parts = parts_for(slots, T, num_seqs ? num_seqs : B, num_seqs > 0, HQ, HKV);
   if (!fits(slots, parts, HQ, HKV)) return 0;
   const size_t sums = parts > 1 ? size_t(parts) * 2 * B * T * HKV * D : 0;
-  return (2 * stat_floats(B, T, HQ) + sums) * sizeof(float);
+  return (2 * kda::attn_stat_floats(B, T, HQ) + sums) * sizeof(float);
 }
 
 extern "C" int kda_attn_backward(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
@@ -467,12 +449,12 @@ extern "C" int kda_attn_backward(const void* q, const void* k, const void* v, in
                         static_cast<const void*>(workspace)})
     if (!kda::aligned16(x)) return KDA_ERR_ALIGN;
   const int seqs = cu_seqlens ? num_seqs : 0, N = cu_seqlens ? num_seqs : B;
-  const int64_t slots = slots_for(B, T, seqs);
+  const int64_t slots = kda::attn_slots(B, T, seqs);
   const int parts = parts_for(slots, T, N, seqs > 0, HQ, HKV);
   if (!fits(slots, parts, HQ, HKV)) return KDA_ERR_SHAPE;
   if (workspace_bytes < kda_attn_backward_workspace_size(B, T, HQ, HKV, Dh, seqs)) return KDA_ERR_WORKSPACE;
   float* ws = static_cast<float*>(workspace);
-  const size_t stats = stat_floats(B, T, HQ), grads = size_t(parts) * B * T * HKV * D;
+  const size_t stats = kda::attn_stat_floats(B, T, HQ), grads = size_t(parts) * B * T * HKV * D;
   const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
                  static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_out), q_stride, k_stride, v_stride,
                  lse, cu_seqlens, N, B, T, HQ, HKV, int(slots), scale, dq, dk, dv,

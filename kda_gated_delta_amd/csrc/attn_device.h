@@ -141,6 +141,14 @@ __device__ __forceinline__ int find_ranked(int own_tiles, int N, int most, int r
   return __builtin_ctzll(have);
 }
 
+// Whether row t, the same for the whole wave, lies in a sequence: the wave looks
+// at 64 of them at a time.
+__device__ __forceinline__ bool in_sequence(const int32_t* cu, int N, int t) {
+  bool in = false;
+  for (int n = threadIdx.x & 63; n < N; n += 64) in |= t >= cu[n] && t < cu[n + 1];
+  return __any(in);
+}
+
 // Workgroups are dealt to the eight XCDs in turn, and each XCD has its own
 // cache.  The query heads of one tile that share a key/value head read the same
 // keys at about the same time: they follow one another on one XCD.  Of a
@@ -329,6 +337,12 @@ __device__ __forceinline__ void store_row32(float* row, const f32x16& acc, float
   for (int i = 0; i < 4; ++i)
     *reinterpret_cast<f32x4*>(row + 8 * i + 4 * h) =
         (f32x4){acc[4 * i] * f, acc[4 * i + 1] * f, acc[4 * i + 2] * f, acc[4 * i + 3] * f};
+}
+
+// Four float32 values, as they are or each rounded to bfloat16 once.
+__device__ __forceinline__ void store4(float* dst, f32x4 x) { *reinterpret_cast<f32x4*>(dst) = x; }
+__device__ __forceinline__ void store4(uint16_t* dst, f32x4 x) {
+  *reinterpret_cast<u32x2*>(dst) = (u32x2){pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
 }
 
 // vmcnt(0), nothing else

@@ -35,6 +35,7 @@ using namespace kda::attn;
 
 constexpr int kWaves = 4;
 constexpr int BM = 32 * kWaves;            // query rows of a workgroup
+static_assert(BM == kda::kAttnRows);
 
 struct Params {
   const uint16_t *q, *k, *v;
@@ -253,7 +254,7 @@ extern "C" int kda_attn_prefill(const void* q, const void* k, const void* v, int
   if (!q || !k || !v || !o) return KDA_ERR_NULL;
   for (const void* x : {q, k, v, static_cast<const void*>(o), static_cast<const void*>(lse)})
     if (!kda::aligned16(x)) return KDA_ERR_ALIGN;            // no lse: a null pointer passes
-  const int64_t slots = cu_seqlens ? int64_t(T) / BM + num_seqs : int64_t(B) * ((int64_t(T) + BM - 1) / BM);
+  const int64_t slots = kda::attn_slots(B, T, cu_seqlens ? num_seqs : 0);
   if (slots > kda::kMostBlocks) return KDA_ERR_SHAPE;
   const int64_t blocks = head_blocks(slots, HQ, HKV);
   if (blocks > kda::kMostBlocks) return KDA_ERR_SHAPE;

@@ -73,6 +73,14 @@ inline int attn_check(const int32_t* cu, int32_t num_seqs, int32_t B, int32_t T,
   return e;
 }
 
+// Row tiles that a prompt call may have (num_seqs: 0 without packed sequences), and the
+// floats that a statistic of every row and head takes.
+constexpr int kAttnRows = 128;
+inline int64_t attn_slots(int64_t B, int64_t T, int64_t num_seqs) {
+  return num_seqs ? T / kAttnRows + num_seqs : B * ((T + kAttnRows - 1) / kAttnRows);
+}
+inline size_t attn_stat_floats(int64_t B, int64_t T, int64_t heads) { return size_t((B * T * heads + 3) / 4 * 4); }
+
 // Length of a typical sequence of a prompt call.
 inline int64_t attn_typical(int T, int num_seqs, bool packed) { return packed ? T / num_seqs : T; }
 // Whether the forward walks a row tile's keys with two sets of waves, which halves

@@ -31,6 +31,7 @@ using namespace kda::latent;
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int BM = 32 * kWaves;
+static_assert(BM == kda::kAttnRows);
 
 struct Params {
   const uint16_t *q, *k, *v, *s, *o, *d_out;
@@ -416,19 +417,6 @@ __global__ __launch_bounds__(2 * kThreads, 2) void latent_dkv_kernel(Params p) {
 
 // ---------------------------------------------------------------- the parts' sums
 
-__device__ __forceinline__ void store4(float* dst, f32x4 x) { *reinterpret_cast<f32x4*>(dst) = x; }
-__device__ __forceinline__ void store4(uint16_t* dst, f32x4 x) {
-  *reinterpret_cast<u32x2*>(dst) = (u32x2){kda::pack_bf16(x[0], x[1]), kda::pack_bf16(x[2], x[3])};
-}
-
-// Whether row t, the same for the whole wave, lies in a sequence: the wave looks
-// at 64 of them at a time.
-__device__ __forceinline__ bool in_sequence(const int32_t* cu, int N, int t) {
-  bool in = false;
-  for (int n = threadIdx.x & 63; n < N; n += 64) in |= t >= cu[n] && t < cu[n + 1];
-  return __any(in);
-}
-
 // `parts` arrays of rows of WIDTH floats added up in order, four elements per
 // thread.  Rows outside the sequences are left as they are.
 template <typename Out>
@@ -482,12 +470,6 @@ int parts_for(int64_t key_slots, int T, int N, bool packed, int H) {
   return int(parts < most ? parts : most);
 }
 
-int64_t slots_for(int B, int T, int num_seqs) {
-  return num_seqs ? int64_t(T) / BM + num_seqs : int64_t(B) * ((int64_t(T) + BM - 1) / BM);
-}
-
-size_t stat_floats(int64_t B, int64_t T, int64_t H) { return size_t((B * T * H + 3) / 4 * 4); }
-
 // Whether weights and score gradients are carried as two bfloat16 terms, which leaves a
 // gradient the error of its own rounding instead of 1.41 times that (by chance more
 // where there are few of them, 1.46 with 300 rows x 5 heads) and there costs little: 48.5 to
@@ -504,11 +486,11 @@ struct Plan {
 };
 Plan plan_for(int64_t B, int T, int T_kv, int H, int num_seqs) {
   Plan x{};
-  x.slots = slots_for(int(B), T, num_seqs);
-  x.key_slots = slots_for(int(B), T_kv, num_seqs);
+  x.slots = kda::attn_slots(B, T, num_seqs);
+  x.key_slots = kda::attn_slots(B, T_kv, num_seqs);
   if (x.slots > kda::kMostBlocks || x.key_slots > kda::kMostBlocks) return x;   // (what follows fits 64 bits then)
   x.parts = parts_for(x.key_slots, T, num_seqs ? num_seqs : int(B), num_seqs > 0, H);
-  x.stats = stat_floats(B, T, H);
+  x.stats = kda::attn_stat_floats(B, T, H);
   const int64_t rows = B * T_kv;
   x.dkv = x.parts > 1 ? size_t(x.parts) * rows * H * 2 * D : 0;
   x.ds = size_t(x.parts) * H * rows * S;

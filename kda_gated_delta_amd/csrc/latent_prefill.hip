@@ -30,6 +30,7 @@ using namespace kda::latent;
 
 constexpr int kWaves = 4;
 constexpr int BM = 32 * kWaves;                      // query rows of a workgroup
+static_assert(BM == kda::kAttnRows);
 constexpr int kBuffer = 2 * kTileBytes + kThinBytes; // K, V, the shared part
 
 struct Params {
@@ -279,7 +280,7 @@ extern "C" int kda_latent_prefill(const void* q, const void* k, const void* k_sh
   if (!q || !o || (T_kv && (!k || !k_shared || !v))) return KDA_ERR_NULL;
   for (const void* y : {q, k, k_shared, v, static_cast<const void*>(o), static_cast<const void*>(lse)})
     if (!kda::aligned16(y)) return KDA_ERR_ALIGN;            // no lse: a null pointer passes
-  const int64_t slots = cu_seqlens ? int64_t(T) / BM + num_seqs : int64_t(B) * ((int64_t(T) + BM - 1) / BM);
+  const int64_t slots = kda::attn_slots(B, T, cu_seqlens ? num_seqs : 0);
   const int64_t blocks = slots * H;
   if (slots > kda::kMostBlocks || blocks > kda::kMostBlocks) return KDA_ERR_SHAPE;
   const Params p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
