@@ -7,10 +7,10 @@
 // the shared part's summed over all heads.
 //
 // Workgroups of 128 query rows walk the keys for dQ (and first make lse in powers of
-// two and delta), then workgroups of 128 keys walk the query rows for dK and dV.  Every head has keys of its own, so a walk belongs to one head;
-// only the shared part's gradient crosses heads.  Its terms are written in float32
-// per head and added in order by latent_sum_kernel, as the parts of a key tile that
-// several workgroups share are.
+// two and delta), then workgroups of 128 keys walk the query rows for dK and dV.  Every
+// head has keys of its own, so a walk belongs to one head; only the shared part's
+// gradient crosses heads.  Its terms are written in float32 per head and added in order
+// by latent_sum_kernel, as the parts of a key tile that several workgroups share are.
 //
 // Weights and score gradients are made in both walks: 1152 products of a pair's numbers
 // where the formulas have 832.  One walk for all would add dQ up across workgroups, in
@@ -120,11 +120,12 @@ __global__ __launch_bounds__(kThreads, 2) void latent_dq_kernel(Params p) {
   };
 
   // delta.  The rounding of o to bfloat16 enters it, and with it every score's
-  // gradient of the row (see attn_backward.hip).  Of rows that see few keys (four
-  // tiles at most) it is made as sum_j P_ij (dO V^T)_ij, to which it is equal: dQ's error,
-  // in halves of a rounding's, is 1.54 with none or two tiles so, 1.43 with four and 1.42 with
-  // all (4 sequences of up to 690 tokens, 2 heads); four cost 5 us where no row sees more and
-  // nothing elsewhere, eight 15 of 570.
+  // gradient of the row (see attn_backward.hip).  Where few keys are seen (four tiles at
+  // most, by the workgroup's last row; the walk is one for all its rows) it is made as
+  // sum_j P_ij (dO V^T)_ij, to which it is equal: dQ's error, in halves of a rounding's, is
+  // 1.54 with none or two tiles so, 1.43 with four and 1.42 with all (4 sequences of up to 690
+  // tokens, 2 heads); four cost 5 us where no row sees more and nothing elsewhere, eight 15 of
+  // 570.
   float delta = 0.0f;
   if (tiles <= 4) {
     if (tiles > 0) issue(0, 0);
@@ -313,7 +314,8 @@ __global__ __launch_bounds__(2 * kThreads, 2) void latent_dkv_kernel(Params p) {
         fence();
         if (j + kAhead - 1 < 20) fetch(j + kAhead - 1);
         if (j >= 6 && j < 10) stat[j - 6] = *reinterpret_cast<const f32x4*>(stats + 32 * w + 8 * (j - 6) + 4 * h);
-        if (j >= 14 && j < 18) del[j - 14] = *reinterpret_cast<const f32x4*>(stats + 64 + 32 * w + 8 * (j - 14) + 4 * h);
+        if (j >= 14 && j < 18)
+          del[j - 14] = *reinterpret_cast<const f32x4*>(stats + 64 + 32 * w + 8 * (j - 14) + 4 * h);
         fence();
         if (j < 12) {
           s = mfma32(a[j % kAhead], kk[j], s);

@@ -72,9 +72,9 @@ struct Params {
   float* lse;
   int rows, tile_rows, row_tiles;         // Q x H; rows of one tile (a multiple of 16); tiles
   int waves;                                 // pieces
-  float* parts;                              // [2 x pieces][tile_rows x kPart]: a piece has one of its first segment, one of its last
-  int *owner, *last_owner;                   // [segments]: first part and last piece of those cut, -1 for the others
-  int* cut;                                  // [pieces]: the segment that is cut behind the piece and begins in it, or -1
+  float* parts;                              // [2 x pieces][tile_rows x kPart]: of a piece's first segment, its last
+  int *owner, *last_owner;                   // [segments]: first part (-1: not cut) and, of those cut, last piece
+  int* cut;                                  // [pieces]: the segment that begins in the piece and is cut behind, or -1
   bool by_piece;                             // pieces, of which few are followed by a cut, are fewer than segments
 };
 
@@ -322,7 +322,8 @@ __global__ __launch_bounds__(kThreads, 2) void latent_decode_kernel(Params p) {
           const int key_at = key * R + ((g4 ^ swirl(key)) * 16);
           const int shared_at = kShared + key * 2 * S + ((g4 ^ swirl2(key)) * 16);
           auto fetch = [&](int i) {
-            a[i % kAhead] = *reinterpret_cast<const u32x4*>(tile + (i < 8 ? key_at ^ i * 64 : shared_at ^ (i - 8) * 64));
+            const int at = i < 8 ? key_at ^ i * 64 : shared_at ^ (i - 8) * 64;
+            a[i % kAhead] = *reinterpret_cast<const u32x4*>(tile + at);
           };
           const uint32_t scales = *reinterpret_cast<const uint32_t*>(exponents_of(tile, key));
 #pragma unroll
@@ -927,7 +928,7 @@ __global__ __launch_bounds__(64 * STREAMS) void latent_decode_join_kernel(Params
   const int64_t segment = p.by_piece ? p.cut[which] : int(which);
   if (segment < 0) return;
   const int row_tile = int(in / (R / 16 / kTiles)), column_tile = int(in % (R / 16 / kTiles)) * kTiles;
-  const int slot = p.owner[segment], last = p.last_owner[segment];
+  const int slot = p.owner[segment], last = p.last_owner[segment];   // (last holds anything unless slot says: cut)
   const int64_t n = segment / p.row_tiles;
   const int r = 16 * row_tile + l16, row = int(segment - n * p.row_tiles) * p.tile_rows + r;
   if (slot < 0 || row - l16 >= p.rows) return; // finished by its workgroup; or no row
@@ -943,7 +944,8 @@ __global__ __launch_bounds__(64 * STREAMS) void latent_decode_join_kernel(Params
   auto fetch = [&](int i, int k) {
     const float* from = at(min(i, count - 1));
 #pragma unroll
-    for (int d = 0; d < kTiles; ++d) x[k][d] = *reinterpret_cast<const f32x4*>(from + in_part(row_tile, column_tile + d, lane));
+    for (int d = 0; d < kTiles; ++d)
+      x[k][d] = *reinterpret_cast<const f32x4*>(from + in_part(row_tile, column_tile + d, lane));
     stat[k] = *reinterpret_cast<const float2*>(from + p.tile_rows * R + 2 * r);
   };
 #pragma unroll
@@ -953,7 +955,8 @@ __global__ __launch_bounds__(64 * STREAMS) void latent_decode_join_kernel(Params
     for (int k = 0; k < kAhead; ++k) {
       if (i0 + k * STREAMS >= count) break;
       const float now = fmaxf(m, stat[k].x);
-      const float f = __builtin_amdgcn_exp2f((m - base(now)) * c), g = __builtin_amdgcn_exp2f((stat[k].x - base(now)) * c);
+      const float f = __builtin_amdgcn_exp2f((m - base(now)) * c);
+      const float g = __builtin_amdgcn_exp2f((stat[k].x - base(now)) * c);
       m = now;
       sum = sum * f + stat[k].y * g;
 #pragma unroll
@@ -1055,12 +1058,14 @@ extern "C" int kda_latent_decode(const void* q, int64_t q_stride, const void* c_
   int* owner = reinterpret_cast<int*>(static_cast<char*>(workspace) + x.parts);
   const Params p{static_cast<const uint16_t*>(q), q_stride, static_cast<const uint8_t*>(c_cache),
                  static_cast<const uint8_t*>(c_scale), static_cast<const uint16_t*>(k_cache), uint32_t(c_page),
-                 uint32_t(scale_page), uint32_t(k_page), page_table, table_stride, kv_lens, N, Q, H, table_width, __builtin_ctz(page_size), num_pages,
-                 scale, static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows, x.row_tiles, x.pieces,
-                 static_cast<float*>(workspace), owner, owner + x.segments, owner + 2 * x.segments, x.segments > x.pieces};
+                 uint32_t(scale_page), uint32_t(k_page), page_table, table_stride, kv_lens, N, Q, H, table_width,
+                 __builtin_ctz(page_size), num_pages, scale, static_cast<uint16_t*>(o), lse, x.rows, x.tile_rows,
+                 x.row_tiles, x.pieces, static_cast<float*>(workspace), owner, owner + x.segments,
+                 owner + 2 * x.segments, x.segments > x.pieces};
   const hipStream_t st = kda::as_stream(stream);
   // No more pieces than units that the tables could hold.
-  const int64_t most = x.segments * ((int64_t(table_width) * page_size + kUnit - 1) / kUnit + (x.many ? kManyExtra : kExtra));
+  const int64_t units = (int64_t(table_width) * page_size + kUnit - 1) / kUnit;
+  const int64_t most = x.segments * (units + (x.many ? kManyExtra : kExtra));
   const int pieces = int(x.pieces < most ? x.pieces : most);
   const dim3 grid{unsigned(pieces)};
   if (x.many)

@@ -44,7 +44,10 @@ struct Params {
   float* lse;
 };
 
+// A tile that all rows of a wave see, one that the diagonal crosses, and such a one of
+// whose values some are not finite.
 constexpr int kWhole = 0, kDiagonal = 1, kPartly = 2;
+
 // Eight bfloat16 values, zero for those that are not finite.
 __device__ __forceinline__ bf16x8 finite_or_zero(bf16x8 x) {
   typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
@@ -79,7 +82,7 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
   float m = -INFINITY, l = 0.0f;                          // l: this lane's keys only, until the end
   const float c = p.scale * kLog2e;
 
-  const int see0 = r0 + keys.shift;                       // the last key that the wave's first row sees, -1 or less: none
+  const int see0 = r0 + keys.shift;                       // the last key that the wave's first row sees (below 0: none)
   const int seen = min(rows.row0 + BM, rows.len) + keys.shift;   // keys that the tile's last row sees
   const int tiles = max(seen + kTile - 1, 0) / kTile;
   TileLoad<kWaves> kload, vload;
@@ -180,7 +183,8 @@ __global__ __launch_bounds__(64 * kWaves * kSplit, 2) void latent_prefill_kernel
   // Tiles that all rows of the wave see, those that the diagonal crosses (two at
   // most, since 32 rows end within 32 keys; none perhaps, or none of this half's),
   // and those that other waves of the workgroup still take.
-  const int whole = min(max(see0 + 1, 0) / kTile, tiles), some = see0 + 31 < 0 ? 0 : min((see0 + 31) / kTile + 1, tiles);
+  const int whole = min(max(see0 + 1, 0) / kTile, tiles);
+  const int some = see0 + 31 < 0 ? 0 : min((see0 + 31) / kTile + 1, tiles);
   int i = 0;
   for (; i * kSplit + half < whole; ++i) {
     arrive(i);
