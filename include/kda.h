@@ -526,8 +526,9 @@ size_t kda_chunk_backward_workspace_size(int32_t B, int32_t T, int32_t H, int32_
  *   o           bf16 [B, T, HQ, 128], dense
  *   lse         fp32 [B, HQ, T], dense, or NULL
  * A token reaches the outputs of its own sequence from its own row on and no
- * others, also where it holds infinities or NaN.  A score of -inf is a weight of
- * zero; a row without any other gives o = 0 and lse = -inf.
+ * others, also where it holds infinities or NaN (the last bits apart of up to 31 rows
+ * before it, whose weights are rounded relative to a maximum that follows all 32).  A
+ * score of -inf is a weight of zero; a row without any other gives o = 0 and lse = -inf.
  * Sizes: B >= 1, T >= 0 (0 enqueues nothing), 1 <= HQ <= 65535, and fewer than
  * 2^24 workgroups: HQ for each of the B * ceil(T / 128) row tiles, or of the
  * T / 128 + num_seqs that packed sequences may have (the backward: HQ + HKV).  o
@@ -705,10 +706,10 @@ size_t kda_attn_decode_workspace_size(int32_t N, int32_t Q, int32_t HQ, int32_t 
  *   o           bf16 [B, T, H, 128], dense
  *   lse         fp32 [B, H, T], dense, or NULL
  * Queries without keys (the first Tq - Tk, where there are more queries) give
- * o = 0 and lse = -inf.  As for kda_attn_prefill: a token reaches its own
- * sequence's outputs from its own row on and no others, also where it holds
- * infinities or NaN; a score of -inf is a weight of zero; rows outside the
- * sequences are neither read nor written.
+ * o = 0 and lse = -inf.  A token reaches its own sequence's outputs from its own row
+ * on and not a bit of any others, also where it holds infinities or NaN.  As for
+ * kda_attn_prefill: a score of -inf is a weight of zero; rows outside the sequences
+ * are neither read nor written.
  * Sizes: B >= 1, T, T_kv >= 0, 1 <= H <= 43690 (q_stride is H * 192 to 2^23), fewer
  * than 2^24 workgroups: H for each of the B * ceil(T / 128) row tiles, or of the
  * T / 128 + num_seqs that packed sequences may have.  o and lse must not alias inputs.  Deterministic.
@@ -733,8 +734,10 @@ int kda_latent_prefill(const void* q, const void* k, const void* k_shared, const
  *               were; keys that no query sees have gradients of zero.
  *   workspace   at least kda_latent_backward_workspace_size(...) bytes; contents on
  *               entry do not matter; calls that share one must not overlap
- * What is not finite reaches what it does in kda_attn_backward.  Sizes as for
- * kda_latent_prefill, workgroups counted for queries and keys together, and fewer
+ * A token reaches only its own sequence's gradients, whatever it holds; there an
+ * infinity or NaN may also reach gradients of up to 62 tokens beside it that do not
+ * depend on it (as a product with a weight of 0, in the 32 rows by 32 keys that the
+ * diagonal crosses).  Sizes as for kda_latent_prefill, workgroups counted for queries and keys together, and fewer
  * than 2^23 for keys: H for each row tile of keys (and each part of it, see below).
  * Deterministic: no atomics, one order of every sum.
  */
@@ -779,7 +782,7 @@ size_t kda_latent_backward_workspace_size(int32_t B, int32_t T, int32_t T_kv, in
  * scale is e + 127 and a code is value / 2^e, rounded to nearest even; infinities
  * and NaN become NaN.  (Values above 448 * 2^119, which only the last 3% of
  * bfloat16's largest binade are, become that.)  Other tokens are left as they are.
- * The slots that are stored must differ.  T < 2^27.
+ * The slots that are stored must differ.  T <= 2^27 - 8.
  */
 int kda_latent_cache_store(const void* c, const void* k_shared, int64_t c_stride, int64_t s_stride,
                            const int32_t* slots, int32_t T, void* c_cache, void* c_scale, void* k_cache,
@@ -798,8 +801,8 @@ int kda_latent_cache_store(const void* c, const void* k_shared, int64_t c_stride
  *   k_shared    bf16 [num_tokens, 64], dense
  * Values are exact.  A token without a page (its entry outside [0, num_pages), or
  * past table_width) gives zeros; rows outside the sequences are left as they were.
- * Sizes: num_seqs, num_pages, table_width >= 1, 0 <= num_tokens < 2^29 (0 enqueues
- * nothing).
+ * Sizes: num_seqs, num_pages, table_width >= 1, 0 <= num_tokens <= 2^29 - 32 (0
+ * enqueues nothing).
  */
 int kda_latent_cache_load(const void* c_cache, const void* c_scale, const void* k_cache, int32_t page_size,
                           int64_t c_page, int64_t scale_page, int64_t k_page, int32_t num_pages,

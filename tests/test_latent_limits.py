@@ -5,7 +5,7 @@ dK and dV.  Without a GPU; only refused calls are made."""
 import pytest
 
 import kda_gated_delta_amd as kda
-from test_latent_abi import E_SHAPE, FAKE, backward, prefill
+from test_latent_abi import E_ALIGN, E_NULL, E_SHAPE, FAKE, NULL, OFF, backward, load, prefill, store
 
 MOST = (1 << 23) - 1               # of 512 threads
 
@@ -53,3 +53,9 @@ def test_the_most_heads():
     assert kda.latent_backward_workspace_size(1, 1, 1, most) > 0
     for H in (most + 1, 65535):
         assert kda.latent_backward_workspace_size(1, 1, 1, H) == 0
+
+
+def test_the_most_tokens():
+    """Of a store 8 to a workgroup, of a load 32: the last size that is taken fails for something else."""
+    assert store(T=(1 << 27) - 8, slots=NULL) == E_NULL and store(T=(1 << 27) - 7, slots=NULL) == E_SHAPE
+    assert load(T=(1 << 29) - 31) == E_SHAPE and load(T=(1 << 29) - 32, c=OFF) == E_ALIGN
