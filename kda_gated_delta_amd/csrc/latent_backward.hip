@@ -16,7 +16,7 @@
 // where the formulas have 832.  One walk for all would add dQ up across workgroups, in
 // float32 through memory and in order (attn_backward.hip has no such sums either).
 // What bounds the walks are the products, at the power limit (8192 tokens x 16 heads:
-// dK and dV 609 to 646 us, 0.69 TFLOP, 1070 TFLOP/s; dQ 476 to 491 us, 0.55 TFLOP, 1120;
+// dK and dV 609 to 646 us, 0.69 TFLOP, 1070 TFLOP/s; dQ 476 to 512 us, 0.55 TFLOP, 1120;
 // sum 8; a large matrix product reaches 1224 on this card).  lse2 and delta in a launch of
 // their own cost 7 to 13 us (6 samples of up to 500 tokens x 16 heads 89 to 82).  With all
 // of a walk in one wave and both walks in one launch of one workgroup to a compute

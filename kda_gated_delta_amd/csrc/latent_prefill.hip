@@ -14,11 +14,12 @@
 // unit.  The shared part is read for every head, from the caches: it is a fifth of
 // a tile and never stored 32-fold as a concatenated key would be.
 //
-// What bounds it: the products, at the power limit (8192 tokens x 32 heads 630 us, 1090
-// TFLOP/s, the matrix units 58% busy at 1.8 GHz; a large matrix product reaches 1224),
-// and with few rows a walk's latency (129 tokens x 8 heads: 8.4 us).  Parts of prompts
-// over long caches end unevenly (6 of up to 1500 tokens over up to 6000: 840 TFLOP/s; 10% of
-// the tiles' pairs are masked, 9% of the time waits for the last).
+// What bounds it: the products, at the power limit (8192 tokens x 32 heads 626 to 669 us by
+// the card, 1030 to 1090 TFLOP/s, the matrix units 57% busy at 1.75 to 1.8 GHz; a large
+// matrix product reaches 1224 on the faster cards), and with few rows a walk's latency (129
+// tokens x 8 heads: 8.4 us).  Parts of prompts over long caches end unevenly (6 of up to 1500
+// tokens over up to 6000: 765 to 840 TFLOP/s; 10% of the tiles' pairs are masked, 9% of the
+// time waits for the last).
 #include "kda_host.h"
 #include "latent_device.h"
 
